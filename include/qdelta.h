@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define QDELTA_ABI_VERSION 6
+#define QDELTA_ABI_VERSION 7
 
 typedef enum qd_status {
     QD_OK = 0,
@@ -274,6 +274,130 @@ int qdelta_eda_chunk_fwd(const void *q, const void *k, const void *v, const void
  * [N][H][d_v]; S [N][H][d_v][d_k] fp32 updated in place.  d_k, d_v in {64, 128}. */
 int qdelta_eda_step(const void *q, const void *k, const void *v, const void *e, float *S,
                     void *o, int N, int H, int d_k, int d_v, int dtype, void *stream);
+
+/*
+ * Operators around the recurrence: the short causal convolution before it, a selective
+ * state space scan that can stand in its place, and the gated norm after it.  Ownership,
+ * streams and errors are those above.  Element tensors and fp32 states are 16-byte aligned
+ * (QD_ERR_INVALID_ARG otherwise); weights, biases and their gradients are fp32, dtype one of
+ * qd_dtype.  Outputs and workspaces must be disjoint from every input and one another.
+ * Sizes whose launch would not fit 32 bits return QD_ERR_UNSUPPORTED.  Results do not depend
+ * on timing: sums over workgroups are taken from the workspace in a fixed order.
+ */
+
+/*
+ * Short causal depthwise convolution, channels last, with an optional SiLU:
+ *
+ *     pre[b,t,c] = bias[c] + sum_{j<W} w[c][j] x[b, t-W+1+j, c],   y = pre or silu(pre)
+ *
+ *   x, y      [B][T][D] elements (a layer's q, k or v viewed with D = H*d)
+ *   w [D][W], bias [D] or NULL (zero), fp32; W in {2, 3, 4}
+ *   S0, S_T   [B][W-1][D] elements: the W-1 inputs before the first token, and before the
+ *             next one, oldest first.  S0 NULL means zeros; S_T NULL is not written; S_T may
+ *             equal S0.
+ *   lens      [B] int32 or NULL: sequence b has lens[b] tokens (clamped to 0..T), followed by
+ *             padding.  Padding is not read as input, its rows of y are left as they were,
+ *             and S_T is the window at the sequence's end.
+ * B, T, D >= 0; T == 0 writes S_T = S0 (or zeros).
+ */
+int qdelta_conv_fwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens,
+                    void *y, void *S_T, int B, int T, int D, int W, int silu, int dtype, void *stream);
+
+/* One token for N sequences: x, y [N][D]; S [N][W-1][D] elements, shifted in place. */
+int qdelta_conv_step(const void *x, const float *w, const float *bias, void *S, void *y, int N, int D,
+                     int W, int silu, int dtype, void *stream);
+
+/*
+ * Gradients of sum(y dy) + sum(S_T dS_T) for the qdelta_conv_fwd of the same inputs (without
+ * lens: the convolution is causal, so padding only needs dy = 0 there).
+ *   dy [B][T][D], dS_T [B][W-1][D] or NULL (zero), elements
+ *   dx [B][T][D] and dS0 [B][W-1][D] or NULL (not written), elements; dw [D][W], and dbias [D]
+ *   or NULL (not written), fp32, summed over tokens and sequences.
+ * workspace: at least qdelta_conv_bwd_workspace_bytes, 16-byte aligned, overwritten.
+ */
+size_t qdelta_conv_bwd_workspace_bytes(int B, int T, int D, int W, int dtype);
+int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const void *dy,
+                    const void *dS_T, void *dx, float *dw, float *dbias, void *dS0, int B, int T, int D,
+                    int W, int silu, int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Selective state space scan.  Per sequence b, channel d of group g = d / (D / G), state n:
+ *
+ *     delta_t = softplus(dt_t + dt_bias)        (dt_t + dt_bias itself when softplus == 0)
+ *     h_t[n]  = exp(delta_t A[d][n]) h_{t-1}[n] + delta_t u_t B_t[g][n]
+ *     o_t     = (sum_n C_t[g][n] h_t[n] + Dskip[d] u_t) * silu(z_t)
+ *
+ *   u, dt, o  [B][T][D] elements;  Bm, Cm [B][T][G][N] elements;  D divisible by G
+ *   A         [D][N] fp32 (negative in the layer), 16-byte aligned; N in {16, 32, 64}
+ *   Dskip, dt_bias  [D] fp32 or NULL (zero);  z [B][T][D] elements or NULL (no gate factor)
+ *   S0, S_T   [B][D][N] fp32 (row = channel, column = state), 16-byte aligned; S0 NULL means
+ *             zeros, S_T NULL is not written, S_T may equal S0.
+ *   lens      as for qdelta_conv_fwd.
+ * T == 0 writes S_T = S0 (or zeros).  workspace: at least qdelta_ssm_fwd_workspace_bytes
+ * (non-zero where few channels make the call cut the time axis into segments), 16-byte
+ * aligned, overwritten; NULL when that is 0.
+ */
+size_t qdelta_ssm_fwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype);
+int qdelta_ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                   const float *Dskip, const void *z, const float *dt_bias, const float *S0,
+                   const int *lens, void *o, float *S_T, int B, int T, int D, int G, int N, int softplus,
+                   int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* One token for N_seq sequences: u, dt, z, o [N_seq][D], Bm, Cm [N_seq][G][N]; S
+ * [N_seq][D][N] fp32 updated in place. */
+int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                    const float *Dskip, const void *z, const float *dt_bias, float *S, void *o, int N_seq,
+                    int D, int G, int N, int softplus, int dtype, void *stream);
+
+/*
+ * Gradients of sum(o d_o) + sum(S_T dS_T) for the qdelta_ssm_fwd of the same inputs (without
+ * lens: padding only needs d_o = 0 there).
+ *   d_o [B][T][D] elements, dS_T [B][D][N] fp32 or NULL (zero)
+ *   du, ddt [B][T][D], dB, dC [B][T][G][N] (summed over the group's channels), elements;
+ *   dz [B][T][D] elements, required with z and NULL without;
+ *   dA [D][N] fp32; dDskip, ddt_bias [D] and dS0 [B][D][N] fp32, each NULL for not written.
+ * A non-finite gradient or state at one token can make dB and dC of its neighbour in the pair
+ * (2i, 2i + 1), counted within its segment of the time axis, non-finite too.
+ * workspace: at least qdelta_ssm_bwd_workspace_bytes, 16-byte aligned, overwritten (the
+ * states before every eighth token and the channel blocks' sums).
+ */
+size_t qdelta_ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype);
+int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                   const float *Dskip, const void *z, const float *dt_bias, const float *S0,
+                   const void *d_o, const float *dS_T, void *du, void *ddt, float *dA, void *dB, void *dC,
+                   float *dDskip, void *dz, float *ddt_bias, float *dS0, int B, int T, int D, int G, int N,
+                   int softplus, int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Group norm, channels last, with an optional SiLU and an optional gate.  The statistics of
+ * sample n, group g are over its L positions and the group's E = C / G channels:
+ *
+ *     v = (x - mean) / sqrt(var + eps) * weight[c] + bias[c],  f = v or silu(v)
+ *     y = f, or f * silu(gate) when gate is given
+ *
+ *   x, gate, y  [N][L][C] elements, gate NULL for none; C divisible by G.  A layer's output
+ *             [B][T][H][d] normed per token and head is N = B*T, L = 1, C = H*d, G = H.
+ *   weight, bias  [C] fp32 or NULL (one, zero);  eps >= 0 and finite
+ *   stats     [N][G][2] fp32, mean and 1 / sqrt(var + eps), or NULL (not written)
+ * workspace: at least qdelta_group_norm_fwd_workspace_bytes (0 where L == 1 and a group fits
+ * a workgroup's registers), 16-byte aligned, overwritten.
+ */
+size_t qdelta_group_norm_fwd_workspace_bytes(int N, int L, int C, int G, int dtype);
+int qdelta_group_norm_fwd(const void *x, const float *weight, const float *bias, const void *gate, void *y,
+                          float *stats, int N, int L, int C, int G, float eps, int silu, int dtype,
+                          void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of sum(y dy) for the qdelta_group_norm_fwd of the same inputs, whose stats are
+ * required.  dx [N][L][C] elements; dgate [N][L][C] elements, required with gate and NULL
+ * without; dweight, dbias [C] fp32, each NULL for not written.  workspace: at least
+ * qdelta_group_norm_bwd_workspace_bytes, 16-byte aligned, overwritten.
+ */
+size_t qdelta_group_norm_bwd_workspace_bytes(int N, int L, int C, int G, int dtype);
+int qdelta_group_norm_bwd(const void *x, const float *weight, const float *bias, const void *gate,
+                          const float *stats, const void *dy, void *dx, float *dweight, float *dbias,
+                          void *dgate, int N, int L, int C, int G, int silu, int dtype, void *workspace,
+                          size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -12,6 +12,14 @@ fallback path.
     qdelta_step(q, k, v, alpha, beta, lam, S, o=None) -> o        (S updated in place)
     qdelta_chunk_bwd(q, k, v, alpha, beta, lam, S0, d_o, dS_T=None, C=64)
         -> dict(dq, dk, dv, dalpha, dbeta, dlam, dS0)
+
+The operators around the recurrence (a short causal convolution before it, a selective state
+space scan beside it, a gated group norm after it), each forward, backward and, where it
+carries a state, for one token:
+
+    qdelta_conv_fwd / qdelta_conv_step / qdelta_conv_bwd
+    qdelta_ssm_fwd / qdelta_ssm_step / qdelta_ssm_bwd
+    qdelta_group_norm_fwd / qdelta_group_norm_bwd
 """
 import ctypes
 import os
@@ -71,6 +79,23 @@ def load_library():
     lib.qdelta_chunk_bwd_workspace_bytes.argtypes = [i] * 7
     lib.qdelta_chunk_bwd.restype = i
     lib.qdelta_chunk_bwd.argtypes = [vp] * 16 + [i] * 7 + [vp, sz, vp]
+    f = ctypes.c_float
+    for name, restype, argtypes in (
+            ("conv_fwd", i, [vp] * 7 + [i] * 6 + [vp]),
+            ("conv_step", i, [vp] * 5 + [i] * 5 + [vp]),
+            ("conv_bwd_workspace_bytes", sz, [i] * 5),
+            ("conv_bwd", i, [vp] * 10 + [i] * 6 + [vp, sz, vp]),
+            ("ssm_fwd_workspace_bytes", sz, [i] * 6),
+            ("ssm_fwd", i, [vp] * 12 + [i] * 7 + [vp, sz, vp]),
+            ("ssm_step", i, [vp] * 10 + [i] * 6 + [vp]),
+            ("ssm_bwd_workspace_bytes", sz, [i] * 6),
+            ("ssm_bwd", i, [vp] * 20 + [i] * 7 + [vp, sz, vp]),
+            ("group_norm_fwd_workspace_bytes", sz, [i] * 5),
+            ("group_norm_fwd", i, [vp] * 6 + [i] * 4 + [f] + [i] * 2 + [vp, sz, vp]),
+            ("group_norm_bwd_workspace_bytes", sz, [i] * 5),
+            ("group_norm_bwd", i, [vp] * 10 + [i] * 6 + [vp, sz, vp])):
+        fn = getattr(lib, "qdelta_" + name)
+        fn.restype, fn.argtypes = restype, argtypes
     _lib = lib
     return lib
 
@@ -383,3 +408,295 @@ def qdelta_step(q, k, v, alpha, beta, lam, S, o=None, stream=None, raw: bool = F
                 N, H, dk, dv, _dtype_code(dt), ctypes.c_void_p(s.cuda_stream))
         _raise(rc, "qdelta_step_raw" if raw else "qdelta_step")
         return o
+
+
+# ---------------------------------------------------------------- around the recurrence
+def _shape(t, name, dims):
+    """Shape of a device tensor with `dims` dimensions."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise QDeltaError(f"{name} must be a device tensor")
+    if t.dim() != dims:
+        raise QDeltaError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _check_all(device, checks):
+    """_check for each (tensor, name, dtype, shape), and that every tensor is on `device`."""
+    for t, name, dtype, shape in checks:
+        _check(t, name, dtype, shape)
+        if t is not None and t.device != device:
+            raise QDeltaError(f"{name} must be on {device}, got {t.device}")
+
+
+def _result(t, shape, dtype, device):
+    import torch
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+
+
+def _results(out, specs, device):
+    """The tensors named in specs {name: (wanted, shape, dtype)}: those the caller supplied in
+    out, new ones for the rest, None where not wanted."""
+    got = dict(out or {})
+    for name, (wanted, shape, dtype) in specs.items():
+        got[name] = _result(got.get(name), shape, dtype, device) if wanted else None
+    _check_all(device, [(got[name], name, dtype, shape) for name, (_, shape, dtype) in specs.items()])
+    return got
+
+
+def _workspace(workspace, need, device):
+    """(pointer, bytes) of the caller's workspace, or of a new one, and the tensor itself."""
+    import torch
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return None, 0, None
+    _check_all(device, [(workspace, "workspace", None, None)])
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+
+
+def _handle(s):
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=None, S_T=None,
+                    want_state: bool = True, stream=None):
+    """Short causal depthwise convolution over x [B,T,D] (fp32 or bf16), y = silu(pre) or pre.
+    w [D,W] and bias [D] fp32, W in 2..4; S0 [B,W-1,D] like x, the inputs before the first
+    token (None: zeros).  lens [B] int32: the tokens of each right-padded sequence; rows of y
+    past them are left as they were.  Returns (y, S_T); S_T is None when want_state is False,
+    and may be passed as S0."""
+    import torch
+    lib = load_library()
+    B, T, D = _shape(x, "x", 3)
+    W = _shape(w, "w", 2)[1]
+    s = _launch_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        dt, dev, f32 = x.dtype, x.device, torch.float32
+        code = _dtype_code(dt)
+        y = _result(y, (B, T, D), dt, dev)
+        if want_state:
+            S_T = _result(S_T, (B, W - 1, D), dt, dev)
+        _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
+                         (S0, "S0", dt, (B, W - 1, D)), (lens, "lens", torch.int32, (B,)), (y, "y", dt, (B, T, D)),
+                         (S_T, "S_T", dt, (B, W - 1, D))])
+        rc = lib.qdelta_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, D, W,
+                                 int(silu), code, _handle(s))
+        _raise(rc, "qdelta_conv_fwd")
+        return y, S_T
+
+
+def qdelta_conv_step(x, w, bias, S, silu: bool = True, y=None, stream=None):
+    """One token of the short convolution for N sequences: x [N,D]; S [N,W-1,D] like x, the
+    last inputs, shifted in place.  Returns y [N,D]."""
+    import torch
+    lib = load_library()
+    N, D = _shape(x, "x", 2)
+    W = _shape(w, "w", 2)[1]
+    s = _launch_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        dt, dev, f32 = x.dtype, x.device, torch.float32
+        code = _dtype_code(dt)
+        y = _result(y, (N, D), dt, dev)
+        _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)), (S, "S", dt, (N, W - 1, D)),
+                         (y, "y", dt, (N, D))])
+        rc = lib.qdelta_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(S), _ptr(y), N, D, W, int(silu), code, _handle(s))
+        _raise(rc, "qdelta_conv_step")
+        return y
+
+
+def qdelta_conv_bwd_workspace_bytes(B, T, D, W, dtype) -> int:
+    return int(load_library().qdelta_conv_bwd_workspace_bytes(B, T, D, W, _dtype_code(dtype)))
+
+
+def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: bool = True, out=None, workspace=None,
+                    stream=None):
+    """Gradients of sum(y * dy) + sum(S_T * dS_T) for qdelta_conv_fwd on the same inputs.
+    Returns a dict with dx, dw, dbias (None without bias) and dS0 (None unless want_dS0; also
+    given when S0 is None).  ``out`` may supply any of them; ``workspace`` a device buffer of
+    at least qdelta_conv_bwd_workspace_bytes(...) bytes (allocated when None)."""
+    import torch
+    lib = load_library()
+    B, T, D = _shape(x, "x", 3)
+    W = _shape(w, "w", 2)[1]
+    s = _launch_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        dt, dev, f32 = x.dtype, x.device, torch.float32
+        code = _dtype_code(dt)
+        _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
+                         (S0, "S0", dt, (B, W - 1, D)), (dy, "dy", dt, (B, T, D)), (dS_T, "dS_T", dt, (B, W - 1, D))])
+        out = _results(out, dict(dx=(True, (B, T, D), dt), dw=(True, (D, W), f32), dbias=(bias is not None, (D,), f32),
+                                 dS0=(want_dS0, (B, W - 1, D), dt)), dev)
+        p, n, workspace = _workspace(workspace, lib.qdelta_conv_bwd_workspace_bytes(B, T, D, W, code), dev)
+        rc = lib.qdelta_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(dy), _ptr(dS_T), _ptr(out["dx"]),
+                                 _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dS0"]), B, T, D, W, int(silu), code, p, n,
+                                 _handle(s))
+        _raise(rc, "qdelta_conv_bwd")
+        return out
+
+
+def _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, token_dims):
+    """Sizes (tokens.., channels, G, N) and the checks of the inputs that a token has."""
+    import torch
+    shape = tuple(_shape(u, "u", token_dims + 1))
+    G, N = _shape(Bm, "Bm", token_dims + 2)[token_dims:]
+    f32, e, ch = torch.float32, u.dtype, shape[-1]
+    if G < 1 or ch % G:
+        raise QDeltaError(f"the {ch} channels of u must divide into the {G} groups of Bm")
+    bc = shape[:-1] + (G, N)
+    return shape + (G, N), [(u, "u", e, None), (dt, "dt", e, shape), (A, "A", f32, (ch, N)), (Bm, "Bm", e, bc),
+                            (Cm, "Cm", e, bc), (D, "D", f32, (ch,)), (z, "z", e, shape), (dt_bias, "dt_bias", f32, (ch,))]
+
+
+def qdelta_ssm_fwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
+    return int(load_library().qdelta_ssm_fwd_workspace_bytes(B, T, D, G, N, _dtype_code(dtype)))
+
+
+def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, softplus: bool = True, lens=None, o=None,
+                   S_T=None, want_state: bool = True, workspace=None, stream=None):
+    """Selective state space scan.  u, dt, z [B,T,D] and Bm, Cm [B,T,G,N] (fp32 or bf16, same
+    dtype); A [D,N], D [D], dt_bias [D], S0 [B,D,N] fp32, all but A optional; N in 16, 32, 64.
+    softplus: delta = softplus(dt + dt_bias), else dt + dt_bias.  lens [B] int32: the tokens of
+    each right-padded sequence; rows of o past them are left as they were.  Returns (o, S_T);
+    S_T is None when want_state is False, and may be passed as S0.  workspace: at least
+    qdelta_ssm_fwd_workspace_bytes(...) bytes, allocated here when None and needed."""
+    import torch
+    lib = load_library()
+    (B, T, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    s = _launch_stream(stream, u.device)
+    with torch.cuda.stream(s):
+        dev, f32, code = u.device, torch.float32, _dtype_code(u.dtype)
+        o = _result(o, (B, T, ch), u.dtype, dev)
+        if want_state:
+            S_T = _result(S_T, (B, ch, N), f32, dev)
+        _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
+                                  (o, "o", u.dtype, (B, T, ch)), (S_T, "S_T", f32, (B, ch, N))])
+        p, n, workspace = _workspace(workspace, lib.qdelta_ssm_fwd_workspace_bytes(B, T, ch, G, N, code), dev)
+        rc = lib.qdelta_ssm_fwd(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S0),
+                                _ptr(lens), _ptr(o), _ptr(S_T), B, T, ch, G, N, int(softplus), code, p, n, _handle(s))
+        _raise(rc, "qdelta_ssm_fwd")
+        return o, S_T
+
+
+def qdelta_ssm_step(u, dt, A, Bm, Cm, D, z, dt_bias, S, softplus: bool = True, o=None, stream=None):
+    """One token of the selective scan for N sequences: u, dt, z [N,D], Bm, Cm [N,G,states];
+    S [N,D,states] fp32, updated in place.  Returns o [N,D]."""
+    import torch
+    lib = load_library()
+    (n_seq, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 1)
+    s = _launch_stream(stream, u.device)
+    with torch.cuda.stream(s):
+        dev, code = u.device, _dtype_code(u.dtype)
+        o = _result(o, (n_seq, ch), u.dtype, dev)
+        _check_all(dev, checks + [(S, "S", torch.float32, (n_seq, ch, N)), (o, "o", u.dtype, (n_seq, ch))])
+        rc = lib.qdelta_ssm_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S),
+                                 _ptr(o), n_seq, ch, G, N, int(softplus), code, _handle(s))
+        _raise(rc, "qdelta_ssm_step")
+        return o
+
+
+def qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
+    return int(load_library().qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, _dtype_code(dtype)))
+
+
+def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus: bool = True, want_dS0: bool = True,
+                   out=None, workspace=None, stream=None):
+    """Gradients of sum(o * d_o) + sum(S_T * dS_T) for qdelta_ssm_fwd on the same inputs.
+    Returns a dict with du, ddt, dB, dC (like their inputs), dA, and, None where the input is
+    None, dD, dz, ddt_bias, and dS0 (None unless want_dS0; also given when S0 is None).
+    ``out`` may supply any of them; ``workspace`` a device buffer of at least
+    qdelta_ssm_bwd_workspace_bytes(...) bytes (allocated when None)."""
+    import torch
+    lib = load_library()
+    (B, T, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    s = _launch_stream(stream, u.device)
+    with torch.cuda.stream(s):
+        dev, f32, e, code = u.device, torch.float32, u.dtype, _dtype_code(u.dtype)
+        _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (d_o, "d_o", e, (B, T, ch)), (dS_T, "dS_T", f32, (B, ch, N))])
+        tok, bc = (B, T, ch), (B, T, G, N)
+        out = _results(out, dict(du=(True, tok, e), ddt=(True, tok, e), dA=(True, (ch, N), f32), dB=(True, bc, e),
+                                 dC=(True, bc, e), dD=(D is not None, (ch,), f32), dz=(z is not None, tok, e),
+                                 ddt_bias=(dt_bias is not None, (ch,), f32), dS0=(want_dS0, (B, ch, N), f32)), dev)
+        p, n, workspace = _workspace(workspace, lib.qdelta_ssm_bwd_workspace_bytes(B, T, ch, G, N, code), dev)
+        rc = lib.qdelta_ssm_bwd(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S0),
+                                _ptr(d_o), _ptr(dS_T), _ptr(out["du"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
+                                _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]), _ptr(out["dS0"]),
+                                B, T, ch, G, N, int(softplus), code, p, n, _handle(s))
+        _raise(rc, "qdelta_ssm_bwd")
+        return out
+
+
+def _norm_sizes(x, groups):
+    """(samples, positions, channels) of x [N, .., C]: the dimensions between are the positions."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise QDeltaError("x must be a device tensor")
+    if x.dim() < 2:
+        raise QDeltaError("x must have at least 2 dimensions")
+    n, c = x.shape[0], x.shape[-1]
+    length = 1
+    for d in x.shape[1:-1]:
+        length *= d
+    if groups < 1 or c % groups:
+        raise QDeltaError(f"the {c} channels of x must divide into {groups} groups")
+    return n, length, c
+
+
+def qdelta_group_norm_fwd_workspace_bytes(N, L, C, G, dtype) -> int:
+    return int(load_library().qdelta_group_norm_fwd_workspace_bytes(N, L, C, G, _dtype_code(dtype)))
+
+
+def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, silu: bool = False, eps: float = 1e-5,
+                          y=None, stats=None, want_stats: bool = True, workspace=None, stream=None):
+    """Group norm of x [N,..,C] (fp32 or bf16), channels last: statistics per sample and group
+    over the dimensions between and C / groups channels; weight, bias [C] fp32 (None: 1, 0).
+    silu applies SiLU to the normed value; gate, like x, multiplies it by silu(gate).  The
+    output norm of a layer's o [B,T,H,d] per token and head is
+    ``qdelta_group_norm_fwd(o.view(B * T, H * d), H, ...)``.  Returns (y, stats), stats
+    [N,groups,2] the mean and 1/std the backward needs (None when want_stats is False)."""
+    import torch
+    lib = load_library()
+    N, L, C = _norm_sizes(x, groups)
+    s = _launch_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
+        y = _result(y, x.shape, dt, dev)
+        if want_stats:
+            stats = _result(stats, (N, groups, 2), f32, dev)
+        _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
+                         (gate, "gate", dt, x.shape), (y, "y", dt, x.shape), (stats, "stats", f32, (N, groups, 2))])
+        p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_fwd_workspace_bytes(N, L, C, groups, code), dev)
+        rc = lib.qdelta_group_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), _ptr(stats), N, L, C, groups,
+                                       float(eps), int(silu), code, p, n, _handle(s))
+        _raise(rc, "qdelta_group_norm_fwd")
+        return y, stats
+
+
+def qdelta_group_norm_bwd_workspace_bytes(N, L, C, G, dtype) -> int:
+    return int(load_library().qdelta_group_norm_bwd_workspace_bytes(N, L, C, G, _dtype_code(dtype)))
+
+
+def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: bool = False, out=None, workspace=None,
+                          stream=None):
+    """Gradients of sum(y * dy) for qdelta_group_norm_fwd on the same inputs, whose stats are
+    given.  Returns a dict with dx and, None where the input is None, dweight, dbias, dgate.
+    ``out`` may supply any of them; ``workspace`` a device buffer of at least
+    qdelta_group_norm_bwd_workspace_bytes(...) bytes (allocated when None)."""
+    import torch
+    lib = load_library()
+    N, L, C = _norm_sizes(x, groups)
+    s = _launch_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
+        if stats is None:
+            raise QDeltaError("stats must be the forward's")
+        _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
+                         (gate, "gate", dt, x.shape), (stats, "stats", f32, (N, groups, 2)), (dy, "dy", dt, x.shape)])
+        out = _results(out, dict(dx=(True, tuple(x.shape), dt), dweight=(weight is not None, (C,), f32),
+                                 dbias=(bias is not None, (C,), f32), dgate=(gate is not None, tuple(x.shape), dt)), dev)
+        p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_bwd_workspace_bytes(N, L, C, groups, code), dev)
+        rc = lib.qdelta_group_norm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(stats), _ptr(dy), _ptr(out["dx"]),
+                                       _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dgate"]), N, L, C, groups,
+                                       int(silu), code, p, n, _handle(s))
+        _raise(rc, "qdelta_group_norm_bwd")
+        return out

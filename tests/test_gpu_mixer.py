@@ -1,0 +1,165 @@
+"""The operators around the recurrence used together: a whole mixer forward and backward, a
+prompt followed by single tokens, another stream, captured graphs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mixer_cases import dev, gen, randn
+from oracle import mixer
+
+pytestmark = pytest.mark.gpu
+
+
+def params(D, N, W, seed):
+    g = gen(seed)
+    return dict(w=randn(g, D, W) * 0.5, b=randn(g, D) * 0.1, A=-(0.2 + torch.rand(D, N, generator=g)), D=randn(g, D),
+                dt_bias=randn(g, D) - 2, nw=1 + 0.1 * randn(g, D), nb=0.1 * randn(g, D))
+
+
+def tokens(B, T, D, G, N, seed):
+    g = gen(seed)
+    return dict(x=randn(g, B, T, D), dt=randn(g, B, T, D), z=randn(g, B, T, D), Bm=randn(g, B, T, G, N), Cm=randn(g, B, T, G, N))
+
+
+def forward(qd, p, t, H, stream=None):
+    """conv -> scan -> norm per head with the gate: outputs, states and what a backward needs."""
+    B, T, D = t["x"].shape
+    u, Sc = qd.qdelta_conv_fwd(t["x"], p["w"], p["b"], stream=stream)
+    o, Ss = qd.qdelta_ssm_fwd(u, t["dt"], p["A"], t["Bm"], t["Cm"], p["D"], None, p["dt_bias"], stream=stream)
+    y, stats = qd.qdelta_group_norm_fwd(o.view(B * T, D), H, p["nw"], p["nb"], t["z"].view(B * T, D), stream=stream)
+    return y.view(B, T, D), Sc, Ss, u, o, stats
+
+
+def reference(p, t, H):
+    """The same mixer in torch float64 on the CPU, differentiable."""
+    q = {k: v.double() for k, v in p.items()}
+    s = {k: v.double() for k, v in t.items()}
+    leaves = {**q, **s}
+    for v in leaves.values():
+        v.requires_grad_()
+    B, T, D = t["x"].shape
+    W, G, N = p["w"].shape[1], t["Bm"].shape[2], t["Bm"].shape[3]
+    full = torch.cat([torch.zeros(B, W - 1, D, dtype=torch.float64), s["x"]], 1)
+    u = torch.nn.functional.silu(sum(full[:, j:j + T] * q["w"][:, j] for j in range(W)) + q["b"])
+    delta = torch.nn.functional.softplus(s["dt"] + q["dt_bias"])
+    h, rows = torch.zeros(B, D, N, dtype=torch.float64), []
+    for i in range(T):
+        h = torch.exp(delta[:, i, :, None] * q["A"]) * h + (delta * u)[:, i, :, None] * s["Bm"][:, i].repeat_interleave(D // G, 1)
+        rows.append((h * s["Cm"][:, i].repeat_interleave(D // G, 1)).sum(-1) + q["D"] * u[:, i])
+    o = torch.stack(rows, 1).view(B, T, H, D // H)
+    hat = (o - o.mean(-1, keepdim=True)) / torch.sqrt(o.var(-1, correction=0, keepdim=True) + 1e-5)
+    y = (hat.view(B, T, D) * q["nw"] + q["nb"]) * torch.nn.functional.silu(s["z"])
+    return y, leaves
+
+
+def close(got, want, name, bar=2e-5):
+    """fp32 end to end: a mixer is three operators of some hundred roundings each (2^-24), and the
+    norm can enlarge a relative error by the size of its input over its spread, a few here:
+    a few hundred units, 2e-5 of the largest value."""
+    err = float((got.double().cpu() - want).abs().max() / want.abs().max())
+    print(f"  {name}: {err:.2e}", flush=True)
+    assert err <= bar, name
+
+
+def test_mixer_forward_and_backward(qd):
+    B, T, D, G, N, H = 2, 37, 96, 2, 16, 4
+    p, t = params(D, N, 4, 1), tokens(B, T, D, G, N, 2)
+    dy = randn(gen(3), B, T, D)
+    ref, leaves = reference(p, t, H)
+    (ref * dy.double()).sum().backward()
+    P, X = {k: dev(v.detach().float()) for k, v in p.items()}, {k: dev(v.detach().float()) for k, v in t.items()}
+    y, _, _, u, o, stats = forward(qd, P, X, H)
+    close(y, ref.detach(), "y")
+    n = qd.qdelta_group_norm_bwd(o.view(B * T, D), H, P["nw"], P["nb"], X["z"].view(B * T, D), stats, dev(dy).view(B * T, D))
+    s = qd.qdelta_ssm_bwd(u, X["dt"], P["A"], X["Bm"], X["Cm"], P["D"], None, P["dt_bias"], None, n["dx"].view(B, T, D))
+    c = qd.qdelta_conv_bwd(X["x"], P["w"], P["b"], None, s["du"], want_dS0=False)
+    got = dict(x=c["dx"], w=c["dw"], b=c["dbias"], dt=s["ddt"], A=s["dA"], Bm=s["dB"], Cm=s["dC"], D=s["dD"], dt_bias=s["ddt_bias"],
+               z=n["dgate"].view(B, T, D), nw=n["dweight"], nb=n["dbias"])
+    for k, v in got.items():
+        close(v, leaves[k].grad, "d" + k, 1e-4)
+
+
+def test_prompt_then_tokens(qd):
+    """Prefill, then decode token by token through all three, against one call over everything."""
+    B, T, D, G, N, H = 3, 24, 64, 1, 16, 2
+    p, t = {k: dev(v) for k, v in params(D, N, 4, 5).items()}, {k: dev(v) for k, v in tokens(B, T, D, G, N, 6).items()}
+    whole = forward(qd, p, t, H)[0]
+    _, Sc, Ss, *_ = forward(qd, p, {k: v[:, :20].contiguous() for k, v in t.items()}, H)
+    for i in range(20, T):
+        c = {k: v[:, i].contiguous() for k, v in t.items()}
+        u = qd.qdelta_conv_step(c["x"], p["w"], p["b"], Sc)
+        o = qd.qdelta_ssm_step(u, c["dt"], p["A"], c["Bm"], c["Cm"], p["D"], None, p["dt_bias"], Ss)
+        y, _ = qd.qdelta_group_norm_fwd(o, H, p["nw"], p["nb"], c["z"], want_stats=False)
+        close(y, whole[:, i].double().cpu(), f"token {i}")
+
+
+def test_around_the_delta_rule(qd):
+    """conv -> Q-Delta (normalising q and k, gates as logits) -> norm per head with the gate."""
+    B, T, H, d = 2, 100, 2, 64
+    D = H * d
+    g = gen(8)
+    x = [randn(g, B, T, D, dtype="bf16") for _ in range(3)]
+    ws = [(randn(g, D, 4) * 0.5) for _ in range(3)]
+    al, be, la = (randn(g, B, T, H) - m for m in (4, 0, 0))
+    z, nw = randn(g, B, T, D, dtype="bf16"), 1 + 0.1 * randn(g, D)
+    qkv = [qd.qdelta_conv_fwd(dev(a), dev(w), want_state=False)[0].view(B, T, H, d) for a, w in zip(x, ws)]
+    o, _ = qd.qdelta_chunk_fwd(*qkv, dev(al), dev(be), dev(la), C=64, raw=True)
+    y, _ = qd.qdelta_group_norm_fwd(o.view(B * T, D), H, dev(nw), None, dev(z).view(B * T, D))
+    from oracle import prologue
+    ref = [mixer.conv_fwd(a, w)[0].reshape(B, T, H, d) for a, w in zip(x, ws)]
+    ref = [torch.from_numpy(r).bfloat16().double().numpy() for r in ref]
+    qh, kh, a, b, lam = prologue.prologue(ref[0], ref[1], al, be, la)
+    ro, _ = oracle.qdelta_fwd(qh, kh, ref[2], a, b, lam, None)
+    want, _, _ = mixer.norm_fwd(np.asarray(ro).reshape(B * T, 1, D), H, nw, None, z.reshape(B * T, 1, D))
+    # the recurrence in bf16 is held to 2e-2 of its largest value per head; the norm divides by the spread
+    spread = np.asarray(ro).reshape(B * T, H, d).std(-1)
+    ratio = (np.abs(ro).max() / np.maximum(spread, 1e-6)).reshape(B * T, H, 1).repeat(d, 2).reshape(B * T, D)
+    gate = np.abs(mixer.silu(z.double().numpy().reshape(B * T, D)))
+    bound = 2e-2 * 3 * ratio * np.abs(nw.double().numpy()) * gate + 2.0 ** -8 * np.abs(want[:, 0]) + 1e-3
+    assert (np.abs(y.double().cpu().numpy() - want[:, 0]) <= bound).all()
+
+
+def test_on_another_stream(qd):
+    B, T, D, G, N, H = 2, 700, 64, 1, 16, 2
+    p, t = {k: dev(v) for k, v in params(D, N, 4, 5).items()}, {k: dev(v) for k, v in tokens(B, T, D, G, N, 6).items()}
+    want = forward(qd, p, t, H)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = forward(qd, p, t, H, stream=s)
+    s.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_captured_and_replayed(qd):
+    """Two captured graphs of forward and backward, replayed in turn on new inputs with eager
+    work between: every replay gives the eager call's bits."""
+    B, T, D, G, N, H = 1, 400, 64, 1, 16, 2
+    p = {k: dev(v) for k, v in params(D, N, 4, 5).items()}
+
+    def work(t):
+        y, Sc, Ss, u, o, stats = forward(qd, p, t, H)
+        n = qd.qdelta_group_norm_bwd(o.view(B * T, D), H, p["nw"], p["nb"], t["z"].view(B * T, D), stats, t["x"].view(B * T, D))
+        s = qd.qdelta_ssm_bwd(u, t["dt"], p["A"], t["Bm"], t["Cm"], p["D"], None, p["dt_bias"], None, n["dx"].view(B, T, D))
+        c = qd.qdelta_conv_bwd(t["x"], p["w"], p["b"], None, s["du"])
+        return [y, Sc, Ss] + [v for r in (n, s, c) for v in r.values() if v is not None]
+
+    graphs = []
+    for seed in (1, 2):
+        t = {k: dev(v) for k, v in tokens(B, T, D, G, N, seed).items()}
+        work(t)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = work(t)
+        graphs.append((graph, t, out))
+    for step in range(3):
+        for k, (graph, t, out) in enumerate(graphs):
+            fresh = {n: dev(v) for n, v in tokens(B, T, D, G, N, 10 + 2 * step + k).items()}
+            for n in t:
+                t[n].copy_(fresh[n])
+            graph.replay()
+            want = work(fresh)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want)), (step, k)
