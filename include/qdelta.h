@@ -334,8 +334,8 @@ int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void
  *             zeros, S_T NULL is not written, S_T may equal S0.
  *   lens      as for qdelta_conv_fwd.
  * T == 0 writes S_T = S0 (or zeros).  workspace: at least qdelta_ssm_fwd_workspace_bytes
- * (non-zero where few channels make the call cut the time axis into segments), 16-byte
- * aligned, overwritten; NULL when that is 0.
+ * (B and C as the kernels read them, and, where few channels make the call cut the time axis
+ * into segments, the segments' states), 16-byte aligned, overwritten.
  */
 size_t qdelta_ssm_fwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype);
 int qdelta_ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
@@ -356,8 +356,8 @@ int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *B
  *   du, ddt [B][T][D], dB, dC [B][T][G][N] (summed over the group's channels), elements;
  *   dz [B][T][D] elements, required with z and NULL without;
  *   dA [D][N] fp32; dDskip, ddt_bias [D] and dS0 [B][D][N] fp32, each NULL for not written.
- * A non-finite gradient or state at one token can make dB and dC of its neighbour in the pair
- * (2i, 2i + 1), counted within its segment of the time axis, non-finite too.
+ * A non-finite gradient or state at token t can make dB and dC of the other tokens with the
+ * same t / 4 (integer division) non-finite too.
  * workspace: at least qdelta_ssm_bwd_workspace_bytes, 16-byte aligned, overwritten (the
  * states before every eighth token and the channel blocks' sums).
  */

@@ -112,13 +112,15 @@ __device__ __forceinline__ float dsiluf(float x) {
 // The exponent's rounding, amplified by its size in a plain exp2(x log2 e), is put back as
 // a first-order factor.  Above 20 the value is x to fp32 accuracy (exp(-20) = 2e-9).
 __device__ __forceinline__ float softplusf(float x) {
-    if (x > 20.f) return x;
     const float xc = x < -126.f ? -126.f : x;
     const float p = xc * kLog2e;
     const float r = fmaf(xc, 1.925963033500e-8f, fmaf(xc, kLog2e, -p));
     const float e = __builtin_amdgcn_exp2f(p) * fmaf(r, kLn2, 1.f);
     const float s = 1.f + e, d = s - 1.f;
-    return d == 0.f ? e : __builtin_amdgcn_logf(s) * kLn2 * e * __builtin_amdgcn_rcpf(d);
+    // evaluated on every path and selected: a branch would stop the tokens of a tile from overlapping
+    const float small = __builtin_amdgcn_logf(s) * (kLn2 * e) * __builtin_amdgcn_rcpf(d);
+    const float near = d == 0.f ? e : small;
+    return x > 20.f ? x : near;
 }
 
 // V consecutive elements as floats; V * sizeof(element) is 16 bytes (16-byte aligned) or V is 1.

@@ -6,39 +6,54 @@
 
 namespace qd {
 
-constexpr int kTok = 8;              // tokens per tile
+constexpr int kTok = 8;              // tokens between two kept states (backward)
+constexpr int kTile = 16;            // tokens a forward workgroup stages at a time
 
-// One token's B or C values for the wave's NS states, read through the scalar cache: the
-// address is the same for every lane, so the values arrive in scalar registers and enter
-// the vector instructions as they are.  The row start is a multiple of NS elements.
-typedef const __attribute__((address_space(4))) uint32_t scalar_u32;
-template <class P, int NS>
-struct ScalarRow {
-    static constexpr int kDw = NS * P::kBytes / 4;
-    uint32_t q[kDw];
-    __device__ __forceinline__ void load(const typename P::R *p) {
-        scalar_u32 *s = (scalar_u32 *)(reinterpret_cast<uintptr_t>(p));
+// States a wave of the scan owns: N / kStates waves share 64 channels.
+template <int N>
+constexpr int states_per_wave() {
+    return N == 16 ? 2 : 4;
+}
+inline int states_per_wave_of(int N) { return N == 16 ? states_per_wave<16>() : 4; }
+
+// B and C for the scalar cache.  A wave's B and C values are the same for all its lanes, so
+// they enter the vector instructions as scalar registers; read from the inputs they would
+// come four or eight bytes a token.  A first launch writes them as fp32 in the order a wave
+// reads them, [B][G][wave][Tp][states per wave], so that one scalar load brings the values of
+// several tokens.  Rows from a sequence's length up to Tp, the next multiple of kTile and one
+// tile more, are zero: a token past the end then changes nothing.
+struct RowBuf {
+    float *b, *c;
+    int Tp;
+};
+inline int padded_rows(int T) { return (T + kTile - 1) / kTile * kTile + kTile; }
+
+typedef const __attribute__((address_space(4))) float scalar_f32;
+// COUNT tokens' values from row p on.
+template <int COUNT, int NS>
+struct ScalarRows {
+    float v[COUNT][NS];
+    __device__ __forceinline__ void load(const float *p) {
+        scalar_f32 *s = (scalar_f32 *)(reinterpret_cast<uintptr_t>(p));
 #pragma unroll
-        for (int i = 0; i < kDw; ++i) q[i] = s[i];
-    }
-    __device__ __forceinline__ float operator[](int i) const {
-        if constexpr (P::kBytes == 4) return __uint_as_float(q[i]);
-        else return __uint_as_float((i & 1) ? (q[i / 2] & 0xffff0000u) : (q[i / 2] << 16));
+        for (int t = 0; t < COUNT; ++t)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) v[t][i] = s[t * NS + i];
     }
 };
 
-// How the time axis is cut: P segments of `len` tokens (a multiple of kTok), walked at the
-// same time; P = 1 needs no workspace for it.
+// How the time axis is cut: P segments of `len` tokens (a multiple of kTile), walked at the
+// same time; P = 1 needs no segment workspace.
 struct Segments {
     int P, len;
 };
-inline Segments cut_time(int T, int want) {
+inline Segments cut_time(int T, long long want) {
     Segments s;
-    const int tiles = (T + kTok - 1) / kTok;
-    s.P = want < 1 ? 1 : want;
+    const int tiles = (T + kTile - 1) / kTile;
+    s.P = static_cast<int>(want < 1 ? 1 : want > 64 ? 64 : want);
     if (s.P > tiles) s.P = tiles < 1 ? 1 : tiles;
-    s.len = (tiles + s.P - 1) / s.P * kTok;
-    if (s.len < kTok) s.len = kTok;
+    s.len = (tiles + s.P - 1) / s.P * kTile;
+    if (s.len < kTile) s.len = kTile;
     s.P = (T + s.len - 1) / s.len;
     if (s.P < 1) s.P = 1;
     return s;
@@ -51,8 +66,12 @@ struct SegBuf {
     float *s;                        // [B][P][D]: segment q's sum of delta (slot q)
 };
 
-// The scan's launches (qd_ssm.hip) for the backward: the segments' effects, then the walk
+// The launches of qd_ssm.hip that the backward uses: B and C in scalar order, and the walk
 // that keeps the state before every tile of kTok tokens, [B][ceil(T / kTok)][N][D].
-hipError_t launch_ssm_states(int dtype, const SsmArgs &a, Segments seg, SegBuf buf, float *keep, hipStream_t stream);
+size_t row_floats(int B, int T, int G, int N);      // of b and c together
+RowBuf row_buf(float *ws, int B, int T, int G, int N);
+void launch_ssm_rows(int dtype, const SsmArgs &a, RowBuf rows, hipStream_t stream);
+hipError_t launch_ssm_states(int dtype, const SsmArgs &a, Segments seg, SegBuf buf, RowBuf rows, float *keep,
+                             hipStream_t stream);
 
 }  // namespace qd

@@ -5,14 +5,14 @@
 //   o_t     = (sum_n C_t[n] h_t[n] + D_d u_t) silu(z_t)
 //
 // with B and C shared by the channels of a group.  One exponential and four multiply-adds a
-// token, channel and state against four to eight bytes a token and channel: the vector
-// units bound it, not HBM.  The decay differs by channel and state, so there is no matrix
-// product in it; the design keeps everything else off the vector units:
+// token, channel and state against four to eight bytes a token and channel: instruction issue
+// bounds it, not HBM.  The decay differs by channel and state, so there is no matrix product
+// in it; the design keeps everything else off the vector units:
 //   - a lane owns one channel and a wave NS of its N states, so the recurrence and the sum
 //     over the wave's states need no exchange between lanes, and B_t and C_t are the same
-//     for all lanes: they come through the scalar cache into scalar registers;
+//     for all lanes: they are scalar registers (RowBuf);
 //   - the N / NS waves of a workgroup share 64 channels.  They stage delta_t and delta_t u_t
-//     of a tile of kTok tokens once, each wave a part of the tokens, double-buffered in LDS;
+//     of a tile of kTile tokens once, each wave a part of the tokens, double-buffered in LDS;
 //   - the waves' partial sums over their states meet in LDS, and the wave that staged a
 //     token adds them up, applies D and the gate from the u and z it kept, and stores.
 // One barrier a tile.  States and sums are fp32.
@@ -32,15 +32,47 @@ struct ScanArgs {
     int Dg, nblk;                    // channels per group, 64-channel blocks per group
     Segments seg;
     SegBuf buf;
+    RowBuf rows;
     float *keep;                     // kKeep: [B][ceil(T / kTok)][N][D]
 };
 
-template <class P, int N, int NS, int MODE>
-__global__ __launch_bounds__(64 * N / NS) void scan_kernel(const ScanArgs k) {
+// B and C in scalar order; one thread a token and wave.
+template <class P, int NS>
+__global__ __launch_bounds__(256) void ssm_rows_kernel(const ScanArgs k) {
     using R = typename P::R;
-    constexpr int NW = N / NS, TPW = kTok / NW > 0 ? kTok / NW : 1;
-    __shared__ float2 s_in[2][kTok][64];
-    __shared__ float s_y[MODE == kOut ? 2 : 1][MODE == kOut ? NW : 1][kTok][64];
+    const SsmArgs &a = k.a;
+    const int NW = a.N / NS;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<long long>(a.B) * a.G * k.rows.Tp * NW) return;
+    // threads next to each other take a row's waves, so that the reads are whole rows
+    const int w = static_cast<int>(i % NW), t = static_cast<int>(i / NW % k.rows.Tp);
+    const int bg = static_cast<int>(i / NW / k.rows.Tp), g = bg % a.G, b = bg / a.G;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    float vb[NS] = {}, vc[NS] = {};
+    if (t < len) {
+        const size_t at = ((static_cast<size_t>(b) * a.T + t) * a.G + g) * a.N + w * NS;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            vb[j] = P::to_f32(static_cast<const R *>(a.Bm)[at + j]);
+            vc[j] = P::to_f32(static_cast<const R *>(a.Cm)[at + j]);
+        }
+    }
+    const size_t to = ((static_cast<size_t>(bg) * NW + w) * k.rows.Tp + t) * NS;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        k.rows.b[to + j] = vb[j];
+        k.rows.c[to + j] = vc[j];
+    }
+}
+
+template <class P, int N, int MODE>
+__global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(const ScanArgs k) {
+    using R = typename P::R;
+    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = kTile / NW;
+    constexpr int GT = NS == 2 ? 8 : 4;      // tokens whose B and C are in scalar registers
+    static_assert(TPW >= 1 && TPW * NW == kTile, "each wave stages a whole number of tokens");
+    __shared__ float2 s_in[2][kTile][64];
+    __shared__ float s_y[MODE == kOut ? 2 : 1][MODE == kOut ? NW : 1][kTile][64];
     const SsmArgs &a = k.a;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int ncb = a.G * k.nblk, nseg = MODE == kSeg ? k.seg.P - 1 : k.seg.P;
@@ -92,96 +124,167 @@ __global__ __launch_bounds__(64 * N / NS) void scan_kernel(const ScanArgs k) {
         const size_t row0 = static_cast<size_t>(b) * a.T;
         const R *u = static_cast<const R *>(a.u) + row0 * D + ch;
         const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
-        const R *z = a.z ? static_cast<const R *>(a.z) + row0 * D + ch : nullptr;
+        const bool gated = a.z != nullptr;
+        const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : u;
         R *o = MODE == kOut ? static_cast<R *>(a.o) + row0 * D + ch : nullptr;
-        const R *Bm = static_cast<const R *>(a.Bm) + (row0 * a.G + g) * N + n0;
-        const R *Cm = static_cast<const R *>(a.Cm) + (row0 * a.G + g) * N + n0;
-        const size_t bc_row = static_cast<size_t>(a.G) * N;
+        const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
+        const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
         const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
         const float skip = a.Dskip ? a.Dskip[ch] : 0.f;
-        const int ntile = (te - tb + kTok - 1) / kTok;
+        const int ntile = (te - tb + kTile - 1) / kTile;
 
+        // Loaded values stay as they came until they are used: a conversion would wait for the
+        // load.  Rows at and past the end read the last row instead; what they give is not used.
         struct Raw {
-            float u[TPW], dt[TPW], z[TPW];
+            R u[TPW], dt[TPW], z[TPW];
+            float line;
         };
-        // Rows at and past the end read the last row instead; what they give is not used.
         auto fetch = [&](int tile, Raw &r) {
+            // The lines of the tile's scalar loads come to L2 with it: half the lanes for B, half for C.
+            const int tl = min(tb + tile * kTile, (te - 1) / kTile * kTile);
+            r.line = (lane < 32 ? Bw : Cw)[static_cast<size_t>(tl) * NS + (lane & 31) * (kTile * NS / 32)];
 #pragma unroll
             for (int j = 0; j < TPW; ++j) {
-                if (wave + j * NW >= kTok) continue;
-                const size_t t = min(tb + tile * kTok + wave + j * NW, te - 1);
-                r.u[j] = P::to_f32(u[t * D]);
-                r.dt[j] = P::to_f32(dt[t * D]);
-                if (MODE == kOut && z) r.z[j] = P::to_f32(z[t * D]);
+                const size_t t = min(tb + tile * kTile + wave + j * NW, te - 1);
+                r.u[j] = u[t * D];
+                r.dt[j] = dt[t * D];
+                if (MODE == kOut) r.z[j] = z[t * D];
             }
         };
+        struct Kept {                // what the end of a token needs of its rows
+            float u[TPW], z[TPW];
+        };
+        // Tokens past the end enter with delta and delta u zero (and B, C are zero there): the
+        // state passes through them.
         auto stage = [&](int tile, const Raw &r) {
+            Kept f;
+            asm volatile("" ::"v"(r.line));
 #pragma unroll
             for (int j = 0; j < TPW; ++j) {
-                const int i = wave + j * NW;
-                if (i >= kTok) continue;
-                const float x = r.dt[j] + dt_bias;
+                const bool in = tb + tile * kTile + wave + j * NW < te;
+                const float x = P::to_f32(r.dt[j]) + dt_bias;
                 const float delta = a.softplus ? softplusf(x) : x;
-                s_in[tile & 1][i][lane] = make_float2(delta, delta * r.u[j]);
+                f.u[j] = P::to_f32(r.u[j]);
+                f.z[j] = MODE == kOut ? P::to_f32(r.z[j]) : 0.f;
+                s_in[tile & 1][wave + j * NW][lane] = make_float2(in ? delta : 0.f, in ? delta * f.u[j] : 0.f);
             }
+            return f;
         };
-        auto walk = [&](int tile, auto full) {
-            const int t0 = tb + tile * kTok, nt = te - t0;
-            if (MODE == kKeep && live) {
+        ScalarRows<GT, NS> rb, rc;           // the next group's B and C
+        auto load_group = [&](int t0) {
+            rb.load(Bw + static_cast<size_t>(t0) * NS);
+            if constexpr (MODE == kOut) rc.load(Cw + static_cast<size_t>(t0) * NS);
+        };
+        auto keep_state = [&](int t0) {
+            if (MODE == kKeep && live && t0 < te) {
                 const size_t nc = (a.T + kTok - 1) / kTok;
                 float *keep = k.keep + ((b * nc + t0 / kTok) * N + n0) * D + ch;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) keep[i * D] = h[i];
             }
-            ScalarRow<P, NS> rb[kTok], rc[MODE == kOut ? kTok : 1];
+        };
+        // GT tokens from t0 = tile start + j.  `between` is arithmetic of its own that the
+        // compiler may place among the group's.
+        auto group = [&](int tile, int j, auto between) {
+            const int t0 = tb + tile * kTile + j;
+            if (j % kTok == 0) keep_state(t0);
+            float2 in[GT];
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                const size_t row = static_cast<size_t>(full ? t0 + t : min(t0 + t, te - 1)) * bc_row;
-                rb[t].load(Bm + row);
-                if constexpr (MODE == kOut) rc[t].load(Cm + row);
-            }
+            for (int t = 0; t < GT; ++t) in[t] = s_in[tile & 1][j + t][lane];
+            const ScalarRows<GT, NS> cb_ = rb, cc_ = rc;
+            // Scalar and LDS loads count down together and out of order: the wait for this
+            // group's is here, before the next group's scalar loads are issued, which then
+            // have the whole group's arithmetic to arrive.
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                if (!full && t >= nt) break;
-                const float2 in = s_in[tile & 1][t][lane];
+            for (int t = 0; t < GT; ++t) asm volatile("" ::"v"(in[t].x), "v"(in[t].y), "s"(cb_.v[t][0]));
+            __builtin_amdgcn_sched_barrier(0);
+            load_group(t0 + GT);
+            __builtin_amdgcn_sched_barrier(0);
+            // The exponentials and inputs of the group first: independent, so their latency is hidden.
+            float e[GT][NS], x[GT][NS];
+#pragma unroll
+            for (int t = 0; t < GT; ++t)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    e[t][i] = __builtin_amdgcn_exp2f(in[t].x * A2[i]);
+                    x[t][i] = in[t].y * cb_.v[t][i];
+                }
+            between();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < GT; ++t) {
                 float y = 0.f;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    h[i] = fmaf(__builtin_amdgcn_exp2f(in.x * A2[i]), h[i], in.y * rb[t][i]);
-                    if constexpr (MODE == kOut) y = fmaf(rc[t][i], h[i], y);
+                    h[i] = fmaf(e[t][i], h[i], x[t][i]);
+                    if constexpr (MODE == kOut) y = i ? fmaf(cc_.v[t][i], h[i], y) : cc_.v[t][0] * h[0];
                 }
-                if constexpr (MODE == kOut) s_y[tile & 1][wave][t][lane] = y;
-                else if constexpr (MODE == kSeg) sum_delta += in.x;
+                if constexpr (MODE == kOut) s_y[tile & 1][wave][j + t][lane] = y;
+                else if constexpr (MODE == kSeg) sum_delta += in[t].x;
             }
         };
-        auto finish = [&](int tile, const Raw &r) {
+        // The tokens this wave staged: the waves' sums over their states, D, the gate, the store.
+        struct Sums {
+            float y[TPW][NW];
+        };
+        auto gather = [&](int tile, Sums &p) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j)
+#pragma unroll
+                for (int w = 0; w < NW; ++w) p.y[j][w] = s_y[tile & 1][w][wave + j * NW][lane];
+        };
+        auto finish = [&](int tile, const Sums &p, const Kept &r) {
 #pragma unroll
             for (int j = 0; j < TPW; ++j) {
-                const int i = wave + j * NW, t = tb + tile * kTok + i;
-                if (i >= kTok || t >= te) continue;
+                const int t = tb + tile * kTile + wave + j * NW;
                 float y = skip * r.u[j];
 #pragma unroll
-                for (int w = 0; w < NW; ++w) y += s_y[tile & 1][w][i][lane];
-                if (z) y *= siluf(r.z[j]);
-                if (live) o[static_cast<size_t>(t) * D] = P::from_f32(y);
+                for (int w = 0; w < NW; ++w) y += p.y[j][w];
+                const float gate = siluf(r.z[j]);
+                y *= gated ? gate : 1.f;
+                if (live && t < te) o[static_cast<size_t>(t) * D] = P::from_f32(y);
             }
         };
+        auto nothing = [] {};
 
-        Raw cur, nxt;
-        fetch(0, cur);
-        stage(0, cur);
-        nxt = cur;
-        if (ntile > 1) fetch(1, nxt);
-        __syncthreads();
-        for (int i = 0; i < ntile; ++i) {
-            if (tb + (i + 1) * kTok <= te) walk(i, std::true_type{});
-            else walk(i, std::false_type{});
-            if (i + 1 < ntile) stage(i + 1, nxt);
-            const Raw mine = cur;
-            cur = nxt;
-            if (i + 2 < ntile) fetch(i + 2, nxt);
+        // Rows are on their way two tiles before they are staged, in two sets that take turns by
+        // name (a copy would wait for its load): at tile i, `r` holds the rows of i + 1 and is
+        // refilled with those of i + 3.  A tile's end runs among the next tile's arithmetic.
+        Kept cur, old;
+        auto step = [&](int i, Raw &r) {
+            Sums p;
+            if (MODE == kOut) gather(i - 1, p);
+            group(i, 0, [&] {
+                if (MODE == kOut && i > 0) finish(i - 1, p, old);
+            });
+#pragma unroll
+            for (int j = GT; j < kTile; j += GT) group(i, j, nothing);
+            old = cur;
+            cur = stage(i + 1, r);
+            fetch(i + 3, r);
             __syncthreads();
-            if constexpr (MODE == kOut) finish(i, mine);
+        };
+        Raw r0, r1;
+        {
+            Raw first;
+            fetch(0, first);
+            fetch(1, r0);
+            fetch(2, r1);
+            load_group(tb);
+            cur = stage(0, first);
+        }
+        old = cur;
+        __syncthreads();
+        int i = 0;
+        for (; i + 1 < ntile; i += 2) {
+            step(i, r0);
+            step(i + 1, r1);
+        }
+        if (i < ntile) step(i++, r0);
+        if constexpr (MODE == kOut) {
+            Sums p;
+            gather(i - 1, p);
+            finish(i - 1, p, old);
         }
     }
     if (!live) return;
@@ -252,22 +355,18 @@ __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(const SsmArgs a)
 // segment keeps at least 128 tokens.
 Segments fwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    const long long nblk = static_cast<long long>(B) * G * ((D / G + 63) / 64);
-    const long long waves = nblk * (N / 4);
-    if (nblk == 0 || waves >= 4LL * cus) return cut_time(T, 1);
-    long long want = (8LL * cus + waves - 1) / waves;
-    if (want > T / 128) want = T / 128;
-    return cut_time(T, static_cast<int>(want > 64 ? 64 : want));
+    const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * (N / states_per_wave_of(N));
+    if (waves == 0 || waves >= 4LL * cus) return cut_time(T, 1);
+    const long long want = (8LL * cus + waves - 1) / waves;
+    return cut_time(T, want > T / 128 ? T / 128 : want);
 }
 
 template <class P, int N, int MODE>
 hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
-    constexpr int NS = 4;
-    const dim3 blk(64 * N / NS);
+    const dim3 blk(64 * N / states_per_wave<N>());
     const unsigned per = static_cast<unsigned>(k.a.B) * k.a.G * k.nblk;
-    if (k.seg.P > 1)
-        hipLaunchKernelGGL((scan_kernel<P, N, NS, kSeg>), dim3(per * (k.seg.P - 1)), blk, 0, stream, k);
-    hipLaunchKernelGGL((scan_kernel<P, N, NS, MODE>), dim3(per * k.seg.P), blk, 0, stream, k);
+    if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg>), dim3(per * (k.seg.P - 1)), blk, 0, stream, k);
+    hipLaunchKernelGGL((scan_kernel<P, N, MODE>), dim3(per * k.seg.P), blk, 0, stream, k);
     return hipGetLastError();
 }
 
@@ -278,13 +377,14 @@ hipError_t run_scan_n(const ScanArgs &k, hipStream_t stream) {
     return run_scan<P, 64, MODE>(k, stream);
 }
 
-ScanArgs scan_args(const SsmArgs &a, Segments seg) {
+ScanArgs scan_args(const SsmArgs &a, Segments seg, RowBuf rows) {
     ScanArgs k;
     k.a = a;
     k.Dg = a.D / a.G;
     k.nblk = (k.Dg + 63) / 64;
     k.seg = seg;
     k.buf = SegBuf{nullptr, nullptr};
+    k.rows = rows;
     k.keep = nullptr;
     return k;
 }
@@ -303,32 +403,62 @@ hipError_t run_step(const SsmArgs &a, hipStream_t stream) {
 
 bool ssm_supported(int dtype, int N) { return (dtype == 0 || dtype == 1) && (N == 16 || N == 32 || N == 64); }
 
-// Every launch: up to 64 segments a channel block, 16 N lanes a workgroup (N / 4 waves); the
-// sums over blocks take a lane for four values of dB and dC, and 16 for a value of dA.
+// Every launch: up to 64 segments a channel block, 64 lanes for a wave's states; B and C in
+// scalar order, a lane a token and wave; the sums over blocks take a lane for four values of
+// dB and dC, and 16 for a value of dA.
 bool ssm_fits(int B, int T, int D, int G, int N) {
-    const long long blocks = static_cast<long long>(B) * G * ((D / G + 63) / 64), tiles = T / 64 + 1;
-    return blocks < (1LL << 31) && blocks * (tiles < 64 ? tiles : 64) * 16 * N < (1LL << 32) &&
-           static_cast<long long>(B) * T < (1LL << 31) && static_cast<long long>(B) * T * G < (1LL << 32) / N * 2 - 1024 &&
-           static_cast<long long>(D) * N < (1LL << 27);
+    if (N != 16 && N != 32 && N != 64) return false;
+    const long long blocks = static_cast<long long>(B) * G * ((D / G + 63) / 64), tiles = T / kTile + 1;
+    const long long waves = N / states_per_wave_of(N), lim = (1LL << 32) - 1024;
+    return blocks < (1LL << 31) && blocks * (tiles < 64 ? tiles : 64) * 64 * waves < lim &&
+           static_cast<long long>(B) * T < (1LL << 31) && T < 0x7fffff00 &&
+           static_cast<long long>(B) * G < (1LL << 31) && static_cast<long long>(B) * G * (T + 2LL * kTile) < lim / waves &&
+           static_cast<long long>(B) * T * G < lim / N * 2 && static_cast<long long>(D) * N < (1LL << 27);
+}
+
+size_t row_floats(int B, int T, int G, int N) { return 2 * static_cast<size_t>(B) * G * N * padded_rows(T); }
+
+RowBuf row_buf(float *ws, int B, int T, int G, int N) {
+    return RowBuf{ws, ws + row_floats(B, T, G, N) / 2, padded_rows(T)};
+}
+
+void launch_ssm_rows(int dtype, const SsmArgs &a, RowBuf rows, hipStream_t stream) {
+    const ScanArgs k = scan_args(a, Segments{1, a.T}, rows);
+    const long long n = static_cast<long long>(a.B) * a.G * rows.Tp * (a.N / states_per_wave_of(a.N));
+    const dim3 grid(static_cast<unsigned>((n + 255) / 256)), blk(256);
+    if (a.N == 16) {
+        constexpr int NS = states_per_wave<16>();
+        if (dtype == 1) hipLaunchKernelGGL((ssm_rows_kernel<Bf16, NS>), grid, blk, 0, stream, k);
+        else hipLaunchKernelGGL((ssm_rows_kernel<F32, NS>), grid, blk, 0, stream, k);
+    } else {
+        static_assert(states_per_wave<32>() == 4 && states_per_wave<64>() == 4, "one instance for both");
+        if (dtype == 1) hipLaunchKernelGGL((ssm_rows_kernel<Bf16, 4>), grid, blk, 0, stream, k);
+        else hipLaunchKernelGGL((ssm_rows_kernel<F32, 4>), grid, blk, 0, stream, k);
+    }
 }
 
 size_t ssm_fwd_workspace(int dtype, int B, int T, int D, int G, int N) {
     (void)dtype;
+    if (T == 0) return 0;
     const Segments s = fwd_segments(B, T, D, G, N);
-    return s.P > 1 ? static_cast<size_t>(B) * s.P * D * (N + 1) * sizeof(float) : 0;
+    const size_t seg = s.P > 1 ? static_cast<size_t>(B) * s.P * D * (N + 1) : 0;
+    return (row_floats(B, T, G, N) + seg) * sizeof(float);
 }
 
 hipError_t launch_ssm_fwd(int dtype, const SsmArgs &a, void *ws, hipStream_t stream) {
-    ScanArgs k = scan_args(a, fwd_segments(a.B, a.T, a.D, a.G, a.N));
+    float *w = static_cast<float *>(ws);
+    ScanArgs k = scan_args(a, fwd_segments(a.B, a.T, a.D, a.G, a.N), row_buf(w, a.B, a.T, a.G, a.N));
     if (k.seg.P > 1) {
-        k.buf.h = static_cast<float *>(ws);
+        k.buf.h = w + row_floats(a.B, a.T, a.G, a.N);
         k.buf.s = k.buf.h + static_cast<size_t>(a.B) * k.seg.P * a.N * a.D;
     }
+    if (a.T > 0) launch_ssm_rows(dtype, a, k.rows, stream);
     return dtype == 1 ? run_scan_n<Bf16, kOut>(k, stream) : run_scan_n<F32, kOut>(k, stream);
 }
 
-hipError_t launch_ssm_states(int dtype, const SsmArgs &a, Segments seg, SegBuf buf, float *keep, hipStream_t stream) {
-    ScanArgs k = scan_args(a, seg);
+hipError_t launch_ssm_states(int dtype, const SsmArgs &a, Segments seg, SegBuf buf, RowBuf rows, float *keep,
+                             hipStream_t stream) {
+    ScanArgs k = scan_args(a, seg, rows);
     k.buf = buf;
     k.keep = keep;
     return dtype == 1 ? run_scan_n<Bf16, kKeep>(k, stream) : run_scan_n<F32, kKeep>(k, stream);

@@ -12,29 +12,28 @@
 // tile of kTok tokens in HBM (4 N / kTok bytes a token and channel); the reverse walk takes a
 // tile's entry state, runs its kTok tokens forward with decays and states in registers, and
 // then backward.  Lanes, waves, staging and segments are those of the forward kernel: a lane
-// is a channel, a wave four of its states, B and C in scalar registers, s1, s2 and y joined
+// is a channel, a wave some of its states, B and C in scalar registers, s1, s2 and y joined
 // through LDS by the wave that staged the token.
 //
-// dB and dC sum over channels, which are lanes: eight values a lane and token.  A chain of
-// fp32 MFMAs does it without a cross-lane instruction: the 64 lanes' values are a 16 x 4
+// dB and dC sum over channels, which are lanes: two values a state, lane and token.  A chain
+// of fp32 MFMAs does it without a cross-lane instruction: the 64 lanes' values are a 16 x 4
 // operand, the other operand has ones in one column j, so the product adds four lanes into
-// column j of each of 16 rows; two tokens fill the 16 columns, and a second product with
-// ones joins the rows.  The fp32 products are by 1 and 0, so only the sum rounds.  (0 times
-// a non-finite value is not 0: one non-finite value makes its pair of tokens' dB and dC
-// non-finite.)  Each 64-channel block leaves its sums in the workspace and a second kernel
+// column j of each of 16 rows; two or four tokens fill the 16 columns, and a second product
+// with ones joins the rows.  The fp32 products are by 1 and 0, so only the sum rounds.  (0 times
+// a non-finite value is not 0: one non-finite value makes dB and dC of its two or four
+// neighbouring tokens non-finite.)  Each 64-channel block leaves its sums in the workspace and a second kernel
 // adds the blocks in order, so the result does not depend on the order of workgroups.
 #include "qd_ssm.h"
 
 namespace qd {
 namespace {
 
-constexpr int kNs = 4;               // states a wave
-
 struct RevArgs {
     SsmBwdArgs a;
     int Dg, nblk;
     Segments seg;
     float *keep;                     // [B][ceil(T / kTok)][N][D]
+    RowBuf rows;                     // B and C in scalar order
     SegBuf rev;                      // segment p's local gradient (slot p) and sum of delta (slot p)
     float *part_bc;                  // [nblk][B][T][G][2][N]
     float *part_a;                   // [B][P][D][N]
@@ -43,10 +42,10 @@ struct RevArgs {
 
 // A segment's effect on the gradient that enters at its end: g_out = exp(A sum(delta)) g_in + g_local.
 template <class P, int N>
-__global__ __launch_bounds__(64 * N / kNs) void seg_grad_kernel(const RevArgs k) {
+__global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel(const RevArgs k) {
     using R = typename P::R;
-    constexpr int NS = kNs, NW = N / NS, TPW = kTok / NW > 0 ? kTok / NW : 1;
-    __shared__ float2 s_in[2][kTok][64];
+    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = kTile / NW, GT = NS == 2 ? 8 : 4;
+    __shared__ float2 s_in[2][kTile][64];
     const SsmBwdArgs &a = k.a;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int ncb = a.G * k.nblk, nseg = k.seg.P - 1;
@@ -54,62 +53,88 @@ __global__ __launch_bounds__(64 * N / kNs) void seg_grad_kernel(const RevArgs k)
     const int g = cb / k.nblk, c_in = (cb % k.nblk) * 64 + lane;
     const int ch = g * k.Dg + min(c_in, k.Dg - 1), n0 = wave * NS;
     const size_t D = a.D, row0 = static_cast<size_t>(b) * a.T;
-    const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTok - 1) / kTok;
+    const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTile - 1) / kTile;
     float A2[NS], G[NS] = {}, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] = a.A[static_cast<size_t>(ch) * N + n0 + i] * kLog2e;
     const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
-    const R *z = a.z ? static_cast<const R *>(a.z) + row0 * D + ch : nullptr;
     const R *d_o = static_cast<const R *>(a.d_o) + row0 * D + ch;
-    const R *Cm = static_cast<const R *>(a.Cm) + (row0 * a.G + g) * N + n0;
-    const size_t bc_row = static_cast<size_t>(a.G) * N;
+    const bool gated = a.z != nullptr;
+    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : d_o;
+    const float *Cw = k.rows.c + ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
     const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
 
     struct Raw {
-        float dt[TPW], z[TPW], d_o[TPW];
+        R dt[TPW], z[TPW], d_o[TPW];
     };
     auto fetch = [&](int tile, Raw &r) {
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            if (wave + j * NW >= kTok) continue;
-            const size_t t = min(tb + tile * kTok + wave + j * NW, te - 1);
-            r.dt[j] = P::to_f32(dt[t * D]);
-            r.d_o[j] = P::to_f32(d_o[t * D]);
-            if (z) r.z[j] = P::to_f32(z[t * D]);
+            const size_t t = max(min(tb + tile * kTile + wave + j * NW, te - 1), tb);
+            r.dt[j] = dt[t * D];
+            r.d_o[j] = d_o[t * D];
+            r.z[j] = z[t * D];
         }
     };
     auto stage = [&](int tile, const Raw &r) {
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int i = wave + j * NW;
-            if (i >= kTok) continue;
-            const float x = r.dt[j] + dt_bias;
+            const bool in = tb + tile * kTile + wave + j * NW < te;
+            const float x = P::to_f32(r.dt[j]) + dt_bias, d = P::to_f32(r.d_o[j]), gate = siluf(P::to_f32(r.z[j]));
             const float delta = a.softplus ? softplusf(x) : x;
-            s_in[tile & 1][i][lane] = make_float2(delta, z ? r.d_o[j] * siluf(r.z[j]) : r.d_o[j]);
+            s_in[tile & 1][wave + j * NW][lane] = in ? make_float2(delta, gated ? d * gate : d) : make_float2(0.f, 0.f);
         }
     };
-    Raw r;
-    fetch(ntile - 1, r);
-    stage(ntile - 1, r);
-    if (ntile > 1) fetch(ntile - 2, r);
-    __syncthreads();
-    for (int tile = ntile - 1; tile >= 0; --tile) {
-        const int t0 = tb + tile * kTok, nt = min(kTok, te - t0);
-        ScalarRow<P, NS> rc[kTok];
+    ScalarRows<GT, NS> rc;
+    auto step = [&](int tile, Raw &r) {      // r: the rows of tile - 1, refilled with tile - 3
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) rc[t].load(Cm + static_cast<size_t>(min(t0 + t, te - 1)) * bc_row);
+        for (int j = kTile - GT; j >= 0; j -= GT) {
+            const int t0 = tb + tile * kTile + j;
+            float2 in[GT];
 #pragma unroll
-        for (int t = kTok - 1; t >= 0; --t) {
-            if (t >= nt) continue;
-            const float2 in = s_in[tile & 1][t][lane];
-            sum += in.x;
+            for (int t = 0; t < GT; ++t) in[t] = s_in[tile & 1][j + t][lane];
+            const ScalarRows<GT, NS> c = rc;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) G[i] = __builtin_amdgcn_exp2f(in.x * A2[i]) * fmaf(rc[t][i], in.y, G[i]);
+            for (int t = 0; t < GT; ++t) asm volatile("" ::"v"(in[t].x), "v"(in[t].y), "s"(c.v[t][0]));
+            __builtin_amdgcn_sched_barrier(0);
+            rc.load(Cw + static_cast<size_t>(max(t0 - GT, 0)) * NS);
+            __builtin_amdgcn_sched_barrier(0);
+            float e[GT][NS], x[GT][NS];
+#pragma unroll
+            for (int t = 0; t < GT; ++t)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    e[t][i] = __builtin_amdgcn_exp2f(in[t].x * A2[i]);
+                    x[t][i] = in[t].y * c.v[t][i];
+                }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = GT - 1; t >= 0; --t) {
+                sum += in[t].x;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) G[i] = e[t][i] * (x[t][i] + G[i]);
+            }
         }
         if (tile > 0) stage(tile - 1, r);
-        if (tile > 1) fetch(tile - 2, r);
+        fetch(tile - 3, r);
         __syncthreads();
+    };
+    Raw r0, r1;
+    {
+        Raw first;
+        fetch(ntile - 1, first);
+        fetch(ntile - 2, r0);
+        fetch(ntile - 3, r1);
+        rc.load(Cw + static_cast<size_t>(tb + (ntile - 1) * kTile + kTile - GT) * NS);
+        stage(ntile - 1, first);
     }
+    __syncthreads();
+    int tile = ntile - 1;
+    for (; tile > 0; tile -= 2) {
+        step(tile, r0);
+        step(tile - 1, r1);
+    }
+    if (tile == 0) step(0, r0);
     if (c_in >= k.Dg) return;
     float *out = k.rev.h + ((static_cast<size_t>(b) * k.seg.P + p) * N + n0) * D + ch;
 #pragma unroll
@@ -118,12 +143,12 @@ __global__ __launch_bounds__(64 * N / kNs) void seg_grad_kernel(const RevArgs k)
 }
 
 template <class P, int N>
-__global__ __launch_bounds__(64 * N / kNs) void ssm_bwd_kernel(const RevArgs k) {
+__global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(const RevArgs k) {
     using R = typename P::R;
-    constexpr int NS = kNs, NW = N / NS, TPW = kTok / NW > 0 ? kTok / NW : 1;
-    // One or two buffers of the partial sums: two (one barrier a tile) while they fit with
-    // room for a second workgroup.
-    constexpr int NB = N <= 16 ? 2 : 1;
+    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = kTok / NW > 0 ? kTok / NW : 1;
+    // Two buffers of the waves' sums and one barrier a tile where LDS holds them, else one and two.
+    constexpr int NB = NW <= 8 ? 2 : 1;
+    constexpr int VPT = 2 * NS, TPC = 16 / VPT, SETS = kTok / TPC;   // channel sums: values a token, tokens and sets of 16
     __shared__ float2 s_in[2][kTok][64];
     __shared__ float s_dy[2][kTok][64];
     __shared__ float s_p[NB][NW][3][kTok][64];
@@ -152,157 +177,217 @@ __global__ __launch_bounds__(64 * N / kNs) void ssm_bwd_kernel(const RevArgs k) 
     }
     const R *u = static_cast<const R *>(a.u) + row0 * D + ch;
     const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
-    const R *z = a.z ? static_cast<const R *>(a.z) + row0 * D + ch : nullptr;
     const R *d_o = static_cast<const R *>(a.d_o) + row0 * D + ch;
-    const R *Bm = static_cast<const R *>(a.Bm) + (row0 * a.G + g) * N + n0;
-    const R *Cm = static_cast<const R *>(a.Cm) + (row0 * a.G + g) * N + n0;
-    const size_t bc_row = static_cast<size_t>(a.G) * N;
+    const bool gated = a.z != nullptr;
+    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : u;
+    const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
+    const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
     const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.Dskip ? a.Dskip[ch] : 0.f;
     const size_t nc = (a.T + kTok - 1) / kTok;
     const float *keep = k.keep + ((static_cast<size_t>(b) * nc + tb / kTok) * N + n0) * D + ch;
     float *part_bc = k.part_bc + (((static_cast<size_t>(cb % k.nblk) * a.B + b) * a.T) * a.G + g) * 2 * N + n0;
     float acc_d = 0.f, acc_b = 0.f;
 
-    struct Tok {                     // what a wave keeps of the tokens it stages
-        float u[TPW], x[TPW], z[TPW], d_o[TPW], delta[TPW], dy[TPW];
+    struct Raw {                     // as loaded: a conversion would wait for the load
+        R u[TPW], x[TPW], z[TPW], d_o[TPW];
+        float h[NS];                 // the tile's entry state
     };
-    auto fetch = [&](int tile, Tok &r) {
+    auto fetch = [&](int tile, Raw &r) {
+        tile = max(tile, 0);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            if (wave + j * NW >= kTok) continue;
+            if (NW > kTok && wave >= kTok) continue;
             const size_t t = min(tb + tile * kTok + wave + j * NW, te - 1);
-            r.u[j] = P::to_f32(u[t * D]);
-            r.x[j] = P::to_f32(dt[t * D]);
-            r.d_o[j] = P::to_f32(d_o[t * D]);
-            if (z) r.z[j] = P::to_f32(z[t * D]);
+            r.u[j] = u[t * D];
+            r.x[j] = dt[t * D];
+            r.d_o[j] = d_o[t * D];
+            r.z[j] = z[t * D];
         }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) r.h[i] = keep[static_cast<size_t>(tile) * N * D + i * D];
     };
-    // Tokens past the end and lanes past the channels enter with delta, u and dy zero: the
+    struct Kept {                    // what the end of a token needs, and the tile's entry state
+        float u[TPW], x[TPW], z[TPW], d_o[TPW], delta[TPW], dy[TPW], h[NS];
+    };
+    // Tokens past the end and lanes past the channels enter with delta, u, dy and state zero: the
     // state passes through them and they add nothing to any sum.
-    auto stage = [&](int tile, Tok &r) {
+    auto stage = [&](int tile, const Raw &r, Kept &f) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) f.h[i] = live ? r.h[i] : 0.f;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int i = wave + j * NW;
-            if (i >= kTok) continue;
+            if (NW > kTok && wave >= kTok) continue;
             const bool in = live && tb + tile * kTok + i < te;
-            r.x[j] += dt_bias;
-            const float delta = a.softplus ? softplusf(r.x[j]) : r.x[j];
-            const float dy = z ? r.d_o[j] * siluf(r.z[j]) : r.d_o[j];
-            r.delta[j] = delta;
-            r.dy[j] = dy;
-            s_in[tile & 1][i][lane] = in ? make_float2(delta, delta * r.u[j]) : make_float2(0.f, 0.f);
-            s_dy[tile & 1][i][lane] = in ? dy : 0.f;
+            f.u[j] = P::to_f32(r.u[j]);
+            f.z[j] = P::to_f32(r.z[j]);
+            f.d_o[j] = P::to_f32(r.d_o[j]);
+            f.x[j] = P::to_f32(r.x[j]) + dt_bias;
+            const float gate = siluf(f.z[j]);
+            f.delta[j] = a.softplus ? softplusf(f.x[j]) : f.x[j];
+            f.dy[j] = gated ? f.d_o[j] * gate : f.d_o[j];
+            s_in[tile & 1][i][lane] = in ? make_float2(f.delta[j], f.delta[j] * f.u[j]) : make_float2(0.f, 0.f);
+            s_dy[tile & 1][i][lane] = in ? f.dy[j] : 0.f;
         }
     };
-    auto entry = [&](int tile, float (&h)[NS]) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = live ? keep[static_cast<size_t>(tile) * N * D + i * D] : 0.f;
-    };
-    float one[16], row_one[4];       // the selecting operands
+    float one[16], row_one[SETS];    // the selecting operands
 #pragma unroll
     for (int j = 0; j < 16; ++j) one[j] = (lane & 15) == j ? 1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) row_one[j] = ((lane & 15) >> 2) == j ? 1.f : 0.f;
+    for (int j = 0; j < SETS; ++j) row_one[j] = ((lane & 15) >> 2) == j ? 1.f : 0.f;
 
-    auto walk = [&](int tile, const float (&h_in)[NS]) {
+    ScalarRows<kTok, NS> rb, rc;     // the tile's B and C, loaded at the end of the tile before
+    auto load_rows = [&](int tile) {
+        const size_t t0 = static_cast<size_t>(tb + max(tile, 0) * kTok) * NS;
+        rb.load(Bw + t0);
+        rc.load(Cw + t0);
+    };
+    auto walk = [&](int tile, const float (&h_in)[NS], auto between) {
         const int t0 = tb + tile * kTok, buf = tile & 1;
-        ScalarRow<P, NS> rb[kTok], rc[kTok];
+        float2 in[kTok];
+        float dy[kTok];
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
-            const size_t row = static_cast<size_t>(min(t0 + t, te - 1)) * bc_row;
-            rb[t].load(Bm + row);
-            rc[t].load(Cm + row);
+            in[t] = s_in[buf][t][lane];
+            dy[t] = s_dy[buf][t][lane];
         }
         float dec[kTok][NS], h[kTok][NS];
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const float2 in = s_in[buf][t][lane];
+        for (int t = 0; t < kTok; ++t)
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                dec[t][i] = __builtin_amdgcn_exp2f(in.x * A2[i]);
-                h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : h_in[i], in.y * rb[t][i]);
+                dec[t][i] = __builtin_amdgcn_exp2f(in[t].x * A2[i]);
+                h[t][i] = in[t].y * rb.v[t][i];
             }
-        }
+        between();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : h_in[i], h[t][i]);
         float dAt[NS] = {};          // this tile's part of dA: fewer roundings against the long sum
-        f32x4 pair = zero4(), joined = zero4();
+        f32x4 set = zero4(), joined = zero4();
 #pragma unroll
         for (int t = kTok - 1; t >= 0; --t) {
-            const float2 in = s_in[buf][t][lane];
-            const float dy = s_dy[buf][t][lane];
             float y = 0.f, s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const float gi = fmaf(rc[t][i], dy, G[i]);
-                y = fmaf(rc[t][i], h[t][i], y);
-                s1 = fmaf(gi, rb[t][i], s1);
+                const float gi = fmaf(rc.v[t][i], dy[t], G[i]);
+                y = fmaf(rc.v[t][i], h[t][i], y);
+                s1 = fmaf(gi, rb.v[t][i], s1);
                 G[i] = dec[t][i] * gi;
                 const float q = G[i] * (t ? h[t - 1][i] : h_in[i]);
                 s2 = fmaf(A2[i], q, s2);
-                dAt[i] = fmaf(in.x, q, dAt[i]);
-                pair = __builtin_amdgcn_mfma_f32_16x16x4f32(gi * in.y, one[(t & 1) * 8 + i], pair, 0, 0, 0);
-                pair = __builtin_amdgcn_mfma_f32_16x16x4f32(dy * h[t][i], one[(t & 1) * 8 + 4 + i], pair, 0, 0, 0);
+                dAt[i] = fmaf(in[t].x, q, dAt[i]);
+                set = __builtin_amdgcn_mfma_f32_16x16x4f32(gi * in[t].y, one[(t % TPC) * VPT + i], set, 0, 0, 0);
+                set = __builtin_amdgcn_mfma_f32_16x16x4f32(dy[t] * h[t][i], one[(t % TPC) * VPT + NS + i], set, 0, 0, 0);
             }
             float *sp = &s_p[NB == 2 ? buf : 0][wave][0][t][lane];
             sp[0] = y;
             sp[kTok * 64] = s1;
             sp[2 * kTok * 64] = s2;
-            if ((t & 1) == 0) {      // both tokens of a pair are in: add the 16 rows
-                joined = __builtin_amdgcn_mfma_f32_16x16x4f32(row_one[t / 2], (pair[0] + pair[1]) + (pair[2] + pair[3]),
-                                                              joined, 0, 0, 0);
-                pair = zero4();
+            if (t % TPC == 0) {      // the set's tokens are in: add the 16 rows
+                joined = __builtin_amdgcn_mfma_f32_16x16x4f32(row_one[t / TPC], (set[0] + set[1]) + (set[2] + set[3]), joined,
+                                                              0, 0, 0);
+                set = zero4();
             }
         }
+        load_rows(tile - 1);
 #pragma unroll
         for (int i = 0; i < NS; ++i) dA[i] += dAt[i];
-        // lane l now holds column l % 16 of pair l / 16
-        const int j = lane & 15, t = t0 + 2 * (lane >> 4) + (j >> 3), e = j & 7;
-        if (t < te) part_bc[static_cast<size_t>(t) * a.G * 2 * N + (e >> 2) * N + (e & 3)] = joined[0];
+        // lane l now holds column l % 16 of set l / 16
+        const int j = lane & 15, t = t0 + TPC * (lane >> 4) + j / VPT, e = j % VPT;
+        if ((lane >> 4) < SETS && t < te) part_bc[static_cast<size_t>(t) * a.G * 2 * N + (e / NS) * N + e % NS] = joined[0];
     };
-    auto finish = [&](int tile, const Tok &r) {
+    struct Sums {
+        float v[TPW][3][NW];
+    };
+    auto gather = [&](int tile, Sums &s) {
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int i = wave + j * NW, t = tb + tile * kTok + i;
-            if (i >= kTok || t >= te) continue;
+            if (NW > kTok && wave >= kTok) continue;
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int v = 0; v < 3; ++v) s.v[j][v][w] = s_p[NB == 2 ? tile & 1 : 0][w][v][wave + j * NW][lane];
+        }
+    };
+    auto finish = [&](int tile, const Sums &s, const Kept &r) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            if (NW > kTok && wave >= kTok) continue;
+            const int t = tb + tile * kTok + wave + j * NW;
             float y = 0.f, s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float *sp = &s_p[NB == 2 ? tile & 1 : 0][w][0][i][lane];
-                y += sp[0];
-                s1 += sp[kTok * 64];
-                s2 += sp[2 * kTok * 64];
+                y += s.v[j][0][w];
+                s1 += s.v[j][1][w];
+                s2 += s.v[j][2][w];
             }
             float dd = fmaf(r.u[j], s1, s2 * kLn2);
-            if (a.softplus) dd *= sigmoidf(r.x[j]);
-            acc_d = fmaf(r.dy[j], r.u[j], acc_d);
-            acc_b += dd;
-            if (!live) continue;
-            const size_t at = (row0 + t) * D + ch;
-            static_cast<R *>(a.du)[at] = P::from_f32(fmaf(r.delta[j], s1, skip * r.dy[j]));
-            static_cast<R *>(a.ddt)[at] = P::from_f32(dd);
-            if (z) static_cast<R *>(a.dz)[at] = P::from_f32(r.d_o[j] * fmaf(skip, r.u[j], y) * dsiluf(r.z[j]));
+            const float slope = sigmoidf(r.x[j]);
+            dd *= a.softplus ? slope : 1.f;
+            const bool in = t < te;
+            acc_d = in ? fmaf(r.dy[j], r.u[j], acc_d) : acc_d;
+            acc_b += in ? dd : 0.f;
+            const float du = fmaf(r.delta[j], s1, skip * r.dy[j]);
+            const float dz = r.d_o[j] * fmaf(skip, r.u[j], y) * dsiluf(r.z[j]);
+            if (live && in) {
+                const size_t at = (row0 + t) * D + ch;
+                static_cast<R *>(a.du)[at] = P::from_f32(du);
+                static_cast<R *>(a.ddt)[at] = P::from_f32(dd);
+                if (gated) static_cast<R *>(a.dz)[at] = P::from_f32(dz);
+            }
         }
     };
 
-    Tok cur, nxt;
-    float h_cur[NS], h_nxt[NS];
-    fetch(ntile - 1, cur);
-    entry(ntile - 1, h_cur);
-    stage(ntile - 1, cur);
-    nxt = cur;
-    if (ntile > 1) fetch(ntile - 2, nxt);
+    // As in the forward: rows two tiles ahead in two sets by name; where the sums have two
+    // buffers, a tile's end runs among the next tile's arithmetic.
+    Kept cur, old;
+    auto step = [&](int tile, Raw &r) {
+        if constexpr (NB == 2) {
+            Sums s;
+            gather(tile + 1, s);
+            walk(tile, cur.h, [&] {
+                if (tile + 1 < ntile) finish(tile + 1, s, old);
+            });
+            old = cur;
+            if (tile > 0) stage(tile - 1, r, cur);
+            fetch(tile - 3, r);
+            __syncthreads();
+        } else {
+            walk(tile, cur.h, [] {});
+            old = cur;
+            if (tile > 0) stage(tile - 1, r, cur);
+            fetch(tile - 3, r);
+            __syncthreads();
+            Sums s;
+            gather(tile, s);
+            finish(tile, s, old);
+            __syncthreads();
+        }
+    };
+    Raw r0, r1;
+    {
+        Raw first;
+        fetch(ntile - 1, first);
+        fetch(ntile - 2, r0);
+        fetch(ntile - 3, r1);
+        load_rows(ntile - 1);
+        stage(ntile - 1, first, cur);
+    }
+    old = cur;
     __syncthreads();
-    for (int tile = ntile - 1; tile >= 0; --tile) {
-        if (tile > 0) entry(tile - 1, h_nxt);
-        walk(tile, h_cur);
-        if (tile > 0) stage(tile - 1, nxt);
-        const Tok mine = cur;
-        cur = nxt;
-        if (tile > 1) fetch(tile - 2, nxt);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) h_cur[i] = h_nxt[i];
-        __syncthreads();
-        finish(tile, mine);
-        if (NB == 1) __syncthreads();
+    int tile = ntile - 1;
+    for (; tile > 0; tile -= 2) {
+        step(tile, r0);
+        step(tile - 1, r1);
+    }
+    if (tile == 0) step(0, r0);
+    if constexpr (NB == 2) {
+        Sums s;
+        gather(0, s);
+        finish(0, s, old);
     }
     __syncthreads();
     float (*ends)[NW][64] = reinterpret_cast<float (*)[NW][64]>(&s_p[0][0][0][0][0]);
@@ -375,21 +460,21 @@ __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) 
 // Segments of the time axis: two waves a SIMD, as long as a segment keeps 64 tokens.
 Segments bwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * (N / kNs);
+    const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * (N / states_per_wave_of(N));
     if (waves == 0) return cut_time(T, 1);
-    long long want = (8LL * cus + waves - 1) / waves;
-    if (want > T / 64) want = T / 64;
-    return cut_time(T, static_cast<int>(want > 64 ? 64 : want));
+    const long long want = (8LL * cus + waves - 1) / waves;
+    return cut_time(T, want > T / 64 ? T / 64 : want);
 }
 
 struct Sizes {                       // floats of each part of the workspace, every one a multiple of four
-    size_t seg_h, seg_s, keep, bc, pa, pd;
-    size_t total() const { return 2 * (seg_h + seg_s) + keep + bc + pa + pd; }
+    size_t rows, seg_h, seg_s, keep, bc, pa, pd;
+    size_t total() const { return rows + 2 * (seg_h + seg_s) + keep + bc + pa + pd; }
 };
 size_t up4(size_t n) { return (n + 3) & ~static_cast<size_t>(3); }
 Sizes sizes(int B, int T, int D, int G, int N, Segments s) {
     Sizes z;
     const size_t b = B, d = D, n = N, P = s.P, nc = (T + kTok - 1) / kTok, nblk = (D / G + 63) / 64;
+    z.rows = row_floats(B, T, G, N);
     z.seg_h = s.P > 1 ? up4(b * P * n * d) : 0;
     z.seg_s = s.P > 1 ? up4(b * P * d) : 0;
     z.keep = up4(b * nc * n * d);
@@ -401,7 +486,7 @@ Sizes sizes(int B, int T, int D, int G, int N, Segments s) {
 
 template <class P, int N>
 hipError_t run_bwd(const RevArgs &k, hipStream_t stream) {
-    const dim3 blk(64 * N / kNs);
+    const dim3 blk(64 * N / states_per_wave<N>());
     const unsigned per = static_cast<unsigned>(k.a.B) * k.a.G * k.nblk;
     if (k.seg.P > 1) hipLaunchKernelGGL((seg_grad_kernel<P, N>), dim3(per * (k.seg.P - 1)), blk, 0, stream, k);
     hipLaunchKernelGGL((ssm_bwd_kernel<P, N>), dim3(per * k.seg.P), blk, 0, stream, k);
@@ -440,6 +525,8 @@ hipError_t launch_ssm_bwd(int dtype, const SsmBwdArgs &a, void *ws, hipStream_t 
     k.seg = bwd_segments(a.B, a.T, a.D, a.G, a.N);
     const Sizes z = sizes(a.B, a.T, a.D, a.G, a.N, k.seg);
     float *w = static_cast<float *>(ws);
+    k.rows = row_buf(w, a.B, a.T, a.G, a.N);
+    w += z.rows;
     SegBuf fwd{w, w + z.seg_h};
     w += z.seg_h + z.seg_s;
     k.rev = SegBuf{w, w + z.seg_h};
@@ -453,7 +540,8 @@ hipError_t launch_ssm_bwd(int dtype, const SsmBwdArgs &a, void *ws, hipStream_t 
     f.A = a.A; f.dt_bias = a.dt_bias; f.S0 = a.S0;
     f.B = a.B; f.T = a.T; f.D = a.D; f.G = a.G; f.N = a.N;
     f.softplus = a.softplus;
-    const hipError_t err = launch_ssm_states(dtype, f, k.seg, fwd, k.keep, stream);
+    launch_ssm_rows(dtype, f, k.rows, stream);
+    const hipError_t err = launch_ssm_states(dtype, f, k.seg, fwd, k.rows, k.keep, stream);
     if (err != hipSuccess) return err;
     return dtype == 1 ? run_bwd_n<Bf16>(k, stream) : run_bwd_n<F32>(k, stream);
 }

@@ -35,7 +35,7 @@ conv_step = caller("qdelta_conv_step", CSTEP, dict(at(*CSTEP[:5]), N=2, D=64, W=
 CBWD = ["x", "w", "bias", "S0", "dy", "dS_T", "dx", "dw", "dbias", "dS0", "B", "T", "D", "W", "silu", "dtype", "ws", "n"]
 conv_bwd = caller("qdelta_conv_bwd", CBWD, dict(at(*CBWD[:10]), B=2, T=8, D=64, W=4, silu=1, dtype=1, ws=64 * M, n=M))
 SSM = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S0", "lens", "o", "S_T", "B", "T", "D", "G", "N", "sp", "dtype", "ws", "n"]
-ssm = caller("qdelta_ssm_fwd", SSM, dict(at(*SSM[:12]), B=2, T=8, D=64, G=2, N=16, sp=1, dtype=1, ws=None, n=0))
+ssm = caller("qdelta_ssm_fwd", SSM, dict(at(*SSM[:12]), B=2, T=8, D=64, G=2, N=16, sp=1, dtype=1, ws=64 * M, n=M))
 SSTEP = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S", "o", "n_seq", "D", "G", "N", "sp", "dtype"]
 ssm_step = caller("qdelta_ssm_step", SSTEP, dict(at(*SSTEP[:10]), n_seq=2, D=64, G=2, N=16, sp=1, dtype=1))
 SBWD = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S0", "d_o", "dS_T", "du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddtb",
@@ -72,8 +72,11 @@ def test_ssm_refusals(lib):
                      (dict(D=1 << 28, G=1), UNSUPPORTED), (dict(B=0), OK), (dict(D=0), OK)):
         assert ssm(lib, **kw) == want, kw
     need = lib.qdelta_ssm_fwd_workspace_bytes(1, 4096, 64, 1, 16, 1)
-    assert need > 0                                                        # few channels: segments
-    assert ssm(lib, B=1, T=4096, G=1) == WORKSPACE
+    rows = lambda B, T, G, N: 2 * B * G * N * ((T + 15) // 16 * 16 + 16) * 4  # noqa: E731  (B and C in fp32)
+    assert need > rows(1, 4096, 1, 16)                                     # few channels: segments too
+    assert lib.qdelta_ssm_fwd_workspace_bytes(8, 4096, 2048, 1, 16, 1) == rows(8, 4096, 1, 16)
+    assert lib.qdelta_ssm_fwd_workspace_bytes(8, 0, 2048, 1, 16, 1) == 0
+    assert ssm(lib, ws=None) == WORKSPACE and ssm(lib, n=64) == WORKSPACE and ssm(lib, ws=64 * M + 4) == WORKSPACE
     assert ssm(lib, B=1, T=4096, G=1, ws=64 * M, n=need - 1) == WORKSPACE
     assert ssm(lib, B=1, T=4096, G=1, ws=11 * M, n=need) == INVALID        # over o
     for kw, want in ((dict(n_seq=-1), INVALID), (dict(N=20), UNSUPPORTED), (dict(S=None), INVALID), (dict(S=9 * M + 4), INVALID),
