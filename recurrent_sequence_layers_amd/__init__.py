@@ -21,6 +21,7 @@ carries a state, for one token:
     qdelta_ssm_fwd / qdelta_ssm_step / qdelta_ssm_bwd
     qdelta_group_norm_fwd / qdelta_group_norm_bwd
 """
+import contextlib
 import ctypes
 import os
 
@@ -422,11 +423,32 @@ def _shape(t, name, dims):
 
 
 def _check_all(device, checks):
-    """_check for each (tensor, name, dtype, shape), and that every tensor is on `device`."""
+    """_check for each (tensor, name, dtype, shape), and that every tensor is on `device`.  A
+    decode step is a few microseconds on the GPU, so what is right costs four comparisons."""
     for t, name, dtype, shape in checks:
+        if t is None:
+            continue
+        try:
+            if t.dtype == dtype and t.device == device and (shape is None or t.shape == shape) and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
         _check(t, name, dtype, shape)
-        if t is not None and t.device != device:
+        if t.device != device:
             raise QDeltaError(f"{name} must be on {device}, got {t.device}")
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _enter(stream, device):
+    """(context, stream handle) for a call's allocations and launches: `device` and the stream
+    current, and no context at all where they are already."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return _NO_CONTEXT, torch.cuda.current_stream(device).cuda_stream
+    s = _launch_stream(stream, device)
+    return torch.cuda.stream(s), s.cuda_stream
 
 
 def _result(t, shape, dtype, device):
@@ -445,18 +467,19 @@ def _results(out, specs, device):
 
 
 def _workspace(workspace, need, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one, and the tensor itself."""
+    """(address, bytes) of the caller's workspace, or of a new one, and the tensor itself."""
     import torch
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is None:
-        return None, 0, None
-    _check_all(device, [(workspace, "workspace", None, None)])
-    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    _check_all(device, [(workspace, "workspace", workspace.dtype, None)])
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _handle(s):
-    return ctypes.c_void_p(s.cuda_stream)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=None, S_T=None,
@@ -470,8 +493,8 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
     lib = load_library()
     B, T, D = _shape(x, "x", 3)
     W = _shape(w, "w", 2)[1]
-    s = _launch_stream(stream, x.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, x.device)
+    with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
         y = _result(y, (B, T, D), dt, dev)
@@ -480,8 +503,8 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
                          (S0, "S0", dt, (B, W - 1, D)), (lens, "lens", torch.int32, (B,)), (y, "y", dt, (B, T, D)),
                          (S_T, "S_T", dt, (B, W - 1, D))])
-        rc = lib.qdelta_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, D, W,
-                                 int(silu), code, _handle(s))
+        rc = lib.qdelta_conv_fwd(_at(x), _at(w), _at(bias), _at(S0), _at(lens), _at(y), _at(S_T), B, T, D, W,
+                                 int(silu), code, handle)
         _raise(rc, "qdelta_conv_fwd")
         return y, S_T
 
@@ -493,14 +516,14 @@ def qdelta_conv_step(x, w, bias, S, silu: bool = True, y=None, stream=None):
     lib = load_library()
     N, D = _shape(x, "x", 2)
     W = _shape(w, "w", 2)[1]
-    s = _launch_stream(stream, x.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, x.device)
+    with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
         y = _result(y, (N, D), dt, dev)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)), (S, "S", dt, (N, W - 1, D)),
                          (y, "y", dt, (N, D))])
-        rc = lib.qdelta_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(S), _ptr(y), N, D, W, int(silu), code, _handle(s))
+        rc = lib.qdelta_conv_step(_at(x), _at(w), _at(bias), _at(S), _at(y), N, D, W, int(silu), code, handle)
         _raise(rc, "qdelta_conv_step")
         return y
 
@@ -519,8 +542,8 @@ def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: 
     lib = load_library()
     B, T, D = _shape(x, "x", 3)
     W = _shape(w, "w", 2)[1]
-    s = _launch_stream(stream, x.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, x.device)
+    with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
@@ -528,9 +551,9 @@ def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: 
         out = _results(out, dict(dx=(True, (B, T, D), dt), dw=(True, (D, W), f32), dbias=(bias is not None, (D,), f32),
                                  dS0=(want_dS0, (B, W - 1, D), dt)), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_conv_bwd_workspace_bytes(B, T, D, W, code), dev)
-        rc = lib.qdelta_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(dy), _ptr(dS_T), _ptr(out["dx"]),
-                                 _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dS0"]), B, T, D, W, int(silu), code, p, n,
-                                 _handle(s))
+        rc = lib.qdelta_conv_bwd(_at(x), _at(w), _at(bias), _at(S0), _at(dy), _at(dS_T), _at(out["dx"]),
+                                 _at(out["dw"]), _at(out["dbias"]), _at(out["dS0"]), B, T, D, W, int(silu), code, p, n,
+                                 handle)
         _raise(rc, "qdelta_conv_bwd")
         return out
 
@@ -563,8 +586,8 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
     import torch
     lib = load_library()
     (B, T, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
-    s = _launch_stream(stream, u.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, u.device)
+    with context:
         dev, f32, code = u.device, torch.float32, _dtype_code(u.dtype)
         o = _result(o, (B, T, ch), u.dtype, dev)
         if want_state:
@@ -572,8 +595,8 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
         _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
                                   (o, "o", u.dtype, (B, T, ch)), (S_T, "S_T", f32, (B, ch, N))])
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_fwd_workspace_bytes(B, T, ch, G, N, code), dev)
-        rc = lib.qdelta_ssm_fwd(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S0),
-                                _ptr(lens), _ptr(o), _ptr(S_T), B, T, ch, G, N, int(softplus), code, p, n, _handle(s))
+        rc = lib.qdelta_ssm_fwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
+                                _at(lens), _at(o), _at(S_T), B, T, ch, G, N, int(softplus), code, p, n, handle)
         _raise(rc, "qdelta_ssm_fwd")
         return o, S_T
 
@@ -584,13 +607,13 @@ def qdelta_ssm_step(u, dt, A, Bm, Cm, D, z, dt_bias, S, softplus: bool = True, o
     import torch
     lib = load_library()
     (n_seq, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 1)
-    s = _launch_stream(stream, u.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, u.device)
+    with context:
         dev, code = u.device, _dtype_code(u.dtype)
         o = _result(o, (n_seq, ch), u.dtype, dev)
         _check_all(dev, checks + [(S, "S", torch.float32, (n_seq, ch, N)), (o, "o", u.dtype, (n_seq, ch))])
-        rc = lib.qdelta_ssm_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S),
-                                 _ptr(o), n_seq, ch, G, N, int(softplus), code, _handle(s))
+        rc = lib.qdelta_ssm_step(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S),
+                                 _at(o), n_seq, ch, G, N, int(softplus), code, handle)
         _raise(rc, "qdelta_ssm_step")
         return o
 
@@ -609,8 +632,8 @@ def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus
     import torch
     lib = load_library()
     (B, T, ch, G, N), checks = _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
-    s = _launch_stream(stream, u.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, u.device)
+    with context:
         dev, f32, e, code = u.device, torch.float32, u.dtype, _dtype_code(u.dtype)
         _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (d_o, "d_o", e, (B, T, ch)), (dS_T, "dS_T", f32, (B, ch, N))])
         tok, bc = (B, T, ch), (B, T, G, N)
@@ -618,10 +641,10 @@ def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus
                                  dC=(True, bc, e), dD=(D is not None, (ch,), f32), dz=(z is not None, tok, e),
                                  ddt_bias=(dt_bias is not None, (ch,), f32), dS0=(want_dS0, (B, ch, N), f32)), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_bwd_workspace_bytes(B, T, ch, G, N, code), dev)
-        rc = lib.qdelta_ssm_bwd(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(S0),
-                                _ptr(d_o), _ptr(dS_T), _ptr(out["du"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
-                                _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]), _ptr(out["dS0"]),
-                                B, T, ch, G, N, int(softplus), code, p, n, _handle(s))
+        rc = lib.qdelta_ssm_bwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
+                                _at(d_o), _at(dS_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA"]), _at(out["dB"]),
+                                _at(out["dC"]), _at(out["dD"]), _at(out["dz"]), _at(out["ddt_bias"]), _at(out["dS0"]),
+                                B, T, ch, G, N, int(softplus), code, p, n, handle)
         _raise(rc, "qdelta_ssm_bwd")
         return out
 
@@ -657,8 +680,8 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
     import torch
     lib = load_library()
     N, L, C = _norm_sizes(x, groups)
-    s = _launch_stream(stream, x.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, x.device)
+    with context:
         dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
         y = _result(y, x.shape, dt, dev)
         if want_stats:
@@ -666,8 +689,8 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
         _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
                          (gate, "gate", dt, x.shape), (y, "y", dt, x.shape), (stats, "stats", f32, (N, groups, 2))])
         p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_fwd_workspace_bytes(N, L, C, groups, code), dev)
-        rc = lib.qdelta_group_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), _ptr(stats), N, L, C, groups,
-                                       float(eps), int(silu), code, p, n, _handle(s))
+        rc = lib.qdelta_group_norm_fwd(_at(x), _at(weight), _at(bias), _at(gate), _at(y), _at(stats), N, L, C, groups,
+                                       float(eps), int(silu), code, p, n, handle)
         _raise(rc, "qdelta_group_norm_fwd")
         return y, stats
 
@@ -685,8 +708,8 @@ def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: b
     import torch
     lib = load_library()
     N, L, C = _norm_sizes(x, groups)
-    s = _launch_stream(stream, x.device)
-    with torch.cuda.stream(s):
+    context, handle = _enter(stream, x.device)
+    with context:
         dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
         if stats is None:
             raise QDeltaError("stats must be the forward's")
@@ -695,8 +718,8 @@ def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: b
         out = _results(out, dict(dx=(True, tuple(x.shape), dt), dweight=(weight is not None, (C,), f32),
                                  dbias=(bias is not None, (C,), f32), dgate=(gate is not None, tuple(x.shape), dt)), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_bwd_workspace_bytes(N, L, C, groups, code), dev)
-        rc = lib.qdelta_group_norm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(stats), _ptr(dy), _ptr(out["dx"]),
-                                       _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dgate"]), N, L, C, groups,
-                                       int(silu), code, p, n, _handle(s))
+        rc = lib.qdelta_group_norm_bwd(_at(x), _at(weight), _at(bias), _at(gate), _at(stats), _at(dy), _at(out["dx"]),
+                                       _at(out["dweight"]), _at(out["dbias"]), _at(out["dgate"]), N, L, C, groups,
+                                       int(silu), code, p, n, handle)
         _raise(rc, "qdelta_group_norm_bwd")
         return out

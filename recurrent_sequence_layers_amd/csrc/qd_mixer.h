@@ -107,20 +107,19 @@ __device__ __forceinline__ float dsiluf(float x) {
     return s * fmaf(x, 1.f - s, 1.f);
 }
 
-// log(1 + exp(x)).  With e = exp(x) and r = fl(1 + e), log(1 + e) = log(r) e / (r - 1) to
-// rounding accuracy also where e is far below 1 (the error of r cancels in the quotient).
+// log(1 + exp(x)).  With e = exp(x) and r = fl(1 + e), log(1 + e) = log(r) + (e - (r - 1)) / r to
+// rounding accuracy also where e is far below 1: the second term is what the sum r lost.
 // The exponent's rounding, amplified by its size in a plain exp2(x log2 e), is put back as
-// a first-order factor.  Above 20 the value is x to fp32 accuracy (exp(-20) = 2e-9).
+// a first-order factor.  Above 20 the value is x to fp32 accuracy (exp(-20) = 2e-9); a NaN
+// takes that branch too.  No branches: they would stop the tokens of a tile from overlapping.
 __device__ __forceinline__ float softplusf(float x) {
-    const float xc = x < -126.f ? -126.f : x;
+    const float xc = fmaxf(x, -126.f);
     const float p = xc * kLog2e;
-    const float r = fmaf(xc, 1.925963033500e-8f, fmaf(xc, kLog2e, -p));
-    const float e = __builtin_amdgcn_exp2f(p) * fmaf(r, kLn2, 1.f);
-    const float s = 1.f + e, d = s - 1.f;
-    // evaluated on every path and selected: a branch would stop the tokens of a tile from overlapping
-    const float small = __builtin_amdgcn_logf(s) * (kLn2 * e) * __builtin_amdgcn_rcpf(d);
-    const float near = d == 0.f ? e : small;
-    return x > 20.f ? x : near;
+    const float q = fmaf(xc, 1.925963033500e-8f, fmaf(xc, kLog2e, -p));
+    const float e = __builtin_amdgcn_exp2f(p) * fmaf(q, kLn2, 1.f);
+    const float r = 1.f + e;
+    const float small = fmaf(__builtin_amdgcn_logf(r), kLn2, (e - (r - 1.f)) * __builtin_amdgcn_rcpf(r));
+    return x <= 20.f ? small : x;
 }
 
 // V consecutive elements as floats; V * sizeof(element) is 16 bytes (16-byte aligned) or V is 1.

@@ -43,63 +43,81 @@ __device__ __forceinline__ float unit_sum(float x, int LG, float *red) {
     return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// A lane keeps its group and columns over all its units (the grid's step is a multiple of G
+// units), so weight and bias are read once.
 template <class P, int V, int K>
 __global__ __launch_bounds__(kThreads) void norm_rows_kernel(const RowArgs k) {
     using R = typename P::R;
     __shared__ float red[kThreads / kWave];
     const NormArgs &a = k.a;
     const int sub = threadIdx.x & (k.LG - 1);
-    const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / k.LG;
-    const bool live = unit < k.units;
-    const long long un = live ? unit : k.units - 1;
-    const size_t base = static_cast<size_t>(un) * k.E;
-    const int g = static_cast<int>(un % a.G), c0 = g * k.E;
-    const R *x = static_cast<const R *>(a.x) + base;
-    const R *gate = a.gate ? static_cast<const R *>(a.gate) + base : nullptr;
-
-    float v[K][V], z[K][V];
-    float s = 0.f;
+    const long long slot = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / k.LG;
+    const long long step = static_cast<long long>(gridDim.x) * kThreads / k.LG;
+    const int c0 = static_cast<int>(slot % a.G) * k.E;
+    const bool gated = a.gate != nullptr;
+    float w[K][V], bias[K][V];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const int e = (sub + j * k.LG) * V;
-        const bool in = e < k.E;
-        load_vec<P, V>(x + (in ? e : 0), v[j]);
-        if (gate) load_vec<P, V>(gate + (in ? e : 0), z[j]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += in ? v[j][i] : 0.f;
-    }
-    // divided, not multiplied by a rounded reciprocal: a constant group's mean is its value
-    const float mean = unit_sum(s, k.LG, red) / static_cast<float>(k.E);
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const bool in = (sub + j * k.LG) * V < k.E;
+    for (int j = 0; j < K; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            v[j][i] -= mean;
-            q = in ? fmaf(v[j][i], v[j][i], q) : q;
+            const int e = (sub + j * k.LG) * V + i;
+            w[j][i] = a.w && e < k.E ? a.w[c0 + e] : 1.f;
+            bias[j][i] = a.bias && e < k.E ? a.bias[c0 + e] : 0.f;
         }
-    }
-    const float rstd = 1.f / sqrtf(unit_sum(q, k.LG, red) / static_cast<float>(k.E) + a.eps);
-    if (!live) return;
-    if (a.stats && sub == 0) {
-        a.stats[2 * un] = mean;
-        a.stats[2 * un + 1] = rstd;
-    }
-    R *y = static_cast<R *>(a.y) + base;
+    // every lane of a workgroup makes the same number of steps: the sums' barriers are met by all
+    for (long long first = static_cast<long long>(blockIdx.x) * kThreads / k.LG; first < k.units; first += step) {
+        const long long unit = first + threadIdx.x / k.LG;
+        const bool live = unit < k.units;
+        const long long un = live ? unit : k.units - 1;
+        const size_t base = static_cast<size_t>(un) * k.E;
+        const R *x = static_cast<const R *>(a.x) + base;
+        const R *gate = gated ? static_cast<const R *>(a.gate) + base : x;
+        float v[K][V], z[K][V];
+        float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const int e = (sub + j * k.LG) * V;
-        if (e >= k.E) continue;
-        float out[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float w = a.w ? a.w[c0 + e + i] : 1.f, bias = a.bias ? a.bias[c0 + e + i] : 0.f;
-            float f = fmaf(v[j][i] * rstd, w, bias);
-            if (a.silu) f = siluf(f);
-            out[i] = gate ? f * siluf(z[j][i]) : f;
+        for (int j = 0; j < K; ++j) {
+            const int e0 = (sub + j * k.LG) * V, e = e0 < k.E ? e0 : 0;
+            load_vec<P, V>(x + e, v[j]);
+            if (gated) load_vec<P, V>(gate + e, z[j]);
         }
-        store_vec<P, V>(y + e, out);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool in = (sub + j * k.LG) * V < k.E;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += in ? v[j][i] : 0.f;
+        }
+        // divided, not multiplied by a rounded reciprocal: a constant group's mean is its value
+        const float mean = unit_sum(s, k.LG, red) / static_cast<float>(k.E);
+        float q = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool in = (sub + j * k.LG) * V < k.E;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[j][i] -= mean;
+                q = in ? fmaf(v[j][i], v[j][i], q) : q;
+            }
+        }
+        const float rstd = 1.f / sqrtf(unit_sum(q, k.LG, red) / static_cast<float>(k.E) + a.eps);
+        if (!live) continue;
+        if (a.stats && sub == 0) {
+            a.stats[2 * un] = mean;
+            a.stats[2 * un + 1] = rstd;
+        }
+        R *y = static_cast<R *>(a.y) + base;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int e = (sub + j * k.LG) * V;
+            if (e >= k.E) continue;
+            float out[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float f = fmaf(v[j][i] * rstd, w[j][i], bias[j][i]);
+                if (a.silu) f = siluf(f);
+                out[i] = gated ? f * siluf(z[j][i]) : f;
+            }
+            store_vec<P, V>(y + e, out);
+        }
     }
 }
 
@@ -287,17 +305,17 @@ __global__ __launch_bounds__(kThreads) void norm_group_kernel(const LongArgs k) 
     __shared__ float red[kThreads / kWave];
     const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
     const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
-    const long long items = static_cast<long long>(k.S) * k.E;
+    const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
     const float M = static_cast<float>(k.a.L) * static_cast<float>(k.E);
     float s = 0.f;
-    for (long long i = threadIdx.x; i < items; i += kThreads) {
-        const int run = static_cast<int>(i / k.E), e = static_cast<int>(i % k.E);
+    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+        const int run = i / E, e = i - run * E;
         s += part[static_cast<size_t>(run) * 2 * k.a.C + e] * static_cast<float>(min(k.RL, k.a.L - run * k.RL));
     }
     const float mean = block_sum(s, red) / M;
     float q = 0.f;
-    for (long long i = threadIdx.x; i < items; i += kThreads) {
-        const int run = static_cast<int>(i / k.E), e = static_cast<int>(i % k.E);
+    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+        const int run = i / E, e = i - run * E;
         const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
         const float d = p[0] - mean;
         q += fmaf(d * d, static_cast<float>(min(k.RL, k.a.L - run * k.RL)), p[k.a.C]);
@@ -315,10 +333,10 @@ __global__ __launch_bounds__(kThreads) void norm_group_bwd_kernel(const LongArgs
     __shared__ float red[kThreads / kWave];
     const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
     const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
-    const long long items = static_cast<long long>(k.S) * k.E;
+    const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
     float sa = 0.f, sx = 0.f;
-    for (long long i = threadIdx.x; i < items; i += kThreads) {
-        const int run = static_cast<int>(i / k.E), e = static_cast<int>(i % k.E);
+    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+        const int run = i / E, e = i - run * E;
         const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
         const float w = k.a.w ? k.a.w[g * k.E + e] : 1.f;
         sa = fmaf(w, p[0], sa);
@@ -461,8 +479,18 @@ __global__ __launch_bounds__(kThreads) void norm_zero_kernel(float *dw, float *d
 // ---------------------------------------------------------------- plans
 struct RowPlan {
     bool use;
-    int V, LG, K, grid, R;           // grid, R: backward
+    int V, LG, K, grid, R;           // grid: workgroups of the backward; R: its rows of partial sums
 };
+// Workgroups of a persistent row kernel: at most `most`, and their slots a multiple of G, so
+// that a slot's units are all of one group.
+int row_grid(int N, int G, int LG, int most) {
+    const int upb = kThreads / LG;
+    int step = G;
+    for (int d = upb; d > 1 && step % 2 == 0; d /= 2) step /= 2;
+    const long long need = (static_cast<long long>(N) * G + upb - 1) / upb;
+    const long long grid = need < most ? need : most;
+    return static_cast<int>((grid + step - 1) / step * step);
+}
 int max_vec(int dtype) { return dtype == 1 ? 8 : 4; }
 RowPlan row_plan(int dtype, int N, int L, int C, int G) {
     RowPlan p{};
@@ -478,16 +506,8 @@ RowPlan row_plan(int dtype, int N, int L, int C, int G) {
     if (nv > p.LG * wave_k) p.LG = kThreads;
     p.K = 1;
     while (p.LG * p.K < nv) p.K *= 2;
-    // Backward: a whole number of groups' worth of slots, about four workgroups a compute unit.
-    const int upb = kThreads / p.LG;
-    int step = G;                     // workgroups so that workgroups * upb is a multiple of G
-    for (int d = upb; d > 1; d /= 2)
-        if (step % 2 == 0) step /= 2;
-    const long long units = static_cast<long long>(N) * G, need = (units + upb - 1) / upb;
-    long long grid = need < 1024 ? need : 1024;
-    grid = (grid + step - 1) / step * step;
-    p.grid = static_cast<int>(grid);
-    p.R = static_cast<int>(grid * upb / G);
+    p.grid = row_grid(N, G, p.LG, 1024);
+    p.R = static_cast<int>(static_cast<long long>(p.grid) * (kThreads / p.LG) / G);
     return p;
 }
 struct LongPlan {
@@ -548,7 +568,8 @@ bool norm_fits(int dtype, int N, int L, int C, int G) {
     if (static_cast<long long>(N) * L >= (1LL << 31) || C >= (1 << 26)) return false;
     if (r.use) return static_cast<long long>(N) * G * r.LG < lim;
     const LongPlan p = long_plan(dtype, N, L, C);
-    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(N) * G * kThreads < lim;
+    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(N) * G * kThreads < lim &&
+           static_cast<long long>(p.S) * (C / G) < lim;
 }
 
 size_t norm_fwd_workspace(int dtype, int N, int L, int C, int G) {
@@ -569,7 +590,10 @@ hipError_t launch_norm_fwd(int dtype, const NormArgs &a, void *ws, hipStream_t s
     const RowPlan r = row_plan(dtype, a.N, a.L, a.C, a.G);
     if (r.use) {
         RowArgs k{a, a.C / a.G, r.LG, static_cast<long long>(a.N) * a.G, nullptr, 0};
-        const int upb = kThreads / r.LG, grid = static_cast<int>((k.units + upb - 1) / upb);
+#ifndef QD_NG
+#define QD_NG 2048
+#endif
+        const int grid = row_grid(a.N, a.G, r.LG, QD_NG);
         if (dtype == 1) rows<Bf16>(k, r, grid, false, stream);
         else rows<F32>(k, r, grid, false, stream);
         return hipGetLastError();

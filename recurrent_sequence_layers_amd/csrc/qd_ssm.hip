@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
     const int cb = blockIdx.x % ncb, bp = blockIdx.x / ncb, p = bp % nseg, b = bp / nseg;
     const int g = cb / k.nblk, c_in = (cb % k.nblk) * 64 + lane;
     const bool live = c_in < k.Dg;
-    const int ch = g * k.Dg + min(c_in, k.Dg - 1);
+    const uint32_t ch = g * k.Dg + min(c_in, k.Dg - 1);
     const int n0 = wave * NS;
     const size_t D = a.D;
     const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
@@ -122,11 +122,11 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
 
     if (tb < te) {
         const size_t row0 = static_cast<size_t>(b) * a.T;
-        const R *u = static_cast<const R *>(a.u) + row0 * D + ch;
-        const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
+        const R *u = static_cast<const R *>(a.u) + row0 * D;
+        const R *dt = static_cast<const R *>(a.dt) + row0 * D;
         const bool gated = a.z != nullptr;
-        const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : u;
-        R *o = MODE == kOut ? static_cast<R *>(a.o) + row0 * D + ch : nullptr;
+        const R *z = gated ? static_cast<const R *>(a.z) + row0 * D : u;
+        R *o = MODE == kOut ? static_cast<R *>(a.o) + row0 * D : nullptr;
         const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
         const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
         const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
@@ -146,9 +146,9 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
 #pragma unroll
             for (int j = 0; j < TPW; ++j) {
                 const size_t t = min(tb + tile * kTile + wave + j * NW, te - 1);
-                r.u[j] = u[t * D];
-                r.dt[j] = dt[t * D];
-                if (MODE == kOut) r.z[j] = z[t * D];
+                r.u[j] = (u + t * D)[ch];
+                r.dt[j] = (dt + t * D)[ch];
+                if (MODE == kOut) r.z[j] = (z + t * D)[ch];
             }
         };
         struct Kept {                // what the end of a token needs of its rows
@@ -178,9 +178,9 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
         auto keep_state = [&](int t0) {
             if (MODE == kKeep && live && t0 < te) {
                 const size_t nc = (a.T + kTok - 1) / kTok;
-                float *keep = k.keep + ((b * nc + t0 / kTok) * N + n0) * D + ch;
+                float *keep = k.keep + ((b * nc + t0 / kTok) * N + n0) * D;
 #pragma unroll
-                for (int i = 0; i < NS; ++i) keep[i * D] = h[i];
+                for (int i = 0; i < NS; ++i) (keep + i * D)[ch] = h[i];
             }
         };
         // GT tokens from t0 = tile start + j.  `between` is arithmetic of its own that the
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
                 for (int w = 0; w < NW; ++w) y += p.y[j][w];
                 const float gate = siluf(r.z[j]);
                 y *= gated ? gate : 1.f;
-                if (live && t < te) o[static_cast<size_t>(t) * D] = P::from_f32(y);
+                if (live && t < te) (o + static_cast<size_t>(t) * D)[ch] = P::from_f32(y);
             }
         };
         auto nothing = [] {};

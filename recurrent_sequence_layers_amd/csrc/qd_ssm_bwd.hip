@@ -24,6 +24,9 @@
 // neighbouring tokens non-finite.)  Each 64-channel block leaves its sums in the workspace and a second kernel
 // adds the blocks in order, so the result does not depend on the order of workgroups.
 #include "qd_ssm.h"
+#ifndef QD_SG
+#define QD_SG 6
+#endif
 
 namespace qd {
 namespace {
@@ -51,16 +54,17 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel
     const int ncb = a.G * k.nblk, nseg = k.seg.P - 1;
     const int cb = blockIdx.x % ncb, bp = blockIdx.x / ncb, p = 1 + bp % nseg, b = bp / nseg;
     const int g = cb / k.nblk, c_in = (cb % k.nblk) * 64 + lane;
-    const int ch = g * k.Dg + min(c_in, k.Dg - 1), n0 = wave * NS;
+    const uint32_t ch = g * k.Dg + min(c_in, k.Dg - 1);
+    const int n0 = wave * NS;
     const size_t D = a.D, row0 = static_cast<size_t>(b) * a.T;
     const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTile - 1) / kTile;
     float A2[NS], G[NS] = {}, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] = a.A[static_cast<size_t>(ch) * N + n0 + i] * kLog2e;
-    const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
-    const R *d_o = static_cast<const R *>(a.d_o) + row0 * D + ch;
+    const R *dt = static_cast<const R *>(a.dt) + row0 * D;
+    const R *d_o = static_cast<const R *>(a.d_o) + row0 * D;
     const bool gated = a.z != nullptr;
-    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : d_o;
+    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D : d_o;
     const float *Cw = k.rows.c + ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
     const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
 
@@ -71,9 +75,9 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const size_t t = max(min(tb + tile * kTile + wave + j * NW, te - 1), tb);
-            r.dt[j] = dt[t * D];
-            r.d_o[j] = d_o[t * D];
-            r.z[j] = z[t * D];
+            r.dt[j] = (dt + t * D)[ch];
+            r.d_o[j] = (d_o + t * D)[ch];
+            r.z[j] = (z + t * D)[ch];
         }
     };
     auto stage = [&](int tile, const Raw &r) {
@@ -158,7 +162,8 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
     const int cb = blockIdx.x % ncb, bp = blockIdx.x / ncb, p = bp % k.seg.P, b = bp / k.seg.P;
     const int g = cb / k.nblk, c_in = (cb % k.nblk) * 64 + lane;
     const bool live = c_in < k.Dg;
-    const int ch = g * k.Dg + min(c_in, k.Dg - 1), n0 = wave * NS;
+    const uint32_t ch = g * k.Dg + min(c_in, k.Dg - 1);
+    const int n0 = wave * NS;
     const size_t D = a.D, row0 = static_cast<size_t>(b) * a.T;
     const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTok - 1) / kTok;
     const size_t st = (static_cast<size_t>(b) * D + ch) * N + n0;
@@ -175,16 +180,16 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
 #pragma unroll
         for (int i = 0; i < NS; ++i) G[i] = live ? fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), G[i], gq[i * D]) : 0.f;
     }
-    const R *u = static_cast<const R *>(a.u) + row0 * D + ch;
-    const R *dt = static_cast<const R *>(a.dt) + row0 * D + ch;
-    const R *d_o = static_cast<const R *>(a.d_o) + row0 * D + ch;
+    const R *u = static_cast<const R *>(a.u) + row0 * D;
+    const R *dt = static_cast<const R *>(a.dt) + row0 * D;
+    const R *d_o = static_cast<const R *>(a.d_o) + row0 * D;
     const bool gated = a.z != nullptr;
-    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D + ch : u;
+    const R *z = gated ? static_cast<const R *>(a.z) + row0 * D : u;
     const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
     const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
     const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.Dskip ? a.Dskip[ch] : 0.f;
     const size_t nc = (a.T + kTok - 1) / kTok;
-    const float *keep = k.keep + ((static_cast<size_t>(b) * nc + tb / kTok) * N + n0) * D + ch;
+    const float *keep = k.keep + ((static_cast<size_t>(b) * nc + tb / kTok) * N + n0) * D;
     float *part_bc = k.part_bc + (((static_cast<size_t>(cb % k.nblk) * a.B + b) * a.T) * a.G + g) * 2 * N + n0;
     float acc_d = 0.f, acc_b = 0.f;
 
@@ -198,13 +203,13 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
         for (int j = 0; j < TPW; ++j) {
             if (NW > kTok && wave >= kTok) continue;
             const size_t t = min(tb + tile * kTok + wave + j * NW, te - 1);
-            r.u[j] = u[t * D];
-            r.x[j] = dt[t * D];
-            r.d_o[j] = d_o[t * D];
-            r.z[j] = z[t * D];
+            r.u[j] = (u + t * D)[ch];
+            r.x[j] = (dt + t * D)[ch];
+            r.d_o[j] = (d_o + t * D)[ch];
+            r.z[j] = (z + t * D)[ch];
         }
 #pragma unroll
-        for (int i = 0; i < NS; ++i) r.h[i] = keep[static_cast<size_t>(tile) * N * D + i * D];
+        for (int i = 0; i < NS; ++i) r.h[i] = (keep + (static_cast<size_t>(tile) * N + i) * D)[ch];
     };
     struct Kept {                    // what the end of a token needs, and the tile's entry state
         float u[TPW], x[TPW], z[TPW], d_o[TPW], delta[TPW], dy[TPW], h[NS];
@@ -292,6 +297,14 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
                 set = zero4();
             }
         }
+        // Spread the channel sums: one MFMA (32 cycles of its own pipe) to the vector instructions
+        // that fill that time, instead of runs of them that the wave would wait for.
+#pragma unroll
+        for (int m = 0; m < 2 * NS * kTok; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x2, QD_SG, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         load_rows(tile - 1);
 #pragma unroll
         for (int i = 0; i < NS; ++i) dA[i] += dAt[i];
@@ -333,10 +346,10 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
             const float du = fmaf(r.delta[j], s1, skip * r.dy[j]);
             const float dz = r.d_o[j] * fmaf(skip, r.u[j], y) * dsiluf(r.z[j]);
             if (live && in) {
-                const size_t at = (row0 + t) * D + ch;
-                static_cast<R *>(a.du)[at] = P::from_f32(du);
-                static_cast<R *>(a.ddt)[at] = P::from_f32(dd);
-                if (gated) static_cast<R *>(a.dz)[at] = P::from_f32(dz);
+                const size_t at = (row0 + t) * D;
+                (static_cast<R *>(a.du) + at)[ch] = P::from_f32(du);
+                (static_cast<R *>(a.ddt) + at)[ch] = P::from_f32(dd);
+                if (gated) (static_cast<R *>(a.dz) + at)[ch] = P::from_f32(dz);
             }
         }
     };
