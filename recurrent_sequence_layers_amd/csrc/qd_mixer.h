@@ -122,17 +122,19 @@ __device__ __forceinline__ float softplusf(float x) {
     return x <= 20.f ? small : x;
 }
 
-// V consecutive elements as floats; V * sizeof(element) is 16 bytes (16-byte aligned) or V is 1.
+// V consecutive elements as floats; V elements are 16 or 8 bytes (aligned to that) or one.
 template <class P, int V>
 __device__ __forceinline__ void load_vec(const typename P::R *p, float (&v)[V]) {
     if constexpr (V == 1) {
         v[0] = P::to_f32(p[0]);
     } else {
-        static_assert(V * P::kBytes == 16, "16-byte vectors");
-        const uint4 r = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t q[4] = {r.x, r.y, r.z, r.w};
+        constexpr int W = V * P::kBytes / 4;
+        static_assert(W == 4 || W == 2, "16 or 8 bytes");
+        uint32_t q[W];
+        if constexpr (W == 4) *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(p);
+        else *reinterpret_cast<uint2 *>(q) = *reinterpret_cast<const uint2 *>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < W; ++i) {
             if constexpr (P::kBytes == 2) {
                 v[2 * i] = __uint_as_float(q[i] << 16);
                 v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
@@ -147,15 +149,17 @@ __device__ __forceinline__ void store_vec(typename P::R *p, const float (&v)[V])
     if constexpr (V == 1) {
         p[0] = P::from_f32(v[0]);
     } else {
-        uint32_t q[4];
+        constexpr int W = V * P::kBytes / 4;
+        uint32_t q[W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < W; ++i) {
             if constexpr (P::kBytes == 2)
                 q[i] = static_cast<uint32_t>(P::from_f32(v[2 * i])) | (static_cast<uint32_t>(P::from_f32(v[2 * i + 1])) << 16);
             else
                 q[i] = __float_as_uint(v[i]);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+        if constexpr (W == 4) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(q);
+        else *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(q);
     }
 }
 

@@ -291,30 +291,32 @@ __global__ __launch_bounds__(kThreads) void norm_partial_kernel(const LongArgs k
     }
 }
 
+// A group's runs: one workgroup, wide because its loads are what it waits for.
+constexpr int kGroupThreads = 1024, kGroupWaves = kGroupThreads / kWave;
 __device__ __forceinline__ float block_sum(float x, float *red) {
     x = group_sum(x, kWave);
     __syncthreads();
     if (lane_id() == 0) red[wave_id()] = x;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    return group_sum(red[lane_id() & (kGroupWaves - 1)], kGroupWaves);
 }
 
 // Statistics of one group from its channels' runs: the mean of the means, then the square
 // sums moved to it.
-__global__ __launch_bounds__(kThreads) void norm_group_kernel(const LongArgs k) {
-    __shared__ float red[kThreads / kWave];
+__global__ __launch_bounds__(kGroupThreads) void norm_group_kernel(const LongArgs k) {
+    __shared__ float red[kGroupWaves];
     const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
     const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
     const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
     const float M = static_cast<float>(k.a.L) * static_cast<float>(k.E);
     float s = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
         const int run = i / E, e = i - run * E;
         s += part[static_cast<size_t>(run) * 2 * k.a.C + e] * static_cast<float>(min(k.RL, k.a.L - run * k.RL));
     }
     const float mean = block_sum(s, red) / M;
     float q = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
         const int run = i / E, e = i - run * E;
         const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
         const float d = p[0] - mean;
@@ -329,13 +331,13 @@ __global__ __launch_bounds__(kThreads) void norm_group_kernel(const LongArgs k) 
 }
 
 // The group's two sums for dx, over its channels' runs, divided by M.
-__global__ __launch_bounds__(kThreads) void norm_group_bwd_kernel(const LongArgs k) {
-    __shared__ float red[kThreads / kWave];
+__global__ __launch_bounds__(kGroupThreads) void norm_group_bwd_kernel(const LongArgs k) {
+    __shared__ float red[kGroupWaves];
     const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
     const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
     const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
     float sa = 0.f, sx = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
         const int run = i / E, e = i - run * E;
         const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
         const float w = k.a.w ? k.a.w[g * k.E + e] : 1.f;
@@ -410,21 +412,28 @@ __global__ __launch_bounds__(kThreads) void norm_partial_bwd_kernel(const LongAr
     const size_t C = k.a.C, base = static_cast<size_t>(at.n) * k.a.L * C + at.c;
     const Cols<V> o = columns<V>(k, at, k.a.stats);
     float sb[V] = {}, sw[V] = {};
-    for (int r = at.r0; r < at.r1; ++r) {
-        const size_t row = base + static_cast<size_t>(r) * C;
-        float x[V], dy[V], z[V], dg[V];
-        load_vec<P, V>(static_cast<const R *>(k.a.x) + row, x);
-        load_vec<P, V>(static_cast<const R *>(k.a.dy) + row, dy);
-        if (k.a.gate) load_vec<P, V>(static_cast<const R *>(k.a.gate) + row, z);
+    for (int r = at.r0; r < at.r1; r += 2) {
+        float x[2][V], dy[2][V], z[2][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float xh = (x[i] - o.m[i]) * o.r[i];
-            const ElemGrad e = elem_grad(fmaf(xh, o.w[i], o.bias[i]), dy[i], z[i], k.a.gate != nullptr, k.a.silu);
-            dg[i] = e.dgate;
-            sb[i] += e.gv;
-            sw[i] = fmaf(e.gv, xh, sw[i]);
+        for (int j = 0; j < 2; ++j) {
+            const size_t row = base + static_cast<size_t>(min(r + j, at.r1 - 1)) * C;
+            load_vec<P, V>(static_cast<const R *>(k.a.x) + row, x[j]);
+            load_vec<P, V>(static_cast<const R *>(k.a.dy) + row, dy[j]);
+            if (k.a.gate) load_vec<P, V>(static_cast<const R *>(k.a.gate) + row, z[j]);
         }
-        if (k.a.gate) store_vec<P, V>(static_cast<R *>(k.a.dgate) + row, dg);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (r + j >= at.r1) break;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xh = (x[j][i] - o.m[i]) * o.r[i];
+                const ElemGrad e = elem_grad(fmaf(xh, o.w[i], o.bias[i]), dy[j][i], z[j][i], k.a.gate != nullptr, k.a.silu);
+                z[j][i] = e.dgate;
+                sb[i] += e.gv;
+                sw[i] = fmaf(e.gv, xh, sw[i]);
+            }
+            if (k.a.gate) store_vec<P, V>(static_cast<R *>(k.a.dgate) + base + static_cast<size_t>(r + j) * C, z[j]);
+        }
     }
     float *part = k.part + (static_cast<size_t>(at.n) * k.S + at.s) * 2 * C + at.c;
 #pragma unroll
@@ -441,19 +450,25 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(const LongArgs
     if (!at.live) return;
     const size_t C = k.a.C, base = static_cast<size_t>(at.n) * k.a.L * C + at.c;
     const Cols<V> o = columns<V>(k, at, k.a.stats), t = columns<V>(k, at, k.group);
-    for (int r = at.r0; r < at.r1; ++r) {
-        const size_t row = base + static_cast<size_t>(r) * C;
-        float x[V], dy[V], z[V];
-        load_vec<P, V>(static_cast<const R *>(k.a.x) + row, x);
-        load_vec<P, V>(static_cast<const R *>(k.a.dy) + row, dy);
-        if (k.a.gate) load_vec<P, V>(static_cast<const R *>(k.a.gate) + row, z);
+    for (int r = at.r0; r < at.r1; r += 2) {
+        float x[2][V], dy[2][V], z[2][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float xh = (x[i] - o.m[i]) * o.r[i];
-            const ElemGrad e = elem_grad(fmaf(xh, o.w[i], o.bias[i]), dy[i], z[i], k.a.gate != nullptr, k.a.silu);
-            x[i] = o.r[i] * (fmaf(e.gv, o.w[i], -t.m[i]) - xh * t.r[i]);
+        for (int j = 0; j < 2; ++j) {
+            const size_t row = base + static_cast<size_t>(min(r + j, at.r1 - 1)) * C;
+            load_vec<P, V>(static_cast<const R *>(k.a.x) + row, x[j]);
+            load_vec<P, V>(static_cast<const R *>(k.a.dy) + row, dy[j]);
+            if (k.a.gate) load_vec<P, V>(static_cast<const R *>(k.a.gate) + row, z[j]);
         }
-        store_vec<P, V>(static_cast<R *>(k.a.dx) + row, x);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xh = (x[j][i] - o.m[i]) * o.r[i];
+                const ElemGrad e = elem_grad(fmaf(xh, o.w[i], o.bias[i]), dy[j][i], z[j][i], k.a.gate != nullptr, k.a.silu);
+                x[j][i] = o.r[i] * (fmaf(e.gv, o.w[i], -t.m[i]) - xh * t.r[i]);
+            }
+            if (r + j < at.r1) store_vec<P, V>(static_cast<R *>(k.a.dx) + base + static_cast<size_t>(r + j) * C, x[j]);
+        }
     }
 }
 
@@ -548,7 +563,7 @@ void long_fwd(const LongArgs &k, hipStream_t stream) {
     const long long n = static_cast<long long>(k.a.N) * k.S * (k.a.C / V);
     const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads)), blk(kThreads);
     hipLaunchKernelGGL((norm_partial_kernel<P, V>), grid, blk, 0, stream, k);
-    hipLaunchKernelGGL(norm_group_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), blk, 0, stream, k);
+    hipLaunchKernelGGL(norm_group_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), dim3(kGroupThreads), 0, stream, k);
     hipLaunchKernelGGL((norm_apply_kernel<P, V>), grid, blk, 0, stream, k);
 }
 template <class P, int V>
@@ -556,7 +571,7 @@ void long_bwd(const LongArgs &k, hipStream_t stream) {
     const long long n = static_cast<long long>(k.a.N) * k.S * (k.a.C / V);
     const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads)), blk(kThreads);
     hipLaunchKernelGGL((norm_partial_bwd_kernel<P, V>), grid, blk, 0, stream, k);
-    hipLaunchKernelGGL(norm_group_bwd_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), blk, 0, stream, k);
+    hipLaunchKernelGGL(norm_group_bwd_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), dim3(kGroupThreads), 0, stream, k);
     hipLaunchKernelGGL((norm_apply_bwd_kernel<P, V>), grid, blk, 0, stream, k);
 }
 
@@ -568,7 +583,7 @@ bool norm_fits(int dtype, int N, int L, int C, int G) {
     if (static_cast<long long>(N) * L >= (1LL << 31) || C >= (1 << 26)) return false;
     if (r.use) return static_cast<long long>(N) * G * r.LG < lim;
     const LongPlan p = long_plan(dtype, N, L, C);
-    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(N) * G * kThreads < lim &&
+    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(N) * G * kGroupThreads < lim &&
            static_cast<long long>(p.S) * (C / G) < lim;
 }
 
@@ -590,10 +605,9 @@ hipError_t launch_norm_fwd(int dtype, const NormArgs &a, void *ws, hipStream_t s
     const RowPlan r = row_plan(dtype, a.N, a.L, a.C, a.G);
     if (r.use) {
         RowArgs k{a, a.C / a.G, r.LG, static_cast<long long>(a.N) * a.G, nullptr, 0};
-#ifndef QD_NG
-#define QD_NG 2048
-#endif
-        const int grid = row_grid(a.N, a.G, r.LG, QD_NG);
+        // eight workgroups a compute unit: 90 us at 32768 rows of 16 x 128 bf16, gated, against 95
+        // with four and 94 with sixteen
+        const int grid = row_grid(a.N, a.G, r.LG, 2048);
         if (dtype == 1) rows<Bf16>(k, r, grid, false, stream);
         else rows<F32>(k, r, grid, false, stream);
         return hipGetLastError();

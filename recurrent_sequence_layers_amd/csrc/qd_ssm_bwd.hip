@@ -15,18 +15,15 @@
 // is a channel, a wave some of its states, B and C in scalar registers, s1, s2 and y joined
 // through LDS by the wave that staged the token.
 //
-// dB and dC sum over channels, which are lanes: two values a state, lane and token.  A chain
-// of fp32 MFMAs does it without a cross-lane instruction: the 64 lanes' values are a 16 x 4
-// operand, the other operand has ones in one column j, so the product adds four lanes into
-// column j of each of 16 rows; two or four tokens fill the 16 columns, and a second product
-// with ones joins the rows.  The fp32 products are by 1 and 0, so only the sum rounds.  (0 times
-// a non-finite value is not 0: one non-finite value makes dB and dC of its two or four
-// neighbouring tokens non-finite.)  Each 64-channel block leaves its sums in the workspace and a second kernel
-// adds the blocks in order, so the result does not depend on the order of workgroups.
+// dB and dC sum over channels, which are lanes: two values a state, lane and token.  A wave
+// puts 16 values a lane into its part of LDS, reads them back across the lanes four at a
+// time, and joins the readers: about 1.8 instructions a value.  (Adding the lanes by fp32 MFMA
+// products with ones, whose 36 cycles a value came on top of the vector instructions', took
+// 266 of 897 us at 8 x 2048 tokens, 2048 channels, 16 states; exchanges in registers alone
+// take 35 instructions a set against 28.)  Each 64-channel block leaves its sums in the
+// workspace and a second kernel adds the blocks in order, so the result does not depend on the
+// order of workgroups.
 #include "qd_ssm.h"
-#ifndef QD_SG
-#define QD_SG 6
-#endif
 
 namespace qd {
 namespace {
@@ -146,16 +143,21 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel
     if (wave == 0) k.rev.s[(static_cast<size_t>(b) * k.seg.P + p) * D + ch] = sum;
 }
 
+// Eight waves a workgroup, one token of a tile each to stage and finish.
+constexpr int kBwdWaves = kTok;
 template <class P, int N>
-__global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(const RevArgs k) {
+__global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k) {
     using R = typename P::R;
-    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = kTok / NW > 0 ? kTok / NW : 1;
-    // Two buffers of the waves' sums and one barrier a tile where LDS holds them, else one and two.
-    constexpr int NB = NW <= 8 ? 2 : 1;
+    constexpr int NW = kBwdWaves, NS = N / NW;
+    constexpr int NR = states_per_wave<N>(), SUB = NS / NR;          // states of a scalar row, rows a wave
+    constexpr int RT = NS <= 4 ? kTok : kTok / 2;                    // tokens whose B and C are in scalar registers
     constexpr int VPT = 2 * NS, TPC = 16 / VPT, SETS = kTok / TPC;   // channel sums: values a token, tokens and sets of 16
+    constexpr bool kHold = NS <= 4;  // decays of a tile stay in registers; at eight states they do not fit
+    constexpr int kPitch = 20;       // floats a lane in s_v: 16-byte accesses of eight lanes meet no bank twice
     __shared__ float2 s_in[2][kTok][64];
     __shared__ float s_dy[2][kTok][64];
-    __shared__ float s_p[NB][NW][3][kTok][64];
+    __shared__ float s_p[2][NW][3][kTok][64];
+    __shared__ __attribute__((aligned(16))) float s_v[NW][64 * kPitch];
     const SsmBwdArgs &a = k.a;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int ncb = a.G * k.nblk;
@@ -185,7 +187,8 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
     const R *d_o = static_cast<const R *>(a.d_o) + row0 * D;
     const bool gated = a.z != nullptr;
     const R *z = gated ? static_cast<const R *>(a.z) + row0 * D : u;
-    const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
+    const size_t row_step = static_cast<size_t>(k.rows.Tp) * NR;
+    const size_t rows = ((static_cast<size_t>(b) * a.G + g) * (N / NR) + wave * SUB) * row_step;
     const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
     const float dt_bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.Dskip ? a.Dskip[ch] : 0.f;
     const size_t nc = (a.T + kTok - 1) / kTok;
@@ -194,58 +197,88 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
     float acc_d = 0.f, acc_b = 0.f;
 
     struct Raw {                     // as loaded: a conversion would wait for the load
-        R u[TPW], x[TPW], z[TPW], d_o[TPW];
+        R u, x, z, d_o;
         float h[NS];                 // the tile's entry state
     };
     auto fetch = [&](int tile, Raw &r) {
         tile = max(tile, 0);
-#pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-            if (NW > kTok && wave >= kTok) continue;
-            const size_t t = min(tb + tile * kTok + wave + j * NW, te - 1);
-            r.u[j] = (u + t * D)[ch];
-            r.x[j] = (dt + t * D)[ch];
-            r.d_o[j] = (d_o + t * D)[ch];
-            r.z[j] = (z + t * D)[ch];
-        }
+        const size_t t = min(tb + tile * kTok + wave, te - 1);
+        r.u = (u + t * D)[ch];
+        r.x = (dt + t * D)[ch];
+        r.d_o = (d_o + t * D)[ch];
+        r.z = (z + t * D)[ch];
 #pragma unroll
         for (int i = 0; i < NS; ++i) r.h[i] = (keep + (static_cast<size_t>(tile) * N + i) * D)[ch];
     };
     struct Kept {                    // what the end of a token needs, and the tile's entry state
-        float u[TPW], x[TPW], z[TPW], d_o[TPW], delta[TPW], dy[TPW], h[NS];
+        float u, x, z, d_o, delta, dy, h[NS];
     };
     // Tokens past the end and lanes past the channels enter with delta, u, dy and state zero: the
     // state passes through them and they add nothing to any sum.
     auto stage = [&](int tile, const Raw &r, Kept &f) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) f.h[i] = live ? r.h[i] : 0.f;
+        const bool in = live && tb + tile * kTok + wave < te;
+        f.u = P::to_f32(r.u);
+        f.z = P::to_f32(r.z);
+        f.d_o = P::to_f32(r.d_o);
+        f.x = P::to_f32(r.x) + dt_bias;
+        const float gate = siluf(f.z);
+        f.delta = a.softplus ? softplusf(f.x) : f.x;
+        f.dy = gated ? f.d_o * gate : f.d_o;
+        s_in[tile & 1][wave][lane] = in ? make_float2(f.delta, f.delta * f.u) : make_float2(0.f, 0.f);
+        s_dy[tile & 1][wave][lane] = in ? f.dy : 0.f;
+    };
+
+    // Channel sums.  A set of 16 values a lane goes to LDS as it is; a lane reads four of them
+    // from every sixteenth lane, adds those, and six exchanges join the 16 readers of a value.
+    float *mine = s_v[wave];
+    auto put = [&](const float (&v)[16]) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-            const int i = wave + j * NW;
-            if (NW > kTok && wave >= kTok) continue;
-            const bool in = live && tb + tile * kTok + i < te;
-            f.u[j] = P::to_f32(r.u[j]);
-            f.z[j] = P::to_f32(r.z[j]);
-            f.d_o[j] = P::to_f32(r.d_o[j]);
-            f.x[j] = P::to_f32(r.x[j]) + dt_bias;
-            const float gate = siluf(f.z[j]);
-            f.delta[j] = a.softplus ? softplusf(f.x[j]) : f.x[j];
-            f.dy[j] = gated ? f.d_o[j] * gate : f.d_o[j];
-            s_in[tile & 1][i][lane] = in ? make_float2(f.delta[j], f.delta[j] * f.u[j]) : make_float2(0.f, 0.f);
-            s_dy[tile & 1][i][lane] = in ? f.dy[j] : 0.f;
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4 *>(mine + lane * kPitch + 4 * j) = f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    struct Quads {
+        f32x4 q[4];
+    };
+    auto take = [&](Quads &r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.q[j] = *reinterpret_cast<const f32x4 *>(mine + ((lane >> 2) + 16 * j) * kPitch + 4 * (lane & 3));
+    };
+    // Lane l gets the sum of value 4 (l % 4) + {0, 2, 1, 3}[l / 16].
+    auto join = [&](const Quads &r) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (r.q[0][i] + r.q[1][i]) + (r.q[2][i] + r.q[3][i]);
+        auto half = [](float x, float y) {       // lanes 0-31: x over both halves; 32-63: y
+            const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+            return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+        };
+        const float lo = half(v[0], v[1]), hi = half(v[2], v[3]);
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
+        float x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+        x += dpp_src<0x124, 0xf>(x);             // row_ror:4
+        x += dpp_src<0x128, 0xf>(x);             // row_ror:8
+        return x;
+    };
+
+    ScalarRows<RT, NR> rb[SUB], rc[SUB];         // B and C of RT tokens, loaded a part of a tile ahead
+    auto load_rows = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            rb[j].load(Bw + j * row_step + static_cast<size_t>(max(t0, 0)) * NR);
+            rc[j].load(Cw + j * row_step + static_cast<size_t>(max(t0, 0)) * NR);
         }
     };
-    float one[16], row_one[SETS];    // the selecting operands
-#pragma unroll
-    for (int j = 0; j < 16; ++j) one[j] = (lane & 15) == j ? 1.f : 0.f;
-#pragma unroll
-    for (int j = 0; j < SETS; ++j) row_one[j] = ((lane & 15) >> 2) == j ? 1.f : 0.f;
-
-    ScalarRows<kTok, NS> rb, rc;     // the tile's B and C, loaded at the end of the tile before
-    auto load_rows = [&](int tile) {
-        const size_t t0 = static_cast<size_t>(tb + max(tile, 0) * kTok) * NS;
-        rb.load(Bw + t0);
-        rc.load(Cw + t0);
+    // The sums of four sets (or all of a tile's) from token t0 on: set (l / 4) % 4 in lane l.
+    auto emit = [&](int t0, float x) {
+        const int set = (lane >> 2) & 3, row = lane >> 4;
+        const int v = 4 * (lane & 3) + (row == 1 ? 2 : row == 2 ? 1 : row), t = t0 + set * TPC + v / VPT, e = v % VPT;
+        if (set < SETS && t < te) part_bc[static_cast<size_t>(t) * a.G * 2 * N + (e / NS) * N + e % NS] = x;
     };
     auto walk = [&](int tile, const float (&h_in)[NS], auto between) {
         const int t0 = tb + tile * kTok, buf = tile & 1;
@@ -257,128 +290,125 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
             dy[t] = s_dy[buf][t][lane];
         }
         float dec[kTok][NS], h[kTok][NS];
+        auto advance = [&](int t) {
 #pragma unroll
-        for (int t = 0; t < kTok; ++t)
+            for (int i = 0; i < NS; ++i) h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : h_in[i], h[t][i]);
+        };
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            if (RT < kTok && t % RT == 0) {
+#pragma unroll
+                for (int j = 0; j < SUB; ++j) rb[j].load(Bw + j * row_step + static_cast<size_t>(t0 + t) * NR);
+            }
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 dec[t][i] = __builtin_amdgcn_exp2f(in[t].x * A2[i]);
-                h[t][i] = in[t].y * rb.v[t][i];
+                h[t][i] = in[t].y * rb[i / NR].v[t % RT][i % NR];
             }
+            if (!kHold) advance(t);
+        }
         between();
         __builtin_amdgcn_sched_barrier(0);
+        if (kHold) {
 #pragma unroll
-        for (int t = 0; t < kTok; ++t)
+            for (int t = 0; t < kTok; ++t) advance(t);
+        } else {                     // the same decays again on the way back, not kept: A2 is made to look new
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[t][i] = fmaf(dec[t][i], t ? h[t - 1][i] : h_in[i], h[t][i]);
+            for (int i = 0; i < NS; ++i) asm volatile("" : "+v"(A2[i]));
+        }
+        if (RT < kTok) {             // the upper half's C comes while the states are walked
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) rc[j].load(Cw + j * row_step + static_cast<size_t>(t0 + kTok - RT) * NR);
+        }
         float dAt[NS] = {};          // this tile's part of dA: fewer roundings against the long sum
-        f32x4 set = zero4(), joined = zero4();
+        float val[16], out = 0.f;
+        Quads due;
 #pragma unroll
         for (int t = kTok - 1; t >= 0; --t) {
+            if (RT < kTok && t == RT - 1) load_rows(t0);
             float y = 0.f, s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const float gi = fmaf(rc.v[t][i], dy[t], G[i]);
-                y = fmaf(rc.v[t][i], h[t][i], y);
-                s1 = fmaf(gi, rb.v[t][i], s1);
-                G[i] = dec[t][i] * gi;
+                const float b = rb[i / NR].v[t % RT][i % NR], c = rc[i / NR].v[t % RT][i % NR];
+                const float gi = fmaf(c, dy[t], G[i]);
+                val[(t % TPC) * VPT + i] = gi * in[t].y;
+                val[(t % TPC) * VPT + NS + i] = dy[t] * h[t][i];
+                y = i ? fmaf(c, h[t][i], y) : c * h[t][0];
+                s1 = i ? fmaf(gi, b, s1) : gi * b;
+                G[i] = (kHold ? dec[t][i] : __builtin_amdgcn_exp2f(in[t].x * A2[i])) * gi;
                 const float q = G[i] * (t ? h[t - 1][i] : h_in[i]);
-                s2 = fmaf(A2[i], q, s2);
+                s2 = i ? fmaf(A2[i], q, s2) : A2[0] * q;
                 dAt[i] = fmaf(in[t].x, q, dAt[i]);
-                set = __builtin_amdgcn_mfma_f32_16x16x4f32(gi * in[t].y, one[(t % TPC) * VPT + i], set, 0, 0, 0);
-                set = __builtin_amdgcn_mfma_f32_16x16x4f32(dy[t] * h[t][i], one[(t % TPC) * VPT + NS + i], set, 0, 0, 0);
             }
-            float *sp = &s_p[NB == 2 ? buf : 0][wave][0][t][lane];
+            float *sp = &s_p[buf][wave][0][t][lane];
             sp[0] = y;
             sp[kTok * 64] = s1;
             sp[2 * kTok * 64] = s2;
-            if (t % TPC == 0) {      // the set's tokens are in: add the 16 rows
-                joined = __builtin_amdgcn_mfma_f32_16x16x4f32(row_one[t / TPC], (set[0] + set[1]) + (set[2] + set[3]), joined,
-                                                              0, 0, 0);
-                set = zero4();
+            if (t % TPC == 0) {      // a set is whole: join the one before, whose values have arrived
+                constexpr int last = SETS - 1;
+                const int set = t / TPC;
+                if (set < last) {
+                    const float x = join(due);           // by every lane
+                    out = ((lane >> 2) & 3) == ((set + 1) & 3) ? x : out;
+                }
+                if (SETS > 4 && set + 1 == 4) emit(t0 + 4 * TPC, out);
+                put(val);
+                take(due);
             }
         }
-        // Spread the channel sums: one MFMA (32 cycles of its own pipe) to the vector instructions
-        // that fill that time, instead of runs of them that the wave would wait for.
-#pragma unroll
-        for (int m = 0; m < 2 * NS * kTok; ++m) {
-            __builtin_amdgcn_sched_group_barrier(0x2, QD_SG, 0);
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load_rows(tile - 1);
+        if (RT == kTok) load_rows(t0 - kTok);
 #pragma unroll
         for (int i = 0; i < NS; ++i) dA[i] += dAt[i];
-        // lane l now holds column l % 16 of set l / 16
-        const int j = lane & 15, t = t0 + TPC * (lane >> 4) + j / VPT, e = j % VPT;
-        if ((lane >> 4) < SETS && t < te) part_bc[static_cast<size_t>(t) * a.G * 2 * N + (e / NS) * N + e % NS] = joined[0];
+        const float x = join(due);
+        emit(t0, ((lane >> 2) & 3) == 0 ? x : out);
     };
     struct Sums {
-        float v[TPW][3][NW];
+        float v[3][NW];
     };
     auto gather = [&](int tile, Sums &s) {
 #pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-            if (NW > kTok && wave >= kTok) continue;
+        for (int w = 0; w < NW; ++w)
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-#pragma unroll
-                for (int v = 0; v < 3; ++v) s.v[j][v][w] = s_p[NB == 2 ? tile & 1 : 0][w][v][wave + j * NW][lane];
-        }
+            for (int v = 0; v < 3; ++v) s.v[v][w] = s_p[tile & 1][w][v][wave][lane];
     };
     auto finish = [&](int tile, const Sums &s, const Kept &r) {
+        const int t = tb + tile * kTok + wave;
+        float y = s.v[0][0], s1 = s.v[1][0], s2 = s.v[2][0];
 #pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-            if (NW > kTok && wave >= kTok) continue;
-            const int t = tb + tile * kTok + wave + j * NW;
-            float y = 0.f, s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                y += s.v[j][0][w];
-                s1 += s.v[j][1][w];
-                s2 += s.v[j][2][w];
-            }
-            float dd = fmaf(r.u[j], s1, s2 * kLn2);
-            const float slope = sigmoidf(r.x[j]);
-            dd *= a.softplus ? slope : 1.f;
-            const bool in = t < te;
-            acc_d = in ? fmaf(r.dy[j], r.u[j], acc_d) : acc_d;
-            acc_b += in ? dd : 0.f;
-            const float du = fmaf(r.delta[j], s1, skip * r.dy[j]);
-            const float dz = r.d_o[j] * fmaf(skip, r.u[j], y) * dsiluf(r.z[j]);
-            if (live && in) {
-                const size_t at = (row0 + t) * D;
-                (static_cast<R *>(a.du) + at)[ch] = P::from_f32(du);
-                (static_cast<R *>(a.ddt) + at)[ch] = P::from_f32(dd);
-                if (gated) (static_cast<R *>(a.dz) + at)[ch] = P::from_f32(dz);
-            }
+        for (int w = 1; w < NW; ++w) {
+            y += s.v[0][w];
+            s1 += s.v[1][w];
+            s2 += s.v[2][w];
+        }
+        float dd = fmaf(r.u, s1, s2 * kLn2);
+        const float slope = sigmoidf(r.x);
+        dd *= a.softplus ? slope : 1.f;
+        const bool in = t < te;
+        acc_d = in ? fmaf(r.dy, r.u, acc_d) : acc_d;
+        acc_b += in ? dd : 0.f;
+        const float du = fmaf(r.delta, s1, skip * r.dy);
+        const float dz = r.d_o * fmaf(skip, r.u, y) * dsiluf(r.z);
+        if (live && in) {
+            const size_t at = (row0 + t) * D;
+            (static_cast<R *>(a.du) + at)[ch] = P::from_f32(du);
+            (static_cast<R *>(a.ddt) + at)[ch] = P::from_f32(dd);
+            if (gated) (static_cast<R *>(a.dz) + at)[ch] = P::from_f32(dz);
         }
     };
 
-    // As in the forward: rows two tiles ahead in two sets by name; where the sums have two
-    // buffers, a tile's end runs among the next tile's arithmetic.
+    // As in the forward: rows two tiles ahead in two sets by name, a tile's end among the next
+    // tile's arithmetic.
     Kept cur, old;
     auto step = [&](int tile, Raw &r) {
-        if constexpr (NB == 2) {
-            Sums s;
-            gather(tile + 1, s);
-            walk(tile, cur.h, [&] {
-                if (tile + 1 < ntile) finish(tile + 1, s, old);
-            });
-            old = cur;
-            if (tile > 0) stage(tile - 1, r, cur);
-            fetch(tile - 3, r);
-            __syncthreads();
-        } else {
-            walk(tile, cur.h, [] {});
-            old = cur;
-            if (tile > 0) stage(tile - 1, r, cur);
-            fetch(tile - 3, r);
-            __syncthreads();
-            Sums s;
-            gather(tile, s);
-            finish(tile, s, old);
-            __syncthreads();
-        }
+        Sums s;
+        gather(tile + 1, s);
+        walk(tile, cur.h, [&] {
+            if (tile + 1 < ntile) finish(tile + 1, s, old);
+        });
+        old = cur;
+        if (tile > 0) stage(tile - 1, r, cur);
+        fetch(tile - 3, r);
+        __syncthreads();
     };
     Raw r0, r1;
     {
@@ -386,7 +416,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
         fetch(ntile - 1, first);
         fetch(ntile - 2, r0);
         fetch(ntile - 3, r1);
-        load_rows(ntile - 1);
+        if (RT == kTok) load_rows(tb + (ntile - 1) * kTok);
         stage(ntile - 1, first, cur);
     }
     old = cur;
@@ -397,7 +427,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void ssm_bwd_kernel(
         step(tile - 1, r1);
     }
     if (tile == 0) step(0, r0);
-    if constexpr (NB == 2) {
+    {
         Sums s;
         gather(0, s);
         finish(0, s, old);
@@ -473,7 +503,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) 
 // Segments of the time axis: two waves a SIMD, as long as a segment keeps 64 tokens.
 Segments bwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * (N / states_per_wave_of(N));
+    const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * kBwdWaves;
     if (waves == 0) return cut_time(T, 1);
     const long long want = (8LL * cus + waves - 1) / waves;
     return cut_time(T, want > T / 64 ? T / 64 : want);
@@ -499,10 +529,10 @@ Sizes sizes(int B, int T, int D, int G, int N, Segments s) {
 
 template <class P, int N>
 hipError_t run_bwd(const RevArgs &k, hipStream_t stream) {
-    const dim3 blk(64 * N / states_per_wave<N>());
     const unsigned per = static_cast<unsigned>(k.a.B) * k.a.G * k.nblk;
-    if (k.seg.P > 1) hipLaunchKernelGGL((seg_grad_kernel<P, N>), dim3(per * (k.seg.P - 1)), blk, 0, stream, k);
-    hipLaunchKernelGGL((ssm_bwd_kernel<P, N>), dim3(per * k.seg.P), blk, 0, stream, k);
+    if (k.seg.P > 1)
+        hipLaunchKernelGGL((seg_grad_kernel<P, N>), dim3(per * (k.seg.P - 1)), dim3(64 * N / states_per_wave<N>()), 0, stream, k);
+    hipLaunchKernelGGL((ssm_bwd_kernel<P, N>), dim3(per * k.seg.P), dim3(64 * kBwdWaves), 0, stream, k);
     const long long n4 = static_cast<long long>(k.a.B) * k.a.T * k.a.G * 2 * N / 4;
     hipLaunchKernelGGL((bc_sum_kernel<P>), dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, stream, k);
     const int rows = k.a.B * k.seg.P;
