@@ -112,15 +112,20 @@ __device__ __forceinline__ float dsiluf(float x) {
 // The exponent's rounding, amplified by its size in a plain exp2(x log2 e), is put back as
 // a first-order factor.  Above 20 the value is x to fp32 accuracy (exp(-20) = 2e-9); a NaN
 // takes that branch too.  No branches: they would stop the tokens of a tile from overlapping.
-__device__ __forceinline__ float softplusf(float x) {
+struct Softplus {
+    float value, slope;              // slope: the derivative, sigmoid(x) = e / (1 + e)
+};
+__device__ __forceinline__ Softplus softplus_grad(float x) {
     const float xc = fmaxf(x, -126.f);
     const float p = xc * kLog2e;
     const float q = fmaf(xc, 1.925963033500e-8f, fmaf(xc, kLog2e, -p));
     const float e = __builtin_amdgcn_exp2f(p) * fmaf(q, kLn2, 1.f);
     const float r = 1.f + e;
-    const float small = fmaf(__builtin_amdgcn_logf(r), kLn2, (e - (r - 1.f)) * __builtin_amdgcn_rcpf(r));
-    return x <= 20.f ? small : x;
+    const float inv = __builtin_amdgcn_rcpf(r);
+    const float small = fmaf(__builtin_amdgcn_logf(r), kLn2, (e - (r - 1.f)) * inv);
+    return Softplus{x <= 20.f ? small : x, x > 20.f ? 1.f : e * inv};
 }
+__device__ __forceinline__ float softplusf(float x) { return softplus_grad(x).value; }
 
 // V consecutive elements as floats; V elements are 16 or 8 bytes (aligned to that) or one.
 template <class P, int V>

@@ -211,7 +211,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
         for (int i = 0; i < NS; ++i) r.h[i] = (keep + (static_cast<size_t>(tile) * N + i) * D)[ch];
     };
     struct Kept {                    // what the end of a token needs, and the tile's entry state
-        float u, x, z, d_o, delta, dy, h[NS];
+        float u, slope, dgate, delta, dy, h[NS];   // dgate: d_o silu'(z)
     };
     // Tokens past the end and lanes past the channels enter with delta, u, dy and state zero: the
     // state passes through them and they add nothing to any sum.
@@ -220,12 +220,13 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
         for (int i = 0; i < NS; ++i) f.h[i] = live ? r.h[i] : 0.f;
         const bool in = live && tb + tile * kTok + wave < te;
         f.u = P::to_f32(r.u);
-        f.z = P::to_f32(r.z);
-        f.d_o = P::to_f32(r.d_o);
-        f.x = P::to_f32(r.x) + dt_bias;
-        const float gate = siluf(f.z);
-        f.delta = a.softplus ? softplusf(f.x) : f.x;
-        f.dy = gated ? f.d_o * gate : f.d_o;
+        const float z = P::to_f32(r.z), d = P::to_f32(r.d_o), x = P::to_f32(r.x) + dt_bias;
+        const float s = sigmoidf(z);
+        const Softplus sp = softplus_grad(x);
+        f.delta = a.softplus ? sp.value : x;
+        f.slope = a.softplus ? sp.slope : 1.f;
+        f.dy = gated ? d * (z * s) : d;
+        f.dgate = d * (s * fmaf(z, 1.f - s, 1.f));
         s_in[tile & 1][wave][lane] = in ? make_float2(f.delta, f.delta * f.u) : make_float2(0.f, 0.f);
         s_dy[tile & 1][wave][lane] = in ? f.dy : 0.f;
     };
@@ -380,14 +381,12 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
             s1 += s.v[1][w];
             s2 += s.v[2][w];
         }
-        float dd = fmaf(r.u, s1, s2 * kLn2);
-        const float slope = sigmoidf(r.x);
-        dd *= a.softplus ? slope : 1.f;
+        const float dd = fmaf(r.u, s1, s2 * kLn2) * r.slope;
         const bool in = t < te;
         acc_d = in ? fmaf(r.dy, r.u, acc_d) : acc_d;
         acc_b += in ? dd : 0.f;
         const float du = fmaf(r.delta, s1, skip * r.dy);
-        const float dz = r.d_o * fmaf(skip, r.u, y) * dsiluf(r.z);
+        const float dz = r.dgate * fmaf(skip, r.u, y);
         if (live && in) {
             const size_t at = (row0 + t) * D;
             (static_cast<R *>(a.du) + at)[ch] = P::from_f32(du);
