@@ -186,12 +186,12 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
 // the 16 sums through LDS.  The row loop's sum is kept in four parts, so no addend meets a
 // sum of more than rows / 64 others.
 constexpr int kColThreads = 1024, kColLanes = 16;
+typedef float ColShared[kColLanes][64];
 template <class Store>
-__global__ __launch_bounds__(kColThreads) void column_sum_kernel(const float *__restrict__ m, int rows, long long cols,
-                                                                 Store store) {
-    __shared__ float s[kColLanes][64];
+__device__ __forceinline__ void column_sum_block(const float *__restrict__ m, int rows, long long cols, long long block,
+                                                 Store store, ColShared &s) {
     const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
-    const long long c = static_cast<long long>(blockIdx.x) * 64 + lane;
+    const long long c = block * 64 + lane;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < cols) {
         const float *p = m + c;
@@ -210,6 +210,12 @@ __global__ __launch_bounds__(kColThreads) void column_sum_kernel(const float *__
         for (int k = 0; k < kColLanes; ++k) t += s[k][lane];
         store(c, t);
     }
+}
+template <class Store>
+__global__ __launch_bounds__(kColThreads) void column_sum_kernel(const float *__restrict__ m, int rows, long long cols,
+                                                                 Store store) {
+    __shared__ ColShared s;
+    column_sum_block(m, rows, cols, blockIdx.x, store, s);
 }
 template <class Store>
 void column_sum(const float *m, int rows, long long cols, Store store, hipStream_t stream) {

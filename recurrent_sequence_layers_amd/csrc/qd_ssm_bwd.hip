@@ -456,22 +456,6 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
     }
 }
 
-// dB and dC from the channel blocks' sums, added in block order.
-template <class P>
-__global__ __launch_bounds__(256) void bc_sum_kernel(const RevArgs k) {
-    using R = typename P::R;
-    const int N = k.a.N;
-    const long long rows = static_cast<long long>(k.a.B) * k.a.T * k.a.G;
-    const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;   // four states of one row
-    if (i >= rows * 2 * N) return;
-    f32x4 s = zero4();
-    for (int blk = 0; blk < k.nblk; ++blk) s += *reinterpret_cast<const f32x4 *>(k.part_bc + static_cast<size_t>(blk) * rows * 2 * N + i);
-    const long long row = i / (2 * N);
-    const int e = static_cast<int>(i % (2 * N));
-    R *out = static_cast<R *>(e < N ? k.a.dB : k.a.dC) + row * N + (e < N ? e : e - N);
-    P::st4(out, s);
-}
-
 struct StoreA {
     float *dA;
     __device__ __forceinline__ void operator()(long long c, float v) const { dA[c] = v; }
@@ -487,6 +471,43 @@ struct StoreD {
         }
     }
 };
+
+// The sums over workgroups, in one launch: dA's columns, those of dD and ddt_bias, and dB and
+// dC from the channel blocks' sums, added in block order.
+struct SumGrid {
+    unsigned a, d, bc;               // workgroups of each
+};
+template <class P>
+__global__ __launch_bounds__(kColThreads) void ssm_sums_kernel(const RevArgs k, const SumGrid grid) {
+    using R = typename P::R;
+    __shared__ ColShared sh;
+    const int N = k.a.N, segs = k.a.B * k.seg.P;
+    const unsigned blk = blockIdx.x;
+    if (blk < grid.a) {
+        column_sum_block(k.part_a, segs, static_cast<long long>(k.a.D) * N, blk, StoreA{k.a.dA}, sh);
+        return;
+    }
+    if (blk < grid.a + grid.d) {
+        column_sum_block(k.part_d, segs, 2LL * k.a.D, blk - grid.a, StoreD{k.a.dD, k.a.ddt_bias, k.a.D}, sh);
+        return;
+    }
+    const long long rows = static_cast<long long>(k.a.B) * k.a.T * k.a.G;
+    const long long i = (static_cast<long long>(blk - grid.a - grid.d) * kColThreads + threadIdx.x) * 4;   // four states of a row
+    if (i >= rows * 2 * N) return;
+    f32x4 s = zero4();
+    int b = 0;
+    for (; b + 3 < k.nblk; b += 4) {
+        f32x4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f32x4 *>(k.part_bc + static_cast<size_t>(b + j) * rows * 2 * N + i);
+        s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; b < k.nblk; ++b) s += *reinterpret_cast<const f32x4 *>(k.part_bc + static_cast<size_t>(b) * rows * 2 * N + i);
+    const long long row = i / (2 * N);
+    const int e = static_cast<int>(i % (2 * N));
+    R *out = static_cast<R *>(e < N ? k.a.dB : k.a.dC) + row * N + (e < N ? e : e - N);
+    P::st4(out, s);
+}
 
 // With no tokens the gradients of what the tokens share are zero and dS0 is dS_T.
 __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) {
@@ -533,10 +554,11 @@ hipError_t run_bwd(const RevArgs &k, hipStream_t stream) {
         hipLaunchKernelGGL((seg_grad_kernel<P, N>), dim3(per * (k.seg.P - 1)), dim3(64 * N / states_per_wave<N>()), 0, stream, k);
     hipLaunchKernelGGL((ssm_bwd_kernel<P, N>), dim3(per * k.seg.P), dim3(64 * kBwdWaves), 0, stream, k);
     const long long n4 = static_cast<long long>(k.a.B) * k.a.T * k.a.G * 2 * N / 4;
-    hipLaunchKernelGGL((bc_sum_kernel<P>), dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, stream, k);
-    const int rows = k.a.B * k.seg.P;
-    column_sum(k.part_a, rows, static_cast<long long>(k.a.D) * N, StoreA{k.a.dA}, stream);
-    if (k.a.dD || k.a.ddt_bias) column_sum(k.part_d, rows, 2LL * k.a.D, StoreD{k.a.dD, k.a.ddt_bias, k.a.D}, stream);
+    SumGrid grid;
+    grid.a = static_cast<unsigned>((static_cast<long long>(k.a.D) * N + 63) / 64);
+    grid.d = k.a.dD || k.a.ddt_bias ? static_cast<unsigned>((2LL * k.a.D + 63) / 64) : 0;
+    grid.bc = static_cast<unsigned>((n4 + kColThreads - 1) / kColThreads);
+    hipLaunchKernelGGL((ssm_sums_kernel<P>), dim3(grid.a + grid.d + grid.bc), dim3(kColThreads), 0, stream, k, grid);
     return hipGetLastError();
 }
 template <class P>
