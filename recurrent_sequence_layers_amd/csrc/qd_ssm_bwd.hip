@@ -520,13 +520,15 @@ __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) 
     if (a.dS0 && i < a.B * DN) a.dS0[i] = a.dS_T ? a.dS_T[i] : 0.f;
 }
 
-// Segments of the time axis: two waves a SIMD, as long as a segment keeps 64 tokens.
+// Segments of the time axis: a workgroup (eight waves) for every compute unit, down to one tile
+// a segment.  3 x 203 tokens, 142 channels in two groups, 32 states: 56 us; segments of at least
+// 32 tokens 64, 64 tokens 85, 96 tokens 106.
 Segments bwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
     const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * kBwdWaves;
     if (waves == 0) return cut_time(T, 1);
     const long long want = (8LL * cus + waves - 1) / waves;
-    return cut_time(T, want > T / 64 ? T / 64 : want);
+    return cut_time(T, want);
 }
 
 struct Sizes {                       // floats of each part of the workspace, every one a multiple of four
