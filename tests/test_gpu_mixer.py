@@ -163,3 +163,126 @@ def test_captured_and_replayed(qd):
             want = work(fresh)
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), (step, k)
+
+
+def every_call(qd, seed, workspace=None):
+    """Each operator that takes a workspace, on sizes that use all of it; `workspace(bytes)` makes one."""
+    ws = workspace or (lambda n: None)
+    B, T, D, G, N = 2, 400, 72, 2, 16
+    t = {k: dev(v) for k, v in tokens(B, T, D, G, N, seed).items()}
+    p = {k: dev(v) for k, v in params(D, N, 4, seed + 1).items()}
+    f32 = torch.float32
+    o, S = qd.qdelta_ssm_fwd(t["x"], t["dt"], p["A"], t["Bm"], t["Cm"], p["D"], t["z"], p["dt_bias"],
+                             workspace=ws(qd.qdelta_ssm_fwd_workspace_bytes(B, T, D, G, N, f32)))
+    s = qd.qdelta_ssm_bwd(t["x"], t["dt"], p["A"], t["Bm"], t["Cm"], p["D"], t["z"], p["dt_bias"], None, o,
+                          workspace=ws(qd.qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, f32)))
+    c = qd.qdelta_conv_bwd(t["x"], p["w"], p["b"], None, t["z"], workspace=ws(qd.qdelta_conv_bwd_workspace_bytes(B, T, D, 4, f32)))
+    y, st = qd.qdelta_group_norm_fwd(t["x"], 4, p["nw"], p["nb"], t["z"],
+                                     workspace=ws(qd.qdelta_group_norm_fwd_workspace_bytes(B, T, D, 4, f32)))
+    n = qd.qdelta_group_norm_bwd(t["x"], 4, p["nw"], p["nb"], t["z"], st, t["dt"],
+                                 workspace=ws(qd.qdelta_group_norm_bwd_workspace_bytes(B, T, D, 4, f32)))
+    rows = t["x"].view(B * T, D)
+    _, st1 = qd.qdelta_group_norm_fwd(rows, 4, p["nw"], p["nb"])
+    r = qd.qdelta_group_norm_bwd(rows, 4, p["nw"], p["nb"], None, st1, t["dt"].view(B * T, D),
+                                 workspace=ws(qd.qdelta_group_norm_bwd_workspace_bytes(B * T, 1, D, 4, f32)))
+    return [o, S, y, st] + [v for d in (s, c, n, r) for v in d.values() if v is not None]
+
+
+def test_workspaces_are_not_read_before_they_are_written(qd):
+    """Exactly the bytes asked for, filled with NaN, and a guard behind them that stays."""
+    guards = []
+
+    def poisoned(n):
+        w = torch.full((n // 4 + 64,), float("nan"), device="cuda")
+        guards.append(w[n // 4:])
+        return w[:n // 4].view(torch.uint8)
+    want, got = every_call(qd, 31), every_call(qd, 31, poisoned)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert len(guards) == 6 and all(torch.isnan(g).all() for g in guards)
+
+
+def test_two_streams_at_once(qd):
+    """The same operators on two streams, without an order between them."""
+    want = [every_call(qd, s) for s in (41, 43)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, every_call(qd, 41 + 2 * k)))
+    torch.cuda.synchronize()
+    for k, g in got:
+        for a, b in zip(want[k], g):
+            assert torch.equal(a, b)
+
+
+def test_tensors_of_another_device_are_refused(qd):
+    x = torch.zeros(1, 4, 8, device="cuda")
+    with pytest.raises(qd.QDeltaError, match="device"):
+        qd.qdelta_conv_fwd(x, torch.zeros(8, 4))
+    with pytest.raises(qd.QDeltaError, match="device"):
+        qd.qdelta_group_norm_fwd(x, 2, torch.ones(8))
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+LONG_T, LONG_D = 1_050_000, 2048          # 2.15e9 elements a tensor
+
+
+def wide(seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+
+def test_convolution_past_32_bit_offsets(qd):
+    """Rows whose element offsets pass 2^31: the last rows against a call on those rows alone."""
+    x, w, b = wide(1, 1, LONG_T, LONG_D), dev(randn(gen(2), LONG_D, 4)), dev(randn(gen(3), LONG_D))
+    y, S = qd.qdelta_conv_fwd(x, w, b)
+    tail = x[:, -50:].contiguous()
+    alone, S1 = qd.qdelta_conv_fwd(tail, w, b)
+    assert torch.equal(y[:, -47:], alone[:, 3:]) and torch.equal(S, S1)
+    got = qd.qdelta_conv_bwd(x, w, b, None, y)
+    want = qd.qdelta_conv_bwd(tail, w, b, None, y[:, -50:].contiguous())
+    assert torch.equal(got["dx"][:, -47:], want["dx"][:, 3:])
+
+
+def test_norm_past_32_bit_offsets(qd):
+    x, w = wide(4, LONG_T, LONG_D), dev(randn(gen(5), LONG_D))
+    y, st = qd.qdelta_group_norm_fwd(x, 16, w, gate=x)
+    tail = x[-50:].contiguous()
+    alone, st1 = qd.qdelta_group_norm_fwd(tail, 16, w, gate=tail)
+    assert torch.equal(y[-50:], alone) and torch.equal(st[-50:], st1)
+    got = qd.qdelta_group_norm_bwd(x, 16, w, None, x, st, y)
+    want = qd.qdelta_group_norm_bwd(tail, 16, w, None, tail, st1, alone)
+    assert torch.equal(got["dx"][-50:], want["dx"]) and torch.equal(got["dgate"][-50:], want["dgate"])
+
+
+def test_scan_past_32_bit_offsets(qd):
+    """The last tokens against a call on them alone from the state before them.  The long call
+    cuts its time axis elsewhere, so states differ by fp32 roundings: their errors decay with
+    the states, and the outputs may differ by one rounding to bf16, 2^-8 of the value, and by
+    2^-14 (2^10 roundings of 2^-24) of the largest."""
+    T, D, N, tail = LONG_T, LONG_D, 16, 64
+    p = {k: dev(v) for k, v in params(D, N, 4, 7).items()}
+    u, Bm, Cm = wide(8, 1, T, D), wide(9, 1, T, 1, N), wide(10, 1, T, 1, N)
+    dt, d_o = wide(11, 1, T, D), wide(12, 1, T, D)
+    o, S = qd.qdelta_ssm_fwd(u, dt, p["A"], Bm, Cm, p["D"], None, p["dt_bias"])
+    cut = lambda t, a, b: t[:, a:b]  # noqa: E731  (contiguous: one sequence)
+    _, S1 = qd.qdelta_ssm_fwd(*[cut(t, 0, T - tail) if t.dim() > 2 else t for t in (u, dt, p["A"], Bm, Cm)], p["D"], None,
+                              p["dt_bias"])
+    last = [cut(t, T - tail, T) if t.dim() > 2 else t for t in (u, dt, p["A"], Bm, Cm)]
+    o1, S2 = qd.qdelta_ssm_fwd(*last, p["D"], None, p["dt_bias"], S1)
+
+    def near(a, b, name):
+        a, b = a.double(), b.double()
+        worst = ((a - b).abs() / (2.0 ** -8 * b.abs() + 2.0 ** -14 * b.abs().max())).max()
+        print(f"  {name}: {worst:.3f} of the bound", flush=True)
+        assert worst <= 1, name
+    near(o[:, -tail:], o1, "o")
+    near(S, S2, "S_T")
+    got = qd.qdelta_ssm_bwd(u, dt, p["A"], Bm, Cm, p["D"], None, p["dt_bias"], None, d_o, S)
+    want = qd.qdelta_ssm_bwd(*last, p["D"], None, p["dt_bias"], S1, d_o[:, -tail:], S)
+    for k in ("du", "ddt", "dB", "dC"):
+        near(got[k][:, -tail:], want[k], k)
