@@ -149,7 +149,8 @@ __device__ __forceinline__ void load_vec(const typename P::R *p, float (&v)[V]) 
         }
     }
 }
-template <class P, int V>
+// AROUND: past the caches, for an output that would push out what is still to be read.
+template <class P, int V, bool AROUND = false>
 __device__ __forceinline__ void store_vec(typename P::R *p, const float (&v)[V]) {
     if constexpr (V == 1) {
         p[0] = P::from_f32(v[0]);
@@ -163,8 +164,12 @@ __device__ __forceinline__ void store_vec(typename P::R *p, const float (&v)[V])
             else
                 q[i] = __float_as_uint(v[i]);
         }
-        if constexpr (W == 4) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(q);
-        else *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(q);
+        typedef __attribute__((ext_vector_type(W))) uint32_t vec;
+        vec w;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = q[i];
+        if constexpr (AROUND) __builtin_nontemporal_store(w, reinterpret_cast<vec *>(p));
+        else *reinterpret_cast<vec *>(p) = w;
     }
 }
 

@@ -345,7 +345,8 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
 
 // One token for each of B sequences, the state updated in place: bound by reading and
 // writing the fp32 state.  N / 4 lanes share a channel, four states (16 bytes) each, so a
-// wave reads 1 KB in a row; kStepReps channels a lane are in flight.
+// wave reads 1 KB in a row; kStepReps channels a lane are in flight.  256 sequences, 2048
+// channels, 16 states: 14.5 us, 4.9 TB/s (one channel a lane 15.2 us, four 16.7).
 constexpr int kStepThreads = 256, kStepReps = 2;
 template <class P, int N>
 __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(const SsmArgs a) {

@@ -69,6 +69,19 @@ def test_gradients_of_many_rows(qd):
         within(v, want[k], scale[k], 2 * units(1, 64) + 9000, k)
 
 
+def test_large_outputs_go_around_the_caches(qd):
+    """From 64 MiB a tensor on, the second pass stores past the caches."""
+    x, w, b, z, dy = make("f32", 1, 4400, 8, 500, True, False, 21)
+    assert x.numel() * 4 >= 64 << 20
+    y, stats = qd.qdelta_group_norm_fwd(dev(x), 8, dev(w), dev(b), silu=True)
+    want, _, scale = mixer.norm_fwd(x, 8, w, b, None, True)
+    within(y, want, scale, units(4400, 500), "y")
+    got = qd.qdelta_group_norm_bwd(dev(x), 8, dev(w), dev(b), None, stats, dev(dy), silu=True)
+    want, scale = mixer.norm_bwd(x, 8, w, b, None, stats, dy, True)
+    for k in ("dx", "dweight", "dbias"):
+        within(got[k], want[k], scale[k], 2 * units(4400, 500) + (4400 if k != "dx" else 0), k)
+
+
 @pytest.mark.parametrize("L", [1, 40])
 def test_a_mean_far_above_the_spread(qd, L):
     """x = 1000 + N(0, 1) in fp32: the square sum is of centred values, so 1/std keeps the
