@@ -15,7 +15,16 @@
 //     of a tile of kTile tokens once, each wave a part of the tokens, double-buffered in LDS;
 //   - the waves' partial sums over their states meet in LDS, and the wave that staged a
 //     token adds them up, applies D and the gate from the u and z it kept, and stores.
-// One barrier a tile.  States and sums are fp32.
+// One barrier a tile.  States and sums are fp32.  A wave in its recurrence goes before one that
+// stages or waits (s_setprio): with two workgroups a compute unit 5 % (16 x 2048 tokens, 4096
+// channels, 16 states 538 -> 522 us).
+//
+// 8 x 4096 tokens, 2048 channels, 16 states, bf16, gated: 360 us, 7 operations a token, channel
+// and state at 24 TFLOP/s; one exponential and four multiply-adds alone would take 145 us at
+// the rate that four waves a SIMD reach (21.2 cycles for 64 lanes), the 537 MB 105 us.  What is
+// between: softplus, the gate and the sums over waves (a third of the vector instructions),
+// and with one workgroup a compute unit two waves a SIMD do not cover each other's waits (at
+// two workgroups the same work takes 261 us).
 //
 // Few channels (B D / 64 workgroups below the card's size): the time axis is cut into P
 // segments.  A first launch walks all but the last from zero for their local end states and
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
             for (int t = 0; t < GT; ++t) asm volatile("" ::"v"(in[t].x), "v"(in[t].y), "s"(cb_.v[t][0]));
             __builtin_amdgcn_sched_barrier(0);
             load_group(t0 + GT);
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
             // The exponentials and inputs of the group first: independent, so their latency is hidden.
             float e[GT][NS], x[GT][NS];
 #pragma unroll
@@ -239,7 +248,6 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
                     x[t][i] = in[t].y * cb_.v[t][i];
                 }
             between();
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
                 float y = 0.f;
@@ -302,6 +310,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
             });
 #pragma unroll
             for (int j = GT; j < kTile; j += GT) group(i, j, nothing);
+            __builtin_amdgcn_s_setprio(0);
             old = cur;
             cur = stage(i + 1, r);
             fetch(i + 3, r);
