@@ -407,9 +407,9 @@ __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(const SsmArgs a)
 // Segments of the time axis: where a call leaves a compute unit fewer than six waves, enough
 // for sixteen, as long as a segment keeps at least 64 tokens (2 x 512 tokens, 1024 channels, 16
 // states: 23 us; at least 128 tokens 30, 32 tokens 23, and 4 x 100 tokens then 23 against 21
-// us).  With 2048 channels and 16 states: 16384 tokens of one sequence 274 us (eight waves 343, twenty-four 280), 4 x 4096
-// tokens 272 us against 383 uncut; at 8 x 4096, eight waves a unit, the cut costs more than it
-// gives (442 against 387 us).
+// us).  With 2048 channels and 16 states, all of one build: 16384 tokens of one sequence 274 us
+// (eight waves 343, twenty-four 280), 4 x 4096 tokens 272 us against 383 uncut; at 8 x 4096,
+// eight waves a unit, the cut costs more than it gives (442 against 387 us).
 Segments fwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
     const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * (N / states_per_wave_of(N));

@@ -26,9 +26,10 @@
 // walk that keeps states 155 and the sums over workgroups 25.  Its bytes would take 95 us; two
 // exponentials and sixteen multiply-adds a token, channel and state 225 us at the rate four
 // waves a SIMD reach.  LDS (148 KB) holds one workgroup a compute unit, so two waves a SIMD; of
-// the 490 us the channel sums are 107 and the ends of tokens 71.  Each 64-channel block leaves its sums in the
-// workspace and a second kernel adds the blocks in order, so the result does not depend on the
-// order of workgroups.
+// the 490 us the channel sums are 107 and the ends of tokens 71.
+//
+// Each 64-channel block leaves its sums in the workspace and a second kernel adds the blocks in
+// order, so the result does not depend on the order of workgroups.
 #include "qd_ssm.h"
 
 namespace qd {
