@@ -446,7 +446,8 @@ def _enter(stream, device):
     current, and no context at all where they are already."""
     import torch
     if stream is None and device.index == torch.cuda.current_device():
-        return _NO_CONTEXT, torch.cuda.current_stream(device).cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the handle without a Stream object around it
+        return _NO_CONTEXT, raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
     s = _launch_stream(stream, device)
     return torch.cuda.stream(s), s.cuda_stream
 
@@ -454,6 +455,11 @@ def _enter(stream, device):
 def _result(t, shape, dtype, device):
     import torch
     return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+
+
+def _result_like(t, like):
+    import torch
+    return torch.empty_like(like) if t is None else t
 
 
 def _results(out, specs, device):
@@ -474,6 +480,7 @@ def _workspace(workspace, need, device):
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
+    _check(workspace, "workspace")
     _check_all(device, [(workspace, "workspace", workspace.dtype, None)])
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -497,7 +504,7 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
     with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
-        y = _result(y, (B, T, D), dt, dev)
+        y = _result_like(y, x)
         if want_state:
             S_T = _result(S_T, (B, W - 1, D), dt, dev)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
@@ -520,7 +527,7 @@ def qdelta_conv_step(x, w, bias, S, silu: bool = True, y=None, stream=None):
     with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
-        y = _result(y, (N, D), dt, dev)
+        y = _result_like(y, x)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)), (S, "S", dt, (N, W - 1, D)),
                          (y, "y", dt, (N, D))])
         rc = lib.qdelta_conv_step(_at(x), _at(w), _at(bias), _at(S), _at(y), N, D, W, int(silu), code, handle)
@@ -589,7 +596,7 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
     context, handle = _enter(stream, u.device)
     with context:
         dev, f32, code = u.device, torch.float32, _dtype_code(u.dtype)
-        o = _result(o, (B, T, ch), u.dtype, dev)
+        o = _result_like(o, u)
         if want_state:
             S_T = _result(S_T, (B, ch, N), f32, dev)
         _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
@@ -610,7 +617,7 @@ def qdelta_ssm_step(u, dt, A, Bm, Cm, D, z, dt_bias, S, softplus: bool = True, o
     context, handle = _enter(stream, u.device)
     with context:
         dev, code = u.device, _dtype_code(u.dtype)
-        o = _result(o, (n_seq, ch), u.dtype, dev)
+        o = _result_like(o, u)
         _check_all(dev, checks + [(S, "S", torch.float32, (n_seq, ch, N)), (o, "o", u.dtype, (n_seq, ch))])
         rc = lib.qdelta_ssm_step(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S),
                                  _at(o), n_seq, ch, G, N, int(softplus), code, handle)
@@ -683,7 +690,7 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
     context, handle = _enter(stream, x.device)
     with context:
         dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
-        y = _result(y, x.shape, dt, dev)
+        y = _result_like(y, x)
         if want_stats:
             stats = _result(stats, (N, groups, 2), f32, dev)
         _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),

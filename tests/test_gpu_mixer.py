@@ -286,3 +286,13 @@ def test_scan_past_32_bit_offsets(qd):
     want = qd.qdelta_ssm_bwd(*last, p["D"], None, p["dt_bias"], S1, d_o[:, -tail:], S)
     for k in ("du", "ddt", "dB", "dC"):
         near(got[k][:, -tail:], want[k], k)
+
+
+def test_workspaces_that_are_not_device_tensors_are_refused(qd):
+    x = torch.randn(2, 6, 16, device="cuda")
+    for bad in (torch.empty(1 << 20, dtype=torch.uint8), np.zeros(1 << 20, np.uint8), 1 << 20,
+                torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(qd.QDeltaError, match="workspace"):
+            qd.qdelta_conv_bwd(x, torch.randn(16, 4, device="cuda"), None, None, x.clone(), workspace=bad)
+        with pytest.raises(qd.QDeltaError, match="workspace"):
+            qd.qdelta_group_norm_fwd(x, 2, workspace=bad)
