@@ -30,7 +30,7 @@ extern "C" {
 int qdelta_conv_fwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens, void *y, void *S_T,
                     int B, int T, int D, int W, int silu, int dtype, void *stream) {
     if (B < 0 || T < 0 || D < 0) return QD_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(dtype, B, T, D))) return QD_ERR_UNSUPPORTED;
+    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(B, T, D))) return QD_ERR_UNSUPPORTED;
     if (B == 0 || D == 0) return QD_OK;
     if (!w || (T > 0 && (!x || !y))) return QD_ERR_INVALID_ARG;
     if (!all_aligned({x, y, S0, S_T})) return QD_ERR_INVALID_ARG;
@@ -44,7 +44,7 @@ int qdelta_conv_fwd(const void *x, const float *w, const float *bias, const void
 int qdelta_conv_step(const void *x, const float *w, const float *bias, void *S, void *y, int N, int D, int W, int silu,
                      int dtype, void *stream) {
     if (N < 0 || D < 0) return QD_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(dtype, N, 1, D))) return QD_ERR_UNSUPPORTED;
+    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(N, 1, D))) return QD_ERR_UNSUPPORTED;
     if (N == 0 || D == 0) return QD_OK;
     if (!x || !w || !S || !y) return QD_ERR_INVALID_ARG;
     if (!all_aligned({x, y, S})) return QD_ERR_INVALID_ARG;
@@ -55,15 +55,15 @@ int qdelta_conv_step(const void *x, const float *w, const float *bias, void *S, 
 }
 
 size_t qdelta_conv_bwd_workspace_bytes(int B, int T, int D, int W, int dtype) {
-    if (B <= 0 || T <= 0 || D <= 0 || W < 2 || W > 4 || !dtype_ok(dtype) || !qd::conv_fits(dtype, B, T, D)) return 0;
-    return qd::conv_bwd_workspace(dtype, B, T, D, W);
+    if (B <= 0 || T <= 0 || D <= 0 || W < 2 || W > 4 || !dtype_ok(dtype) || !qd::conv_fits(B, T, D)) return 0;
+    return qd::conv_bwd_workspace(B, T, D, W);
 }
 
 int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const void *dy, const void *dS_T,
                     void *dx, float *dw, float *dbias, void *dS0, int B, int T, int D, int W, int silu, int dtype,
                     void *workspace, size_t ws_bytes, void *stream) {
     if (B < 0 || T < 0 || D < 0) return QD_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(dtype, B, T, D))) return QD_ERR_UNSUPPORTED;
+    if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(B, T, D))) return QD_ERR_UNSUPPORTED;
     if (D == 0) return QD_OK;
     if (!w || !dw || (prod(B, T) > 0 && (!x || !dy || !dx))) return QD_ERR_INVALID_ARG;
     const size_t need = qdelta_conv_bwd_workspace_bytes(B, T, D, W, dtype);
@@ -80,7 +80,7 @@ int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void
 
 size_t qdelta_ssm_fwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype) {
     if (!ssm_sizes(B, T, D, G, N) || !qd::ssm_supported(dtype, N) || !qd::ssm_fits(B, T, D, G, N)) return 0;
-    return prod(B, D) == 0 ? 0 : qd::ssm_fwd_workspace(dtype, B, T, D, G, N);
+    return prod(B, D) == 0 ? 0 : qd::ssm_fwd_workspace(B, T, D, G, N);
 }
 
 int qdelta_ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm, const float *Dskip,
@@ -122,7 +122,7 @@ int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *B
 
 size_t qdelta_ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype) {
     if (!ssm_sizes(B, T, D, G, N) || !qd::ssm_supported(dtype, N) || !qd::ssm_fits(B, T, D, G, N)) return 0;
-    return qd::ssm_bwd_workspace(dtype, B, T, D, G, N);
+    return qd::ssm_bwd_workspace(B, T, D, G, N);
 }
 
 int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm, const float *Dskip,

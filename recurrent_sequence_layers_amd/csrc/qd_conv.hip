@@ -219,7 +219,8 @@ template <class P>
 __global__ __launch_bounds__(kThreads) void conv_bwd_empty_kernel(const ConvBwdArgs a) {
     using R = typename P::R;
     const size_t n = static_cast<size_t>(a.B) * (a.W - 1) * a.D, i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i < n && a.dS0) static_cast<R *>(a.dS0)[i] = a.dS_T ? static_cast<const R *>(a.dS_T)[i] : P::from_f32(0.f);
+    for (size_t j = i; j < n && a.dS0; j += static_cast<size_t>(gridDim.x) * kThreads)
+        static_cast<R *>(a.dS0)[j] = a.dS_T ? static_cast<const R *>(a.dS_T)[j] : P::from_f32(0.f);
     if (i < static_cast<size_t>(a.D) * a.W) a.dw[i] = 0.f;
     if (i < static_cast<size_t>(a.D) && a.dbias) a.dbias[i] = 0.f;
 }
@@ -265,7 +266,7 @@ struct BwdPlan {
 // TL tokens a thread: long runs read fewer rows twice (the W - 1 rows on either side of a
 // run) and leave fewer partial sums, short ones fill the card.  At the size above 32 tokens take
 // 108 us, 64 take 98 and 128 take 98.
-BwdPlan bwd_plan(int dtype, int B, int T, int D) {
+BwdPlan bwd_plan(int B, int T, int D) {
     const int nvec = D / vec_of(D);
     BwdPlan p;
     p.NX = 8;
@@ -280,7 +281,7 @@ BwdPlan bwd_plan(int dtype, int B, int T, int D) {
 
 // Tokens a thread walks in the forward: long runs read fewer rows twice, short ones fill the
 // card.  At the size above 16 tokens take 73 us, 32 take 65 and 64 take 65.
-int fwd_run(int dtype, int B, int T, int D) {
+int fwd_run(int B, int T, int D) {
     int TL = 32;
     while (TL > 4 && static_cast<long long>(B) * ((T + TL - 1) / TL) * (D / vec_of(D)) < 262144) TL /= 2;
     return TL;
@@ -288,37 +289,38 @@ int fwd_run(int dtype, int B, int T, int D) {
 
 }  // namespace
 
-bool conv_fits(int dtype, int B, int T, int D) {
+// The backward's runs are at least eight tokens, and its workgroups up to 32 runs of up to 64
+// channel vectors.
+bool conv_fits(int B, int T, int D) {
     const long long rows = static_cast<long long>(B) * T, nvec = D / vec_of(D);
     const long long runs = static_cast<long long>(B) * max(1, (T + 7) / 8);
-    return rows < (1LL << 31) && D < (1 << 25) && runs * ((nvec + 63) / 64 * 64) < (1LL << 32);
+    return rows < (1LL << 31) && D < (1 << 25) && (runs + 31) * ((nvec + 63) / 64 * 64) < (1LL << 32);
 }
 
 hipError_t launch_conv_fwd(int dtype, const ConvArgs &args, hipStream_t stream) {
     ConvArgs a = args;
     const int V = vec_of(a.D);
-    a.TL = fwd_run(dtype, a.B, a.T, a.D);
+    a.TL = fwd_run(a.B, a.T, a.D);
     if (dtype == 1) return V == kVec ? fwd_w<Bf16, kVec>(a, stream) : fwd_w<Bf16, 1>(a, stream);
     return V == kVec ? fwd_w<F32, kVec>(a, stream) : fwd_w<F32, 1>(a, stream);
 }
 
 hipError_t launch_conv_step(int dtype, const ConvArgs &a, hipStream_t stream) { return launch_conv_fwd(dtype, a, stream); }
 
-size_t conv_bwd_workspace(int dtype, int B, int T, int D, int W) {
+size_t conv_bwd_workspace(int B, int T, int D, int W) {
     if (static_cast<long long>(B) * T * D == 0) return 0;
-    return static_cast<size_t>(bwd_plan(dtype, B, T, D).R) * (W + 1) * D * sizeof(float);
+    return static_cast<size_t>(bwd_plan(B, T, D).R) * (W + 1) * D * sizeof(float);
 }
 
 hipError_t launch_conv_bwd(int dtype, const ConvBwdArgs &args, hipStream_t stream) {
     ConvBwdArgs a = args;
     if (static_cast<long long>(a.B) * a.T == 0) {
-        const size_t n = max(static_cast<size_t>(a.B) * (a.W - 1) * a.D, static_cast<size_t>(a.D) * a.W);
-        const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads)), blk(kThreads);
+        const dim3 grid(static_cast<unsigned>((static_cast<size_t>(a.D) * a.W + kThreads - 1) / kThreads)), blk(kThreads);
         if (dtype == 1) hipLaunchKernelGGL((conv_bwd_empty_kernel<Bf16>), grid, blk, 0, stream, a);
         else hipLaunchKernelGGL((conv_bwd_empty_kernel<F32>), grid, blk, 0, stream, a);
         return hipGetLastError();
     }
-    const BwdPlan p = bwd_plan(dtype, a.B, a.T, a.D);
+    const BwdPlan p = bwd_plan(a.B, a.T, a.D);
     a.TL = p.TL; a.NX = p.NX; a.R = p.R;
     const int V = vec_of(a.D);
     if (dtype == 1) return V == kVec ? bwd_w<Bf16, kVec>(a, stream) : bwd_w<Bf16, 1>(a, stream);

@@ -34,10 +34,10 @@ struct ConvBwdArgs {
     int TL, NX, R;                  // tokens per thread, channel vectors per block (power of two), partial rows
 };
 // *_fits: the sizes stay within the kernels' 32-bit launch and row counts.
-bool conv_fits(int dtype, int B, int T, int D);
+bool conv_fits(int B, int T, int D);
 hipError_t launch_conv_fwd(int dtype, const ConvArgs &a, hipStream_t stream);
 hipError_t launch_conv_step(int dtype, const ConvArgs &a, hipStream_t stream);   // T = 1, S0 == S_T in place
-size_t conv_bwd_workspace(int dtype, int B, int T, int D, int W);
+size_t conv_bwd_workspace(int B, int T, int D, int W);
 hipError_t launch_conv_bwd(int dtype, const ConvBwdArgs &a, hipStream_t stream);
 
 // ---------------------------------------------------------------- selective scan
@@ -66,10 +66,10 @@ struct SsmBwdArgs {
 };
 bool ssm_supported(int dtype, int N);
 bool ssm_fits(int B, int T, int D, int G, int N);
-size_t ssm_fwd_workspace(int dtype, int B, int T, int D, int G, int N);
+size_t ssm_fwd_workspace(int B, int T, int D, int G, int N);
 hipError_t launch_ssm_fwd(int dtype, const SsmArgs &a, void *ws, hipStream_t stream);
 hipError_t launch_ssm_step(int dtype, const SsmArgs &a, hipStream_t stream);      // T = 1, S0 == S_T in place
-size_t ssm_bwd_workspace(int dtype, int B, int T, int D, int G, int N);
+size_t ssm_bwd_workspace(int B, int T, int D, int G, int N);
 hipError_t launch_ssm_bwd(int dtype, const SsmBwdArgs &a, void *ws, hipStream_t stream);
 
 // ---------------------------------------------------------------- group norm
@@ -91,7 +91,7 @@ size_t norm_fwd_workspace(int dtype, int N, int L, int C, int G);
 hipError_t launch_norm_fwd(int dtype, const NormArgs &a, void *ws, hipStream_t stream);
 size_t norm_bwd_workspace(int dtype, int N, int L, int C, int G);
 hipError_t launch_norm_bwd(int dtype, const NormArgs &a, void *ws, hipStream_t stream);
-hipError_t launch_norm_zero(float *dw, float *dbias, int C, hipStream_t stream);
+hipError_t launch_norm_zero(float *dw, float *dbias, int C, hipStream_t stream);   // both may be null
 
 // ---------------------------------------------------------------- device helpers
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;

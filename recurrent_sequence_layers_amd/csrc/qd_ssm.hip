@@ -504,8 +504,7 @@ void launch_ssm_rows(int dtype, const SsmArgs &a, RowBuf rows, hipStream_t strea
     }
 }
 
-size_t ssm_fwd_workspace(int dtype, int B, int T, int D, int G, int N) {
-    (void)dtype;
+size_t ssm_fwd_workspace(int B, int T, int D, int G, int N) {
     if (T == 0) return 0;
     const Segments s = fwd_segments(B, T, D, G, N);
     const size_t seg = s.P > 1 ? static_cast<size_t>(B) * s.P * D * (N + 1) : 0;

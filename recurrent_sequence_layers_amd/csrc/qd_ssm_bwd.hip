@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) 
         if (a.dD) a.dD[i] = 0.f;
         if (a.ddt_bias) a.ddt_bias[i] = 0.f;
     }
-    if (a.dS0 && i < a.B * DN) a.dS0[i] = a.dS_T ? a.dS_T[i] : 0.f;
+    for (size_t j = i; a.dS0 && j < a.B * DN; j += static_cast<size_t>(gridDim.x) * 256) a.dS0[j] = a.dS_T ? a.dS_T[j] : 0.f;
 }
 
 // Segments of the time axis: a workgroup (eight waves) for every compute unit, down to one tile
@@ -581,15 +581,14 @@ hipError_t run_bwd_n(const RevArgs &k, hipStream_t stream) {
 
 }  // namespace
 
-size_t ssm_bwd_workspace(int dtype, int B, int T, int D, int G, int N) {
-    (void)dtype;
+size_t ssm_bwd_workspace(int B, int T, int D, int G, int N) {
     if (static_cast<long long>(B) * T * D == 0) return 0;
     return sizes(B, T, D, G, N, bwd_segments(B, T, D, G, N)).total() * sizeof(float);
 }
 
 hipError_t launch_ssm_bwd(int dtype, const SsmBwdArgs &a, void *ws, hipStream_t stream) {
     if (static_cast<long long>(a.B) * a.T == 0) {
-        const size_t n = static_cast<size_t>(a.B > 0 ? a.B : 1) * a.D * a.N;
+        const size_t n = static_cast<size_t>(a.D) * a.N;
         hipLaunchKernelGGL(ssm_bwd_empty_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a);
         return hipGetLastError();
     }

@@ -296,3 +296,18 @@ def test_workspaces_that_are_not_device_tensors_are_refused(qd):
             qd.qdelta_conv_bwd(x, torch.randn(16, 4, device="cuda"), None, None, x.clone(), workspace=bad)
         with pytest.raises(qd.QDeltaError, match="workspace"):
             qd.qdelta_group_norm_fwd(x, 2, workspace=bad)
+
+
+def test_states_of_no_tokens_past_32_bit_offsets(qd):
+    """With no tokens the state's gradient is a copy: more elements than a launch has threads."""
+    B, D, W = 5_600_000, 256, 4
+    dS = torch.empty(B, W - 1, D, device="cuda", dtype=torch.bfloat16).normal_()
+    x = torch.empty(B, 0, D, device="cuda", dtype=torch.bfloat16)
+    got = qd.qdelta_conv_bwd(x, torch.ones(D, W, device="cuda"), None, None, x, dS)
+    assert torch.equal(got["dS0"], dS) and not got["dw"].any()
+    del dS, got
+    B, D, N = (1 << 22) + 3, 64, 16
+    dS = torch.empty(B, D, N, device="cuda").normal_()
+    u, Bm = torch.empty(B, 0, D, device="cuda"), torch.empty(B, 0, 1, N, device="cuda")
+    got = qd.qdelta_ssm_bwd(u, u, -torch.ones(D, N, device="cuda"), Bm, Bm, None, None, None, None, u, dS)
+    assert torch.equal(got["dS0"], dS) and not got["dA"].any()

@@ -132,3 +132,14 @@ def test_binding_refuses_host_tensors():
         qd.qdelta_ssm_fwd(x, x, torch.zeros(8, 16), torch.zeros(1, 2, 1, 16), torch.zeros(1, 2, 1, 16))
     with pytest.raises(qd.QDeltaError, match="device tensor"):
         qd.qdelta_group_norm_fwd(x, 2)
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    """One more run of a backward's workgroups, or a group count no power of two divides, and
+    the launch has 2^32 threads."""
+    big = (1 << 26) - 1
+    assert conv_bwd(lib, B=big, T=1, D=256) == UNSUPPORTED and conv(lib, B=big, T=1, D=256) == UNSUPPORTED
+    assert lib.qdelta_conv_bwd_workspace_bytes(big, 1, 256, 4, 1) == 0
+    odd = (1 << 25) - 1
+    assert norm(lib, N=1, C=odd, G=odd) == UNSUPPORTED and norm_bwd(lib, N=1, C=odd, G=odd) == UNSUPPORTED
+    assert lib.qdelta_group_norm_bwd_workspace_bytes(1, 1, odd, odd, 1) == 0
