@@ -683,7 +683,8 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
     silu applies SiLU to the normed value; gate, like x, multiplies it by silu(gate).  The
     output norm of a layer's o [B,T,H,d] per token and head is
     ``qdelta_group_norm_fwd(o.view(B * T, H * d), H, ...)``.  Returns (y, stats), stats
-    [N,groups,2] the mean and 1/std the backward needs (None when want_stats is False)."""
+    [N,groups,2] the mean and 1/std the backward needs (None when want_stats is False; zeros for
+    groups without elements)."""
     import torch
     lib = load_library()
     N, L, C = _norm_sizes(x, groups)
@@ -695,6 +696,8 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
             stats = _result(stats, (N, groups, 2), f32, dev)
         _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
                          (gate, "gate", dt, x.shape), (y, "y", dt, x.shape), (stats, "stats", f32, (N, groups, 2))])
+        if want_stats and not L * C:
+            stats.zero_()                              # no elements: no kernel writes them
         p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_fwd_workspace_bytes(N, L, C, groups, code), dev)
         rc = lib.qdelta_group_norm_fwd(_at(x), _at(weight), _at(bias), _at(gate), _at(y), _at(stats), N, L, C, groups,
                                        float(eps), int(silu), code, p, n, handle)

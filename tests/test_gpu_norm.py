@@ -139,3 +139,14 @@ def test_refusals(qd):
         qd.qdelta_group_norm_bwd(x, 2, w, None, None, None, x.clone())
     with pytest.raises(qd.QDeltaError, match="workspace"):
         qd.qdelta_group_norm_fwd(x, 2, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("shape", [(3, 0, 8), (3, 5, 0)])
+def test_groups_without_elements_have_zero_statistics(qd, shape):
+    stats = torch.full((3, 2, 2), 7.0, device="cuda")
+    x = torch.zeros(shape, device="cuda")
+    y, st = qd.qdelta_group_norm_fwd(x, 2, stats=stats)
+    assert y.shape == shape and st is stats and not st.any()
+    w = torch.ones(shape[-1], device="cuda")
+    got = qd.qdelta_group_norm_bwd(x, 2, w, w, None, st, x)
+    assert got["dx"].shape == shape and not got["dweight"].any() and not got["dbias"].any()
