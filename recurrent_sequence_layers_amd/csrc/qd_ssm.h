@@ -28,6 +28,20 @@ struct RowBuf {
 };
 inline int padded_rows(int T) { return (T + kTile - 1) / kTile * kTile + kTile; }
 
+// The decay exponent's factor A log2 e.  A decay without bound (A = -inf, or one that the
+// product makes so) becomes the largest finite one: a token past the end has delta = 0 and has
+// to leave the state as it is, where 0 times infinity would be NaN.
+__device__ __forceinline__ float decay_rate(float A) {
+    const float r = A * kLog2e;
+    return r < -3.4028234e38f ? -3.4028234e38f : r;
+}
+// A state through a segment.  Nothing carried stays nothing also where a growing state's factor
+// (A > 0) overflows.
+__device__ __forceinline__ float carry(float rate, float sum_delta, float h, float local) {
+    const float through = fmaf(__builtin_amdgcn_exp2f(rate * sum_delta), h, local);
+    return h == 0.f ? local : through;
+}
+
 typedef const __attribute__((address_space(4))) float scalar_f32;
 // COUNT tokens' values from row p on.
 template <int COUNT, int NS>

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
     float A2[NS], h[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[static_cast<size_t>(ch) * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[static_cast<size_t>(ch) * N + n0 + i]);
         h[i] = 0.f;
     }
     float *seg_h = k.buf.h + (static_cast<size_t>(b) * k.seg.P * N + n0) * D + ch;   // slot q at q N D
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
             const float *hq = seg_h + static_cast<size_t>(q + 1) * N * D;
             const float sum = seg_s[static_cast<size_t>(q) * D];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), h[i], hq[i * D]);
+            for (int i = 0; i < NS; ++i) h[i] = carry(A2[i], sum, h[i], hq[i * D]);
         }
     }
     if (MODE == kSeg) {              // the local effect starts from zero
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(const SsmArgs a)
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hp[i] = fmaf(__builtin_amdgcn_exp2f(delta * (Ap[i] * kLog2e)), hp[i], du * P::to_f32(Bm[i]));
+            hp[i] = fmaf(__builtin_amdgcn_exp2f(delta * decay_rate(Ap[i])), hp[i], du * P::to_f32(Bm[i]));
             y = fmaf(P::to_f32(Cm[i]), hp[i], y);
         }
         y = group_sum(y, LPC);

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel
     const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTile - 1) / kTile;
     float A2[NS], G[NS] = {}, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A2[i] = a.A[static_cast<size_t>(ch) * N + n0 + i] * kLog2e;
+    for (int i = 0; i < NS; ++i) A2[i] = decay_rate(a.A[static_cast<size_t>(ch) * N + n0 + i]);
     const R *dt = static_cast<const R *>(a.dt) + row0 * D;
     const R *d_o = static_cast<const R *>(a.d_o) + row0 * D;
     const bool gated = a.z != nullptr;
@@ -180,14 +180,14 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
     float A2[NS], G[NS], dA[NS] = {};
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[static_cast<size_t>(ch) * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[static_cast<size_t>(ch) * N + n0 + i]);
         G[i] = a.dS_T && live ? a.dS_T[st + i] : 0.f;
     }
     for (int q = k.seg.P - 1; q > p; --q) {
         const float *gq = k.rev.h + ((static_cast<size_t>(b) * k.seg.P + q) * N + n0) * D + ch;
         const float sum = k.rev.s[(static_cast<size_t>(b) * k.seg.P + q) * D + ch];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) G[i] = live ? fmaf(__builtin_amdgcn_exp2f(A2[i] * sum), G[i], gq[i * D]) : 0.f;
+        for (int i = 0; i < NS; ++i) G[i] = live ? carry(A2[i], sum, G[i], gq[i * D]) : 0.f;
     }
     const R *u = static_cast<const R *>(a.u) + row0 * D;
     const R *dt = static_cast<const R *>(a.dt) + row0 * D;

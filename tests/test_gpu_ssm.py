@@ -177,3 +177,45 @@ def test_refusals(qd):
     with pytest.raises(qd.QDeltaError):
         qd.qdelta_ssm_step(x["u"][:, 0].contiguous(), x["dt"][:, 0].contiguous(), x["A"], x["Bm"][:, 0].contiguous(),
                            x["Cm"][:, 0].contiguous(), None, None, None, x["S0"].bfloat16())
+
+
+@pytest.mark.parametrize("T", [21, 600])
+@pytest.mark.parametrize("N", [16, 64])
+def test_decays_without_bound(qd, N, T):
+    """A = -inf forgets at once, as -1e30 does to the last bit: tokens past the end, which leave
+    the state as it is, must not turn it into NaN.  T = 600 is cut into segments."""
+    x = ssm_inputs(3, T, 34, 2, N, "f32", 5)
+    lens = dev(torch.tensor([T, T // 2 + 1, 3], dtype=torch.int32))
+    x["A"][::3, 1::2] = -1e30
+    near = [dev(x[k]) for k in FWD]
+    x["A"][::3, 1::2] = float("-inf")
+    none = [dev(x[k]) for k in FWD]
+    zeros = torch.zeros(3, T, 34, device="cuda")
+    for kw in (dict(), dict(lens=lens)):
+        got, want = qd.qdelta_ssm_fwd(*none, **kw, o=zeros.clone()), qd.qdelta_ssm_fwd(*near, **kw, o=zeros.clone())
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[1].isfinite().all()
+    got, want = (qd.qdelta_ssm_bwd(*a, dev(x["d_o"]), dev(x["dS_T"])) for a in (none, near))
+    for k in got:
+        assert torch.equal(got[k], want[k]) and got[k].isfinite().all(), k
+    tok = [t[:, 0].contiguous() if t.dim() > 2 and t.shape[1] == T else t for t in none[:-1]]
+    got, want = none[-1].clone(), none[-1].clone()
+    o = qd.qdelta_ssm_step(*tok, got)
+    tok[2] = near[2]
+    assert torch.equal(o, qd.qdelta_ssm_step(*tok, want)) and torch.equal(got, want) and got.isfinite().all()
+
+
+def test_nothing_carried_through_a_growing_segment(qd):
+    """A > 0: a segment's factor overflows where nothing is there to grow."""
+    x = ssm_inputs(2, 600, 36, 2, 16, "f32", 6, state=False, plus=False, extras=False)
+    x["A"], x["dt"] = torch.full_like(x["A"], 2.0), torch.ones_like(x["dt"])
+    x["u"][:, :-5] = 0
+    x["d_o"][:, 5:] = 0
+    o, S = run_fwd(qd, x, False)
+    want, S_T, so, sS = mixer.ssm_fwd(*[x[k] for k in FWD], plus=False)
+    within(o, want, so, ssm_u(x, False), "o")
+    within(S, S_T, sS, ssm_u(x, False), "S_T")
+    got = qd.qdelta_ssm_bwd(*[dev(x[k]) for k in FWD], dev(x["d_o"]), softplus=False)
+    want, scale = mixer.ssm_bwd(*[x[k] for k in FWD], x["d_o"], None, False)
+    for k, v in got.items():
+        if v is not None:
+            within(v, want[k], scale[k], 2 * ssm_u(x, False), k)
