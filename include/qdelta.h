@@ -308,17 +308,17 @@ int qdelta_conv_step(const void *x, const float *w, const float *bias, void *S, 
                      int W, int silu, int dtype, void *stream);
 
 /*
- * Gradients of sum(y dy) + sum(S_T dS_T) for the qdelta_conv_fwd of the same inputs (without
- * lens: the convolution is causal, so padding only needs dy = 0 there).
+ * Gradients of sum(y dy) + sum(S_T dS_T) for the qdelta_conv_fwd of the same inputs.  With
+ * lens, padding is not read (dy's rows neither) and the gradients of its rows are zero.
  *   dy [B][T][D], dS_T [B][W-1][D] or NULL (zero), elements
  *   dx [B][T][D] and dS0 [B][W-1][D] or NULL (not written), elements; dw [D][W], and dbias [D]
  *   or NULL (not written), fp32, summed over tokens and sequences.
  * workspace: at least qdelta_conv_bwd_workspace_bytes, 16-byte aligned, overwritten.
  */
 size_t qdelta_conv_bwd_workspace_bytes(int B, int T, int D, int W, int dtype);
-int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const void *dy,
-                    const void *dS_T, void *dx, float *dw, float *dbias, void *dS0, int B, int T, int D,
-                    int W, int silu, int dtype, void *workspace, size_t ws_bytes, void *stream);
+int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens,
+                    const void *dy, const void *dS_T, void *dx, float *dw, float *dbias, void *dS0, int B,
+                    int T, int D, int W, int silu, int dtype, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * Selective state space scan.  Per sequence b, channel d of group g = d / (D / G), state n:
@@ -350,8 +350,8 @@ int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *B
                     int D, int G, int N, int softplus, int dtype, void *stream);
 
 /*
- * Gradients of sum(o d_o) + sum(S_T dS_T) for the qdelta_ssm_fwd of the same inputs (without
- * lens: padding only needs d_o = 0 there).
+ * Gradients of sum(o d_o) + sum(S_T dS_T) for the qdelta_ssm_fwd of the same inputs.  With
+ * lens, padding is not read (d_o's rows neither) and the gradients of its rows are zero.
  *   d_o [B][T][D] elements, dS_T [B][D][N] fp32 or NULL (zero)
  *   du, ddt [B][T][D], dB, dC [B][T][G][N] (summed over the group's channels), elements;
  *   dz [B][T][D] elements, required with z and NULL without;
@@ -362,9 +362,10 @@ int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *B
 size_t qdelta_ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, int dtype);
 int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
                    const float *Dskip, const void *z, const float *dt_bias, const float *S0,
-                   const void *d_o, const float *dS_T, void *du, void *ddt, float *dA, void *dB, void *dC,
-                   float *dDskip, void *dz, float *ddt_bias, float *dS0, int B, int T, int D, int G, int N,
-                   int softplus, int dtype, void *workspace, size_t ws_bytes, void *stream);
+                   const int *lens, const void *d_o, const float *dS_T, void *du, void *ddt, float *dA,
+                   void *dB, void *dC, float *dDskip, void *dz, float *ddt_bias, float *dS0, int B, int T,
+                   int D, int G, int N, int softplus, int dtype, void *workspace, size_t ws_bytes,
+                   void *stream);
 
 /*
  * Group norm, channels last, with an optional SiLU and an optional gate.  The statistics of

@@ -225,3 +225,26 @@ def norm_bwd(x, groups, weight, bias, gate, stats, dy, act=False):
             out["dx"][i, :, at] = rstd * (gw - gw.mean() - hat * (gw * hat).mean())
             mag["dx"][i, :, at] = rstd * (sgw + sgw.mean() + shat * (sgw * shat).mean())
     return out, mag
+
+
+def each_sequence(fn, lens, shared, per, *args):
+    """fn's (gradients, scales) for a right-padded batch: one sequence at a time without its
+    padding, whose rows are zero.  shared: names of the gradients summed over sequences; per:
+    indices of the arguments that have a row a sequence and token, or (negative, -1 - index) a
+    row a sequence."""
+    T = f64(args[per[0]]).shape[1]
+    tokens, rows = {p for p in per if p >= 0}, {-1 - p for p in per if p < 0}
+    whole = None
+    for b, n in enumerate(lens):
+        n = int(min(max(int(n), 0), T))
+        part = [a if a is None else f64(a)[b:b + 1, :n] if i in tokens else f64(a)[b:b + 1] if i in rows else a
+                for i, a in enumerate(args)]
+        got = fn(*part)
+        if whole is None:
+            whole = tuple({k: [] for k in d} for d in got)
+        for w, d in zip(whole, got):
+            for k, v in d.items():
+                if k not in shared and k != "dS0":
+                    v = np.concatenate([v, np.zeros((1, T - n) + v.shape[2:])], 1)
+                w[k].append(v)
+    return tuple({k: sum(v) if k in shared else np.concatenate(v) for k, v in w.items()} for w in whole)

@@ -85,12 +85,12 @@ def load_library():
             ("conv_fwd", i, [vp] * 7 + [i] * 6 + [vp]),
             ("conv_step", i, [vp] * 5 + [i] * 5 + [vp]),
             ("conv_bwd_workspace_bytes", sz, [i] * 5),
-            ("conv_bwd", i, [vp] * 10 + [i] * 6 + [vp, sz, vp]),
+            ("conv_bwd", i, [vp] * 11 + [i] * 6 + [vp, sz, vp]),
             ("ssm_fwd_workspace_bytes", sz, [i] * 6),
             ("ssm_fwd", i, [vp] * 12 + [i] * 7 + [vp, sz, vp]),
             ("ssm_step", i, [vp] * 10 + [i] * 6 + [vp]),
             ("ssm_bwd_workspace_bytes", sz, [i] * 6),
-            ("ssm_bwd", i, [vp] * 20 + [i] * 7 + [vp, sz, vp]),
+            ("ssm_bwd", i, [vp] * 21 + [i] * 7 + [vp, sz, vp]),
             ("group_norm_fwd_workspace_bytes", sz, [i] * 5),
             ("group_norm_fwd", i, [vp] * 6 + [i] * 4 + [f] + [i] * 2 + [vp, sz, vp]),
             ("group_norm_bwd_workspace_bytes", sz, [i] * 5),
@@ -539,10 +539,10 @@ def qdelta_conv_bwd_workspace_bytes(B, T, D, W, dtype) -> int:
     return int(load_library().qdelta_conv_bwd_workspace_bytes(B, T, D, W, _dtype_code(dtype)))
 
 
-def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: bool = True, out=None, workspace=None,
-                    stream=None):
-    """Gradients of sum(y * dy) + sum(S_T * dS_T) for qdelta_conv_fwd on the same inputs.
-    Returns a dict with dx, dw, dbias (None without bias) and dS0 (None unless want_dS0; also
+def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: bool = True, lens=None, out=None,
+                    workspace=None, stream=None):
+    """Gradients of sum(y * dy) + sum(S_T * dS_T) for qdelta_conv_fwd on the same inputs.  With
+    lens, rows past a sequence's end are not read, dy's neither, and their dx is zero.  Returns a dict with dx, dw, dbias (None without bias) and dS0 (None unless want_dS0; also
     given when S0 is None).  ``out`` may supply any of them; ``workspace`` a device buffer of
     at least qdelta_conv_bwd_workspace_bytes(...) bytes (allocated when None)."""
     import torch
@@ -554,13 +554,14 @@ def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: 
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
-                         (S0, "S0", dt, (B, W - 1, D)), (dy, "dy", dt, (B, T, D)), (dS_T, "dS_T", dt, (B, W - 1, D))])
+                         (S0, "S0", dt, (B, W - 1, D)), (lens, "lens", torch.int32, (B,)), (dy, "dy", dt, (B, T, D)),
+                         (dS_T, "dS_T", dt, (B, W - 1, D))])
         out = _results(out, dict(dx=(True, (B, T, D), dt), dw=(True, (D, W), f32), dbias=(bias is not None, (D,), f32),
                                  dS0=(want_dS0, (B, W - 1, D), dt)), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_conv_bwd_workspace_bytes(B, T, D, W, code), dev)
-        rc = lib.qdelta_conv_bwd(_at(x), _at(w), _at(bias), _at(S0), _at(dy), _at(dS_T), _at(out["dx"]),
-                                 _at(out["dw"]), _at(out["dbias"]), _at(out["dS0"]), B, T, D, W, int(silu), code, p, n,
-                                 handle)
+        rc = lib.qdelta_conv_bwd(_at(x), _at(w), _at(bias), _at(S0), _at(lens), _at(dy), _at(dS_T),
+                                 _at(out["dx"]), _at(out["dw"]), _at(out["dbias"]), _at(out["dS0"]), B, T, D, W,
+                                 int(silu), code, p, n, handle)
         _raise(rc, "qdelta_conv_bwd")
         return out
 
@@ -630,8 +631,9 @@ def qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
 
 
 def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus: bool = True, want_dS0: bool = True,
-                   out=None, workspace=None, stream=None):
-    """Gradients of sum(o * d_o) + sum(S_T * dS_T) for qdelta_ssm_fwd on the same inputs.
+                   lens=None, out=None, workspace=None, stream=None):
+    """Gradients of sum(o * d_o) + sum(S_T * dS_T) for qdelta_ssm_fwd on the same inputs.  With
+    lens, rows past a sequence's end are not read, d_o's neither, and their gradients are zero.
     Returns a dict with du, ddt, dB, dC (like their inputs), dA, and, None where the input is
     None, dD, dz, ddt_bias, and dS0 (None unless want_dS0; also given when S0 is None).
     ``out`` may supply any of them; ``workspace`` a device buffer of at least
@@ -642,16 +644,17 @@ def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus
     context, handle = _enter(stream, u.device)
     with context:
         dev, f32, e, code = u.device, torch.float32, u.dtype, _dtype_code(u.dtype)
-        _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (d_o, "d_o", e, (B, T, ch)), (dS_T, "dS_T", f32, (B, ch, N))])
+        _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
+                                  (d_o, "d_o", e, (B, T, ch)), (dS_T, "dS_T", f32, (B, ch, N))])
         tok, bc = (B, T, ch), (B, T, G, N)
         out = _results(out, dict(du=(True, tok, e), ddt=(True, tok, e), dA=(True, (ch, N), f32), dB=(True, bc, e),
                                  dC=(True, bc, e), dD=(D is not None, (ch,), f32), dz=(z is not None, tok, e),
                                  ddt_bias=(dt_bias is not None, (ch,), f32), dS0=(want_dS0, (B, ch, N), f32)), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_bwd_workspace_bytes(B, T, ch, G, N, code), dev)
         rc = lib.qdelta_ssm_bwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
-                                _at(d_o), _at(dS_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA"]), _at(out["dB"]),
-                                _at(out["dC"]), _at(out["dD"]), _at(out["dz"]), _at(out["ddt_bias"]), _at(out["dS0"]),
-                                B, T, ch, G, N, int(softplus), code, p, n, handle)
+                                _at(lens), _at(d_o), _at(dS_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA"]),
+                                _at(out["dB"]), _at(out["dC"]), _at(out["dD"]), _at(out["dz"]), _at(out["ddt_bias"]),
+                                _at(out["dS0"]), B, T, ch, G, N, int(softplus), code, p, n, handle)
         _raise(rc, "qdelta_ssm_bwd")
         return out
 

@@ -59,9 +59,9 @@ size_t qdelta_conv_bwd_workspace_bytes(int B, int T, int D, int W, int dtype) {
     return qd::conv_bwd_workspace(B, T, D, W);
 }
 
-int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const void *dy, const void *dS_T,
-                    void *dx, float *dw, float *dbias, void *dS0, int B, int T, int D, int W, int silu, int dtype,
-                    void *workspace, size_t ws_bytes, void *stream) {
+int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens, const void *dy,
+                    const void *dS_T, void *dx, float *dw, float *dbias, void *dS0, int B, int T, int D, int W, int silu,
+                    int dtype, void *workspace, size_t ws_bytes, void *stream) {
     if (B < 0 || T < 0 || D < 0) return QD_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || W < 2 || W > 4 || (D > 0 && !qd::conv_fits(B, T, D))) return QD_ERR_UNSUPPORTED;
     if (D == 0) return QD_OK;
@@ -70,10 +70,10 @@ int qdelta_conv_bwd(const void *x, const float *w, const float *bias, const void
     if (ws_bytes < need || (need > 0 && (!workspace || !aligned16(workspace)))) return QD_ERR_WORKSPACE;
     if (!all_aligned({x, S0, dy, dS_T, dx, dS0})) return QD_ERR_INVALID_ARG;
     const size_t n = prod(B, T, D, elem(dtype)), st = prod(B, W - 1, D, elem(dtype));
-    if (!disjoint({{x, n}, {w, prod(D, W, 4)}, {bias, prod(D, 4)}, {S0, st}, {dy, n}, {dS_T, st}},
+    if (!disjoint({{x, n}, {w, prod(D, W, 4)}, {bias, prod(D, 4)}, {S0, st}, {lens, prod(B, 4)}, {dy, n}, {dS_T, st}},
                   {{dx, n}, {dw, prod(D, W, 4)}, {dbias, prod(D, 4)}, {dS0, st}, {need ? workspace : nullptr, need}}))
         return QD_ERR_INVALID_ARG;
-    return status(qd::launch_conv_bwd(dtype, qd::ConvBwdArgs{x, w, bias, S0, dy, dS_T, dx, dS0, dw, dbias,
+    return status(qd::launch_conv_bwd(dtype, qd::ConvBwdArgs{x, w, bias, S0, lens, dy, dS_T, dx, dS0, dw, dbias,
                                                              static_cast<float *>(workspace), B, T, D, W, silu != 0, 0, 0, 0},
                                       static_cast<hipStream_t>(stream)));
 }
@@ -126,9 +126,10 @@ size_t qdelta_ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, int dty
 }
 
 int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm, const float *Dskip,
-                   const void *z, const float *dt_bias, const float *S0, const void *d_o, const float *dS_T, void *du,
-                   void *ddt, float *dA, void *dB, void *dC, float *dDskip, void *dz, float *ddt_bias, float *dS0, int B,
-                   int T, int D, int G, int N, int softplus, int dtype, void *workspace, size_t ws_bytes, void *stream) {
+                   const void *z, const float *dt_bias, const float *S0, const int *lens, const void *d_o, const float *dS_T,
+                   void *du, void *ddt, float *dA, void *dB, void *dC, float *dDskip, void *dz, float *ddt_bias, float *dS0,
+                   int B, int T, int D, int G, int N, int softplus, int dtype, void *workspace, size_t ws_bytes,
+                   void *stream) {
     if (!ssm_sizes(B, T, D, G, N)) return QD_ERR_INVALID_ARG;
     if (!qd::ssm_supported(dtype, N) || !qd::ssm_fits(B, T, D, G, N)) return QD_ERR_UNSUPPORTED;
     if (D == 0) return QD_OK;
@@ -140,12 +141,13 @@ int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm
     if (!all_aligned({u, dt, A, Bm, Cm, z, S0, d_o, dS_T, du, ddt, dA, dB, dC, dz, dS0})) return QD_ERR_INVALID_ARG;
     const size_t n = prod(B, T, D, elem(dtype)), bc = prod(prod(B, T, G), N, elem(dtype)), st = prod(B, D, N, 4);
     const size_t an = prod(D, N, 4), dn = prod(D, 4);
-    if (!disjoint({{u, n}, {dt, n}, {A, an}, {Bm, bc}, {Cm, bc}, {Dskip, dn}, {z, n}, {dt_bias, dn}, {S0, st}, {d_o, n}, {dS_T, st}},
+    if (!disjoint({{u, n}, {dt, n}, {A, an}, {Bm, bc}, {Cm, bc}, {Dskip, dn}, {z, n}, {dt_bias, dn}, {S0, st}, {lens, prod(B, 4)},
+                   {d_o, n}, {dS_T, st}},
                   {{du, n}, {ddt, n}, {dA, an}, {dB, bc}, {dC, bc}, {dDskip, dn}, {dz, n}, {ddt_bias, dn}, {dS0, st},
                    {need ? workspace : nullptr, need}}))
         return QD_ERR_INVALID_ARG;
-    return status(qd::launch_ssm_bwd(dtype, qd::SsmBwdArgs{u, dt, Bm, Cm, A, Dskip, dt_bias, z, S0, d_o, dS_T, du, ddt, dB, dC,
-                                                           dz, dA, dDskip, ddt_bias, dS0, B, T, D, G, N, softplus != 0},
+    return status(qd::launch_ssm_bwd(dtype, qd::SsmBwdArgs{u, dt, Bm, Cm, A, Dskip, dt_bias, z, S0, lens, d_o, dS_T, du, ddt, dB,
+                                                           dC, dz, dA, dDskip, ddt_bias, dS0, B, T, D, G, N, softplus != 0},
                                      workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -104,7 +104,9 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(const ConvArgs a) {
 
 // A block covers NX channel vectors times 256 / NX runs of TL tokens; its threads' sums for
 // dw and dbias are joined in LDS in a fixed order and written as one row of partial results.
-template <class P, int V, int W>
+// LENS: sequences end at their lengths.  A length is a register more in every lane, which at four
+// taps takes a wave of four from each SIMD: 116 against 95 us.
+template <class P, int V, int W, bool LENS>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a) {
     using R = typename P::R;
     __shared__ float red[kThreads][V];
@@ -125,24 +127,29 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a)
         const R *dst = a.dS_T ? static_cast<const R *>(a.dS_T) + static_cast<size_t>(b) * (W - 1) * D + c : nullptr;
         R *dx = static_cast<R *>(a.dx) + static_cast<size_t>(b) * a.T * D + c;
         R *ds0 = a.dS0 ? static_cast<R *>(a.dS0) + static_cast<size_t>(b) * (W - 1) * D + c : nullptr;
-        float w[W][V], bias[V], win[W][V], dp[W][V] = {};
+        float w[W][V], bias[V], win[W][V] = {}, dp[W][V] = {};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             bias[i] = a.bias ? a.bias[c + i] : 0.f;
 #pragma unroll
             for (int j = 0; j < W; ++j) w[j][i] = a.w[static_cast<size_t>(c + i) * W + j];
         }
-        const int t0 = tile * a.TL, t1 = min(t0 + a.TL, a.T);
+        const int len = LENS ? min(max(a.lens[b], 0), a.T) : a.T;
+        const int t0 = tile * a.TL, t1 = max(min(t0 + a.TL, len), t0);
+        if (t0 < len) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) row_or_state<P, V>(x, s0, t0 - (W - 1) + k, W, D, win[k]);
+            for (int k = 0; k < W - 1; ++k) row_or_state<P, V>(x, s0, t0 - (W - 1) + k, W, D, win[k]);
+        }
         // At step t the window holds x[t-W+1 .. t] and dp the gradients dpre[t-W+1 .. t]; the
         // finished row is t - (W - 1): rows t0 .. t1-1 need t up to t1 + W - 2.  The first run
-        // also finishes the rows before the sequence, which are the state's.
-        for (int tb = t0; tb < t1 + W - 1; tb += kAheadBwd) {
+        // also finishes the rows before the sequence, which are the state's, also of one that
+        // has no tokens: then the rows loaded are not used.
+        const int end = t0 < t1 || tile == 0 ? t1 + W - 1 : t0;
+        for (int tb = t0; tb < end; tb += kAheadBwd) {
             float in[kAheadBwd][V], gy[kAheadBwd][V];
 #pragma unroll
             for (int k = 0; k < kAheadBwd; ++k) {
-                const int tc = min(tb + k, a.T - 1);
+                const int tc = max(min(tb + k, len - 1), 0);
                 load_vec<P, V>(x + static_cast<size_t>(tc) * D, in[k]);
                 load_vec<P, V>(dy + static_cast<size_t>(tc) * D, gy[k]);
             }
@@ -150,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a)
 #pragma unroll
             for (int k = 0; k < kAheadBwd; ++k) {
                 const int t = tb + k, tr = t - (W - 1);
-                const bool in_seq = t < a.T, mine = t < t1;
+                const bool in_seq = t < len, mine = t < t1;
                 float out[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -177,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a)
                 }
                 const bool row = tr >= t0 && tr < t1, state = tile == 0 && tr < 0 && ds0;
                 if (row || state) {
-                    const int ts = tr - (a.T - (W - 1));        // the row's place in the final state
+                    const int ts = tr - (len - (W - 1));        // the row's place in the final state
                     if (dst && ts >= 0) {
                         float e[V];
                         load_vec<P, V>(dst + static_cast<size_t>(ts) * D, e);
@@ -195,6 +202,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a)
                 for (int j = 0; j < W; ++j) dw[j][i] += cw[j][i];
             }
         }
+        const float none[V] = {};
+        for (int t = t1; LENS && t < min(t0 + a.TL, a.T); ++t) store_vec<P, V>(dx + static_cast<size_t>(t) * D, none);   // padding
     }
     float *part = a.part + static_cast<size_t>(by) * (W + 1) * D;
 #pragma unroll
@@ -249,13 +258,18 @@ hipError_t fwd_w(const ConvArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <class P, int V, int W>
+void bwd_l(const ConvBwdArgs &a, dim3 grid, dim3 blk, hipStream_t stream) {
+    if (a.lens) hipLaunchKernelGGL((conv_bwd_kernel<P, V, W, true>), grid, blk, 0, stream, a);
+    else hipLaunchKernelGGL((conv_bwd_kernel<P, V, W, false>), grid, blk, 0, stream, a);
+}
 template <class P, int V>
 hipError_t bwd_w(const ConvBwdArgs &a, hipStream_t stream) {
     const int nvec = a.D / V;
     const dim3 grid(static_cast<unsigned>((nvec + a.NX - 1) / a.NX) * a.R), blk(kThreads);
-    if (a.W == 2) hipLaunchKernelGGL((conv_bwd_kernel<P, V, 2>), grid, blk, 0, stream, a);
-    else if (a.W == 3) hipLaunchKernelGGL((conv_bwd_kernel<P, V, 3>), grid, blk, 0, stream, a);
-    else hipLaunchKernelGGL((conv_bwd_kernel<P, V, 4>), grid, blk, 0, stream, a);
+    if (a.W == 2) bwd_l<P, V, 2>(a, grid, blk, stream);
+    else if (a.W == 3) bwd_l<P, V, 3>(a, grid, blk, stream);
+    else bwd_l<P, V, 4>(a, grid, blk, stream);
     column_sum(a.part, a.R, static_cast<long long>(a.W + 1) * a.D, ConvStore{a.dw, a.dbias, a.D, a.W}, stream);
     return hipGetLastError();
 }

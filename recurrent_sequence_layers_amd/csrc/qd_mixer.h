@@ -25,7 +25,9 @@ struct ConvArgs {
 struct ConvBwdArgs {
     const void *x;
     const float *w, *bias;
-    const void *S0, *dy, *dS_T;
+    const void *S0;
+    const int *lens;                // [B] or null
+    const void *dy, *dS_T;
     void *dx, *dS0;                 // dS0 null: not written
     float *dw, *dbias;              // dbias null: not written
     float *part;                    // workspace [R][W + 1][D]
@@ -57,6 +59,7 @@ struct SsmBwdArgs {
     const float *A, *Dskip, *dt_bias;
     const void *z;
     const float *S0;
+    const int *lens;                // [B] or null
     const void *d_o;
     const float *dS_T;              // [B][D][N] or null
     void *du, *ddt, *dB, *dC, *dz;  // dz null when z is null

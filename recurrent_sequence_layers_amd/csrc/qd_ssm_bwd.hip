@@ -61,7 +61,8 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void seg_grad_kernel
     const uint32_t ch = g * k.Dg + min(c_in, k.Dg - 1);
     const int n0 = wave * NS;
     const size_t D = a.D, row0 = static_cast<size_t>(b) * a.T;
-    const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTile - 1) / kTile;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const int tb = p * k.seg.len, te = max(min(len, tb + k.seg.len), tb), ntile = (te - tb + kTile - 1) / kTile;
     float A2[NS], G[NS] = {}, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] = decay_rate(a.A[static_cast<size_t>(ch) * N + n0 + i]);
@@ -174,7 +175,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
     const uint32_t ch = g * k.Dg + min(c_in, k.Dg - 1);
     const int n0 = wave * NS;
     const size_t D = a.D, row0 = static_cast<size_t>(b) * a.T;
-    const int tb = p * k.seg.len, te = min(a.T, tb + k.seg.len), ntile = (te - tb + kTok - 1) / kTok;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const int tb = p * k.seg.len, te = max(min(len, tb + k.seg.len), tb), ntile = (te - tb + kTok - 1) / kTok;
     const size_t st = (static_cast<size_t>(b) * D + ch) * N + n0;
 
     float A2[NS], G[NS], dA[NS] = {};
@@ -194,6 +196,14 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
     const R *d_o = static_cast<const R *>(a.d_o) + row0 * D;
     const bool gated = a.z != nullptr;
     const R *z = gated ? static_cast<const R *>(a.z) + row0 * D : u;
+    // The gradients of padding, before the walk: behind it, where its registers live on, 690
+    // instead of 679 us at the size above.
+    for (int t = te + wave; live && t < min(a.T, tb + k.seg.len); t += NW) {     // padding
+        const size_t at = (row0 + t) * D;
+        (static_cast<R *>(a.du) + at)[ch] = P::from_f32(0.f);
+        (static_cast<R *>(a.ddt) + at)[ch] = P::from_f32(0.f);
+        if (gated) (static_cast<R *>(a.dz) + at)[ch] = P::from_f32(0.f);
+    }
     const size_t row_step = static_cast<size_t>(k.rows.Tp) * NR;
     const size_t rows = ((static_cast<size_t>(b) * a.G + g) * (N / NR) + wave * SUB) * row_step;
     const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
@@ -418,24 +428,24 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
         fetch(tile - 3, r);
         __syncthreads();
     };
-    Raw r0, r1;
-    {
-        Raw first;
-        fetch(ntile - 1, first);
-        fetch(ntile - 2, r0);
-        fetch(ntile - 3, r1);
-        if (RT == kTok) load_rows(tb + (ntile - 1) * kTok);
-        stage(ntile - 1, first, cur);
-    }
-    old = cur;
-    __syncthreads();
-    int tile = ntile - 1;
-    for (; tile > 0; tile -= 2) {
-        step(tile, r0);
-        step(tile - 1, r1);
-    }
-    if (tile == 0) step(0, r0);
-    {
+    if (ntile > 0) {                 // none: the segment lies past the sequence's end
+        Raw r0, r1;
+        {
+            Raw first;
+            fetch(ntile - 1, first);
+            fetch(ntile - 2, r0);
+            fetch(ntile - 3, r1);
+            if (RT == kTok) load_rows(tb + (ntile - 1) * kTok);
+            stage(ntile - 1, first, cur);
+        }
+        old = cur;
+        __syncthreads();
+        int tile = ntile - 1;
+        for (; tile > 0; tile -= 2) {
+            step(tile, r0);
+            step(tile - 1, r1);
+        }
+        if (tile == 0) step(0, r0);
         Sums s;
         gather(0, s);
         finish(0, s, old);
@@ -504,7 +514,12 @@ __global__ __launch_bounds__(kColThreads) void ssm_sums_kernel(const RevArgs k, 
     const long long i = (static_cast<long long>(blk - grid.a - grid.d) * kColThreads + threadIdx.x) * 4;   // four states of a row
     if (i >= rows * 2 * N) return;
     f32x4 s = zero4();
+    const long long row = i / (2 * N);
     int b = 0;
+    if (k.a.lens) {                  // rows of padding were not written: nothing to add
+        const long long token = row / k.a.G;
+        if (token % k.a.T >= k.a.lens[token / k.a.T]) b = k.nblk;
+    }
     for (; b + 3 < k.nblk; b += 4) {
         f32x4 v[4];
 #pragma unroll
@@ -512,7 +527,6 @@ __global__ __launch_bounds__(kColThreads) void ssm_sums_kernel(const RevArgs k, 
         s += (v[0] + v[1]) + (v[2] + v[3]);
     }
     for (; b < k.nblk; ++b) s += *reinterpret_cast<const f32x4 *>(k.part_bc + static_cast<size_t>(b) * rows * 2 * N + i);
-    const long long row = i / (2 * N);
     const int e = static_cast<int>(i % (2 * N));
     R *out = static_cast<R *>(e < N ? k.a.dB : k.a.dC) + row * N + (e < N ? e : e - N);
     P::st4(out, s);
@@ -611,7 +625,7 @@ hipError_t launch_ssm_bwd(int dtype, const SsmBwdArgs &a, void *ws, hipStream_t 
     k.part_d = k.part_a + z.pa;
     SsmArgs f{};
     f.u = a.u; f.dt = a.dt; f.Bm = a.Bm; f.Cm = a.Cm;
-    f.A = a.A; f.dt_bias = a.dt_bias; f.S0 = a.S0;
+    f.A = a.A; f.dt_bias = a.dt_bias; f.S0 = a.S0; f.lens = a.lens;
     f.B = a.B; f.T = a.T; f.D = a.D; f.G = a.G; f.N = a.N;
     f.softplus = a.softplus;
     launch_ssm_rows(dtype, f, k.rows, stream);

@@ -129,3 +129,23 @@ def test_refusals(qd):
             qd.qdelta_conv_fwd(**dict(dict(x=x, w=w, bias=b, S0=S0), **kw))
     with pytest.raises(qd.QDeltaError, match="workspace"):
         qd.qdelta_conv_bwd(x, w, b, S0, x.clone(), workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,T,D,W", [("bf16", 21, 40, 4), ("f32", 21, 7, 3), ("bf16", 150, 520, 4), ("f32", 1, 8, 2)])
+def test_gradients_of_a_padded_batch(qd, dtype, T, D, W):
+    """What padding holds is read neither from x nor from dy, and its gradient is zero; dS_T
+    belongs to the window at the sequence's end."""
+    lens = [0, 1, T // 2, T, T + 19, -3]
+    x, w, b, S0, dy, dS = make(6, T, D, W, dtype, 31)
+    want, scale = mixer.each_sequence(mixer.conv_bwd, lens, ("dw", "dbias"), (0, -1 - 3, 4, -1 - 5), x, w, b, S0, dy, dS)
+    for i, n in enumerate(lens):
+        x[i, max(n, 0):], dy[i, max(n, 0):] = float("nan"), float("inf")
+    got = qd.qdelta_conv_bwd(dev(x), dev(w), dev(b), dev(S0), dev(dy), dev(dS), lens=dev(torch.tensor(lens, dtype=torch.int32)))
+    for k in ("dx", "dw", "dbias", "dS0"):
+        within(got[k], want[k], scale[k], 2 * U_FWD + (6 * T if k in ("dw", "dbias") else 0), k)
+    full = qd.qdelta_conv_bwd(*[dev(t) for t in make(6, T, D, W, dtype, 31)])
+    every = torch.full((6,), T, dtype=torch.int32, device="cuda")
+    got = qd.qdelta_conv_bwd(*[dev(t) for t in make(6, T, D, W, dtype, 31)], lens=every)
+    assert all(torch.equal(got[k], full[k]) for k in got)
+    with pytest.raises(qd.QDeltaError):
+        qd.qdelta_conv_bwd(*[dev(t) for t in make(6, T, D, W, dtype, 31)], lens=every.long())

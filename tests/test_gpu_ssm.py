@@ -219,3 +219,30 @@ def test_nothing_carried_through_a_growing_segment(qd):
     for k, v in got.items():
         if v is not None:
             within(v, want[k], scale[k], 2 * ssm_u(x, False), k)
+
+
+@pytest.mark.parametrize("dtype,T,D,G,N", [("bf16", 20, 36, 2, 16), ("f32", 20, 36, 2, 16), ("f32", 33, 65, 1, 32),
+                                           ("bf16", 17, 40, 1, 64), ("bf16", 600, 36, 2, 16), ("f32", 1, 5, 1, 16)])
+def test_gradients_of_a_padded_batch(qd, dtype, T, D, G, N):
+    """Padding is not read and its rows' gradients are zero, dB's and dC's too; dS_T belongs to
+    the state at the sequence's end.  Segments past an end have no tokens at all."""
+    lens = [T, 0, 1, T // 2 + 1, T + 9, -1]
+    x = ssm_inputs(6, T, D, G, N, dtype, 41)
+    order = FWD + ("d_o", "dS_T")
+    per = tuple(i if k in ("u", "dt", "Bm", "Cm", "z", "d_o") else -1 - i for i, k in enumerate(order)
+                if k not in ("A", "D", "dt_bias"))
+    want, scale = mixer.each_sequence(mixer.ssm_bwd, lens, ("dA", "dD", "ddt_bias"), per, *[x[k] for k in order])
+    u = 2 * ssm_u(x, True)
+    whole = [dev(x[k]) for k in order]
+    for b, n in enumerate(lens):
+        for k in ("u", "dt", "z", "Bm", "Cm", "d_o"):
+            x[k][b, max(n, 0):] = float("nan") if b % 2 else float("inf")
+    got = qd.qdelta_ssm_bwd(*[dev(x[k]) for k in order], lens=dev(torch.tensor(lens, dtype=torch.int32)))
+    for k, v in got.items():
+        within(v, want[k], scale[k], u, k)
+    full = qd.qdelta_ssm_bwd(*whole)
+    every = torch.full((6,), T, dtype=torch.int32, device="cuda")
+    got = qd.qdelta_ssm_bwd(*whole, lens=every)
+    assert all(torch.equal(got[k], full[k]) for k in got)
+    with pytest.raises(qd.QDeltaError):
+        qd.qdelta_ssm_bwd(*whole, lens=every[:5])

@@ -32,15 +32,15 @@ CONV = ["x", "w", "bias", "S0", "lens", "y", "S_T", "B", "T", "D", "W", "silu", 
 conv = caller("qdelta_conv_fwd", CONV, dict(at(*CONV[:7]), B=2, T=8, D=64, W=4, silu=1, dtype=1))
 CSTEP = ["x", "w", "bias", "S", "y", "N", "D", "W", "silu", "dtype"]
 conv_step = caller("qdelta_conv_step", CSTEP, dict(at(*CSTEP[:5]), N=2, D=64, W=4, silu=1, dtype=1))
-CBWD = ["x", "w", "bias", "S0", "dy", "dS_T", "dx", "dw", "dbias", "dS0", "B", "T", "D", "W", "silu", "dtype", "ws", "n"]
-conv_bwd = caller("qdelta_conv_bwd", CBWD, dict(at(*CBWD[:10]), B=2, T=8, D=64, W=4, silu=1, dtype=1, ws=64 * M, n=M))
+CBWD = ["x", "w", "bias", "S0", "lens", "dy", "dS_T", "dx", "dw", "dbias", "dS0", "B", "T", "D", "W", "silu", "dtype", "ws", "n"]
+conv_bwd = caller("qdelta_conv_bwd", CBWD, dict(at(*CBWD[:4], *CBWD[5:11]), lens=None, B=2, T=8, D=64, W=4, silu=1, dtype=1, ws=64 * M, n=M))
 SSM = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S0", "lens", "o", "S_T", "B", "T", "D", "G", "N", "sp", "dtype", "ws", "n"]
 ssm = caller("qdelta_ssm_fwd", SSM, dict(at(*SSM[:12]), B=2, T=8, D=64, G=2, N=16, sp=1, dtype=1, ws=64 * M, n=M))
 SSTEP = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S", "o", "n_seq", "D", "G", "N", "sp", "dtype"]
 ssm_step = caller("qdelta_ssm_step", SSTEP, dict(at(*SSTEP[:10]), n_seq=2, D=64, G=2, N=16, sp=1, dtype=1))
-SBWD = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S0", "d_o", "dS_T", "du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddtb",
+SBWD = ["u", "dt", "A", "Bm", "Cm", "D_", "z", "dtb", "S0", "lens", "d_o", "dS_T", "du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddtb",
         "dS0", "B", "T", "D", "G", "N", "sp", "dtype", "ws", "n"]
-ssm_bwd = caller("qdelta_ssm_bwd", SBWD, dict(at(*SBWD[:20]), B=2, T=8, D=64, G=2, N=16, sp=1, dtype=1, ws=64 * M, n=M))
+ssm_bwd = caller("qdelta_ssm_bwd", SBWD, dict(at(*SBWD[:9], *SBWD[10:21]), lens=None, B=2, T=8, D=64, G=2, N=16, sp=1, dtype=1, ws=64 * M, n=M))
 NFWD = ["x", "w", "bias", "gate", "y", "stats", "N", "L", "C", "G", "eps", "silu", "dtype", "ws", "n"]
 norm = caller("qdelta_group_norm_fwd", NFWD, dict(at(*NFWD[:6]), N=4, L=1, C=64, G=4, eps=1e-5, silu=0, dtype=1, ws=None, n=0))
 NBWD = ["x", "w", "bias", "gate", "stats", "dy", "dx", "dw", "dbias", "dgate", "N", "L", "C", "G", "silu", "dtype", "ws", "n"]
@@ -60,7 +60,7 @@ def test_conv_refusals(lib):
         assert conv_step(lib, **kw) == want, kw
     for kw, want in ((dict(W=5), UNSUPPORTED), (dict(dw=None), INVALID), (dict(dx=None), INVALID), (dict(dy=None), INVALID),
                      (dict(ws=None), WORKSPACE), (dict(n=16), WORKSPACE), (dict(ws=64 * M + 4), WORKSPACE), (dict(dx=M), INVALID),
-                     (dict(dw=7 * M), INVALID), (dict(ws=5 * M), INVALID), (dict(dS0=4 * M), INVALID), (dict(D=0), OK)):
+                     (dict(dw=7 * M), INVALID), (dict(lens=7 * M), INVALID), (dict(ws=5 * M), INVALID), (dict(dS0=4 * M), INVALID), (dict(D=0), OK)):
         assert conv_bwd(lib, **kw) == want, kw
 
 
@@ -85,7 +85,7 @@ def test_ssm_refusals(lib):
     assert lib.qdelta_ssm_bwd_workspace_bytes(2, 8, 64, 2, 16, 1) <= M
     for kw, want in ((dict(T=-1), INVALID), (dict(N=48), UNSUPPORTED), (dict(dA=None), INVALID), (dict(dB=None), INVALID),
                      (dict(d_o=None), INVALID), (dict(dz=None), INVALID), (dict(z=None), INVALID), (dict(ws=None), WORKSPACE),
-                     (dict(n=64), WORKSPACE), (dict(du=M), INVALID), (dict(dB=16 * M), INVALID), (dict(ws=10 * M), INVALID),
+                     (dict(n=64), WORKSPACE), (dict(du=M), INVALID), (dict(lens=12 * M), INVALID), (dict(dB=16 * M), INVALID), (dict(ws=10 * M), INVALID),
                      (dict(dS0=9 * M), INVALID), (dict(du=12 * M + 2), INVALID), (dict(D=0), OK)):
         assert ssm_bwd(lib, **kw) == want, kw
 
