@@ -143,3 +143,8 @@ def test_sizes_past_a_launch_are_refused(lib):
     odd = (1 << 25) - 1
     assert norm(lib, N=1, C=odd, G=odd) == UNSUPPORTED and norm_bwd(lib, N=1, C=odd, G=odd) == UNSUPPORTED
     assert lib.qdelta_group_norm_bwd_workspace_bytes(1, 1, odd, odd, 1) == 0
+
+
+def test_the_unsupported_status_names_the_limits(lib):
+    text = lib.qdelta_status_string(UNSUPPORTED).decode()
+    assert "W in 2..4" in text and "N in {16,32,64}" in text and "2^32" in text
