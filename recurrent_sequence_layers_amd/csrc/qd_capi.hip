@@ -54,7 +54,7 @@ const char *qdelta_status_string(int status) {
     switch (status) {
         case QD_OK: return "ok";
         case QD_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size, misaligned or aliased buffer)";
-        case QD_ERR_UNSUPPORTED: 
+        case QD_ERR_UNSUPPORTED:
             return "unsupported size or dtype (d_k, d_v in {64,128}; C in {16,32,64}; convolution W in 2..4; scan N in {16,32,64};"
                    " fp32 or bf16; launches of fewer than 2^32 threads)";
         case QD_ERR_WORKSPACE: return "workspace too small";

@@ -19,12 +19,12 @@
 // stages or waits (s_setprio): with two workgroups a compute unit 5 % (16 x 2048 tokens, 4096
 // channels, 16 states 538 -> 522 us).
 //
-// 8 x 4096 tokens, 2048 channels, 16 states, bf16, gated: 360 us, 7 operations a token, channel
-// and state at 24 TFLOP/s; one exponential and four multiply-adds alone would take 145 us at
+// 8 x 4096 tokens, 2048 channels, 16 states, bf16, gated: 339 us, 7 operations a token, channel
+// and state at 25 TFLOP/s; one exponential and four multiply-adds alone would take 145 us at
 // the rate that four waves a SIMD reach (21.2 cycles for 64 lanes), the 537 MB 105 us.  What is
 // between: softplus, the gate and the sums over waves (a third of the vector instructions),
 // and with one workgroup a compute unit two waves a SIMD do not cover each other's waits (at
-// two workgroups the same work takes 261 us).
+// two workgroups the same work takes 258 us).
 //
 // Few channels (B D / 64 workgroups below the card's size): the time axis is cut into P
 // segments.  A first launch walks all but the last from zero for their local end states and
@@ -77,19 +77,22 @@ __global__ __launch_bounds__(256) void ssm_rows_kernel(const ScanArgs k) {
 // PAIR: a lane stages two neighbouring channels of one token, the wave's halves two tokens: half
 // the loads, stores and LDS accesses of one channel and token a lane.  It needs an even number
 // of channels in a group and two tokens a wave (N = 16, 32).
-template <class P, int N, int MODE, bool PAIR>
+// TILE tokens are staged at a time.  A tile of 32 fills LDS, so it is for one workgroup a compute
+// unit: half the barriers, and each group's inputs come while the group before it is computed.
+template <class P, int N, int MODE, bool PAIR, int TILE>
 __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(const ScanArgs k) {
     using R = typename P::R;
-    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = kTile / NW;
+    constexpr int NS = states_per_wave<N>(), NW = N / NS, TPW = TILE / NW;
     constexpr int CPL = PAIR ? 2 : 1, SLOTS = TPW / CPL;     // channels a lane stages, and how often
     static_assert(SLOTS >= 1, "pairs of tokens");
     struct __attribute__((aligned(CPL * P::kBytes))) Cell {
         R v[CPL];
     };
     constexpr int GT = NS == 2 ? 8 : 4;      // tokens whose B and C are in scalar registers
-    static_assert(TPW >= 1 && TPW * NW == kTile, "each wave stages a whole number of tokens");
-    __shared__ __attribute__((aligned(16))) float2 s_in[2][kTile][64];
-    __shared__ __attribute__((aligned(16))) float s_y[MODE == kOut ? 2 : 1][MODE == kOut ? NW : 1][kTile][64];
+    constexpr bool kLong = TILE > kTile;
+    static_assert(TPW >= 1 && TPW * NW == TILE, "each wave stages a whole number of tokens");
+    __shared__ __attribute__((aligned(16))) float2 s_in[2][TILE][64];
+    __shared__ __attribute__((aligned(16))) float s_y[MODE == kOut ? 2 : 1][MODE == kOut ? NW : 1][TILE][64];
     const SsmArgs &a = k.a;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int ncb = a.G * k.nblk, nseg = MODE == kSeg ? k.seg.P - 1 : k.seg.P;
@@ -135,6 +138,10 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
 #pragma unroll
         for (int i = 0; i < NS; ++i) h[i] = 0.f;
     }
+    // A segment's sum of delta: pairs add what they stage, a sixteenth of the additions (16384 tokens
+    // of one sequence 252 -> 248 us); one channel a lane, every wave adds as it walks (odd channel
+    // counts, 2 x 4096 tokens: 130 us against 135).
+    constexpr bool kStagedSum = MODE == kSeg && PAIR;
     float sum_delta = 0.f;
 
     if (tb < te) {
@@ -146,14 +153,14 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
         R *o = MODE == kOut ? static_cast<R *>(a.o) + row0 * D : nullptr;
         const size_t rows = ((static_cast<size_t>(b) * a.G + g) * NW + wave) * k.rows.Tp * NS;
         const float *Bw = k.rows.b + rows, *Cw = k.rows.c + rows;
-        const int ntile = (te - tb + kTile - 1) / kTile;
+        const int ntile = (te - tb + TILE - 1) / TILE;
 
         // What this lane stages: channels sc, .. of the block, token `sub` of each slot's CPL.
         const int sc = PAIR ? 2 * (lane & 31) : lane, sub = PAIR ? lane >> 5 : 0;
         const int s_in_blk = (cb % k.nblk) * 64 + sc;
         const bool s_live = s_in_blk < k.Dg;
         const uint32_t s_ch = g * k.Dg + min(s_in_blk, k.Dg - CPL), s_off = sub * a.D + s_ch;
-        float dt_bias[CPL], skip[CPL];
+        float dt_bias[CPL], skip[CPL], staged[CPL] = {};
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             dt_bias[c] = a.dt_bias ? a.dt_bias[s_ch + c] : 0.f;
@@ -169,11 +176,11 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
         };
         auto fetch = [&](int tile, Raw &r) {
             // The lines of the tile's scalar loads come to L2 with it: half the lanes for B, half for C.
-            const int tl = min(tb + tile * kTile, (te - 1) / kTile * kTile);
-            r.line = (lane < 32 ? Bw : Cw)[static_cast<size_t>(tl) * NS + (lane & 31) * (kTile * NS / 32)];
+            const int tl = min(tb + tile * TILE, (te - 1) / TILE * TILE);
+            r.line = (lane < 32 ? Bw : Cw)[static_cast<size_t>(tl) * NS + (lane & 31) * (TILE * NS / 32)];
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
-                const int t = min(tb + tile * kTile + slot_token(j), te - 1);
+                const int t = min(tb + tile * TILE + slot_token(j), te - 1);
                 const size_t row = static_cast<size_t>(t) * D;
                 const uint32_t at = t + CPL <= te ? s_off : s_ch;
                 r.u[j] = *reinterpret_cast<const Cell *>(u + row + at);
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const int i = slot_token(j) + sub;
-                const bool in = tb + tile * kTile + i < te;
+                const bool in = tb + tile * TILE + i < te;
                 float v[2 * CPL];
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
@@ -202,6 +209,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
                     f.z[j][c] = MODE == kOut ? P::to_f32(r.z[j].v[c]) : 0.f;
                     v[2 * c] = in ? delta : 0.f;
                     v[2 * c + 1] = in ? delta * f.u[j][c] : 0.f;
+                    if constexpr (kStagedSum) staged[c] += v[2 * c];
                 }
                 if constexpr (PAIR) *reinterpret_cast<f32x4 *>(&s_in[tile & 1][i][sc]) = f32x4{v[0], v[1], v[2], v[3]};
                 else s_in[tile & 1][i][sc] = make_float2(v[0], v[1]);
@@ -209,7 +217,9 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
             return f;
         };
         ScalarRows<GT, NS> rb, rc;           // the next group's B and C
+        float2 ahead[kLong ? GT : 1];        // and, within a long tile, its inputs
         auto load_group = [&](int t0) {
+            if constexpr (kLong) t0 = min(t0, k.rows.Tp - GT);     // past a long last tile there are no rows
             rb.load(Bw + static_cast<size_t>(t0) * NS);
             if constexpr (MODE == kOut) rc.load(Cw + static_cast<size_t>(t0) * NS);
         };
@@ -224,11 +234,17 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
         // GT tokens from t0 = tile start + j.  `between` is arithmetic of its own that the
         // compiler may place among the group's.
         auto group = [&](int tile, int j, auto between) {
-            const int t0 = tb + tile * kTile + j;
+            const int t0 = tb + tile * TILE + j;
             if (j % kTok == 0) keep_state(t0);
             float2 in[GT];
 #pragma unroll
-            for (int t = 0; t < GT; ++t) in[t] = s_in[tile & 1][j + t][lane];
+            for (int t = 0; t < GT; ++t) in[t] = kLong && j > 0 ? ahead[kLong ? t : 0] : s_in[tile & 1][j + t][lane];
+            if constexpr (kLong) {
+                if (j + GT < TILE) {
+#pragma unroll
+                    for (int t = 0; t < GT; ++t) ahead[t] = s_in[tile & 1][j + GT + t][lane];
+                }
+            }
             const ScalarRows<GT, NS> cb_ = rb, cc_ = rc;
             // Scalar and LDS loads count down together and out of order: the wait for this
             // group's is here, before the next group's scalar loads are issued, which then
@@ -257,7 +273,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
                     if constexpr (MODE == kOut) y = i ? fmaf(cc_.v[t][i], h[i], y) : cc_.v[t][0] * h[0];
                 }
                 if constexpr (MODE == kOut) s_y[tile & 1][wave][j + t][lane] = y;
-                else if constexpr (MODE == kSeg) sum_delta += in[t].x;
+                else if constexpr (MODE == kSeg && !kStagedSum) sum_delta += in[t].x;
             }
         };
         // The tokens this wave staged: the waves' sums over their states, D, the gate, the store.
@@ -282,7 +298,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
         auto finish = [&](int tile, const Sums &p, const Kept &r) {
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
-                const int t0 = tb + tile * kTile + slot_token(j);
+                const int t0 = tb + tile * TILE + slot_token(j);
                 Cell out;
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
@@ -309,7 +325,7 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
                 if (MODE == kOut && i > 0) finish(i - 1, p, old);
             });
 #pragma unroll
-            for (int j = GT; j < kTile; j += GT) group(i, j, nothing);
+            for (int j = GT; j < TILE; j += GT) group(i, j, nothing);
             __builtin_amdgcn_s_setprio(0);
             old = cur;
             cur = stage(i + 1, r);
@@ -337,6 +353,15 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
             Sums p;
             gather(i - 1, p);
             finish(i - 1, p, old);
+        }
+        if constexpr (kStagedSum) {          // the sums meet where the inputs were
+            float (*sums)[64] = reinterpret_cast<float (*)[64]>(&s_in[0][0][0]);
+            static_assert(NW * CPL <= 2 * 2 * TILE, "rows of sums fit the tiles");
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) sums[wave * CPL + sub][sc + c] = staged[c];
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < NW * CPL; ++r) sum_delta += wave == 0 ? sums[r][lane] : 0.f;
         }
     }
     if (!live) return;
@@ -418,6 +443,15 @@ Segments fwd_segments(int B, int T, int D, int G, int N) {
     return cut_time(T, want > T / 64 ? T / 64 : want);
 }
 
+// Tiles of 32 tokens for 16 states where a compute unit has at most one workgroup: 8 x 4096 tokens,
+// 2048 channels 362 -> 339 us, 8 x 2048 in fp32 201 -> 185, 6 x 2000 180 -> 170; 8 x 200 in fp32
+// 26.7 -> 28.0.  With 32 or 64 states a wave has twice the independent work, and they bring nothing
+// (32 states, 8 x 1024: 145 and 146 us).
+bool long_tiles(const ScanArgs &k, unsigned workgroups) {
+    const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
+    return k.seg.P == 1 && k.a.T >= 512 && workgroups <= static_cast<unsigned>(cus);
+}
+
 template <class P, int N, int MODE>
 hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
     const dim3 blk(64 * N / states_per_wave<N>());
@@ -427,13 +461,19 @@ hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
     // states, with no output to finish, is 5 us slower with them.
     if constexpr (MODE != kKeep && kTile / (N / states_per_wave<N>()) >= 2) {
         if (k.Dg % 2 == 0) {         // with D = G Dg even every row starts on a pair
-            if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg, true>), first, blk, 0, stream, k);
-            hipLaunchKernelGGL((scan_kernel<P, N, MODE, true>), all, blk, 0, stream, k);
+            if constexpr (MODE == kOut && N == 16) {
+                if (long_tiles(k, per)) {
+                    hipLaunchKernelGGL((scan_kernel<P, N, kOut, true, 2 * kTile>), all, blk, 0, stream, k);
+                    return hipGetLastError();
+                }
+            }
+            if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg, true, kTile>), first, blk, 0, stream, k);
+            hipLaunchKernelGGL((scan_kernel<P, N, MODE, true, kTile>), all, blk, 0, stream, k);
             return hipGetLastError();
         }
     }
-    if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg, false>), first, blk, 0, stream, k);
-    hipLaunchKernelGGL((scan_kernel<P, N, MODE, false>), all, blk, 0, stream, k);
+    if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg, false, kTile>), first, blk, 0, stream, k);
+    hipLaunchKernelGGL((scan_kernel<P, N, MODE, false, kTile>), all, blk, 0, stream, k);
     return hipGetLastError();
 }
 

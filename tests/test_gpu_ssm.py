@@ -246,3 +246,25 @@ def test_gradients_of_a_padded_batch(qd, dtype, T, D, G, N):
     assert all(torch.equal(got[k], full[k]) for k in got)
     with pytest.raises(qd.QDeltaError):
         qd.qdelta_ssm_bwd(*whole, lens=every[:5])
+
+
+@pytest.mark.parametrize("dtype,B,T,D,G", [("bf16", 8, 530, 2048, 1), ("f32", 12, 545, 1030, 1), ("bf16", 6, 560, 2040, 12)])
+def test_long_tiles(qd, dtype, B, T, D, G):
+    """Nearly a workgroup for every compute unit and no segments: tiles of 32 tokens, whole and
+    ragged, with and without lens, against the same tokens in shorter calls, which take the short
+    tiles.  States go over in fp32 and every sum has the same order: the results are the same."""
+    x = {k: dev(v) for k, v in ssm_inputs(B, T, D, G, 16, dtype, 51).items()}
+    tok = ("u", "dt", "z", "Bm", "Cm")
+    need = qd.qdelta_ssm_fwd_workspace_bytes(B, T, D, G, 16, DT[dtype])
+    assert need == 2 * B * G * 16 * ((T + 15) // 16 * 16 + 16) * 4          # B and C in fp32 only
+    o, S = qd.qdelta_ssm_fwd(*[x[k] for k in FWD])
+    lens = torch.arange(B, dtype=torch.int32, device="cuda") * (T // B)
+    ol, Sl = qd.qdelta_ssm_fwd(*[x[k] for k in FWD], lens=lens, o=torch.zeros_like(o))
+    state, rows = x["S0"], []
+    for a in range(0, T, 64):
+        part, state = qd.qdelta_ssm_fwd(*[x[k][:, a:a + 64].contiguous() if k in tok else x[k] for k in FWD[:-1]], state)
+        rows.append(part)
+    assert torch.equal(o, torch.cat(rows, 1)) and torch.equal(S, state)
+    for b, n in enumerate(lens.tolist()):
+        assert torch.equal(ol[b, :n], o[b, :n]) and not ol[b, n:].any()
+    assert torch.equal(Sl[0], x["S0"][0])
