@@ -446,7 +446,8 @@ Segments fwd_segments(int B, int T, int D, int G, int N) {
 // Tiles of 32 tokens for 16 states where a compute unit has at most one workgroup: 8 x 4096 tokens,
 // 2048 channels 362 -> 339 us, 8 x 2048 in fp32 201 -> 185, 6 x 2000 180 -> 170; 8 x 200 in fp32
 // 26.7 -> 28.0.  With 32 or 64 states a wave has twice the independent work, and they bring nothing
-// (32 states, 8 x 1024: 145 and 146 us).
+// (32 states, 8 x 1024: 145 and 146 us).  The walk that keeps states: gradients of 8 x 2048 tokens
+// 680 -> 667 us.
 bool long_tiles(const ScanArgs &k, unsigned workgroups) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
     return k.seg.P == 1 && k.a.T >= 512 && workgroups <= static_cast<unsigned>(cus);
@@ -469,6 +470,12 @@ hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
             }
             if (k.seg.P > 1) hipLaunchKernelGGL((scan_kernel<P, N, kSeg, true, kTile>), first, blk, 0, stream, k);
             hipLaunchKernelGGL((scan_kernel<P, N, MODE, true, kTile>), all, blk, 0, stream, k);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (MODE == kKeep && N == 16) {
+        if (long_tiles(k, per)) {
+            hipLaunchKernelGGL((scan_kernel<P, N, kKeep, false, 2 * kTile>), all, blk, 0, stream, k);
             return hipGetLastError();
         }
     }
