@@ -22,11 +22,11 @@
 // 266 of 897 us at 8 x 2048 tokens, 2048 channels, 16 states; exchanges in registers alone
 // take 35 instructions a set against 28.)
 //
-// 8 x 2048 tokens, 2048 channels, 16 states, bf16, gated: 680 us, of which this kernel 490, the
-// walk that keeps states 155 and the sums over workgroups 25.  Its bytes would take 95 us; two
-// exponentials and sixteen multiply-adds a token, channel and state 225 us at the rate four
-// waves a SIMD reach.  LDS (148 KB) holds one workgroup a compute unit, so two waves a SIMD; of
-// the 490 us the channel sums are 107 and the ends of tokens 71.
+// 8 x 2048 tokens, 2048 channels, 16 states, bf16, gated: 668 us, of which this kernel 515, the
+// walk that keeps states 127 and the sums over workgroups 16 (the least of 50 traced launches).
+// Its bytes would take 95 us; two exponentials and sixteen multiply-adds a token, channel and state
+// 225 us at the rate four waves a SIMD reach.  LDS (148 KB) holds one workgroup a compute unit, so
+// two waves a SIMD; of this kernel's time the channel sums are 107 and the ends of tokens 71.
 //
 // Each 64-channel block leaves its sums in the workspace and a second kernel adds the blocks in
 // order, so the result does not depend on the order of workgroups.
