@@ -457,9 +457,12 @@ def _result(t, shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else t
 
 
-def _result_like(t, like):
+def _result_like(t, like, lens=None):
+    """The output t, or a new one like `like`: zeros where lens leaves rows of padding unwritten."""
     import torch
-    return torch.empty_like(like) if t is None else t
+    if t is not None:
+        return t
+    return torch.empty_like(like) if lens is None else torch.zeros_like(like)
 
 
 def _results(out, specs, device):
@@ -494,7 +497,7 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
     """Short causal depthwise convolution over x [B,T,D] (fp32 or bf16), y = silu(pre) or pre.
     w [D,W] and bias [D] fp32, W in 2..4; S0 [B,W-1,D] like x, the inputs before the first
     token (None: zeros).  lens [B] int32: the tokens of each right-padded sequence; rows of y
-    past them are left as they were.  Returns (y, S_T); S_T is None when want_state is False,
+    past them are left as they were (zeros in a y allocated here).  Returns (y, S_T); S_T is None when want_state is False,
     and may be passed as S0."""
     import torch
     lib = load_library()
@@ -504,7 +507,7 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
     with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
-        y = _result_like(y, x)
+        y = _result_like(y, x, lens)
         if want_state:
             S_T = _result(S_T, (B, W - 1, D), dt, dev)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
@@ -588,7 +591,8 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
     """Selective state space scan.  u, dt, z [B,T,D] and Bm, Cm [B,T,G,N] (fp32 or bf16, same
     dtype); A [D,N], D [D], dt_bias [D], S0 [B,D,N] fp32, all but A optional; N in 16, 32, 64.
     softplus: delta = softplus(dt + dt_bias), else dt + dt_bias.  lens [B] int32: the tokens of
-    each right-padded sequence; rows of o past them are left as they were.  Returns (o, S_T);
+    each right-padded sequence; rows of o past them are left as they were (zeros in an o
+    allocated here).  Returns (o, S_T);
     S_T is None when want_state is False, and may be passed as S0.  workspace: at least
     qdelta_ssm_fwd_workspace_bytes(...) bytes, allocated here when None and needed."""
     import torch
@@ -597,7 +601,7 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
     context, handle = _enter(stream, u.device)
     with context:
         dev, f32, code = u.device, torch.float32, _dtype_code(u.dtype)
-        o = _result_like(o, u)
+        o = _result_like(o, u, lens)
         if want_state:
             S_T = _result(S_T, (B, ch, N), f32, dev)
         _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),

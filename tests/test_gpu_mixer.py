@@ -311,3 +311,41 @@ def test_states_of_no_tokens_past_32_bit_offsets(qd):
     u, Bm = torch.empty(B, 0, D, device="cuda"), torch.empty(B, 0, 1, N, device="cuda")
     got = qd.qdelta_ssm_bwd(u, u, -torch.ones(D, N, device="cuda"), Bm, Bm, None, None, None, None, u, dS)
     assert torch.equal(got["dS0"], dS) and not got["dA"].any()
+
+
+def test_padded_mixer_forward_and_backward(qd):
+    """Convolution, scan and gated norm over a right-padded batch whose padding is NaN up to the
+    gate: outputs and every gradient against the sequences one by one, padding's gradients zero."""
+    B, T, D, G, N, H, lens = 4, 24, 96, 2, 16, 4, [24, 0, 7, 1]
+    p, t = params(D, N, 4, 61), tokens(B, T, D, G, N, 62)
+    dy = randn(gen(63), B, T, D)
+    sums = {k: torch.zeros(v.shape, dtype=torch.float64) for k, v in {**p, **t}.items()}
+    want = torch.zeros(B, T, D, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        if n:
+            y, leaves = reference(p, {k: v[b:b + 1, :n] for k, v in t.items()}, H)
+            (y * dy[b:b + 1, :n]).sum().backward()
+            want[b, :n] = y.detach()[0]
+            for k, v in leaves.items():
+                (sums[k][b, :n] if k in t else sums[k]).add_(v.grad[0] if k in t else v.grad)
+        dy[b, n:] = 0
+        for k in ("x", "dt", "Bm", "Cm"):
+            t[k][b, n:] = float("nan")
+    P, X, ln = {k: dev(v) for k, v in p.items()}, {k: dev(v) for k, v in t.items()}, torch.tensor(lens, dtype=torch.int32).cuda()
+    u, _ = qd.qdelta_conv_fwd(X["x"], P["w"], P["b"], lens=ln)
+    o, _ = qd.qdelta_ssm_fwd(u, X["dt"], P["A"], X["Bm"], X["Cm"], P["D"], None, P["dt_bias"], lens=ln)
+    rows = (B * T, D)
+    y, stats = qd.qdelta_group_norm_fwd(o.view(rows), H, P["nw"], P["nb"], X["z"].view(rows))
+    for b, n in enumerate(lens):
+        assert not u[b, n:].any() and not o[b, n:].any()
+        if n:
+            close(y.view(B, T, D)[b, :n], want[b, :n], f"y {b}")
+    g = qd.qdelta_group_norm_bwd(o.view(rows), H, P["nw"], P["nb"], X["z"].view(rows), stats, dev(dy).view(rows))
+    s = qd.qdelta_ssm_bwd(u, X["dt"], P["A"], X["Bm"], X["Cm"], P["D"], None, P["dt_bias"], None, g["dx"].view(B, T, D), lens=ln)
+    c = qd.qdelta_conv_bwd(X["x"], P["w"], P["b"], None, s["du"], lens=ln)
+    got = dict(x=c["dx"], w=c["dw"], b=c["dbias"], dt=s["ddt"], A=s["dA"], Bm=s["dB"], Cm=s["dC"], D=s["dD"],
+               dt_bias=s["ddt_bias"], z=g["dgate"].view(B, T, D), nw=g["dweight"], nb=g["dbias"])
+    for k, v in got.items():
+        close(v, sums[k], "d" + k, 1e-4)
+        if k in t:
+            assert all(not v[b, n:].any() for b, n in enumerate(lens)), k
