@@ -127,11 +127,19 @@ __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(con
     if (MODE != kSeg && k.seg.P > 1) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) h[i] = seg_h[i * D];
-        for (int q = 0; q < p; ++q) {
-            const float *hq = seg_h + static_cast<size_t>(q + 1) * N * D;
-            const float sum = seg_s[static_cast<size_t>(q) * D];
+        for (int q0 = 0; q0 < p; q0 += kCompose) {
+            float local[kCompose][NS], sum[kCompose];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = carry(A2[i], sum, h[i], hq[i * D]);
+            for (int j = 0; j < kCompose; ++j) {
+                const size_t q = min(q0 + j, p - 1);
+                sum[j] = seg_s[q * D];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) local[j][i] = seg_h[(q + 1) * N * D + i * D];
+            }
+#pragma unroll
+            for (int j = 0; j < kCompose; ++j)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) h[i] = q0 + j < p ? carry(A2[i], sum[j], h[i], local[j][i]) : h[i];
         }
     }
     if (MODE == kSeg) {              // the local effect starts from zero

@@ -185,11 +185,20 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
         A2[i] = decay_rate(a.A[static_cast<size_t>(ch) * N + n0 + i]);
         G[i] = a.dS_T && live ? a.dS_T[st + i] : 0.f;
     }
-    for (int q = k.seg.P - 1; q > p; --q) {
-        const float *gq = k.rev.h + ((static_cast<size_t>(b) * k.seg.P + q) * N + n0) * D + ch;
-        const float sum = k.rev.s[(static_cast<size_t>(b) * k.seg.P + q) * D + ch];
+    for (int q0 = k.seg.P - 1; q0 > p; q0 -= kCompose) {
+        float local[kCompose][NS], sum[kCompose];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) G[i] = live ? carry(A2[i], sum, G[i], gq[i * D]) : 0.f;
+        for (int j = 0; j < kCompose; ++j) {
+            const size_t q = static_cast<size_t>(b) * k.seg.P + max(q0 - j, p + 1);
+            sum[j] = k.rev.s[q * D + ch];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) local[j][i] = k.rev.h[(q * N + n0 + i) * D + ch];
+        }
+#pragma unroll
+        for (int j = 0; j < kCompose; ++j)
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                G[i] = !live ? 0.f : q0 - j > p ? carry(A2[i], sum[j], G[i], local[j][i]) : G[i];
     }
     const R *u = static_cast<const R *>(a.u) + row0 * D;
     const R *dt = static_cast<const R *>(a.dt) + row0 * D;
