@@ -466,12 +466,19 @@ def _result_like(t, like, lens=None):
 
 
 def _results(out, specs, device):
-    """The tensors named in specs {name: (wanted, shape, dtype)}: those the caller supplied in
-    out, new ones for the rest, None where not wanted."""
+    """The tensors named in specs: those the caller supplied in out, checked, and new ones for the
+    rest.  A spec is a tensor the result is like, a (shape, dtype), or None where not wanted."""
+    import torch
     got = dict(out or {})
-    for name, (wanted, shape, dtype) in specs.items():
-        got[name] = _result(got.get(name), shape, dtype, device) if wanted else None
-    _check_all(device, [(got[name], name, dtype, shape) for name, (_, shape, dtype) in specs.items()])
+    for name, like in specs.items():
+        t = got.get(name)
+        if like is None:
+            got[name] = None
+        elif t is None:
+            got[name] = torch.empty_like(like) if isinstance(like, torch.Tensor) else torch.empty(like[0], dtype=like[1], device=device)
+        else:
+            shape, dtype = (like.shape, like.dtype) if isinstance(like, torch.Tensor) else like
+            _check_all(device, [(t, name, dtype, shape)])
     return got
 
 
@@ -559,8 +566,8 @@ def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: 
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
                          (S0, "S0", dt, (B, W - 1, D)), (lens, "lens", torch.int32, (B,)), (dy, "dy", dt, (B, T, D)),
                          (dS_T, "dS_T", dt, (B, W - 1, D))])
-        out = _results(out, dict(dx=(True, (B, T, D), dt), dw=(True, (D, W), f32), dbias=(bias is not None, (D,), f32),
-                                 dS0=(want_dS0, (B, W - 1, D), dt)), dev)
+        dS0 = S0 if S0 is not None else ((B, W - 1, D), dt)
+        out = _results(out, dict(dx=x, dw=w, dbias=bias, dS0=dS0 if want_dS0 else None), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_conv_bwd_workspace_bytes(B, T, D, W, code), dev)
         rc = lib.qdelta_conv_bwd(_at(x), _at(w), _at(bias), _at(S0), _at(lens), _at(dy), _at(dS_T),
                                  _at(out["dx"]), _at(out["dw"]), _at(out["dbias"]), _at(out["dS0"]), B, T, D, W,
@@ -650,10 +657,9 @@ def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus
         dev, f32, e, code = u.device, torch.float32, u.dtype, _dtype_code(u.dtype)
         _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
                                   (d_o, "d_o", e, (B, T, ch)), (dS_T, "dS_T", f32, (B, ch, N))])
-        tok, bc = (B, T, ch), (B, T, G, N)
-        out = _results(out, dict(du=(True, tok, e), ddt=(True, tok, e), dA=(True, (ch, N), f32), dB=(True, bc, e),
-                                 dC=(True, bc, e), dD=(D is not None, (ch,), f32), dz=(z is not None, tok, e),
-                                 ddt_bias=(dt_bias is not None, (ch,), f32), dS0=(want_dS0, (B, ch, N), f32)), dev)
+        dS0 = S0 if S0 is not None else ((B, ch, N), f32)
+        out = _results(out, dict(du=u, ddt=dt, dA=A, dB=Bm, dC=Cm, dD=D, dz=z, ddt_bias=dt_bias,
+                                 dS0=dS0 if want_dS0 else None), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_bwd_workspace_bytes(B, T, ch, G, N, code), dev)
         rc = lib.qdelta_ssm_bwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
                                 _at(lens), _at(d_o), _at(dS_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA"]),
@@ -732,8 +738,7 @@ def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: b
             raise QDeltaError("stats must be the forward's")
         _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
                          (gate, "gate", dt, x.shape), (stats, "stats", f32, (N, groups, 2)), (dy, "dy", dt, x.shape)])
-        out = _results(out, dict(dx=(True, tuple(x.shape), dt), dweight=(weight is not None, (C,), f32),
-                                 dbias=(bias is not None, (C,), f32), dgate=(gate is not None, tuple(x.shape), dt)), dev)
+        out = _results(out, dict(dx=x, dweight=weight, dbias=bias, dgate=gate), dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_bwd_workspace_bytes(N, L, C, groups, code), dev)
         rc = lib.qdelta_group_norm_bwd(_at(x), _at(weight), _at(bias), _at(gate), _at(stats), _at(dy), _at(out["dx"]),
                                        _at(out["dweight"]), _at(out["dbias"]), _at(out["dgate"]), N, L, C, groups,

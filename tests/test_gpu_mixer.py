@@ -349,3 +349,27 @@ def test_padded_mixer_forward_and_backward(qd):
         close(v, sums[k], "d" + k, 1e-4)
         if k in t:
             assert all(not v[b, n:].any() for b, n in enumerate(lens)), k
+
+
+def test_gradients_into_the_callers_tensors(qd):
+    """``out`` supplies any of the results: used and returned, the others new, the same values;
+    a tensor of another shape, type or device, or an input's memory, is refused."""
+    B, T, D, G, N = 2, 9, 16, 2, 16
+    p, t = {k: dev(v) for k, v in params(D, N, 4, 71).items()}, {k: dev(v) for k, v in tokens(B, T, D, G, N, 72).items()}
+    dy, S0, C0 = dev(randn(gen(73), B, T, D)), dev(randn(gen(74), B, D, N)), dev(randn(gen(75), B, 3, D))
+    _, stats = qd.qdelta_group_norm_fwd(t["x"].view(B * T, D), G, p["nw"], p["nb"], t["z"].view(B * T, D))
+    calls = [(lambda **kw: qd.qdelta_conv_bwd(t["x"], p["w"], p["b"], C0, dy, **kw), "dx", "dw", t["x"]),
+             (lambda **kw: qd.qdelta_ssm_bwd(t["x"], t["dt"], p["A"], t["Bm"], t["Cm"], p["D"], t["z"], p["dt_bias"], S0, dy, **kw),
+              "du", "dS0", t["dt"]),
+             (lambda **kw: qd.qdelta_group_norm_bwd(t["x"].view(B * T, D), G, p["nw"], p["nb"], t["z"].view(B * T, D), stats,
+                                                    dy.view(B * T, D), **kw), "dx", "dbias", t["z"].view(B * T, D))]
+    for call, a, b, taken in calls:
+        want = call()
+        mine = {k: torch.full_like(want[k], 7.0) for k in (a, b)}
+        got = call(out=mine)
+        assert got[a] is mine[a] and got[b] is mine[b] and set(got) == set(want)
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
+        for bad in (want[a][:1].contiguous(), want[a].double(), want[a].cpu(), want[a].transpose(0, 1), taken):
+            with pytest.raises(qd.QDeltaError):
+                call(out={a: bad})
