@@ -452,33 +452,25 @@ def _enter(stream, device):
     return torch.cuda.stream(s), s.cuda_stream
 
 
-def _result(t, shape, dtype, device):
+def _result(t, name, like, device, empty=True):
+    """The caller's t, checked, or a new tensor.  `like` is a tensor of the same shape and type, or
+    (shape, dtype).  Not empty: new ones are zeros, where a kernel leaves rows of padding unwritten."""
     import torch
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
-
-
-def _result_like(t, like, lens=None):
-    """The output t, or a new one like `like`: zeros where lens leaves rows of padding unwritten."""
-    import torch
+    tensor = isinstance(like, torch.Tensor)
     if t is not None:
+        shape, dtype = (like.shape, like.dtype) if tensor else like
+        _check_all(device, [(t, name, dtype, shape)])
         return t
-    return torch.empty_like(like) if lens is None else torch.zeros_like(like)
+    if tensor:
+        return torch.empty_like(like) if empty else torch.zeros_like(like)
+    return torch.empty(like[0], dtype=like[1], device=device)
 
 
 def _results(out, specs, device):
-    """The tensors named in specs: those the caller supplied in out, checked, and new ones for the
-    rest.  A spec is a tensor the result is like, a (shape, dtype), or None where not wanted."""
-    import torch
+    """The tensors that specs {name: like, or None where not wanted} names, from out or new."""
     got = dict(out or {})
     for name, like in specs.items():
-        t = got.get(name)
-        if like is None:
-            got[name] = None
-        elif t is None:
-            got[name] = torch.empty_like(like) if isinstance(like, torch.Tensor) else torch.empty(like[0], dtype=like[1], device=device)
-        else:
-            shape, dtype = (like.shape, like.dtype) if isinstance(like, torch.Tensor) else like
-            _check_all(device, [(t, name, dtype, shape)])
+        got[name] = None if like is None else _result(got.get(name), name, like, device)
     return got
 
 
@@ -514,12 +506,12 @@ def qdelta_conv_fwd(x, w, bias=None, S0=None, silu: bool = True, lens=None, y=No
     with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
-        y = _result_like(y, x, lens)
-        if want_state:
-            S_T = _result(S_T, (B, W - 1, D), dt, dev)
+        state = ((B, W - 1, D), dt)
         _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)),
-                         (S0, "S0", dt, (B, W - 1, D)), (lens, "lens", torch.int32, (B,)), (y, "y", dt, (B, T, D)),
-                         (S_T, "S_T", dt, (B, W - 1, D))])
+                         (S0, "S0", dt, state[0]), (lens, "lens", torch.int32, (B,))])
+        y = _result(y, "y", x, dev, empty=lens is None)
+        if want_state or S_T is not None:
+            S_T = _result(S_T, "S_T", state if S0 is None else S0, dev)
         rc = lib.qdelta_conv_fwd(_at(x), _at(w), _at(bias), _at(S0), _at(lens), _at(y), _at(S_T), B, T, D, W,
                                  int(silu), code, handle)
         _raise(rc, "qdelta_conv_fwd")
@@ -537,9 +529,8 @@ def qdelta_conv_step(x, w, bias, S, silu: bool = True, y=None, stream=None):
     with context:
         dt, dev, f32 = x.dtype, x.device, torch.float32
         code = _dtype_code(dt)
-        y = _result_like(y, x)
-        _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)), (S, "S", dt, (N, W - 1, D)),
-                         (y, "y", dt, (N, D))])
+        _check_all(dev, [(x, "x", dt, None), (w, "w", f32, (D, W)), (bias, "bias", f32, (D,)), (S, "S", dt, (N, W - 1, D))])
+        y = _result(y, "y", x, dev)
         rc = lib.qdelta_conv_step(_at(x), _at(w), _at(bias), _at(S), _at(y), N, D, W, int(silu), code, handle)
         _raise(rc, "qdelta_conv_step")
         return y
@@ -608,11 +599,11 @@ def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, soft
     context, handle = _enter(stream, u.device)
     with context:
         dev, f32, code = u.device, torch.float32, _dtype_code(u.dtype)
-        o = _result_like(o, u, lens)
-        if want_state:
-            S_T = _result(S_T, (B, ch, N), f32, dev)
-        _check_all(dev, checks + [(S0, "S0", f32, (B, ch, N)), (lens, "lens", torch.int32, (B,)),
-                                  (o, "o", u.dtype, (B, T, ch)), (S_T, "S_T", f32, (B, ch, N))])
+        state = ((B, ch, N), f32)
+        _check_all(dev, checks + [(S0, "S0", f32, state[0]), (lens, "lens", torch.int32, (B,))])
+        o = _result(o, "o", u, dev, empty=lens is None)
+        if want_state or S_T is not None:
+            S_T = _result(S_T, "S_T", state if S0 is None else S0, dev)
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_fwd_workspace_bytes(B, T, ch, G, N, code), dev)
         rc = lib.qdelta_ssm_fwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
                                 _at(lens), _at(o), _at(S_T), B, T, ch, G, N, int(softplus), code, p, n, handle)
@@ -629,8 +620,8 @@ def qdelta_ssm_step(u, dt, A, Bm, Cm, D, z, dt_bias, S, softplus: bool = True, o
     context, handle = _enter(stream, u.device)
     with context:
         dev, code = u.device, _dtype_code(u.dtype)
-        o = _result_like(o, u)
-        _check_all(dev, checks + [(S, "S", torch.float32, (n_seq, ch, N)), (o, "o", u.dtype, (n_seq, ch))])
+        _check_all(dev, checks + [(S, "S", torch.float32, (n_seq, ch, N))])
+        o = _result(o, "o", u, dev)
         rc = lib.qdelta_ssm_step(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S),
                                  _at(o), n_seq, ch, G, N, int(softplus), code, handle)
         _raise(rc, "qdelta_ssm_step")
@@ -704,12 +695,12 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
     context, handle = _enter(stream, x.device)
     with context:
         dt, dev, f32, code = x.dtype, x.device, torch.float32, _dtype_code(x.dtype)
-        y = _result_like(y, x)
-        if want_stats:
-            stats = _result(stats, (N, groups, 2), f32, dev)
         _check_all(dev, [(x, "x", dt, None), (weight, "weight", f32, (C,)), (bias, "bias", f32, (C,)),
-                         (gate, "gate", dt, x.shape), (y, "y", dt, x.shape), (stats, "stats", f32, (N, groups, 2))])
-        if want_stats and not L * C:
+                         (gate, "gate", dt, x.shape)])
+        y = _result(y, "y", x, dev)
+        if want_stats or stats is not None:
+            stats = _result(stats, "stats", ((N, groups, 2), f32), dev)
+        if stats is not None and not L * C:
             stats.zero_()                              # no elements: no kernel writes them
         p, n, workspace = _workspace(workspace, lib.qdelta_group_norm_fwd_workspace_bytes(N, L, C, groups, code), dev)
         rc = lib.qdelta_group_norm_fwd(_at(x), _at(weight), _at(bias), _at(gate), _at(y), _at(stats), N, L, C, groups,
