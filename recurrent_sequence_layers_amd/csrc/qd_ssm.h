@@ -37,7 +37,8 @@ __device__ __forceinline__ float decay_rate(float A) {
 }
 // Segments whose effects are loaded before they are composed: one after the other each would wait
 // for its own loads (gradients of 3 x 203 tokens, 142 channels, 32 states 52 -> 45 us, of 2 x 128
-// tokens, 256 channels, 64 states 67 -> 57; one prompt of 16000 tokens, 512 channels 92 -> 89).
+// tokens, 256 channels, 64 states 67 -> 57; one prompt of 16000 tokens, 512 channels 92 -> 89; eight
+// or sixteen at a time differ by 2 % either way).
 constexpr int kCompose = 4;
 
 // A state through a segment.  Nothing carried stays nothing also where a growing state's factor
