@@ -41,10 +41,15 @@ __device__ __forceinline__ float decay_rate(float A) {
 // or sixteen at a time differ by 2 % either way).
 constexpr int kCompose = 4;
 
-// A state through a segment.  Nothing carried stays nothing also where a growing state's factor
-// (A > 0) overflows.
+// A state through a segment, 2^r h + local with r = rate sum_delta.  Where 2^r is no normal number
+// the product may still be one (a small state that grows, a large one that decays): r's whole part
+// then goes into the exponent of 2^(r - k) h, which is at most |h|.  At 400 either way every h has
+// become infinity or zero.  Nothing carried stays nothing also where the factor overflows.
 __device__ __forceinline__ float carry(float rate, float sum_delta, float h, float local) {
-    const float through = fmaf(__builtin_amdgcn_exp2f(rate * sum_delta), h, local);
+    const float r = rate * sum_delta;
+    const float c = r > 400.f ? 400.f : r < -400.f ? -400.f : r, k = ceilf(c);
+    const float beyond = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(c - k) * h, static_cast<int>(k)) + local;
+    const float through = fabsf(r) > 126.f ? beyond : fmaf(__builtin_amdgcn_exp2f(r), h, local);
     return h == 0.f ? local : through;
 }
 

@@ -268,3 +268,30 @@ def test_long_tiles(qd, dtype, B, T, D, G):
     for b, n in enumerate(lens.tolist()):
         assert torch.equal(ol[b, :n], o[b, :n]) and not ol[b, n:].any()
     assert torch.equal(Sl[0], x["S0"][0])
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_states_carried_through_segments_by_factors_beyond_fp32(qd, sign):
+    """A state of 1e-30 that the first sixteen tokens multiply by e^94 (or one of 1e30 by e^-94): the
+    product is an ordinary number, the segment's factor alone is beyond 2^128 (below 2^-126).  The
+    gradient that those tokens carry back is scaled alike."""
+    small = 10.0 ** (-30 * sign)
+    x = ssm_inputs(2, 600, 36, 2, 16, "f32", 9, plus=False, extras=False, gate=False)
+    x["A"], x["dt"] = torch.full_like(x["A"], float(sign)), torch.full_like(x["dt"], -sign * 1e-3)
+    x["dt"][:, :16] = 94 / 16
+    x["S0"] *= small
+    x["u"][:, :16] = 0
+    x["u"][:, 16:] *= 1e-12
+    x["d_o"][:, :16] = 0
+    x["d_o"][:, 16:] *= small
+    x["dS_T"] *= small
+    o, S = run_fwd(qd, x, False)
+    want, S_T, so, sS = mixer.ssm_fwd(*[x[k] for k in FWD], plus=False)
+    within(o, want, so, ssm_u(x, False), "o")
+    within(S, S_T, sS, ssm_u(x, False), "S_T")
+    assert np.abs(S_T).min() > (1e5 if sign > 0 else 1e-17)
+    got = qd.qdelta_ssm_bwd(*[dev(x[k]) for k in FWD], dev(x["d_o"]), dev(x["dS_T"]), softplus=False)
+    want, scale = mixer.ssm_bwd(*[x[k] for k in FWD], x["d_o"], x["dS_T"], False)
+    for k, v in got.items():
+        if v is not None:
+            within(v, want[k], scale[k], 2 * ssm_u(x, False), k)
