@@ -356,6 +356,7 @@ int qdelta_ssm_step(const void *u, const void *dt, const float *A, const void *B
  *   du, ddt [B][T][D], dB, dC [B][T][G][N] (summed over the group's channels), elements;
  *   dz [B][T][D] elements, required with z and NULL without;
  *   dA [D][N] fp32; dDskip, ddt_bias [D] and dS0 [B][D][N] fp32, each NULL for not written.
+ * With D == 0 nothing is written: dB and dC, sums over no channels, are the caller's to clear.
  * workspace: at least qdelta_ssm_bwd_workspace_bytes, 16-byte aligned, overwritten (the
  * states before every eighth token and the channel blocks' sums).
  */

@@ -651,6 +651,9 @@ def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus
         dS0 = S0 if S0 is not None else ((B, ch, N), f32)
         out = _results(out, dict(du=u, ddt=dt, dA=A, dB=Bm, dC=Cm, dD=D, dz=z, ddt_bias=dt_bias,
                                  dS0=dS0 if want_dS0 else None), dev)
+        if not ch:
+            for name in ("dB", "dC"):
+                out[name].zero_()                      # sums over no channels: no kernel writes them
         p, n, workspace = _workspace(workspace, lib.qdelta_ssm_bwd_workspace_bytes(B, T, ch, G, N, code), dev)
         rc = lib.qdelta_ssm_bwd(_at(u), _at(dt), _at(A), _at(Bm), _at(Cm), _at(D), _at(z), _at(dt_bias), _at(S0),
                                 _at(lens), _at(d_o), _at(dS_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA"]),

@@ -295,3 +295,18 @@ def test_states_carried_through_segments_by_factors_beyond_fp32(qd, sign):
     for k, v in got.items():
         if v is not None:
             within(v, want[k], scale[k], 2 * ssm_u(x, False), k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_without_channels(qd, dtype):
+    """dB and dC sum over channels: without any they are zeros, in new tensors and in the caller's."""
+    u, Bm = torch.empty(2, 5, 0, dtype=DT[dtype], device="cuda"), torch.ones(2, 5, 3, 16, dtype=DT[dtype], device="cuda")
+    A = torch.empty(0, 16, device="cuda")
+    mine = {k: torch.full_like(Bm, 7.0) for k in ("dB", "dC")}
+    got = qd.qdelta_ssm_bwd(u, u, A, Bm, Bm, None, None, None, None, u, out=mine)
+    assert all(got[k] is mine[k] and not got[k].any() for k in mine)
+    left = torch.full_like(Bm, float("nan"))           # memory that a new tensor may be given
+    del left
+    got = qd.qdelta_ssm_bwd(u, u, A, Bm, Bm, None, None, None, None, u)
+    assert all(got[k].shape == Bm.shape and not got[k].any() for k in mine)
+    assert got["du"].shape == u.shape and got["dA"].shape == A.shape and got["dS0"].shape == (2, 0, 16)
