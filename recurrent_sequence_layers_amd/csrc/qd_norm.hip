@@ -297,8 +297,12 @@ __global__ __launch_bounds__(kThreads) void norm_partial_kernel(const LongArgs k
     }
 }
 
-// A group's runs: one workgroup, wide because its loads are what it waits for.
+// A group's runs: one workgroup, wide because its loads are what it waits for.  The grid is groups x
+// samples; past these sizes a workgroup takes several, so that every launch fits.  32768 samples of
+// 2 rows, 16 groups of 32 channels, fp32: 1.61 ms forward with 2048 samples a grid, 1.66 with 8192,
+// 1.82 with all of them; gradients 1.54, 1.62 and 1.74.
 constexpr int kGroupThreads = 1024, kGroupWaves = kGroupThreads / kWave;
+constexpr int kGridGroups = 1 << 20, kGridSamples = 1 << 11;
 __device__ __forceinline__ float block_sum(float x, float *red) {
     x = group_sum(x, kWave);
     __syncthreads();
@@ -307,56 +311,64 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
     return group_sum(red[lane_id() & (kGroupWaves - 1)], kGroupWaves);
 }
 
-// Statistics of one group from its channels' runs: the mean of the means, then the square
-// sums moved to it.
+// Statistics of a group from its channels' runs: the mean of the means, then the square sums
+// moved to it.
 __global__ __launch_bounds__(kGroupThreads) void norm_group_kernel(const LongArgs k) {
     __shared__ float red[kGroupWaves];
-    const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
-    const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
     const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
     const float M = static_cast<float>(k.a.L) * static_cast<float>(k.E);
-    float s = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
-        const int run = i / E, e = i - run * E;
-        s += part[static_cast<size_t>(run) * 2 * k.a.C + e] * static_cast<float>(min(k.RL, k.a.L - run * k.RL));
-    }
-    const float mean = block_sum(s, red) / M;
-    float q = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
-        const int run = i / E, e = i - run * E;
-        const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
-        const float d = p[0] - mean;
-        q += fmaf(d * d, static_cast<float>(min(k.RL, k.a.L - run * k.RL)), p[k.a.C]);
-    }
-    q = block_sum(q, red);
-    if (threadIdx.x == 0) {
-        const float rstd = 1.f / sqrtf(q / M + k.a.eps);
-        k.group[2 * static_cast<size_t>(blockIdx.x)] = mean;
-        k.group[2 * static_cast<size_t>(blockIdx.x) + 1] = rstd;
-    }
+    auto one = [&](int n, int g) {
+        const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
+        float s = 0.f;
+        for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
+            const int run = i / E, e = i - run * E;
+            s += part[static_cast<size_t>(run) * 2 * k.a.C + e] * static_cast<float>(min(k.RL, k.a.L - run * k.RL));
+        }
+        const float mean = block_sum(s, red) / M;
+        float q = 0.f;
+        for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
+            const int run = i / E, e = i - run * E;
+            const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
+            const float d = p[0] - mean;
+            q += fmaf(d * d, static_cast<float>(min(k.RL, k.a.L - run * k.RL)), p[k.a.C]);
+        }
+        q = block_sum(q, red);
+        if (threadIdx.x == 0) {
+            const float rstd = 1.f / sqrtf(q / M + k.a.eps);
+            float *to = k.group + 2 * (static_cast<size_t>(n) * k.a.G + g);
+            to[0] = mean;
+            to[1] = rstd;
+        }
+    };
+    for (int n = blockIdx.y; n < k.a.N; n += gridDim.y)
+        for (int g = blockIdx.x; g < k.a.G; g += gridDim.x) one(n, g);
 }
 
-// The group's two sums for dx, over its channels' runs, divided by M.
+// A group's two sums for dx, over its channels' runs, divided by M.
 __global__ __launch_bounds__(kGroupThreads) void norm_group_bwd_kernel(const LongArgs k) {
     __shared__ float red[kGroupWaves];
-    const int g = blockIdx.x % k.a.G, n = blockIdx.x / k.a.G;
-    const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
     const uint32_t items = static_cast<uint32_t>(k.S) * k.E, E = k.E;
-    float sa = 0.f, sx = 0.f;
-    for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
-        const int run = i / E, e = i - run * E;
-        const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
-        const float w = k.a.w ? k.a.w[g * k.E + e] : 1.f;
-        sa = fmaf(w, p[0], sa);
-        sx = fmaf(w, p[k.a.C], sx);
-    }
-    sa = block_sum(sa, red);
-    sx = block_sum(sx, red);
-    if (threadIdx.x == 0) {
-        const float M = static_cast<float>(k.a.L) * static_cast<float>(k.E);
-        k.group[2 * static_cast<size_t>(blockIdx.x)] = sa / M;
-        k.group[2 * static_cast<size_t>(blockIdx.x) + 1] = sx / M;
-    }
+    const float M = static_cast<float>(k.a.L) * static_cast<float>(k.E);
+    auto one = [&](int n, int g) {
+        const float *part = k.part + static_cast<size_t>(n) * k.S * 2 * k.a.C + g * k.E;
+        float sa = 0.f, sx = 0.f;
+        for (uint32_t i = threadIdx.x; i < items; i += kGroupThreads) {
+            const int run = i / E, e = i - run * E;
+            const float *p = part + static_cast<size_t>(run) * 2 * k.a.C + e;
+            const float w = k.a.w ? k.a.w[g * k.E + e] : 1.f;
+            sa = fmaf(w, p[0], sa);
+            sx = fmaf(w, p[k.a.C], sx);
+        }
+        sa = block_sum(sa, red);
+        sx = block_sum(sx, red);
+        if (threadIdx.x == 0) {
+            float *to = k.group + 2 * (static_cast<size_t>(n) * k.a.G + g);
+            to[0] = sa / M;
+            to[1] = sx / M;
+        }
+    };
+    for (int n = blockIdx.y; n < k.a.N; n += gridDim.y)
+        for (int g = blockIdx.x; g < k.a.G; g += gridDim.x) one(n, g);
 }
 
 // A lane's channels with what belongs to each: weight, bias and its group's two numbers.
@@ -567,13 +579,17 @@ void rows(const RowArgs &k, const RowPlan &p, int grid, bool back, hipStream_t s
     else rows_k<P, 16 / P::kBytes>(k, p.K, grid, back, stream);
 }
 
+dim3 group_grid(const LongArgs &k) {
+    return dim3(static_cast<unsigned>(k.a.G < kGridGroups ? k.a.G : kGridGroups),
+                static_cast<unsigned>(k.a.N < kGridSamples ? k.a.N : kGridSamples));
+}
 template <class P, int V>
 void long_fwd(const LongArgs &k, hipStream_t stream) {
     const bool around = static_cast<size_t>(k.a.N) * k.a.L * k.a.C * P::kBytes >= kAroundBytes;
     const long long n = static_cast<long long>(k.a.N) * k.S * (k.a.C / V);
     const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads)), blk(kThreads);
     hipLaunchKernelGGL((norm_partial_kernel<P, V>), grid, blk, 0, stream, k);
-    hipLaunchKernelGGL(norm_group_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), dim3(kGroupThreads), 0, stream, k);
+    hipLaunchKernelGGL(norm_group_kernel, group_grid(k), dim3(kGroupThreads), 0, stream, k);
     if (around) hipLaunchKernelGGL((norm_apply_kernel<P, V, true>), grid, blk, 0, stream, k);
     else hipLaunchKernelGGL((norm_apply_kernel<P, V, false>), grid, blk, 0, stream, k);
 }
@@ -583,7 +599,7 @@ void long_bwd(const LongArgs &k, hipStream_t stream) {
     const long long n = static_cast<long long>(k.a.N) * k.S * (k.a.C / V);
     const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads)), blk(kThreads);
     hipLaunchKernelGGL((norm_partial_bwd_kernel<P, V>), grid, blk, 0, stream, k);
-    hipLaunchKernelGGL(norm_group_bwd_kernel, dim3(static_cast<unsigned>(k.a.N) * k.a.G), dim3(kGroupThreads), 0, stream, k);
+    hipLaunchKernelGGL(norm_group_bwd_kernel, group_grid(k), dim3(kGroupThreads), 0, stream, k);
     if (around) hipLaunchKernelGGL((norm_apply_bwd_kernel<P, V, true>), grid, blk, 0, stream, k);
     else hipLaunchKernelGGL((norm_apply_bwd_kernel<P, V, false>), grid, blk, 0, stream, k);
 }
@@ -596,8 +612,7 @@ bool norm_fits(int dtype, int N, int L, int C, int G) {
     if (static_cast<long long>(N) * L >= (1LL << 31) || C >= (1 << 26)) return false;
     if (r.use) return static_cast<long long>(N) * G * r.LG < lim && static_cast<long long>(row_grid(N, G, r.LG, kGridFwd)) * kThreads < lim;
     const LongPlan p = long_plan(dtype, N, L, C);
-    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(N) * G * kGroupThreads < lim &&
-           static_cast<long long>(p.S) * (C / G) < lim;
+    return static_cast<long long>(N) * p.S * (C / p.V) < lim && static_cast<long long>(p.S) * (C / G) < lim;
 }
 
 size_t norm_fwd_workspace(int dtype, int N, int L, int C, int G) {

@@ -150,3 +150,24 @@ def test_groups_without_elements_have_zero_statistics(qd, shape):
     w = torch.ones(shape[-1], device="cuda")
     got = qd.qdelta_group_norm_bwd(x, 2, w, w, None, st, x)
     assert got["dx"].shape == shape and not got["dweight"].any() and not got["dbias"].any()
+
+
+def test_millions_of_groups_over_rows(qd):
+    """More groups than a launch has workgroups of one each: 2^22 + 12, of two rows and four channels."""
+    N, L, G, E = (1 << 20) + 3, 2, 4, 4
+    x, w, b, _, _ = make("f32", 4, L, G, E, True, False, 17)
+    rows = torch.randn(N, L, G * E, generator=torch.Generator(device="cuda").manual_seed(18), device="cuda") * 1.5 + 0.3
+    dy = torch.randn(N, L, G * E, generator=torch.Generator(device="cuda").manual_seed(19), device="cuda")
+    y, stats = qd.qdelta_group_norm_fwd(rows, G, dev(w), dev(b))
+    got = qd.qdelta_group_norm_bwd(rows, G, dev(w), dev(b), None, stats, dy)
+    for a in (0, (1 << 18) - 4, (1 << 19) + 1, N - 8):         # groups of the first and of later rounds
+        part = slice(a, a + 8)
+        want, st, scale = mixer.norm_fwd(rows[part], G, w, b)
+        within(y[part], want, scale, units(L, E), f"y {a}")
+        grad, size = mixer.norm_bwd(rows[part], G, w, b, None, stats[part], dy[part])
+        within(got["dx"][part], grad["dx"], size["dx"], 2 * units(L, E), f"dx {a}")
+    hat = (rows - stats[:, None, :, :1].expand(N, L, G, E).reshape(N, L, -1)) * stats[:, None, :, 1:].expand(N, L, G, E).reshape(N, L, -1)
+    for k, terms in (("dbias", dy), ("dweight", dy * hat)):
+        # a thread adds a sixteenth of the 2^20 rows in four parts, then 16 sums meet
+        bound = ((1 << 14) + 64) * 2.0 ** -24 * terms.double().abs().sum((0, 1))
+        assert ((got[k].double() - terms.double().sum((0, 1))).abs() <= bound).all(), k

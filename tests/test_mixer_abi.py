@@ -148,3 +148,12 @@ def test_sizes_past_a_launch_are_refused(lib):
 def test_the_unsupported_status_names_the_limits(lib):
     text = lib.qdelta_status_string(UNSUPPORTED).decode()
     assert "W in 2..4" in text and "N in {16,32,64}" in text and "2^32" in text
+
+
+def test_any_number_of_groups_over_rows(lib):
+    """What a norm over rows needs is bounded by its rows and channels, not by its groups."""
+    n = (1 << 20) + 3
+    need = (n * 2 * 16 + n * 4 * 2) * 4                # a run and sample: two sums a channel; two numbers a group
+    assert lib.qdelta_group_norm_fwd_workspace_bytes(n, 2, 16, 4, 0) == need
+    assert lib.qdelta_group_norm_bwd_workspace_bytes(n, 2, 16, 4, 0) == need
+    assert norm(lib, N=n, L=2, C=16, G=4, dtype=0) == WORKSPACE
