@@ -77,8 +77,8 @@ __global__ __launch_bounds__(256) void ssm_rows_kernel(const ScanArgs k) {
 // PAIR: a lane stages two neighbouring channels of one token, the wave's halves two tokens: half
 // the loads, stores and LDS accesses of one channel and token a lane.  It needs an even number
 // of channels in a group and two tokens a wave (N = 16, 32).
-// TILE tokens are staged at a time.  A tile of 32 fills LDS, so it is for one workgroup a compute
-// unit: half the barriers, and each group's inputs come while the group before it is computed.
+// TILE tokens are staged at a time.  With 32 there are half the barriers, and each group's inputs
+// come while the group before it is computed.
 template <class P, int N, int MODE, bool PAIR, int TILE>
 __global__ __launch_bounds__(64 * N / states_per_wave<N>()) void scan_kernel(const ScanArgs k) {
     using R = typename P::R;
@@ -451,14 +451,17 @@ Segments fwd_segments(int B, int T, int D, int G, int N) {
     return cut_time(T, want > T / 64 ? T / 64 : want);
 }
 
-// Tiles of 32 tokens for 16 states where a compute unit has at most one workgroup: 8 x 4096 tokens,
-// 2048 channels 362 -> 339 us, 8 x 2048 in fp32 201 -> 185, 6 x 2000 180 -> 170; 8 x 200 in fp32
-// 26.7 -> 28.0.  With 32 or 64 states a wave has twice the independent work, and they bring nothing
-// (32 states, 8 x 1024: 145 and 146 us).  The walk that keeps states: gradients of 8 x 2048 tokens
-// 680 -> 667 us.
-bool long_tiles(const ScanArgs &k, unsigned workgroups) {
+// Tiles of 32 tokens, for 16 states and walks of at least 512 tokens in one piece.  The full walk's fill
+// LDS, so they are for a compute unit with at most one workgroup: 8 x 4096 tokens, 2048 channels
+// 362 -> 339 us, 8 x 2048 in fp32 201 -> 185, 6 x 2000 180 -> 170; 8 x 200 in fp32 26.7 -> 28.0.  With
+// 32 or 64 states a wave has twice the independent work, and they bring nothing (32 states, 8 x 1024:
+// 145 and 146 us).  The walk that keeps states (40 KB of LDS) takes them up to two workgroups a compute
+// unit; gradients of 2048 channels with the short and the long tiles: 8 x 2048 tokens (256 workgroups)
+// 699 and 688 us, 12 x 700 (384) 454 and 451, 16 x 1024 (512) 667 and 663; of 2112 channels, 8 x 2048
+// (264) 1260 and 1244; of 4096, 16 x 512 (1024) 669 and 677; 16 x 100 (512) 95 and 98.
+bool long_tiles(const ScanArgs &k, unsigned workgroups, int per_unit) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    return k.seg.P == 1 && k.a.T >= 512 && workgroups <= static_cast<unsigned>(cus);
+    return k.seg.P == 1 && k.a.T >= 512 && workgroups <= static_cast<unsigned>(per_unit * cus);
 }
 
 template <class P, int N, int MODE>
@@ -471,7 +474,7 @@ hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
     if constexpr (MODE != kKeep && kTile / (N / states_per_wave<N>()) >= 2) {
         if (k.Dg % 2 == 0) {         // with D = G Dg even every row starts on a pair
             if constexpr (MODE == kOut && N == 16) {
-                if (long_tiles(k, per)) {
+                if (long_tiles(k, per, 1)) {
                     hipLaunchKernelGGL((scan_kernel<P, N, kOut, true, 2 * kTile>), all, blk, 0, stream, k);
                     return hipGetLastError();
                 }
@@ -482,7 +485,7 @@ hipError_t run_scan(const ScanArgs &k, hipStream_t stream) {
         }
     }
     if constexpr (MODE == kKeep && N == 16) {
-        if (long_tiles(k, per)) {
+        if (long_tiles(k, per, 2)) {
             hipLaunchKernelGGL((scan_kernel<P, N, kKeep, false, 2 * kTile>), all, blk, 0, stream, k);
             return hipGetLastError();
         }
