@@ -412,6 +412,13 @@ def qdelta_step(q, k, v, alpha, beta, lam, S, o=None, stream=None, raw: bool = F
 
 
 # ---------------------------------------------------------------- around the recurrence
+def _int_sizes(sizes):
+    """Refuses what the library's 32-bit sizes cannot hold: ctypes would pass the low 32 bits on."""
+    if max(sizes) > 0x7fffffff:
+        raise QDeltaError(f"sizes must be below 2**31, got {tuple(sizes)}")
+    return sizes
+
+
 def _shape(t, name, dims):
     """Shape of a device tensor with `dims` dimensions."""
     import torch
@@ -419,7 +426,7 @@ def _shape(t, name, dims):
         raise QDeltaError(f"{name} must be a device tensor")
     if t.dim() != dims:
         raise QDeltaError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.shape
+    return _int_sizes(t.shape)
 
 
 def _check_all(device, checks):
@@ -537,7 +544,7 @@ def qdelta_conv_step(x, w, bias, S, silu: bool = True, y=None, stream=None):
 
 
 def qdelta_conv_bwd_workspace_bytes(B, T, D, W, dtype) -> int:
-    return int(load_library().qdelta_conv_bwd_workspace_bytes(B, T, D, W, _dtype_code(dtype)))
+    return int(load_library().qdelta_conv_bwd_workspace_bytes(*_int_sizes((B, T, D, W)), _dtype_code(dtype)))
 
 
 def qdelta_conv_bwd(x, w, bias, S0, dy, dS_T=None, silu: bool = True, want_dS0: bool = True, lens=None, out=None,
@@ -581,7 +588,7 @@ def _ssm_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, token_dims):
 
 
 def qdelta_ssm_fwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
-    return int(load_library().qdelta_ssm_fwd_workspace_bytes(B, T, D, G, N, _dtype_code(dtype)))
+    return int(load_library().qdelta_ssm_fwd_workspace_bytes(*_int_sizes((B, T, D, G, N)), _dtype_code(dtype)))
 
 
 def qdelta_ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, softplus: bool = True, lens=None, o=None,
@@ -629,7 +636,7 @@ def qdelta_ssm_step(u, dt, A, Bm, Cm, D, z, dt_bias, S, softplus: bool = True, o
 
 
 def qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
-    return int(load_library().qdelta_ssm_bwd_workspace_bytes(B, T, D, G, N, _dtype_code(dtype)))
+    return int(load_library().qdelta_ssm_bwd_workspace_bytes(*_int_sizes((B, T, D, G, N)), _dtype_code(dtype)))
 
 
 def qdelta_ssm_bwd(u, dt, A, Bm, Cm, D, z, dt_bias, S0, d_o, dS_T=None, softplus: bool = True, want_dS0: bool = True,
@@ -676,11 +683,11 @@ def _norm_sizes(x, groups):
         length *= d
     if groups < 1 or c % groups:
         raise QDeltaError(f"the {c} channels of x must divide into {groups} groups")
-    return n, length, c
+    return _int_sizes((n, length, c))
 
 
 def qdelta_group_norm_fwd_workspace_bytes(N, L, C, G, dtype) -> int:
-    return int(load_library().qdelta_group_norm_fwd_workspace_bytes(N, L, C, G, _dtype_code(dtype)))
+    return int(load_library().qdelta_group_norm_fwd_workspace_bytes(*_int_sizes((N, L, C, G)), _dtype_code(dtype)))
 
 
 def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, silu: bool = False, eps: float = 1e-5,
@@ -713,7 +720,7 @@ def qdelta_group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, sil
 
 
 def qdelta_group_norm_bwd_workspace_bytes(N, L, C, G, dtype) -> int:
-    return int(load_library().qdelta_group_norm_bwd_workspace_bytes(N, L, C, G, _dtype_code(dtype)))
+    return int(load_library().qdelta_group_norm_bwd_workspace_bytes(*_int_sizes((N, L, C, G)), _dtype_code(dtype)))
 
 
 def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: bool = False, out=None, workspace=None,

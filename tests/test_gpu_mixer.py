@@ -373,3 +373,18 @@ def test_gradients_into_the_callers_tensors(qd):
         for bad in (want[a][:1].contiguous(), want[a].double(), want[a].cpu(), want[a].transpose(0, 1), taken):
             with pytest.raises(qd.QDeltaError):
                 call(out={a: bad})
+
+
+def test_sizes_past_32_bits_are_refused(qd):
+    """2^32 + 5 tokens are not the five that their low 32 bits say; nothing of x is read."""
+    x = torch.empty(1, (1 << 32) + 5, 1, device="cuda", dtype=torch.bfloat16)
+    w, one = torch.ones(1, 4, device="cuda"), torch.ones(1, device="cuda")
+    A, Bm = -torch.ones(1, 16, device="cuda"), torch.empty(1, 5, 1, 16, device="cuda", dtype=torch.bfloat16)
+    y = torch.zeros_like(x)
+    for call in (lambda: qd.qdelta_conv_fwd(x, w, y=y), lambda: qd.qdelta_conv_bwd(x, w, one, None, x, out=dict(dx=y)),
+                 lambda: qd.qdelta_conv_step(x[0], w, None, torch.empty(5, 3, 1, device="cuda", dtype=torch.bfloat16)),
+                 lambda: qd.qdelta_ssm_fwd(x, x, A, Bm, Bm, o=y), lambda: qd.qdelta_ssm_bwd(x, x, A, Bm, Bm, None, None, None, None, x),
+                 lambda: qd.qdelta_group_norm_fwd(x, 1, one, y=y), lambda: qd.qdelta_group_norm_fwd(x.view(1, 3, -1, 1), 1, one),
+                 lambda: qd.qdelta_group_norm_bwd(x, 1, one, None, None, torch.ones(1, 1, 2, device="cuda"), x, out=dict(dx=y))):
+        with pytest.raises(qd.QDeltaError, match=r"below 2\*\*31"):
+            call()

@@ -157,3 +157,15 @@ def test_any_number_of_groups_over_rows(lib):
     assert lib.qdelta_group_norm_fwd_workspace_bytes(n, 2, 16, 4, 0) == need
     assert lib.qdelta_group_norm_bwd_workspace_bytes(n, 2, 16, 4, 0) == need
     assert norm(lib, N=n, L=2, C=16, G=4, dtype=0) == WORKSPACE
+
+
+def test_sizes_past_32_bits_are_refused_by_the_binding():
+    """The library takes 32-bit sizes; the low 32 bits of a larger one are another size."""
+    import recurrent_sequence_layers_amd as qd
+    for T in (1 << 31, (1 << 32) + 16):
+        for query, sizes in ((qd.qdelta_conv_bwd_workspace_bytes, (1, T, 1, 4)), (qd.qdelta_ssm_fwd_workspace_bytes, (1, T, 1, 1, 16)),
+                             (qd.qdelta_ssm_bwd_workspace_bytes, (1, T, 1, 1, 16)),
+                             (qd.qdelta_group_norm_fwd_workspace_bytes, (1, T, 1, 1)),
+                             (qd.qdelta_group_norm_bwd_workspace_bytes, (1, T, 1, 1))):
+            with pytest.raises(qd.QDeltaError, match="2\\*\\*31"):
+                query(*sizes, qd.QD_BF16)
