@@ -152,6 +152,8 @@ def _launch_stream(stream, device):
         return torch.cuda.current_stream(device)
     if not isinstance(stream, torch.cuda.Stream):
         raise QDeltaError("stream must be a torch.cuda.Stream or None")
+    if device.type == "cuda" and stream.device != device:     # its kernels could not reach the tensors
+        raise QDeltaError(f"stream must be on {device}, got one on {stream.device}")
     return stream
 
 

@@ -169,3 +169,18 @@ def test_sizes_past_32_bits_are_refused_by_the_binding():
                              (qd.qdelta_group_norm_bwd_workspace_bytes, (1, T, 1, 1))):
             with pytest.raises(qd.QDeltaError, match="2\\*\\*31"):
                 query(*sizes, qd.QD_BF16)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Kernels enqueued there would be given addresses of a device that is not theirs."""
+    import torch
+    import recurrent_sequence_layers_amd as qd
+
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    for enter in (qd._launch_stream, qd._enter):
+        with pytest.raises(qd.QDeltaError, match="stream must be on cuda:0, got one on cuda:1"):
+            enter(Stream(1), torch.device("cuda", 0))
+    assert qd._launch_stream(mine := Stream(1), torch.device("cuda", 1)) is mine
