@@ -41,15 +41,16 @@ __device__ __forceinline__ float decay_rate(float A) {
 // or sixteen at a time differ by 2 % either way).
 constexpr int kCompose = 4;
 
-// A state through a segment, 2^r h + local with r = rate sum_delta.  Where 2^r is no normal number
-// the product may still be one (a small state that grows, a large one that decays): r's whole part
-// then goes into the exponent of 2^(r - k) h, which is at most |h|.  At 400 either way every h has
-// become infinity or zero.  Nothing carried stays nothing also where the factor overflows.
+// A state through a segment, 2^r h + local with r = rate sum_delta.  The factor enters by its root,
+// twice: where 2^r alone would overflow or vanish (a small state that grows, a large one that decays)
+// the product need not, and the root does neither for any r that leaves a normal h a normal product.
+// (r's whole part put into the exponent reaches subnormal h too, but costs the small calls: 2048 tokens,
+// 512 channels forward 27.7 against 24.8 us; gradients of 2 x 128 tokens, 256 channels, 64 states 59.8
+// against 55.8.)
+// Nothing carried stays nothing also where the root overflows.
 __device__ __forceinline__ float carry(float rate, float sum_delta, float h, float local) {
-    const float r = rate * sum_delta;
-    const float c = r > 400.f ? 400.f : r < -400.f ? -400.f : r, k = ceilf(c);
-    const float beyond = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(c - k) * h, static_cast<int>(k)) + local;
-    const float through = fabsf(r) > 126.f ? beyond : fmaf(__builtin_amdgcn_exp2f(r), h, local);
+    const float root = __builtin_amdgcn_exp2f(0.5f * rate * sum_delta);
+    const float through = fmaf(root, root * h, local);
     return h == 0.f ? local : through;
 }
 
