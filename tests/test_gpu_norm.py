@@ -171,3 +171,22 @@ def test_millions_of_groups_over_rows(qd):
         # a thread adds a sixteenth of the 2^20 rows in four parts, then 16 sums meet
         bound = ((1 << 14) + 64) * 2.0 ** -24 * terms.double().abs().sum((0, 1))
         assert ((got[k].double() - terms.double().sum((0, 1))).abs() <= bound).all(), k
+
+
+def test_a_million_groups_of_a_sample(qd):
+    """More groups than the grid is wide: 2^20 + 5 of one channel and three rows."""
+    N, L, G = 2, 3, (1 << 20) + 5
+    rand = lambda seed, *s: torch.randn(*s, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")  # noqa: E731
+    x, dy, w, b = rand(23, N, L, G) * 1.5 + 0.3, rand(24, N, L, G), rand(25, G), rand(26, G)
+    y, stats = qd.qdelta_group_norm_fwd(x, G, w, b)
+    got = qd.qdelta_group_norm_bwd(x, G, w, b, None, stats, dy)
+    for a in (0, (1 << 19) + 3, G - 8):
+        part = slice(a, a + 8)
+        xs, dys = x[..., part].contiguous(), dy[..., part].contiguous()
+        want, st, scale = mixer.norm_fwd(xs, 8, w[part], b[part])
+        # three values may lie close together: their spread's relative error is that of the values over it
+        near = np.maximum(1, (np.abs(xs.double().cpu().numpy()).max(1, keepdims=True) * st[:, None, :, 1]) ** 2)
+        within(y[..., part], want, scale * near, units(L, 1), f"y {a}")
+        grad, size = mixer.norm_bwd(xs, 8, w[part], b[part], None, stats[:, part], dys)
+        for k, v in (("dx", got["dx"][..., part]), ("dweight", got["dweight"][part]), ("dbias", got["dbias"][part])):
+            within(v, grad[k], size[k], 2 * units(L, 1) + N * L, f"{k} {a}")
