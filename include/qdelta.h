@@ -377,7 +377,8 @@ int qdelta_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm
  *
  *   x, gate, y  [N][L][C] elements, gate NULL for none; C divisible by G.  A layer's output
  *             [B][T][H][d] normed per token and head is N = B*T, L = 1, C = H*d, G = H.
- *   weight, bias  [C] fp32 or NULL (one, zero);  eps >= 0 and finite
+ *   weight, bias  [C] fp32 or NULL (one, zero);  eps >= 0 and finite.  A group's sum of centred
+ *             squares is taken in fp32 and has to stay within its range.
  *   stats     [N][G][2] fp32, mean and 1 / sqrt(var + eps), or NULL (not written); not written
  *             either where L or C is 0 and there is nothing to take them of
  * workspace: at least qdelta_group_norm_fwd_workspace_bytes (0 where L == 1 and a group fits

@@ -12,8 +12,9 @@
 // kVec channels over a run of TL tokens and keeps the last W - 1 rows in registers, so a row
 // is loaded once for all W taps; consecutive threads take consecutive channel vectors, so a
 // wave's load covers 512 or 1024 contiguous bytes of a row.  Channel counts that kVec does not
-// divide take one channel a thread.  At 8 x 4096 x 2048 bf16, W = 4: forward 58 us (268 MB, 4.6
-// TB/s), backward 95 us (403 MB, 4.2 TB/s).
+// divide take one channel a thread.  At 8 x 4096 x 2048 bf16, W = 4: forward 62 us (268 MB, 4.3
+// TB/s), backward 98 us (403 MB, 4.1 TB/s), 118 with lens.  These figures and those below are of one
+// build: a call among others over three sets of inputs, the median of five runs.
 #include "qd_internal.h"
 #include "qd_mixer.h"
 
@@ -22,11 +23,11 @@ namespace {
 
 constexpr int kThreads = 256;
 // Channels a thread: 8 bytes of bf16, 16 of fp32.  Eight bf16 channels (16 bytes) take twice the
-// registers: 65 against 62 us forward and 99 against 95 us backward at 8 x 4096 x 2048, W = 4;
-// two fp32 channels 57 against 55 us.
+// registers: forward 67 us against 62, backward 102 against 98 (with lens 102 against 118).  Two fp32
+// channels, at four sequences: forward 59 against 55 us, backward 92 against 94.
 constexpr int kVec = 4;
-// Rows loaded before they are used: forward 58 us with eight, 62 with four; backward, which
-// holds two rows for each and more registers besides, 107 with eight and 95 with four.
+// Rows loaded before they are used: forward 62 us with eight, 66 with four; backward, which
+// holds two rows for each and more registers besides, 109 with eight and 98 with four.
 constexpr int kAhead = 8, kAheadBwd = 4;
 
 // Row t of a sequence with its history: t < 0 comes from the state (or is zero).
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(const ConvArgs a) {
 // A block covers NX channel vectors times 256 / NX runs of TL tokens; its threads' sums for
 // dw and dbias are joined in LDS in a fixed order and written as one row of partial results.
 // LENS: sequences end at their lengths.  A length is a register more in every lane, which at four
-// taps takes a wave of four from each SIMD: 116 against 95 us.
+// taps takes a wave of four from each SIMD (136 registers against 128): 118 against 98 us.
 template <class P, int V, int W, bool LENS>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvBwdArgs a) {
     using R = typename P::R;
@@ -279,7 +280,7 @@ struct BwdPlan {
 };
 // TL tokens a thread: long runs read fewer rows twice (the W - 1 rows on either side of a
 // run) and leave fewer partial sums, short ones fill the card.  At the size above 32 tokens take
-// 108 us, 64 take 98 and 128 take 98.
+// 102 us, 64 take 98 and 128 take 112; in fp32, at four sequences, 102, 94 and 94.
 BwdPlan bwd_plan(int B, int T, int D) {
     const int nvec = D / vec_of(D);
     BwdPlan p;
@@ -294,7 +295,8 @@ BwdPlan bwd_plan(int B, int T, int D) {
 }
 
 // Tokens a thread walks in the forward: long runs read fewer rows twice, short ones fill the
-// card.  At the size above 16 tokens take 73 us, 32 take 65 and 64 take 65.
+// card.  At the size above 16 tokens take 63 us, 32 take 62 and 64 take 60; in fp32, at four
+// sequences, all three 55.
 int fwd_run(int B, int T, int D) {
     int TL = 32;
     while (TL > 4 && static_cast<long long>(B) * ((T + TL - 1) / TL) * (D / vec_of(D)) < 262144) TL /= 2;

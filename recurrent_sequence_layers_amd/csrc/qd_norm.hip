@@ -13,7 +13,9 @@
 // registers (L = 1: the norm of a token's heads).  Then the variance is that of the centred
 // values held in registers.  Longer groups take two passes over x: partial statistics per
 // channel and run of rows, their combination, and the elementwise pass, whose second read is
-// served by the last-level cache while the tensors fit it.
+// served by the last-level cache while the tensors fit it.  Group sizes that 16 bytes do not divide go
+// one element a lane, with one load of a row in flight: 32768 x 16 groups, bf16, SiLU, of 127 channels
+// 145 us forward and 176 backward, of 128 channels 66 and 97.
 #include "qd_internal.h"
 #include "qd_mixer.h"
 

@@ -19,7 +19,7 @@
 // stages or waits (s_setprio): with two workgroups a compute unit 5 % (16 x 2048 tokens, 4096
 // channels, 16 states 538 -> 522 us).
 //
-// 8 x 4096 tokens, 2048 channels, 16 states, bf16, gated: 339 us, 7 operations a token, channel
+// 8 x 4096 tokens, 2048 channels, 16 states, bf16, gated: 340 us, 7 operations a token, channel
 // and state at 25 TFLOP/s; one exponential and four multiply-adds alone would take 145 us at
 // the rate that four waves a SIMD reach (21.2 cycles for 64 lanes), the 537 MB 105 us.  What is
 // between: softplus, the gate and the sums over waves (a third of the vector instructions),
@@ -455,7 +455,7 @@ Segments fwd_segments(int B, int T, int D, int G, int N) {
 // LDS, so they are for a compute unit with at most one workgroup: 8 x 4096 tokens, 2048 channels
 // 362 -> 339 us, 8 x 2048 in fp32 201 -> 185, 6 x 2000 180 -> 170; 8 x 200 in fp32 26.7 -> 28.0.  With
 // 32 or 64 states a wave has twice the independent work, and they bring nothing (32 states, 8 x 1024:
-// 145 and 146 us).  The walk that keeps states (40 KB of LDS) takes them up to two workgroups a compute
+// 145 and 146 us).  The walk that keeps states (32 KB of LDS) takes them up to two workgroups a compute
 // unit; gradients of 2048 channels with the short and the long tiles: 8 x 2048 tokens (256 workgroups)
 // 699 and 688 us, 12 x 700 (384) 454 and 451, 16 x 1024 (512) 667 and 663; of 2112 channels, 8 x 2048
 // (264) 1260 and 1244; of 4096, 16 x 512 (1024) 669 and 677; 16 x 100 (512) 95 and 98.

@@ -22,8 +22,9 @@
 // 266 of 897 us at 8 x 2048 tokens, 2048 channels, 16 states; exchanges in registers alone
 // take 35 instructions a set against 28.)
 //
-// 8 x 2048 tokens, 2048 channels, 16 states, bf16, gated: 668 us, of which this kernel 515, the
-// walk that keeps states 127 and the sums over workgroups 16 (the least of 50 traced launches).
+// 8 x 2048 tokens, 2048 channels, 16 states, bf16, gated: 669 us a call among others; the least of
+// 50 traced launches are 515 us for this kernel, 127 for the walk that keeps states and 16 for the
+// sums over workgroups.
 // Its bytes would take 95 us; two exponentials and sixteen multiply-adds a token, channel and state
 // 225 us at the rate four waves a SIMD reach.  LDS (148 KB) holds one workgroup a compute unit, so
 // two waves a SIMD; of this kernel's time the channel sums are 107 and the ends of tokens 71.
@@ -160,7 +161,9 @@ __global__ __launch_bounds__(64 * kBwdWaves) void ssm_bwd_kernel(const RevArgs k
     constexpr int NR = states_per_wave<N>(), SUB = NS / NR;          // states of a scalar row, rows a wave
     constexpr int RT = NS <= 4 ? kTok : kTok / 2;                    // tokens whose B and C are in scalar registers
     constexpr int VPT = 2 * NS, TPC = 16 / VPT, SETS = kTok / TPC;   // channel sums: values a token, tokens and sets of 16
-    constexpr bool kHold = NS <= 4;  // decays of a tile stay in registers; at eight states they do not fit
+    // Decays of a tile stay in registers; at eight states they do not fit, and also without them that
+    // instance spills 63 of its 256 registers (252 bytes of scratch a lane).
+    constexpr bool kHold = NS <= 4;
     constexpr int kPitch = 20;       // floats a lane in s_v: 16-byte accesses of eight lanes meet no bank twice
     __shared__ float2 s_in[2][kTok][64];
     __shared__ float s_dy[2][kTok][64];
@@ -554,7 +557,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_empty_kernel(const SsmBwdArgs a) 
 
 // Segments of the time axis: a workgroup (eight waves) for every compute unit, down to one tile
 // a segment.  3 x 203 tokens, 142 channels in two groups, 32 states: 56 us; segments of at least
-// 32 tokens 64, 64 tokens 85, 96 tokens 106.
+// 32 tokens 64, 64 tokens 85, 96 tokens 106.  The count is rounded up, so between half a card of
+// workgroups and a whole one the cut brings the reverse walk nothing: 4096 tokens of 16 states take
+// 1586 us with 150 workgroups, 1643 with 255 and, uncut, 1353 with 256.
 Segments bwd_segments(int B, int T, int D, int G, int N) {
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
     const long long waves = static_cast<long long>(B) * G * ((D / G + 63) / 64) * kBwdWaves;
