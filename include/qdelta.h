@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define QDELTA_ABI_VERSION 7
+#define QDELTA_ABI_VERSION 8
 
 typedef enum qd_status {
     QD_OK = 0,
@@ -399,6 +399,94 @@ size_t qdelta_group_norm_bwd_workspace_bytes(int N, int L, int C, int G, int dty
 int qdelta_group_norm_bwd(const void *x, const float *weight, const float *bias, const void *gate,
                           const float *stats, const void *dy, void *dx, float *dweight, float *dbias,
                           void *dgate, int N, int L, int C, int G, int silu, int dtype, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/*
+ * Linear attention with a decay for each head: the recurrence of the layer without its erase,
+ * the state in the same d_v x d_k convention.  Per (batch b, head h), log decay g_t:
+ *
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = S_t q_t
+ *
+ *   q, k      [B][T][H][d_k], v, o [B][T][H][d_v] elements (nothing is normalised or scaled)
+ *   g         log decays, fp32: [B][T][H], or [H] with g_per_head (the same for every token); NULL
+ *             means zero (no decay).  -INFINITY forgets all that came before the token.
+ *   S0, S_T   [B][H][d_v][d_k] fp32; S0 NULL means zeros, S_T NULL is not written, S_T may equal S0.
+ *   lens      as for qdelta_conv_fwd: padding is not read and its rows of o are left as they were.
+ *   d_k, d_v in {64, 128}; H <= 32768.
+ * Evaluated in chunks of 64 (fp32: 32) tokens: a NaN or an infinity in a token reaches the outputs
+ * of its whole chunk, the earlier tokens' too.  T == 0 writes S_T = S0 (or zeros).
+ * workspace: at least qdelta_linattn_fwd_workspace_bytes (0 where B*H*d_v/64 workgroups fill the
+ * card; else the states of the segments that the time axis is cut into), 16-byte aligned.
+ */
+size_t qdelta_linattn_fwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int dtype);
+int qdelta_linattn_fwd(const void *q, const void *k, const void *v, const float *g, const float *S0,
+                       const int *lens, void *o, float *S_T, int B, int T, int H, int d_k, int d_v,
+                       int g_per_head, int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* One token for N sequences x H heads: q, k [N][H][d_k], v, o [N][H][d_v], g [N][H], or [H] with
+ * g_per_head, or NULL; S [N][H][d_v][d_k] fp32 updated in place. */
+int qdelta_linattn_step(const void *q, const void *k, const void *v, const float *g, float *S, void *o,
+                        int N, int H, int d_k, int d_v, int g_per_head, int dtype, void *stream);
+
+/*
+ * Gradients of sum(o d_o) + sum(S_T dS_T) for the qdelta_linattn_fwd of the same inputs.  With
+ * lens, padding is not read (d_o's rows neither) and the gradients of its rows are zero.
+ *   d_o [B][T][H][d_v] elements, dS_T [B][H][d_v][d_k] fp32 or NULL (zero)
+ *   dq, dk [B][T][H][d_k], dv [B][T][H][d_v] elements
+ *   dg        like g, fp32, or NULL (not written); with g_per_head summed over tokens and
+ *             sequences; NULL when g is
+ *   dS0       [B][H][d_v][d_k] fp32 or NULL (not written)
+ * workspace: at least qdelta_linattn_bwd_workspace_bytes (want_dg: whether dg is given), 16-byte
+ * aligned, overwritten.
+ */
+size_t qdelta_linattn_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int want_dg, int dtype);
+int qdelta_linattn_bwd(const void *q, const void *k, const void *v, const float *g, const float *S0,
+                       const int *lens, const void *d_o, const float *dS_T, void *dq, void *dk, void *dv,
+                       float *dg, float *dS0, int B, int T, int H, int d_k, int d_v, int g_per_head,
+                       int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* What a gate multiplies by: itself, its sigmoid, or its SiLU. */
+typedef enum qd_gate_act {
+    QD_GATE_LINEAR = 0,
+    QD_GATE_SIGMOID = 1,
+    QD_GATE_SILU = 2
+} qd_gate_act;
+
+/*
+ * RMS norms after and before a block, joined with the block's gate, its scale and the residual
+ * sum.  Rows of C channels:
+ *
+ *     f = y r1 post,  r1 = 1 / sqrt(mean(y^2) + eps)     (post NULL: f = y)
+ *     h = x + scale act(gate) f                          the residual stream, rounded to the type
+ *     n = h r2 pre,   r2 = 1 / sqrt(mean(h^2) + eps)     of h as stored (pre NULL: no n)
+ *
+ *   y         [N][C] elements, the block's output;  x [N][C] the stream before it, NULL: zeros
+ *   gate      [N][C] elements, NULL: no factor;  act one of qd_gate_act
+ *   post, scale, pre  [C] fp32 or NULL (scale NULL: one).  Without x, gate or pre this is the RMS
+ *             norm alone; per head of a layer's output with N = B*T*H, C = d.
+ *   h, n      [N][C] elements; n NULL exactly when pre is
+ *   stats     [N][2] fp32, r1 and r2, zero where that norm is not taken, or NULL (not written)
+ *   eps >= 0 and finite; C < 2^28.  A row's sum of squares has to stay within fp32.
+ */
+int qdelta_block_norm_fwd(const void *y, const void *x, const float *post, const void *gate,
+                          const float *scale, const float *pre, void *h, void *n, float *stats, int N,
+                          int C, float eps, int act, int dtype, void *stream);
+
+/*
+ * Gradients of sum(h dh) + sum(n dn) for the qdelta_block_norm_fwd of the same inputs; x is not
+ * needed, h and stats are that call's (h only with dn, stats with dn or post).
+ *   dh, dn    [N][C] elements, either may be NULL (zero), not both;  dn only with pre
+ *   dx        [N][C] elements or NULL (not written);  dy, and, with gate, dgate [N][C] elements
+ *   dpost, dscale, dpre  [C] fp32, summed over rows, each NULL for not written and NULL where the
+ *             input is; dpre without dn is zero.
+ * workspace: at least qdelta_block_norm_bwd_workspace_bytes (want_sums: whether any of the three
+ * is given), 16-byte aligned, overwritten.
+ */
+size_t qdelta_block_norm_bwd_workspace_bytes(int N, int C, int want_sums, int dtype);
+int qdelta_block_norm_bwd(const void *y, const void *h, const float *post, const void *gate,
+                          const float *scale, const float *pre, const float *stats, const void *dh,
+                          const void *dn, void *dx, void *dy, void *dgate, float *dpost, float *dscale,
+                          float *dpre, int N, int C, int act, int dtype, void *workspace,
                           size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus

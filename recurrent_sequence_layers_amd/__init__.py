@@ -20,6 +20,12 @@ carries a state, for one token:
     qdelta_conv_fwd / qdelta_conv_step / qdelta_conv_bwd
     qdelta_ssm_fwd / qdelta_ssm_step / qdelta_ssm_bwd
     qdelta_group_norm_fwd / qdelta_group_norm_bwd
+
+Beside the delta rules, linear attention with a decay for each head, and around a block its RMS
+norms with the gate, the scale and the residual sum:
+
+    qdelta_linattn_fwd / qdelta_linattn_step / qdelta_linattn_bwd
+    qdelta_block_norm_fwd / qdelta_block_norm_bwd
 """
 import contextlib
 import ctypes
@@ -94,7 +100,15 @@ def load_library():
             ("group_norm_fwd_workspace_bytes", sz, [i] * 5),
             ("group_norm_fwd", i, [vp] * 6 + [i] * 4 + [f] + [i] * 2 + [vp, sz, vp]),
             ("group_norm_bwd_workspace_bytes", sz, [i] * 5),
-            ("group_norm_bwd", i, [vp] * 10 + [i] * 6 + [vp, sz, vp])):
+            ("group_norm_bwd", i, [vp] * 10 + [i] * 6 + [vp, sz, vp]),
+            ("linattn_fwd_workspace_bytes", sz, [i] * 6),
+            ("linattn_fwd", i, [vp] * 8 + [i] * 7 + [vp, sz, vp]),
+            ("linattn_step", i, [vp] * 6 + [i] * 6 + [vp]),
+            ("linattn_bwd_workspace_bytes", sz, [i] * 7),
+            ("linattn_bwd", i, [vp] * 13 + [i] * 7 + [vp, sz, vp]),
+            ("block_norm_fwd", i, [vp] * 9 + [i] * 2 + [f] + [i] * 2 + [vp]),
+            ("block_norm_bwd_workspace_bytes", sz, [i] * 4),
+            ("block_norm_bwd", i, [vp] * 15 + [i] * 4 + [vp, sz, vp])):
         fn = getattr(lib, "qdelta_" + name)
         fn.restype, fn.argtypes = restype, argtypes
     _lib = lib
@@ -747,4 +761,179 @@ def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: b
                                        _at(out["dweight"]), _at(out["dbias"]), _at(out["dgate"]), N, L, C, groups,
                                        int(silu), code, p, n, handle)
         _raise(rc, "qdelta_group_norm_bwd")
+        return out
+
+
+# ---------------------------------------------------------------- linear attention with a decay for each head
+def _linattn_inputs(q, k, v, g, token_dims):
+    """Sizes (tokens.., heads, d_k, d_v), whether g is per head, and the checks of what a token has."""
+    import torch
+    shape = tuple(_shape(q, "q", token_dims + 2))
+    d_v = _shape(v, "v", token_dims + 2)[-1]
+    dt, head = q.dtype, shape[:-1]
+    per_head = isinstance(g, torch.Tensor) and g.dim() == 1
+    return shape + (d_v,), per_head, [(q, "q", dt, None), (k, "k", dt, shape), (v, "v", dt, head + (d_v,)),
+                                      (g, "g", torch.float32, head[-1:] if per_head else head)]
+
+
+def qdelta_linattn_fwd_workspace_bytes(B, T, H, d_k, d_v, dtype) -> int:
+    return int(load_library().qdelta_linattn_fwd_workspace_bytes(*_int_sizes((B, T, H, d_k, d_v)), _dtype_code(dtype)))
+
+
+def qdelta_linattn_fwd(q, k, v, g=None, S0=None, lens=None, o=None, S_T=None, want_state: bool = True, workspace=None,
+                       stream=None):
+    """Linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = S_t q_t.
+    q, k [B,T,H,d_k], v [B,T,H,d_v] (fp32 or bf16, same dtype; d_k, d_v in 64, 128); g the log
+    decays, fp32 [B,T,H], or [H] for every token alike, or None (no decay); S0 [B,H,d_v,d_k] fp32 or
+    None.  lens [B] int32: the tokens of each right-padded sequence; rows of o past them are left as
+    they were (zeros in an o allocated here).  Returns (o, S_T); S_T is None when want_state is
+    False, and may be passed as S0.  workspace: at least qdelta_linattn_fwd_workspace_bytes(...)
+    bytes, allocated here when None and needed."""
+    import torch
+    lib = load_library()
+    (B, T, H, d_k, d_v), per_head, checks = _linattn_inputs(q, k, v, g, 2)
+    context, handle = _enter(stream, q.device)
+    with context:
+        dev, f32, code = q.device, torch.float32, _dtype_code(q.dtype)
+        state = ((B, H, d_v, d_k), f32)
+        _check_all(dev, checks + [(S0, "S0", f32, state[0]), (lens, "lens", torch.int32, (B,))])
+        o = _result(o, "o", v, dev, empty=lens is None)
+        if want_state or S_T is not None:
+            S_T = _result(S_T, "S_T", state if S0 is None else S0, dev)
+        p, n, workspace = _workspace(workspace, lib.qdelta_linattn_fwd_workspace_bytes(B, T, H, d_k, d_v, code), dev)
+        rc = lib.qdelta_linattn_fwd(_at(q), _at(k), _at(v), _at(g), _at(S0), _at(lens), _at(o), _at(S_T), B, T, H, d_k, d_v,
+                                    int(per_head), code, p, n, handle)
+        _raise(rc, "qdelta_linattn_fwd")
+        return o, S_T
+
+
+def qdelta_linattn_step(q, k, v, g, S, o=None, stream=None):
+    """One token of linear attention for N sequences x H heads: q, k [N,H,d_k], v [N,H,d_v]; g fp32
+    [N,H], or [H], or None; S [N,H,d_v,d_k] fp32, updated in place.  Returns o [N,H,d_v]."""
+    import torch
+    lib = load_library()
+    (N, H, d_k, d_v), per_head, checks = _linattn_inputs(q, k, v, g, 1)
+    context, handle = _enter(stream, q.device)
+    with context:
+        dev, code = q.device, _dtype_code(q.dtype)
+        _check_all(dev, checks + [(S, "S", torch.float32, (N, H, d_v, d_k))])
+        o = _result(o, "o", v, dev)
+        rc = lib.qdelta_linattn_step(_at(q), _at(k), _at(v), _at(g), _at(S), _at(o), N, H, d_k, d_v, int(per_head), code, handle)
+        _raise(rc, "qdelta_linattn_step")
+        return o
+
+
+def qdelta_linattn_bwd_workspace_bytes(B, T, H, d_k, d_v, want_dg, dtype) -> int:
+    return int(load_library().qdelta_linattn_bwd_workspace_bytes(*_int_sizes((B, T, H, d_k, d_v)), int(want_dg),
+                                                                 _dtype_code(dtype)))
+
+
+def qdelta_linattn_bwd(q, k, v, g, S0, d_o, dS_T=None, want_dS0: bool = True, want_dg: bool = True, lens=None, out=None,
+                       workspace=None, stream=None):
+    """Gradients of sum(o * d_o) + sum(S_T * dS_T) for qdelta_linattn_fwd on the same inputs.  With
+    lens, rows past a sequence's end are not read, d_o's neither, and their gradients are zero.
+    Returns a dict with dq, dk, dv (like their inputs), dg (like g, fp32; for a g of [H] summed over
+    tokens and sequences; None without g or unless want_dg) and dS0 (None unless want_dS0; also
+    given when S0 is None).  ``out`` may supply any of them; ``workspace`` a device buffer of at
+    least qdelta_linattn_bwd_workspace_bytes(...) bytes (allocated when None)."""
+    import torch
+    lib = load_library()
+    (B, T, H, d_k, d_v), per_head, checks = _linattn_inputs(q, k, v, g, 2)
+    context, handle = _enter(stream, q.device)
+    with context:
+        dev, f32, dt, code = q.device, torch.float32, q.dtype, _dtype_code(q.dtype)
+        state = (B, H, d_v, d_k)
+        if d_o is None:
+            raise QDeltaError("d_o must be given")
+        _check_all(dev, checks + [(S0, "S0", f32, state), (lens, "lens", torch.int32, (B,)), (d_o, "d_o", dt, v.shape),
+                                  (dS_T, "dS_T", f32, state)])
+        dS0 = S0 if S0 is not None else (state, f32)
+        out = _results(out, dict(dq=q, dk=k, dv=v, dg=g if want_dg else None, dS0=dS0 if want_dS0 else None), dev)
+        need = lib.qdelta_linattn_bwd_workspace_bytes(B, T, H, d_k, d_v, int(out["dg"] is not None), code)
+        p, n, workspace = _workspace(workspace, need, dev)
+        rc = lib.qdelta_linattn_bwd(_at(q), _at(k), _at(v), _at(g), _at(S0), _at(lens), _at(d_o), _at(dS_T), _at(out["dq"]),
+                                    _at(out["dk"]), _at(out["dv"]), _at(out["dg"]), _at(out["dS0"]), B, T, H, d_k, d_v,
+                                    int(per_head), code, p, n, handle)
+        _raise(rc, "qdelta_linattn_bwd")
+        return out
+
+
+# ---------------------------------------------------------------- norms around a block
+_GATE_ACTS = {"linear": 0, "sigmoid": 1, "silu": 2}
+
+
+def _block_norm_sizes(y, act):
+    """(rows, channels) of y [..,C] and the gate's code."""
+    import torch
+    if not isinstance(y, torch.Tensor) or not y.is_cuda:
+        raise QDeltaError("y must be a device tensor")
+    if y.dim() < 1:
+        raise QDeltaError("y must have at least 1 dimension")
+    if act not in _GATE_ACTS:
+        raise QDeltaError(f"act must be one of {', '.join(_GATE_ACTS)}, got {act!r}")
+    rows = 1
+    for d in y.shape[:-1]:
+        rows *= d
+    return *_int_sizes((rows, y.shape[-1])), _GATE_ACTS[act]
+
+
+def qdelta_block_norm_fwd(y, x=None, post=None, gate=None, scale=None, pre=None, act: str = "silu", eps: float = 1e-5, h=None,
+                          n=None, stats=None, want_stats: bool = True, stream=None):
+    """RMS norms after and before a block with its gate, scale and residual sum, over the last
+    dimension: f = rms(y) * post (y itself when post is None), h = x + scale * act(gate) * f, n =
+    rms(h) * pre of h as stored.  y, x, gate [..,C] (fp32 or bf16, same dtype), post, scale, pre [C]
+    fp32; all but y optional.  act: "silu", "sigmoid" or "linear" (the gate itself).  The gated RMS
+    norm of a layer's o [B,T,H,d] per head is ``qdelta_block_norm_fwd(o, post=weight, gate=z)``.
+    Returns (h, n, stats): n is None without pre; stats [rows,2] are the 1/rms of both norms, zero
+    for one that is not taken, which the backward needs (None when want_stats is False)."""
+    import torch
+    lib = load_library()
+    N, C, code_act = _block_norm_sizes(y, act)
+    context, handle = _enter(stream, y.device)
+    with context:
+        dt, dev, f32, code = y.dtype, y.device, torch.float32, _dtype_code(y.dtype)
+        _check_all(dev, [(y, "y", dt, None), (x, "x", dt, y.shape), (gate, "gate", dt, y.shape), (post, "post", f32, (C,)),
+                         (scale, "scale", f32, (C,)), (pre, "pre", f32, (C,))])
+        h = _result(h, "h", y, dev)
+        if pre is not None:
+            n = _result(n, "n", y, dev)
+        elif n is not None:
+            raise QDeltaError("n is only written with pre")
+        if want_stats or stats is not None:
+            stats = _result(stats, "stats", ((N, 2), f32), dev)
+        if stats is not None and not C:
+            stats.zero_()                              # no elements: no kernel writes them
+        rc = lib.qdelta_block_norm_fwd(_at(y), _at(x), _at(post), _at(gate), _at(scale), _at(pre), _at(h), _at(n), _at(stats),
+                                       N, C, float(eps), code_act, code, handle)
+        _raise(rc, "qdelta_block_norm_fwd")
+        return h, n, stats
+
+
+def qdelta_block_norm_bwd_workspace_bytes(N, C, want_sums, dtype) -> int:
+    return int(load_library().qdelta_block_norm_bwd_workspace_bytes(*_int_sizes((N, C)), int(want_sums), _dtype_code(dtype)))
+
+
+def qdelta_block_norm_bwd(y, h, post, gate, scale, pre, stats, dh, dn=None, act: str = "silu", want_dx: bool = True, out=None,
+                          workspace=None, stream=None):
+    """Gradients of sum(h * dh) + sum(n * dn) for qdelta_block_norm_fwd on the same inputs, whose h
+    (needed with dn) and stats (needed with dn or post) are given; either of dh and dn may be None.
+    Returns a dict with dx (None unless want_dx), dy, and, None where the input is None, dgate,
+    dpost, dscale, dpre.  ``out`` may supply any of them; ``workspace`` a device buffer of at least
+    qdelta_block_norm_bwd_workspace_bytes(...) bytes (allocated when None)."""
+    import torch
+    lib = load_library()
+    N, C, code_act = _block_norm_sizes(y, act)
+    context, handle = _enter(stream, y.device)
+    with context:
+        dt, dev, f32, code = y.dtype, y.device, torch.float32, _dtype_code(y.dtype)
+        _check_all(dev, [(y, "y", dt, None), (h, "h", dt, y.shape), (gate, "gate", dt, y.shape), (post, "post", f32, (C,)),
+                         (scale, "scale", f32, (C,)), (pre, "pre", f32, (C,)), (stats, "stats", f32, (N, 2)),
+                         (dh, "dh", dt, y.shape), (dn, "dn", dt, y.shape)])
+        out = _results(out, dict(dx=y if want_dx else None, dy=y, dgate=gate, dpost=post, dscale=scale, dpre=pre), dev)
+        sums = post is not None or scale is not None or pre is not None
+        p, n, workspace = _workspace(workspace, lib.qdelta_block_norm_bwd_workspace_bytes(N, C, int(sums), code), dev)
+        rc = lib.qdelta_block_norm_bwd(_at(y), _at(h), _at(post), _at(gate), _at(scale), _at(pre), _at(stats), _at(dh), _at(dn),
+                                       _at(out["dx"]), _at(out["dy"]), _at(out["dgate"]), _at(out["dpost"]),
+                                       _at(out["dscale"]), _at(out["dpre"]), N, C, code_act, code, p, n, handle)
+        _raise(rc, "qdelta_block_norm_bwd")
         return out

@@ -17,8 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqdelta.so")
-SOURCES = ["qd_capi.hip", "qd_capi_mixer.hip", "qd_chunk_bwd.hip", "qd_chunk_fwd.hip", "qd_chunk_fwd_pipe.hip",
-           "qd_conv.hip", "qd_eda.hip", "qd_norm.hip", "qd_segment.hip", "qd_ssm.hip", "qd_ssm_bwd.hip", "qd_qed.hip",
+SOURCES = ["qd_block_norm.hip", "qd_capi.hip", "qd_capi_layer.hip", "qd_capi_mixer.hip", "qd_chunk_bwd.hip",
+           "qd_chunk_fwd.hip", "qd_chunk_fwd_pipe.hip", "qd_conv.hip", "qd_eda.hip", "qd_linattn.hip",
+           "qd_linattn_bwd.hip", "qd_norm.hip", "qd_segment.hip", "qd_ssm.hip", "qd_ssm_bwd.hip", "qd_qed.hip",
            "qd_step.hip"]
 ARCH = os.environ.get("QDELTA_OFFLOAD_ARCH", "gfx950")
 

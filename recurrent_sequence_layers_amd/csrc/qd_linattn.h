@@ -1,0 +1,271 @@
+// Linear attention with a decay for each head: launch interface, and what its kernels share.
+//
+// Per (batch b, head h), state S in R^{d_v x d_k}, log decay g_t:
+//
+//     S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = S_t q_t
+//
+// Chunks of C tokens, G the inclusive prefix sums of g in the chunk, S the state before it:
+//
+//     O  = e^G (Q S^T) + P V,      P[s][t] = e^{G_s - G_t} (Q K^T)[s][t] for t <= s, else 0
+//     S' = e^{G_C} S + sum_t e^{G_C - G_t} v_t k_t^T
+//
+// The gradients have the same form with the roles changed (dq with the state as it is, dk and
+// dv backwards in time), so every kernel here is a walk over chunks that holds one or two
+// states in registers:
+//
+//   A wave owns 16 columns of the state, each for every contraction index ("rows"): for o the
+//   columns are value indices and the rows key indices.  Tile 2u + h of its accumulators holds
+//   in lane (g = l / 16, c = l % 16), element i, row 32 u + 8 g + 4 h + i and column c.  That is
+//   at once what the 16x16x32 products take as operand, with eight consecutive rows a lane, so
+//   the other operand is one 16-byte LDS read, and the state never leaves the registers.
+//   Outputs are formed transposed: a lane gets four consecutive columns of one token.
+//
+// Precision.  States, sums and statistics are fp32.  A bf16 product rounds P and the state it
+// reads to bf16 once each.  What enters a state (v_t e^{G_C - G_t}) is not rounded: it is split
+// into three bf16 addends (24 bits, all of an fp32), three products for one, since S_T, dS0 and
+// dg are fp32.  Prefix sums of g are taken in 64 bits and kept as the sum of two fp32 numbers:
+// e^{G_s - G_t} of near tokens behind strong decays would lose what the difference cancels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "qd_device.h"
+
+namespace qd {
+
+enum LinDecay { kNoDecay = 0, kTokenDecay = 1, kHeadDecay = 2 };
+
+struct LinArgs {
+    const void *q, *k, *v;           // [B][T][H][DK], [B][T][H][DK], [B][T][H][DV]
+    const float *g;                  // null, [B][T][H] or [H], by `decay`
+    const float *S0;                 // [B][H][DV][DK] or null
+    const int *lens;                 // [B] or null
+    void *o;                         // [B][T][H][DV]
+    float *S_T;                      // [B][H][DV][DK] or null
+    int B, T, H, DK, DV;
+    int decay;
+    // backward only
+    const void *d_o;                 // [B][T][H][DV]
+    const float *dS_T;               // [B][H][DV][DK] or null
+    void *dq, *dk, *dv;
+    float *dg;                       // like g, or null
+    float *dS0;                      // or null
+    // schedule, filled in by the launch: the time axis in `segs` segments of seg_chunks chunks
+    int segs, seg_chunks;
+    float *fwd, *rev;                // [B H][segs - 1][DV][DK]: states at the segments' borders
+    float *fac;                      // [2][B H][segs]: a segment's decay
+    float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
+    float *edge;                     // [B H][8]: <S_T, dS_T> by wave
+    float *head;                     // [B H]: sums of dg over tokens
+};
+
+bool lin_supported(int dtype, int dk, int dv);
+bool lin_fits(int B, int T, int H);
+size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv);
+hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
+hipError_t launch_lin_step(int dtype, const LinArgs &a, float *S, hipStream_t stream);   // T = 1
+size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg);
+hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
+hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, hipStream_t stream);
+hipError_t launch_lin_copy(float *to, const float *from, size_t n, hipStream_t stream);  // from null: zeros
+
+// Tokens of a chunk.  fp32 rows of 64 would not fit the LDS twice.
+template <class P>
+constexpr int kLinChunk = P::kBytes == 2 ? 64 : 32;
+inline int lin_chunk(int dtype) { return dtype == 1 ? 64 : 32; }
+
+constexpr double kLinLog2e = 1.4426950408889634;
+
+typedef __attribute__((ext_vector_type(4))) unsigned lin_u32x4;
+typedef __attribute__((ext_vector_type(2))) unsigned lin_u32x2;
+
+// raw buffer (stride 0): reads at offsets >= bytes give 0, writes there are dropped
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_rsrc(const void *base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ float lin_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+// e^x for a decay.  What the product with log2 e rounds away is put back to first order; below
+// -1000 (-inf too) the result is zero either way.
+__device__ __forceinline__ float lin_exp(float x) {
+    x = x < -1000.f ? -1000.f : x;
+    const float p = x * 1.44269504088896341f;
+    const float q = fmaf(x, 1.925963033500e-8f, fmaf(x, 1.44269504088896341f, -p));
+    return lin_exp2(p) * fmaf(q, 0.69314718055994531f, 1.f);
+}
+
+// ---------------------------------------------------------------- rows of a chunk
+// C rows of COLS elements between global memory (rows `stride` bytes apart) and LDS (rows
+// `pitch` elements apart) over NT threads, 16 bytes a piece.
+template <class P, int C, int COLS, int NT>
+struct LinRows {
+    static constexpr int kPer = COLS * P::kBytes / 16;   // pieces a row
+    static constexpr int N = C * kPer / NT;
+    static_assert(C * kPer % NT == 0 && N >= 1, "pieces must divide over the threads");
+    static constexpr int kPitch = COLS + 16 / P::kBytes;
+    static constexpr int kElems = C * kPitch;
+    lin_u32x4 r[N];
+
+    __device__ __forceinline__ void load(const void *base, int rows, int stride, int tid) {
+        const __amdgpu_buffer_rsrc_t rs = lin_rsrc(base, rows > 0 ? (rows - 1) * stride + COLS * P::kBytes : 0);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int p = tid + j * NT;
+            r[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (p / kPer) * stride + (p % kPer) * 16, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void put(typename P::R *lds, int tid) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int p = tid + j * NT;
+            *reinterpret_cast<lin_u32x4 *>(lds + (p / kPer) * kPitch + (p % kPer) * (16 / P::kBytes)) = r[j];
+        }
+    }
+};
+
+// ---------------------------------------------------------------- decays of a chunk
+template <int C>
+struct LinGates {
+    float before[C];                 // e^{G_t}: from the chunk's start to behind token t
+    float after[C];                  // e^{G_C - G_t}
+    float hi[C], lo[C];              // G in powers of two, as a sum
+    float all[4];                    // e^{G_C}
+};
+
+// log decay of lane's token, in powers of two, for the chunk at t0 with `live` tokens
+__device__ __forceinline__ float lin_gate(const LinArgs &a, int b, int h, int t0, int live, int lane) {
+    if (lane >= live || a.decay == kNoDecay) return 0.f;
+    return a.decay == kHeadDecay ? a.g[h] : a.g[(static_cast<size_t>(b) * a.T + t0 + lane) * a.H + h];
+}
+// One wave.  A decay of zero (g = -inf) forgets all that came before: 4096 powers of two make
+// every factor across it zero, and prefix sums stay finite.
+template <int C>
+__device__ __forceinline__ double lin_gates(LinGates<C> &t, float g, int lane) {
+    double x = static_cast<double>(g) * kLinLog2e;
+    x = x < -4096.0 ? -4096.0 : x;
+#pragma unroll
+    for (int d = 1; d < C; d *= 2) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    const double end = __shfl(x, C - 1);
+    if (lane < C) {
+        const float hi = static_cast<float>(x);
+        t.hi[lane] = hi;
+        t.lo[lane] = static_cast<float>(x - hi);
+        t.before[lane] = lin_exp2(hi);
+        t.after[lane] = lin_exp2(static_cast<float>(end - x));
+        if (lane == 0) t.all[0] = lin_exp2(static_cast<float>(end));
+    }
+    return end;
+}
+// e^{G_s - G_t}
+template <int C>
+__device__ __forceinline__ float lin_between(const LinGates<C> &t, float hs, float ls, int at) {
+    return lin_exp2((hs - t.hi[at]) + (ls - t.lo[at]));
+}
+
+// ---------------------------------------------------------------- operands
+// Four rows r0 + 8 (l / 16) + i, i = 0..3, of column col(l % 16): the operand of a product that
+// contracts over an LDS matrix's rows.  col(c) = c0 + step (c / 4) + c % 4.
+template <class P>
+__device__ __forceinline__ typename P::F lin_down(const typename P::R *m, int pitch, int r0, int c0, int step, int lane) {
+    const int g = lane >> 4, mm = lane & 15;
+    if constexpr (P::kBytes == 2) {
+        // LDS transpose read: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
+        // lane 4p + q receives element q of chunk p of the rows 0..3
+        const uint16_t *p = m + (r0 + 8 * g + (mm >> 2)) * pitch + c0 + step * (mm & 3);
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+    } else {
+        return P::ld4_strided(m + (r0 + 8 * g) * pitch + c0 + step * (mm >> 2) + (mm & 3), pitch);
+    }
+}
+
+// x as a sum of NS operands of the element type; fp32 takes one.
+template <class P, int NS>
+struct LinSplit {
+    static constexpr int N = P::kBytes == 2 ? NS : 1;
+    typename P::F p[N];
+    __device__ __forceinline__ void of(f32x4 x) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            p[j] = P::cvt(x);
+            if (j + 1 < N) x -= P::f32(p[j]);
+        }
+    }
+};
+
+// state += its chunk's part: S = all S + sum_t (row_t) (col_t weight_t), the rows from LDS and the
+// wave's columns in operand registers.
+template <class P, int C, int NS, int N16>
+__device__ __forceinline__ void lin_update(f32x4 (&S)[N16], const typename P::R *rows, int pitch,
+                                           const typename P::F (&col)[C / 32][2], const float *weight, float all, int lane) {
+    const int g4 = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < N16; ++b) S[b] *= all;
+#pragma unroll
+    for (int u = 0; u < C / 32; ++u) {
+        LinSplit<P, NS> lo, hi;
+        lo.of(P::f32(col[u][0]) * lds_f32x4(weight + 32 * u + 8 * g4));
+        hi.of(P::f32(col[u][1]) * lds_f32x4(weight + 32 * u + 8 * g4 + 4));
+#pragma unroll
+        for (int b = 0; b < N16; ++b) {
+            const typename P::F r0 = lin_down<P>(rows, pitch, 32 * u, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
+            const typename P::F r1 = lin_down<P>(rows, pitch, 32 * u + 4, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
+#pragma unroll
+            for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[b] = P::mma2(S[b], r0, r1, lo.p[j], hi.p[j]);
+        }
+    }
+}
+
+// A 16-token tile's product with the state (NS addends of it): four columns of one token a lane.
+template <class P, int NS, int N16>
+__device__ __forceinline__ f32x4 lin_read(const LinSplit<P, NS> (&sf)[N16], const typename P::R *rows, int pitch, int r0, int lane) {
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int u = 0; u < N16 / 2; ++u) {
+        typename P::F x0, x1;
+        frag_oct<P>(rows, pitch, r0, 32 * u, x0, x1, lane);
+#pragma unroll
+        for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j) acc = P::mma2(acc, sf[2 * u].p[j], sf[2 * u + 1].p[j], x0, x1);
+    }
+    return acc;
+}
+
+// A 16 x 16 block of products of LDS rows: lane l gets rows r0 + 4 (l / 16) + i with row c0 + l % 16.
+template <class P, int D>
+__device__ __forceinline__ f32x4 lin_block(const typename P::R *rows, const typename P::R *cols, int pitch, int r0, int c0, int lane) {
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        typename P::F x0, x1, y0, y1;
+        frag_oct<P>(rows, pitch, r0, 32 * u, x0, x1, lane);
+        frag_oct<P>(cols, pitch, c0, 32 * u, y0, y1, lane);
+        acc = P::mma2(acc, x0, x1, y0, y1);
+    }
+    return acc;
+}
+
+// Lower block triangle, row by row: p -> (i, j), j <= i
+__device__ __forceinline__ void lin_pair(int p, int &i, int &j) {
+    i = 0;
+    while ((i + 1) * (i + 2) / 2 <= p) ++i;
+    j = p - i * (i + 1) / 2;
+}
+
+// Four consecutive elements to a buffer (dropped past its end)
+template <class P>
+__device__ __forceinline__ void lin_store4(__amdgpu_buffer_rsrc_t rs, int off, f32x4 v) {
+    if constexpr (P::kBytes == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(lin_u32x2, P::cvt(v)), rs, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(lin_u32x4, v), rs, off, 0, 0);
+}
+
+// Tokens of sequence b
+__device__ __forceinline__ int lin_len(const LinArgs &a, int b) { return a.lens ? min(max(a.lens[b], 0), a.T) : a.T; }
+
+}  // namespace qd
