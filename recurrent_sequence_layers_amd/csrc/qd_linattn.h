@@ -97,15 +97,60 @@ __device__ __forceinline__ float lin_exp(float x) {
 }
 
 // ---------------------------------------------------------------- rows of a chunk
-// C rows of COLS elements between global memory (rows `stride` bytes apart) and LDS (rows
-// `pitch` elements apart) over NT threads, 16 bytes a piece.
+// A matrix of ROWS x COLS elements in LDS, and the two ways it is read:
+//   oct:  row r0 + l % 16, eight columns 32 u + 8 (l / 16) + 0..7 (contraction over columns)
+//   down: rows r0 + 8 (l / 16) + i, i = 0..3, of column c0 + step (c / 4) + c % 4, c = l % 16
+//         (contraction over rows); step 4 or 8
+//
+// bf16: a 16 x 32 block is 64 slots of 16 bytes; columns 8 g .. 8 g + 7 of row r sit in slot
+// 16 g + (r ^ swz(g)).  Sixteen lanes that read one g take 256 contiguous bytes; a transposing read
+// finds its four rows in four quarters.  Blocks are 1040 bytes apart, so the sixteen pieces of a
+// row, written together, meet sixteen different slots.  Each is free of bank conflicts.
+// fp32: rows padded by 16 bytes.
+template <class P, int ROWS, int COLS>
+struct LinTile {
+    using R = typename P::R;
+    using F = typename P::F;
+    static constexpr bool kSwz = P::kBytes == 2;
+    static constexpr int kBlock = 520, kPitch = COLS + 4;
+    static constexpr int kElems = kSwz ? (ROWS / 16) * (COLS / 32) * kBlock : ROWS * kPitch;
+    R m[kElems];
+
+    __device__ __forceinline__ static int slot(int row, int g) { return 8 * (16 * g + ((row & 15) ^ ((12 * g) & 15))); }
+    // 16-byte piece `c` of a row
+    __device__ __forceinline__ R *piece(int row, int c) {
+        if constexpr (kSwz) return m + ((row >> 4) * (COLS / 32) + (c >> 2)) * kBlock + slot(row, c & 3);
+        else return m + row * kPitch + 4 * c;
+    }
+    // four elements of a row, at a column that four divides
+    __device__ __forceinline__ R *four(int row, int col) {
+        if constexpr (kSwz) return piece(row, col >> 3) + (col & 4);
+        else return m + row * kPitch + col;
+    }
+    __device__ __forceinline__ void oct(int r0, int u, int lane, F &lo, F &hi) {
+        if constexpr (kSwz) P::ld8(piece(r0 + (lane & 15), 4 * u + (lane >> 4)), lo, hi);
+        else P::ld8(m + (r0 + (lane & 15)) * kPitch + 32 * u + 8 * (lane >> 4), lo, hi);
+    }
+    __device__ __forceinline__ F down(int r0, int c0, int step, int lane) {
+        const int g = lane >> 4, mm = lane & 15;
+        if constexpr (kSwz) {
+            // LDS transpose read: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
+            // lane 4p + q receives element q of chunk p of the rows 0..3
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                  (lds_s16x4 *)(four(r0 + 8 * g + (mm >> 2), c0 + step * (mm & 3)))));
+        } else {
+            return P::ld4_strided(m + (r0 + 8 * g) * kPitch + c0 + step * (mm >> 2) + (mm & 3), kPitch);
+        }
+    }
+};
+
+// C rows of COLS elements (rows `stride` bytes apart) on their way to a tile, over NT threads
 template <class P, int C, int COLS, int NT>
 struct LinRows {
-    static constexpr int kPer = COLS * P::kBytes / 16;   // pieces a row
+    static constexpr int kPer = COLS * P::kBytes / 16;   // 16-byte pieces a row
     static constexpr int N = C * kPer / NT;
     static_assert(C * kPer % NT == 0 && N >= 1, "pieces must divide over the threads");
-    static constexpr int kPitch = COLS + 16 / P::kBytes;
-    static constexpr int kElems = C * kPitch;
     lin_u32x4 r[N];
 
     __device__ __forceinline__ void load(const void *base, int rows, int stride, int tid) {
@@ -116,11 +161,11 @@ struct LinRows {
             r[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (p / kPer) * stride + (p % kPer) * 16, 0, 0);
         }
     }
-    __device__ __forceinline__ void put(typename P::R *lds, int tid) const {
+    __device__ __forceinline__ void put(LinTile<P, C, COLS> &to, int tid) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int p = tid + j * NT;
-            *reinterpret_cast<lin_u32x4 *>(lds + (p / kPer) * kPitch + (p % kPer) * (16 / P::kBytes)) = r[j];
+            *reinterpret_cast<lin_u32x4 *>(to.piece(p / kPer, p % kPer)) = r[j];
         }
     }
 };
@@ -168,22 +213,6 @@ __device__ __forceinline__ float lin_between(const LinGates<C> &t, float hs, flo
 }
 
 // ---------------------------------------------------------------- operands
-// Four rows r0 + 8 (l / 16) + i, i = 0..3, of column col(l % 16): the operand of a product that
-// contracts over an LDS matrix's rows.  col(c) = c0 + step (c / 4) + c % 4.
-template <class P>
-__device__ __forceinline__ typename P::F lin_down(const typename P::R *m, int pitch, int r0, int c0, int step, int lane) {
-    const int g = lane >> 4, mm = lane & 15;
-    if constexpr (P::kBytes == 2) {
-        // LDS transpose read: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
-        // lane 4p + q receives element q of chunk p of the rows 0..3
-        const uint16_t *p = m + (r0 + 8 * g + (mm >> 2)) * pitch + c0 + step * (mm & 3);
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
-    } else {
-        return P::ld4_strided(m + (r0 + 8 * g) * pitch + c0 + step * (mm >> 2) + (mm & 3), pitch);
-    }
-}
-
 // x as a sum of NS operands of the element type; fp32 takes one.
 template <class P, int NS>
 struct LinSplit {
@@ -200,21 +229,21 @@ struct LinSplit {
 
 // state += its chunk's part: S = all S + sum_t (row_t) (col_t weight_t), the rows from LDS and the
 // wave's columns in operand registers.
-template <class P, int C, int NS, int N16>
-__device__ __forceinline__ void lin_update(f32x4 (&S)[N16], const typename P::R *rows, int pitch,
-                                           const typename P::F (&col)[C / 32][2], const float *weight, float all, int lane) {
+template <class P, int C, int NS, int D>
+__device__ __forceinline__ void lin_update(f32x4 (&S)[D / 16], LinTile<P, C, D> &rows, const typename P::F (&col)[C / 32][2],
+                                           const float *weight, float all, int lane) {
     const int g4 = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < N16; ++b) S[b] *= all;
+    for (int b = 0; b < D / 16; ++b) S[b] *= all;
 #pragma unroll
     for (int u = 0; u < C / 32; ++u) {
         LinSplit<P, NS> lo, hi;
         lo.of(P::f32(col[u][0]) * lds_f32x4(weight + 32 * u + 8 * g4));
         hi.of(P::f32(col[u][1]) * lds_f32x4(weight + 32 * u + 8 * g4 + 4));
 #pragma unroll
-        for (int b = 0; b < N16; ++b) {
-            const typename P::F r0 = lin_down<P>(rows, pitch, 32 * u, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
-            const typename P::F r1 = lin_down<P>(rows, pitch, 32 * u + 4, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
+        for (int b = 0; b < D / 16; ++b) {
+            const typename P::F r0 = rows.down(32 * u, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
+            const typename P::F r1 = rows.down(32 * u + 4, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
 #pragma unroll
             for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[b] = P::mma2(S[b], r0, r1, lo.p[j], hi.p[j]);
         }
@@ -222,13 +251,13 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[N16], const typename P::R 
 }
 
 // A 16-token tile's product with the state (NS addends of it): four columns of one token a lane.
-template <class P, int NS, int N16>
-__device__ __forceinline__ f32x4 lin_read(const LinSplit<P, NS> (&sf)[N16], const typename P::R *rows, int pitch, int r0, int lane) {
+template <class P, int NS, int C, int D>
+__device__ __forceinline__ f32x4 lin_read(const LinSplit<P, NS> (&sf)[D / 16], LinTile<P, C, D> &rows, int r0, int lane) {
     f32x4 acc = zero4();
 #pragma unroll
-    for (int u = 0; u < N16 / 2; ++u) {
+    for (int u = 0; u < D / 32; ++u) {
         typename P::F x0, x1;
-        frag_oct<P>(rows, pitch, r0, 32 * u, x0, x1, lane);
+        rows.oct(r0, u, lane, x0, x1);
 #pragma unroll
         for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j) acc = P::mma2(acc, sf[2 * u].p[j], sf[2 * u + 1].p[j], x0, x1);
     }
@@ -236,14 +265,14 @@ __device__ __forceinline__ f32x4 lin_read(const LinSplit<P, NS> (&sf)[N16], cons
 }
 
 // A 16 x 16 block of products of LDS rows: lane l gets rows r0 + 4 (l / 16) + i with row c0 + l % 16.
-template <class P, int D>
-__device__ __forceinline__ f32x4 lin_block(const typename P::R *rows, const typename P::R *cols, int pitch, int r0, int c0, int lane) {
+template <class P, int C, int D>
+__device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C, D> &cols, int r0, int c0, int lane) {
     f32x4 acc = zero4();
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
         typename P::F x0, x1, y0, y1;
-        frag_oct<P>(rows, pitch, r0, 32 * u, x0, x1, lane);
-        frag_oct<P>(cols, pitch, c0, 32 * u, y0, y1, lane);
+        rows.oct(r0, u, lane, x0, x1);
+        cols.oct(c0, u, lane, y0, y1);
         acc = P::mma2(acc, x0, x1, y0, y1);
     }
     return acc;

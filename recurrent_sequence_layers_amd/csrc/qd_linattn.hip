@@ -23,18 +23,36 @@ __device__ __forceinline__ bool lin_place(int units, int ncb, int &unit, int &cb
 }
 dim3 lin_grid(long long units, int ncb) { return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * ncb)); }
 
+// The state's tiles from and to [DV][DK]: wave's column, four rows at a time
+template <int DK>
+__device__ __forceinline__ void load_state(f32x4 (&S)[DK / 16], const float *from, int col, int g4) {
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1))
+                    : zero4();
+}
+template <int DK>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float *to, int col, int g4) {
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+        *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) = S[t];
+}
+
+// Eight waves in two roles, a barrier a step.  At step n waves 0-3 hold the state and do chunk n's
+// part with it: the outputs, then the state's update.  Waves 4-7 are ahead of them: they form P of
+// chunk n + 1 and bring chunk n + 2 from the registers, where the loads of the step before put it,
+// to LDS.
 template <class P, int DK>
 struct FwdLds {
     static constexpr int C = kLinChunk<P>;
-    using QK = LinRows<P, C, DK, kNT>;
-    using VV = LinRows<P, C, 64, kNT>;
-    static constexpr int kPitchP = C + 16 / P::kBytes;
-    typename P::R q[QK::kElems], k[QK::kElems], v[VV::kElems], p[C * kPitchP];
-    LinGates<C> gates;
+    LinTile<P, C, DK> q[3], k[3];
+    LinTile<P, C, 64> v[3];
+    LinTile<P, C, C> p[2];
+    LinGates<C> gates[3];
 };
 
 template <class P, int DK>
-__global__ __launch_bounds__(kNT) void lin_fwd_kernel(const LinArgs a) {
+__global__ __launch_bounds__(2 * kNT) void lin_fwd_kernel(const LinArgs a) {
     using L = FwdLds<P, DK>;
     constexpr int C = L::C, NB = (C / 16) * (C / 16 + 1) / 2;
     extern __shared__ __align__(16) char smem[];
@@ -43,64 +61,81 @@ __global__ __launch_bounds__(kNT) void lin_fwd_kernel(const LinArgs a) {
     int unit, cb;
     if (!lin_place(a.B * a.H * a.segs, ncb, unit, cb)) return;
     const int seg = unit % a.segs, bh = unit / a.segs, b = bh / a.H, h = bh % a.H;
-    const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x & (kNT - 1), wave = wave_id() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, (a.T + C - 1) / C);
-    const int col = 64 * cb + 16 * wave;
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
     const size_t tok0 = static_cast<size_t>(b) * a.T;
-    const char *gq = static_cast<const char *>(a.q) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
-    const char *gk = static_cast<const char *>(a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
-    const char *gv = static_cast<const char *>(a.v) + tok0 * sdv + (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
-    char *go = static_cast<char *>(a.o) + tok0 * sdv + (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
-    const size_t state = static_cast<size_t>(a.DV) * DK;
+    const size_t vcol = (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
 
-    f32x4 S[DK / 16];
-    const float *from = seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state
-                                : a.S0 ? a.S0 + bh * state : nullptr;
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col + r16) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1))
-                    : zero4();
     // blocks above the diagonal that a pair of tiles reads: never written again
-    for (int e = tid; e < C * L::kPitchP; e += kNT) lds.p[e] = 0;
+    for (int e = threadIdx.x; e < LinTile<P, C, C>::kElems; e += 2 * kNT) lds.p[0].m[e] = lds.p[1].m[e] = 0;
+    __syncthreads();
 
-    typename L::QK rq, rk;
-    typename L::VV rv;
-    float gate = 0.f;
-    auto fetch = [&](int n) {
-        const int t0 = n * C, live = min(max(len - t0, 0), C);
-        rq.load(gq + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
-        rk.load(gk + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
-        rv.load(gv + static_cast<size_t>(t0) * sdv, live, static_cast<int>(sdv), tid);
-        if (wave == 0) gate = lin_gate(a, b, h, t0, live, lane);
-    };
-    fetch(c0);
+    if (threadIdx.x >= kNT) {
+        const char *gq = static_cast<const char *>(a.q) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
+        const char *gk = static_cast<const char *>(a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
+        const char *gv = static_cast<const char *>(a.v) + tok0 * sdv + vcol;
+        LinRows<P, C, DK, kNT> rq, rk;
+        LinRows<P, C, 64, kNT> rv;
+        float gate = 0.f;
+        auto fetch = [&](int n) {
+            const int t0 = n * C, live = min(max(len - t0, 0), C);
+            rq.load(gq + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
+            rk.load(gk + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
+            rv.load(gv + static_cast<size_t>(t0) * sdv, live, static_cast<int>(sdv), tid);
+            if (wave == 3) gate = lin_gate(a, b, h, t0, live, lane);
+        };
+        fetch(c0);
+        int put = 0, now = 2;                    // slots of chunks n + 2 and n + 1
+        for (int n = c0 - 2; n < c1; ++n) {
+            if (n + 2 < c1) {
+                rq.put(lds.q[put], tid);
+                rk.put(lds.k[put], tid);
+                rv.put(lds.v[put], tid);
+                if (wave == 3) lin_gates(lds.gates[put], gate, lane);
+                if (n + 3 < c1) fetch(n + 3);
+            }
+            if (n + 1 >= c0 && n + 1 < c1) {
+                const LinGates<C> &gates = lds.gates[now];
+                for (int p = wave; p < NB; p += 4) {
+                    int i, j;
+                    lin_pair(p, i, j);
+                    f32x4 acc = lin_block<P>(lds.k[now], lds.q[now], 16 * j, 16 * i, lane);
+                    const int s = 16 * i + r16, t = 16 * j + 4 * g4;
+                    const float hs = gates.hi[s], ls = gates.lo[s];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? lin_between(gates, hs, ls, t + e) * acc[e] : 0.f;
+                    P::st4(lds.p[(n + 1 - c0) & 1].four(s, t), acc);
+                }
+            }
+            now = put;
+            put = put == 2 ? 0 : put + 1;
+            __syncthreads();
+        }
+        return;
+    }
+
+    const size_t state = static_cast<size_t>(a.DV) * DK;
+    const int col = 64 * cb + 16 * wave + r16;
+    f32x4 S[DK / 16];
+    load_state<DK>(S, seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
+                   col, g4);
+    char *go = static_cast<char *>(a.o) + tok0 * sdv + vcol;
+    __syncthreads();
+    __syncthreads();
+    int now = 0;
     for (int n = c0; n < c1; ++n) {
         const int t0 = n * C, live = min(max(len - t0, 0), C);
-        __syncthreads();
-        rq.put(lds.q, tid);
-        rk.put(lds.k, tid);
-        rv.put(lds.v, tid);
-        if (wave == 0) lin_gates(lds.gates, gate, lane);
-        __syncthreads();
-        if (n + 1 < c1) fetch(n + 1);
-        for (int p = wave; p < NB; p += 4) {
-            int i, j;
-            lin_pair(p, i, j);
-            f32x4 acc = lin_block<P, DK>(lds.k, lds.q, L::QK::kPitch, 16 * j, 16 * i, lane);
-            const int s = 16 * i + r16, t = 16 * j + 4 * g4;
-            const float hs = lds.gates.hi[s], ls = lds.gates.lo[s];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? lin_between(lds.gates, hs, ls, t + e) * acc[e] : 0.f;
-            P::st4(lds.p + s * L::kPitchP + t, acc);
-        }
-        __syncthreads();
+        LinTile<P, C, DK> &q = lds.q[now], &k = lds.k[now];
+        LinTile<P, C, C> &p = lds.p[(n - c0) & 1];
+        const LinGates<C> &gates = lds.gates[now];
         typename P::F vf[C / 32][2];
 #pragma unroll
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lin_down<P>(lds.v, L::VV::kPitch, 32 * u + 4 * e, 16 * wave, 4, lane);
+            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[now].down(32 * u + 4 * e, 16 * wave, 4, lane);
+        // rows past the buffer's end, that of the last token's row, are dropped by their offset
         const __amdgpu_buffer_rsrc_t ro = lin_rsrc(go + static_cast<size_t>(t0) * sdv,
                                                    live > 0 ? (live - 1) * static_cast<int>(sdv) + 64 * P::kBytes : 0);
         LinSplit<P, 1> sf[DK / 16];
@@ -108,37 +143,32 @@ __global__ __launch_bounds__(kNT) void lin_fwd_kernel(const LinArgs a) {
         for (int t = 0; t < DK / 16; ++t) sf[t].of(S[t]);
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) {
-            f32x4 acc = lin_read<P>(sf, lds.q, L::QK::kPitch, 16 * i, lane);
-            acc *= lds.gates.before[16 * i + r16];
+            f32x4 acc = lin_read<P>(sf, q, 16 * i, lane);
+            acc *= gates.before[16 * i + r16];
 #pragma unroll
             for (int u = 0; u <= i / 2; ++u) {
                 typename P::F p0, p1;
-                frag_oct<P>(lds.p, L::kPitchP, 16 * i, 32 * u, p0, p1, lane);
+                p.oct(16 * i, u, lane, p0, p1);
                 acc = P::mma2(acc, vf[u][0], vf[u][1], p0, p1);
             }
-            const int row = 16 * i + r16;
-            // the end of a buffer is that of its last row: rows past it are dropped by their offset
-            lin_store4<P>(ro, row * static_cast<int>(sdv) + (16 * wave + 4 * g4) * P::kBytes, acc);
+            lin_store4<P>(ro, (16 * i + r16) * static_cast<int>(sdv) + (16 * wave + 4 * g4) * P::kBytes, acc);
         }
-        lin_update<P, C, 3>(S, lds.k, L::QK::kPitch, vf, lds.gates.after, lds.gates.all[0], lane);
+        lin_update<P, C, 3, DK>(S, k, vf, gates.after, gates.all[0], lane);
+        now = now == 2 ? 0 : now + 1;
+        __syncthreads();
     }
-    if (a.S_T && seg == a.segs - 1) {
-        float *to = a.S_T + bh * state;
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
-            *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col + r16) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) = S[t];
-    }
+    if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, g4);
 }
 
 // The states alone, from zero (or S0, dS_T) over one segment: forwards with k, v and the decay to
-// the segment's end, backwards with q, do and the decay from its start.
+// the segment's end, backwards with q, do and the decay from its start.  Four waves; the next
+// chunk goes to LDS while this one is used.
 template <class P, int DK>
 struct StateLds {
     static constexpr int C = kLinChunk<P>;
-    using QK = LinRows<P, C, DK, kNT>;
-    using VV = LinRows<P, C, 64, kNT>;
-    typename P::R k[QK::kElems], v[VV::kElems];
-    LinGates<C> gates;
+    LinTile<P, C, DK> k[2];
+    LinTile<P, C, 64> v[2];
+    LinGates<C> gates[2];
 };
 template <class P, int DK>
 __global__ __launch_bounds__(kNT) void lin_state_kernel(const LinArgs a, const int first_rev) {
@@ -153,52 +183,53 @@ __global__ __launch_bounds__(kNT) void lin_state_kernel(const LinArgs a, const i
     const int slot = unit % nseg, bh = unit / nseg, b = bh / a.H, h = bh % a.H, seg = rev ? slot + 1 : slot;
     const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
     const int len = lin_len(a, b);
-    const int nc = (a.T + C - 1) / C, c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nc);
-    const int col = 64 * cb + 16 * wave;
+    const int c0 = seg * a.seg_chunks, count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
     const size_t tok0 = static_cast<size_t>(b) * a.T;
     const char *gk = static_cast<const char *>(rev ? a.q : a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
     const char *gv = static_cast<const char *>(rev ? a.d_o : a.v) + tok0 * sdv + (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
     const size_t state = static_cast<size_t>(a.DV) * DK;
+    const int col = 64 * cb + 16 * wave + r16;
 
     f32x4 S[DK / 16];
-    const float *from = rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
-                            : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr);
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col + r16) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1))
-                    : zero4();
-    typename L::QK rk;
-    typename L::VV rv;
+    load_state<DK>(S, rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
+                          : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr), col, g4);
+    LinRows<P, C, DK, kNT> rk;
+    LinRows<P, C, 64, kNT> rv;
     float gate = 0.f;
-    auto fetch = [&](int n) {
-        const int t0 = n * C, live = min(max(len - t0, 0), C);
+    double total = 0;
+    auto fetch = [&](int m) {
+        const int t0 = (rev ? c0 + count - 1 - m : c0 + m) * C, live = min(max(len - t0, 0), C);
         rk.load(gk + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
         rv.load(gv + static_cast<size_t>(t0) * sdv, live, static_cast<int>(sdv), tid);
-        if (wave == 0) gate = lin_gate(a, b, h, t0, live, lane);
+        if (wave == 3) gate = lin_gate(a, b, h, t0, live, lane);
     };
-    double total = 0;
-    fetch(rev ? c1 - 1 : c0);
-    for (int m = c0; m < c1; ++m) {
-        const int n = rev ? c1 - 1 - (m - c0) : m;
-        __syncthreads();
-        rk.put(lds.k, tid);
-        rv.put(lds.v, tid);
-        if (wave == 0) total += lin_gates(lds.gates, gate, lane);
-        __syncthreads();
-        if (m + 1 < c1) fetch(rev ? n - 1 : n + 1);
+    auto put = [&](int m) {
+        rk.put(lds.k[m & 1], tid);
+        rv.put(lds.v[m & 1], tid);
+        if (wave == 3) total += lin_gates(lds.gates[m & 1], gate, lane);
+    };
+    fetch(0);
+    put(0);
+    if (count > 1) fetch(1);
+    __syncthreads();
+    for (int m = 0; m < count; ++m) {
+        if (m + 1 < count) {
+            put(m + 1);
+            if (m + 2 < count) fetch(m + 2);
+        }
+        const LinGates<C> &gates = lds.gates[m & 1];
         typename P::F vf[C / 32][2];
 #pragma unroll
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lin_down<P>(lds.v, L::VV::kPitch, 32 * u + 4 * e, 16 * wave, 4, lane);
-        lin_update<P, C, 3>(S, lds.k, L::QK::kPitch, vf, rev ? lds.gates.before : lds.gates.after, lds.gates.all[0], lane);
+            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[m & 1].down(32 * u + 4 * e, 16 * wave, 4, lane);
+        lin_update<P, C, 3, DK>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
+        __syncthreads();
     }
-    float *to = (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state;
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-        *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col + r16) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) = S[t];
-    if (cb == 0 && tid == 0) a.fac[(static_cast<size_t>(rev) * bhs + bh) * a.segs + seg] = lin_exp2(static_cast<float>(total));
+    store_state<DK>(S, (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, g4);
+    if (cb == 0 && wave == 3 && lane == 0)
+        a.fac[(static_cast<size_t>(rev) * bhs + bh) * a.segs + seg] = lin_exp2(static_cast<float>(total));
 }
 
 // Local states to states at the borders: forwards slot j becomes the state behind segment j,
@@ -283,7 +314,7 @@ __global__ __launch_bounds__(kNT) void lin_copy_kernel(f32x4 *to, const f32x4 *f
 
 template <class K>
 hipError_t lin_launch(K kernel, dim3 grid, size_t lds, hipStream_t stream, const LinArgs &a) {
-    hipLaunchKernelGGL(kernel, grid, dim3(kNT), static_cast<unsigned>(lds), stream, a);
+    hipLaunchKernelGGL(kernel, grid, dim3(2 * kNT), static_cast<unsigned>(lds), stream, a);
     return hipGetLastError();
 }
 

@@ -37,9 +37,9 @@ struct BwdLds {
     static constexpr int NB = (C / 16) * (C / 16 + 1) / 2;
     using QK = LinRows<P, C, DK, NT>;
     using VV = LinRows<P, C, DV, NT>;
-    static constexpr int kPitchP = C + 16 / P::kBytes;
-    typename P::R q[QK::kElems], k[QK::kElems], v[VV::kElems], o[VV::kElems];
-    typename P::R p[2][C * kPitchP];
+    LinTile<P, C, DK> q, k;
+    LinTile<P, C, DV> v, o;
+    LinTile<P, C, C> p[2];
     LinGates<C> gates;
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
     float part[NW][C];                 // a or b, by the columns' wave
@@ -108,9 +108,9 @@ struct Walk {
 };
 
 // a or b of one row: the product of the state's part with the row's own q or k, summed over columns
-template <class P, int C>
-__device__ __forceinline__ void row_part(float *part, const typename P::R *rows, int pitch, int row, int col, f32x4 acc, int lane) {
-    const f32x4 y = P::f32(P::ld4(rows + row * pitch + col));
+template <class P, int C, int D>
+__device__ __forceinline__ void row_part(float *part, LinTile<P, C, D> &rows, int row, int col, f32x4 acc, int lane) {
+    const f32x4 y = P::f32(P::ld4(rows.four(row, col)));
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) s = fmaf(acc[e], y[e], s);
@@ -143,7 +143,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[t][e] = from && mine ? from[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col] : 0.f;
-    for (int e = w.tid; e < C * L::kPitchP; e += L::NT) lds.p[0][e] = 0;
+    for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = 0;
     w.fetch(w.c0);
     for (int n = w.c0; n < w.c1; ++n) {
         __syncthreads();
@@ -154,14 +154,14 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         for (int p = wave; p < NB; p += NW) {
             int i, j;
             lin_pair(p, i, j);
-            f32x4 acc = lin_block<P, DV>(lds.v, lds.o, L::VV::kPitch, 16 * j, 16 * i, lane);
+            f32x4 acc = lin_block<P>(lds.v, lds.o, 16 * j, 16 * i, lane);
             const int s = 16 * i + r16, t = 16 * j + 4 * g4;
             const float hs = lds.gates.hi[s], ls = lds.gates.lo[s];
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? lin_between(lds.gates, hs, ls, t + e) * acc[e] : 0.f;
-            P::st4(lds.p[0] + s * L::kPitchP + t, acc);
+            P::st4(lds.p[0].four(s, t), acc);
             if constexpr (DG) {
-                const f32x4 qk = lin_block<P, DK>(lds.k, lds.q, L::QK::kPitch, 16 * j, 16 * i, lane);
+                const f32x4 qk = lin_block<P>(lds.k, lds.q, 16 * j, 16 * i, lane);
                 float row = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -181,7 +181,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) kf[u][e] = lin_down<P>(lds.k, L::QK::kPitch, 32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) kf[u][e] = lds.k.down(32 * u + 4 * e, 16 * wave, 4, lane);
             LinSplit<P, DG ? 3 : 1> sf[DV / 16];
 #pragma unroll
             for (int t = 0; t < DV / 16; ++t) sf[t].of(S[t]);
@@ -189,18 +189,18 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
             for (int i = 0; i < C / 16; ++i) {
                 const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.o, L::VV::kPitch, 16 * i, lane);
+                f32x4 acc = lin_read<P>(sf, lds.o, 16 * i, lane);
                 acc *= lds.gates.before[row];
-                if constexpr (DG) row_part<P, C>(lds.part[wave], lds.q, L::QK::kPitch, row, 16 * wave + 4 * g4, acc, lane);
+                if constexpr (DG) row_part<P>(lds.part[wave], lds.q, row, 16 * wave + 4 * g4, acc, lane);
 #pragma unroll
                 for (int u = 0; u <= i / 2; ++u) {
                     typename P::F p0, p1;
-                    frag_oct<P>(lds.p[0], L::kPitchP, 16 * i, 32 * u, p0, p1, lane);
+                    lds.p[0].oct(16 * i, u, lane, p0, p1);
                     acc = P::mma2(acc, kf[u][0], kf[u][1], p0, p1);
                 }
                 lin_store4<P>(rs, row * static_cast<int>(w.sdk) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
             }
-            lin_update<P, C, 3>(S, lds.v, L::VV::kPitch, kf, lds.gates.after, lds.gates.all[0], lane);
+            lin_update<P, C, 3, DV>(S, lds.v, kf, lds.gates.after, lds.gates.all[0], lane);
         }
         if constexpr (DG) {
             __syncthreads();
@@ -253,7 +253,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             Rk[t][e] = from && mine_k ? from[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col] : 0.f;
-    for (int e = w.tid; e < 2 * C * L::kPitchP; e += L::NT) lds.p[0][e] = 0;
+    for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = lds.p[1].m[e] = 0;
     w.fetch(w.c1 - 1);
     for (int n = w.c1 - 1; n >= w.c0; --n) {
         __syncthreads();
@@ -266,8 +266,8 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
             int i, j;
             lin_pair(p, i, j);                        // s in block i, t in block j
             const int t = 16 * j + r16, s = 16 * i + 4 * g4;
-            f32x4 qk = lin_block<P, DK>(lds.q, lds.k, L::QK::kPitch, 16 * i, 16 * j, lane);
-            f32x4 ov = lin_block<P, DV>(lds.o, lds.v, L::VV::kPitch, 16 * i, 16 * j, lane);
+            f32x4 qk = lin_block<P>(lds.q, lds.k, 16 * i, 16 * j, lane);
+            f32x4 ov = lin_block<P>(lds.o, lds.v, 16 * i, 16 * j, lane);
             const float ht = -lds.gates.hi[t], lt = -lds.gates.lo[t];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -275,8 +275,8 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
                 qk[e] = t <= s + e ? d * qk[e] : 0.f;
                 ov[e] = t <= s + e ? d * ov[e] : 0.f;
             }
-            P::st4(lds.p[0] + t * L::kPitchP + s, qk);
-            P::st4(lds.p[1] + t * L::kPitchP + s, ov);
+            P::st4(lds.p[0].four(t, s), qk);
+            P::st4(lds.p[1].four(t, s), ov);
         }
         __syncthreads();
         if (mine_v) {
@@ -284,7 +284,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) of[u][e] = lin_down<P>(lds.o, L::VV::kPitch, 32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) of[u][e] = lds.o.down(32 * u + 4 * e, 16 * wave, 4, lane);
             LinSplit<P, 1> sf[KC];
 #pragma unroll
             for (int t = 0; t < KC; ++t) sf[t].of(Rv[t]);
@@ -292,24 +292,24 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
             for (int i = 0; i < C / 16; ++i) {
                 const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.k, L::QK::kPitch, 16 * i, lane);
+                f32x4 acc = lin_read<P>(sf, lds.k, 16 * i, lane);
                 acc *= lds.gates.after[row];
 #pragma unroll
                 for (int u = i / 2; u < C / 32; ++u) {
                     typename P::F p0, p1;
-                    frag_oct<P>(lds.p[0], L::kPitchP, 16 * i, 32 * u, p0, p1, lane);
+                    lds.p[0].oct(16 * i, u, lane, p0, p1);
                     acc = P::mma2(acc, of[u][0], of[u][1], p0, p1);
                 }
                 lin_store4<P>(rs, row * static_cast<int>(w.sdv) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
             }
-            lin_update<P, C, 2>(Rv, lds.q, L::QK::kPitch, of, lds.gates.before, lds.gates.all[0], lane);
+            lin_update<P, C, 2, DK>(Rv, lds.q, of, lds.gates.before, lds.gates.all[0], lane);
         }
         if (mine_k) {
             typename P::F qf[C / 32][2];
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) qf[u][e] = lin_down<P>(lds.q, L::QK::kPitch, 32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) qf[u][e] = lds.q.down(32 * u + 4 * e, 16 * wave, 4, lane);
             LinSplit<P, DG ? 3 : 1> sf[VC];
 #pragma unroll
             for (int t = 0; t < VC; ++t) sf[t].of(Rk[t]);
@@ -317,18 +317,18 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
             for (int i = 0; i < C / 16; ++i) {
                 const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.v, L::VV::kPitch, 16 * i, lane);
+                f32x4 acc = lin_read<P>(sf, lds.v, 16 * i, lane);
                 acc *= lds.gates.after[row];
-                if constexpr (DG) row_part<P, C>(lds.part[wave], lds.k, L::QK::kPitch, row, 16 * wave + 4 * g4, acc, lane);
+                if constexpr (DG) row_part<P>(lds.part[wave], lds.k, row, 16 * wave + 4 * g4, acc, lane);
 #pragma unroll
                 for (int u = i / 2; u < C / 32; ++u) {
                     typename P::F p0, p1;
-                    frag_oct<P>(lds.p[1], L::kPitchP, 16 * i, 32 * u, p0, p1, lane);
+                    lds.p[1].oct(16 * i, u, lane, p0, p1);
                     acc = P::mma2(acc, qf[u][0], qf[u][1], p0, p1);
                 }
                 lin_store4<P>(rs, row * static_cast<int>(w.sdk) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
             }
-            lin_update<P, C, 3>(Rk, lds.o, L::VV::kPitch, qf, lds.gates.before, lds.gates.all[0], lane);
+            lin_update<P, C, 3, DV>(Rk, lds.o, qf, lds.gates.before, lds.gates.all[0], lane);
         }
         if constexpr (DG) {
             __syncthreads();
