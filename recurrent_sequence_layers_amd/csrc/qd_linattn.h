@@ -81,9 +81,14 @@ constexpr double kLinLog2e = 1.4426950408889634;
 typedef __attribute__((ext_vector_type(4))) unsigned lin_u32x4;
 typedef __attribute__((ext_vector_type(2))) unsigned lin_u32x2;
 
-// raw buffer (stride 0): reads at offsets >= bytes give 0, writes there are dropped
+// raw buffer (stride 0): reads at offsets >= bytes give 0, writes there are dropped.  base and
+// bytes are the same in every lane; said so, or each access becomes a loop over the lanes' values.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_rsrc(const void *base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(static_cast<uint64_t>(hi) << 32 | lo), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 
 __device__ __forceinline__ float lin_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -206,10 +211,14 @@ __device__ __forceinline__ double lin_gates(LinGates<C> &t, float g, int lane) {
     }
     return end;
 }
-// e^{G_s - G_t}
+// e^{G_s - G_t} for the tokens t..t+3 (an infinity or nonsense where t > s: not used there)
 template <int C>
-__device__ __forceinline__ float lin_between(const LinGates<C> &t, float hs, float ls, int at) {
-    return lin_exp2((hs - t.hi[at]) + (ls - t.lo[at]));
+__device__ __forceinline__ f32x4 lin_between(const LinGates<C> &g, int s, int t) {
+    const f32x4 hi = g.hi[s] - lds_f32x4(g.hi + t), lo = g.lo[s] - lds_f32x4(g.lo + t);
+    f32x4 d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = lin_exp2(hi[e] + lo[e]);
+    return d;
 }
 
 // ---------------------------------------------------------------- operands
@@ -278,12 +287,15 @@ __device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C,
     return acc;
 }
 
-// Lower block triangle, row by row: p -> (i, j), j <= i
+// Lower block triangle of at most four rows, row by row: p -> (i, j), j <= i
 __device__ __forceinline__ void lin_pair(int p, int &i, int &j) {
-    i = 0;
-    while ((i + 1) * (i + 2) / 2 <= p) ++i;
+    i = (p >= 1) + (p >= 3) + (p >= 6);
     j = p - i * (i + 1) / 2;
 }
+// The index of a wave, known to be the same in its lanes
+__device__ __forceinline__ int lin_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
+// Two waves a SIMD: what the LDS leaves room for, and registers for loads ahead
+#define LIN_TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
 
 // Four consecutive elements to a buffer (dropped past its end)
 template <class P>

@@ -52,7 +52,7 @@ struct FwdLds {
 };
 
 template <class P, int DK>
-__global__ __launch_bounds__(2 * kNT) void lin_fwd_kernel(const LinArgs a) {
+__global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const LinArgs a) {
     using L = FwdLds<P, DK>;
     constexpr int C = L::C, NB = (C / 16) * (C / 16 + 1) / 2;
     extern __shared__ __align__(16) char smem[];
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(2 * kNT) void lin_fwd_kernel(const LinArgs a) {
     int unit, cb;
     if (!lin_place(a.B * a.H * a.segs, ncb, unit, cb)) return;
     const int seg = unit % a.segs, bh = unit / a.segs, b = bh / a.H, h = bh % a.H;
-    const int tid = threadIdx.x & (kNT - 1), wave = wave_id() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x & (kNT - 1), role = lin_wave() >> 2, wave = lin_wave() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, (a.T + C - 1) / C);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(2 * kNT) void lin_fwd_kernel(const LinArgs a) {
     for (int e = threadIdx.x; e < LinTile<P, C, C>::kElems; e += 2 * kNT) lds.p[0].m[e] = lds.p[1].m[e] = 0;
     __syncthreads();
 
-    if (threadIdx.x >= kNT) {
+    if (role == 1) {
         const char *gq = static_cast<const char *>(a.q) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gk = static_cast<const char *>(a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gv = static_cast<const char *>(a.v) + tok0 * sdv + vcol;
@@ -103,9 +103,9 @@ __global__ __launch_bounds__(2 * kNT) void lin_fwd_kernel(const LinArgs a) {
                     lin_pair(p, i, j);
                     f32x4 acc = lin_block<P>(lds.k[now], lds.q[now], 16 * j, 16 * i, lane);
                     const int s = 16 * i + r16, t = 16 * j + 4 * g4;
-                    const float hs = gates.hi[s], ls = gates.lo[s];
+                    const f32x4 d = lin_between(gates, s, t);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? lin_between(gates, hs, ls, t + e) * acc[e] : 0.f;
+                    for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
                     P::st4(lds.p[(n + 1 - c0) & 1].four(s, t), acc);
                 }
             }
@@ -171,7 +171,7 @@ struct StateLds {
     LinGates<C> gates[2];
 };
 template <class P, int DK>
-__global__ __launch_bounds__(kNT) void lin_state_kernel(const LinArgs a, const int first_rev) {
+__global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinArgs a, const int first_rev) {
     using L = StateLds<P, DK>;
     constexpr int C = L::C;
     extern __shared__ __align__(16) char smem[];
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kNT) void lin_state_kernel(const LinArgs a, const i
     if (!lin_place(bhs * nseg, ncb, unit, cb)) return;
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
     const int slot = unit % nseg, bh = unit / nseg, b = bh / a.H, h = bh % a.H, seg = rev ? slot + 1 : slot;
-    const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x, wave = lin_wave(), lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;

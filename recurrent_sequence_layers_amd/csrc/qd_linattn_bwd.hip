@@ -64,7 +64,7 @@ struct Walk {
         b = bh / a.H;
         h = bh % a.H;
         tid = threadIdx.x;
-        wave = wave_id();
+        wave = lin_wave();
         lane = lane_id();
         g4 = lane >> 4;
         r16 = lane & 15;
@@ -156,9 +156,9 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
             lin_pair(p, i, j);
             f32x4 acc = lin_block<P>(lds.v, lds.o, 16 * j, 16 * i, lane);
             const int s = 16 * i + r16, t = 16 * j + 4 * g4;
-            const float hs = lds.gates.hi[s], ls = lds.gates.lo[s];
+            const f32x4 d = lin_between(lds.gates, s, t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? lin_between(lds.gates, hs, ls, t + e) * acc[e] : 0.f;
+            for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
             P::st4(lds.p[0].four(s, t), acc);
             if constexpr (DG) {
                 const f32x4 qk = lin_block<P>(lds.k, lds.q, 16 * j, 16 * i, lane);
@@ -268,10 +268,10 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
             const int t = 16 * j + r16, s = 16 * i + 4 * g4;
             f32x4 qk = lin_block<P>(lds.q, lds.k, 16 * i, 16 * j, lane);
             f32x4 ov = lin_block<P>(lds.o, lds.v, 16 * i, 16 * j, lane);
-            const float ht = -lds.gates.hi[t], lt = -lds.gates.lo[t];
+            const f32x4 hi = lds_f32x4(lds.gates.hi + s) - lds.gates.hi[t], lo = lds_f32x4(lds.gates.lo + s) - lds.gates.lo[t];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float d = lin_exp2((lds.gates.hi[s + e] + ht) + (lds.gates.lo[s + e] + lt));
+                const float d = lin_exp2(hi[e] + lo[e]);
                 qk[e] = t <= s + e ? d * qk[e] : 0.f;
                 ov[e] = t <= s + e ? d * ov[e] : 0.f;
             }
@@ -350,7 +350,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 }
 
 template <class P, int DK, int DV, bool DG>
-__global__ __launch_bounds__(64 * ((DK > DV ? DK : DV) / 16)) void lin_bwd_kernel(const LinArgs a) {
+__global__ __launch_bounds__(64 * ((DK > DV ? DK : DV) / 16)) LIN_TWO_WAVES void lin_bwd_kernel(const LinArgs a) {
     extern __shared__ __align__(16) char smem[];
     auto &lds = *reinterpret_cast<BwdLds<P, DK, DV> *>(smem);
     const int unit = blockIdx.x >> 1;
