@@ -21,9 +21,10 @@
 //   Outputs are formed transposed: a lane gets four consecutive columns of one token.
 //
 // Precision.  States, sums and statistics are fp32.  A bf16 product rounds P and the state it
-// reads to bf16 once each.  What enters a state (v_t e^{G_C - G_t}) is not rounded: it is split
-// into three bf16 addends (24 bits, all of an fp32), three products for one, since S_T, dS0 and
-// dg are fp32.  Prefix sums of g are taken in 64 bits and kept as the sum of two fp32 numbers:
+// reads to bf16 once each.  What enters a state (v_t e^{G_C - G_t}) is split into bf16 addends, a
+// product each: three (24 bits, all of an fp32) where S_T, dS0 or dg, which are fp32, come of the
+// state; two (16 bits) where only element outputs do, which a third rounding to 8 bits would put
+// 1.7 instead of 1.4 roundings off.  Prefix sums of g are taken in 64 bits and kept as the sum of two fp32 numbers:
 // e^{G_s - G_t} of near tokens behind strong decays would lose what the difference cancels.
 #pragma once
 
@@ -68,7 +69,8 @@ hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
 hipError_t launch_lin_step(int dtype, const LinArgs &a, float *S, hipStream_t stream);   // T = 1
 size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg);
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
-hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, hipStream_t stream);
+// exact: fp32 results come of the states, not only element outputs
+hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, bool exact, hipStream_t stream);
 hipError_t launch_lin_copy(float *to, const float *from, size_t n, hipStream_t stream);  // from null: zeros
 
 // Tokens of a chunk.  fp32 rows of 64 would not fit the LDS twice.
@@ -184,10 +186,21 @@ struct LinGates {
     float all[4];                    // e^{G_C}
 };
 
-// log decay of lane's token, in powers of two, for the chunk at t0 with `live` tokens
+// log decay of lane's token of the chunk at t0 with `live` tokens, 0 past them.  A buffer load like
+// the rows', so that a wave always has the same number of loads on their way.
 __device__ __forceinline__ float lin_gate(const LinArgs &a, int b, int h, int t0, int live, int lane) {
-    if (lane >= live || a.decay == kNoDecay) return 0.f;
-    return a.decay == kHeadDecay ? a.g[h] : a.g[(static_cast<size_t>(b) * a.T + t0 + lane) * a.H + h];
+    const bool token = a.decay == kTokenDecay;
+    const float *base = token ? a.g + (static_cast<size_t>(b) * a.T + t0) * a.H + h : a.g + h;
+    const int stride = token ? a.H * 4 : 0;
+    const __amdgpu_buffer_rsrc_t rs = lin_rsrc(base, a.decay == kNoDecay || live <= 0 ? 0 : (live - 1) * stride + 4);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, lane < live ? lane * stride : 0x7ffffff0, 0, 0));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lin_dpp(double x) {
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 // One wave.  A decay of zero (g = -inf) forgets all that came before: 4096 powers of two make
 // every factor across it zero, and prefix sums stay finite.
@@ -195,12 +208,17 @@ template <int C>
 __device__ __forceinline__ double lin_gates(LinGates<C> &t, float g, int lane) {
     double x = static_cast<double>(g) * kLinLog2e;
     x = x < -4096.0 ? -4096.0 : x;
-#pragma unroll
-    for (int d = 1; d < C; d *= 2) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    const double end = __shfl(x, C - 1);
+    // inclusive prefix sums over the wave
+    x += lin_dpp<0x111, 0xf>(x);   // row_shr:1
+    x += lin_dpp<0x112, 0xf>(x);   // row_shr:2
+    x += lin_dpp<0x114, 0xf>(x);   // row_shr:4
+    x += lin_dpp<0x118, 0xf>(x);   // row_shr:8
+    x += lin_dpp<0x142, 0xa>(x);   // row_bcast:15 into rows 1 and 3
+    x += lin_dpp<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
+    const uint64_t bits = __builtin_bit_cast(uint64_t, x);
+    const uint32_t e0 = __builtin_amdgcn_readlane(static_cast<int>(bits), C - 1);
+    const uint32_t e1 = __builtin_amdgcn_readlane(static_cast<int>(bits >> 32), C - 1);
+    const double end = __builtin_bit_cast(double, static_cast<uint64_t>(e1) << 32 | e0);
     if (lane < C) {
         const float hi = static_cast<float>(x);
         t.hi[lane] = hi;

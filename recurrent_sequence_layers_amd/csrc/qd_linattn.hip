@@ -51,7 +51,7 @@ struct FwdLds {
     LinGates<C> gates[3];
 };
 
-template <class P, int DK>
+template <class P, int DK, int NS>
 __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const LinArgs a) {
     using L = FwdLds<P, DK>;
     constexpr int C = L::C, NB = (C / 16) * (C / 16 + 1) / 2;
@@ -76,26 +76,28 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         const char *gq = static_cast<const char *>(a.q) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gk = static_cast<const char *>(a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gv = static_cast<const char *>(a.v) + tok0 * sdv + vcol;
-        LinRows<P, C, DK, kNT> rq, rk;
-        LinRows<P, C, 64, kNT> rv;
-        float gate = 0.f;
-        auto fetch = [&](int n) {
-            const int t0 = n * C, live = min(max(len - t0, 0), C);
-            rq.load(gq + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
-            rk.load(gk + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
-            rv.load(gv + static_cast<size_t>(t0) * sdv, live, static_cast<int>(sdv), tid);
-            if (wave == 3) gate = lin_gate(a, b, h, t0, live, lane);
+        // two chunks on their way: the loads of one step are waited for two steps later
+        struct Ahead {
+            LinRows<P, C, DK, kNT> q, k;
+            LinRows<P, C, 64, kNT> v;
+            float gate;
+        } even, odd;
+        auto fetch = [&](Ahead &r, int n) {
+            const int t0 = n * C, live = n < c1 ? min(max(len - t0, 0), C) : 0;
+            r.q.load(gq + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
+            r.k.load(gk + static_cast<size_t>(t0) * sdk, live, static_cast<int>(sdk), tid);
+            r.v.load(gv + static_cast<size_t>(t0) * sdv, live, static_cast<int>(sdv), tid);
+            r.gate = lin_gate(a, b, h, t0, live, lane);
         };
-        fetch(c0);
         int put = 0, now = 2;                    // slots of chunks n + 2 and n + 1
-        for (int n = c0 - 2; n < c1; ++n) {
-            if (n + 2 < c1) {
-                rq.put(lds.q[put], tid);
-                rk.put(lds.k[put], tid);
-                rv.put(lds.v[put], tid);
-                if (wave == 3) lin_gates(lds.gates[put], gate, lane);
-                if (n + 3 < c1) fetch(n + 3);
-            }
+        auto step = [&](Ahead &r, int n) {
+            // also past the last chunk, with zeros: a branch here would make the waits for one
+            // chunk's loads wait for the next one's too
+            r.q.put(lds.q[put], tid);
+            r.k.put(lds.k[put], tid);
+            r.v.put(lds.v[put], tid);
+            if (wave == 3) lin_gates(lds.gates[put], r.gate, lane);
+            fetch(r, n + 4);
             if (n + 1 >= c0 && n + 1 < c1) {
                 const LinGates<C> &gates = lds.gates[now];
                 for (int p = wave; p < NB; p += 4) {
@@ -112,6 +114,12 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
             now = put;
             put = put == 2 ? 0 : put + 1;
             __syncthreads();
+        };
+        fetch(even, c0);
+        fetch(odd, c0 + 1);
+        for (int n = c0 - 2; n < c1; n += 2) {
+            step(even, n);
+            step(odd, n + 1);
         }
         return;
     }
@@ -153,10 +161,11 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
             }
             lin_store4<P>(ro, (16 * i + r16) * static_cast<int>(sdv) + (16 * wave + 4 * g4) * P::kBytes, acc);
         }
-        lin_update<P, C, 3, DK>(S, k, vf, gates.after, gates.all[0], lane);
+        lin_update<P, C, NS, DK>(S, k, vf, gates.after, gates.all[0], lane);
         now = now == 2 ? 0 : now + 1;
         __syncthreads();
     }
+    if ((c1 - c0) & 1) __syncthreads();          // the other role goes by pairs of steps
     if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, g4);
 }
 
@@ -170,7 +179,7 @@ struct StateLds {
     LinTile<P, C, 64> v[2];
     LinGates<C> gates[2];
 };
-template <class P, int DK>
+template <class P, int DK, int NS>
 __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinArgs a, const int first_rev) {
     using L = StateLds<P, DK>;
     constexpr int C = L::C;
@@ -224,7 +233,7 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[m & 1].down(32 * u + 4 * e, 16 * wave, 4, lane);
-        lin_update<P, C, 3, DK>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
+        lin_update<P, C, NS, DK>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
         __syncthreads();
     }
     store_state<DK>(S, (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, g4);
@@ -312,22 +321,27 @@ __global__ __launch_bounds__(kNT) void lin_copy_kernel(f32x4 *to, const f32x4 *f
         to[i] = from ? from[i] : zero4();
 }
 
-template <class K>
-hipError_t lin_launch(K kernel, dim3 grid, size_t lds, hipStream_t stream, const LinArgs &a) {
-    hipLaunchKernelGGL(kernel, grid, dim3(2 * kNT), static_cast<unsigned>(lds), stream, a);
-    return hipGetLastError();
+template <class P, int DK>
+void fwd_sized(const LinArgs &a, hipStream_t stream) {
+    const dim3 grid = lin_grid(static_cast<long long>(a.B) * a.H * a.segs, a.DV / 64), blk(2 * kNT);
+    if (a.S_T) hipLaunchKernelGGL((lin_fwd_kernel<P, DK, 3>), grid, blk, sizeof(FwdLds<P, DK>), stream, a);
+    else hipLaunchKernelGGL((lin_fwd_kernel<P, DK, 2>), grid, blk, sizeof(FwdLds<P, DK>), stream, a);
 }
-
 template <class P>
 hipError_t fwd_typed(const LinArgs &a, hipStream_t stream) {
-    const dim3 grid = lin_grid(static_cast<long long>(a.B) * a.H * a.segs, a.DV / 64);
-    if (a.DK == 128) return lin_launch(lin_fwd_kernel<P, 128>, grid, sizeof(FwdLds<P, 128>), stream, a);
-    return lin_launch(lin_fwd_kernel<P, 64>, grid, sizeof(FwdLds<P, 64>), stream, a);
+    if (a.DK == 128) fwd_sized<P, 128>(a, stream);
+    else fwd_sized<P, 64>(a, stream);
+    return hipGetLastError();
+}
+template <class P, int DK>
+void states_sized(const LinArgs &a, dim3 grid, int first, bool exact, hipStream_t stream) {
+    if (exact) hipLaunchKernelGGL((lin_state_kernel<P, DK, 3>), grid, dim3(kNT), sizeof(StateLds<P, DK>), stream, a, first);
+    else hipLaunchKernelGGL((lin_state_kernel<P, DK, 2>), grid, dim3(kNT), sizeof(StateLds<P, DK>), stream, a, first);
 }
 template <class P>
-void states_typed(const LinArgs &a, dim3 grid, int first, hipStream_t stream) {
-    if (a.DK == 128) hipLaunchKernelGGL((lin_state_kernel<P, 128>), grid, dim3(kNT), sizeof(StateLds<P, 128>), stream, a, first);
-    else hipLaunchKernelGGL((lin_state_kernel<P, 64>), grid, dim3(kNT), sizeof(StateLds<P, 64>), stream, a, first);
+void states_typed(const LinArgs &a, dim3 grid, int first, bool exact, hipStream_t stream) {
+    if (a.DK == 128) states_sized<P, 128>(a, grid, first, exact, stream);
+    else states_sized<P, 64>(a, grid, first, exact, stream);
 }
 template <class P>
 hipError_t step_typed(const LinArgs &a, float *S, hipStream_t stream) {
@@ -371,12 +385,12 @@ size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv) {
     return (bh * (p.segs - 1) * dk * dv + 2 * bh * p.segs) * sizeof(float);
 }
 
-hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, hipStream_t stream) {
+hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, bool exact, hipStream_t stream) {
     const int first = fwd ? 0 : 1, count = (fwd ? 1 : 0) + (rev ? 1 : 0);
     dim3 grid = lin_grid(static_cast<long long>(a.B) * a.H * (a.segs - 1), a.DV / 64);
     grid.y = count;
-    if (dtype == 1) states_typed<Bf16>(a, grid, first, stream);
-    else states_typed<F32>(a, grid, first, stream);
+    if (dtype == 1) states_typed<Bf16>(a, grid, first, exact, stream);
+    else states_typed<F32>(a, grid, first, exact, stream);
     const long long n = static_cast<long long>(a.B) * a.H * (a.DV * a.DK / 4);
     hipLaunchKernelGGL(lin_join_kernel, dim3(static_cast<unsigned>((n + kNT - 1) / kNT), count), dim3(kNT), 0, stream, a, first);
     return hipGetLastError();
@@ -398,7 +412,7 @@ hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (p.segs > 1) {
         a.fwd = static_cast<float *>(ws);
         a.fac = a.fwd + bh * (p.segs - 1) * state;
-        if (hipError_t e = launch_lin_states(dtype, a, true, false, stream)) return e;
+        if (hipError_t e = launch_lin_states(dtype, a, true, false, a.S_T != nullptr, stream)) return e;
     }
     return dtype == 1 ? fwd_typed<Bf16>(a, stream) : fwd_typed<F32>(a, stream);
 }

@@ -516,7 +516,7 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
         a.rev = a.fwd + bh * (a.segs - 1) * state;
         a.fac = a.rev + bh * (a.segs - 1) * state;
         p = a.fac + 2 * bh * a.segs;
-        if (hipError_t e = launch_lin_states(dtype, a, true, true, stream)) return e;
+        if (hipError_t e = launch_lin_states(dtype, a, true, true, a.dg || a.dS0, stream)) return e;
     }
     if (a.dg) {
         a.tok = p;
