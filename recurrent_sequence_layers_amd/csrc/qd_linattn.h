@@ -15,10 +15,11 @@
 //
 //   A wave owns 16 columns of the state, each for every contraction index ("rows"): for o the
 //   columns are value indices and the rows key indices.  Tile 2u + h of its accumulators holds
-//   in lane (g = l / 16, c = l % 16), element i, row 32 u + 8 g + 4 h + i and column c.  That is
-//   at once what the 16x16x32 products take as operand, with eight consecutive rows a lane, so
-//   the other operand is one 16-byte LDS read, and the state never leaves the registers.
-//   Outputs are formed transposed: a lane gets four consecutive columns of one token.
+//   in lane (g = l / 16, c = l % 16), element i, column c and row 32 u + 8 g + 4 h' + i, h' = h for
+//   even g and 1 - h for odd g.  That is at once what the 16x16x32 products take as operand, with
+//   eight consecutive rows a lane, so the other operand is one 16-byte LDS read, and the state
+//   never leaves the registers.  Outputs are formed transposed: a lane gets four consecutive
+//   columns of one token.
 //
 // Precision.  States, sums and statistics are fp32.  A bf16 product rounds P and the state it
 // reads to bf16 once each.  What enters a state (v_t e^{G_C - G_t}) is split into bf16 addends, a
@@ -104,16 +105,21 @@ __device__ __forceinline__ float lin_exp(float x) {
 }
 
 // ---------------------------------------------------------------- rows of a chunk
-// A matrix of ROWS x COLS elements in LDS, and the two ways it is read:
-//   oct:  row r0 + l % 16, eight columns 32 u + 8 (l / 16) + 0..7 (contraction over columns)
-//   down: rows r0 + 8 (l / 16) + i, i = 0..3, of column c0 + step (c / 4) + c % 4, c = l % 16
-//         (contraction over rows); step 4 or 8
+// A matrix of ROWS x COLS elements in LDS, and the ways it is read as an operand:
+//   oct:  row r0 + l % 16, eight columns 32 u + 8 g + .., g = l / 16 (contraction over columns)
+//   down: rows 32 u + 8 g + .. of column c0 + l % 16 (contraction over rows)
+//   across: the same rows of the columns that a state's tile has as its rows
+// Each gives the eight as two halves, in the order of their index for even g and the other way
+// round for odd g; products pair what has the same place, so any two of them agree.
 //
 // bf16: a 16 x 32 block is 64 slots of 16 bytes; columns 8 g .. 8 g + 7 of row r sit in slot
-// 16 g + (r ^ swz(g)).  Sixteen lanes that read one g take 256 contiguous bytes; a transposing read
-// finds its four rows in four quarters.  Blocks are 1040 bytes apart, so the sixteen pieces of a
-// row, written together, meet sixteen different slots.  Each is free of bank conflicts.
+// 16 g + (r ^ 2 g), their halves swapped for odd g.  A cycle serves 128 bytes: eight lanes of an
+// oct read one g and eight rows; the sixteen lanes of a transposing read take four rows of four
+// g, whose slots and halves all differ; blocks are 1040 bytes apart, so what is written together,
+// sixteen pieces of a row, half by half, differs too.
 // fp32: rows padded by 16 bytes.
+__device__ __forceinline__ int lin_half(int e, int lane) { return 4 * (e ^ ((lane >> 4) & 1)); }
+
 template <class P, int ROWS, int COLS>
 struct LinTile {
     using R = typename P::R;
@@ -123,31 +129,56 @@ struct LinTile {
     static constexpr int kElems = kSwz ? (ROWS / 16) * (COLS / 32) * kBlock : ROWS * kPitch;
     R m[kElems];
 
-    __device__ __forceinline__ static int slot(int row, int g) { return 8 * (16 * g + ((row & 15) ^ ((12 * g) & 15))); }
-    // 16-byte piece `c` of a row
-    __device__ __forceinline__ R *piece(int row, int c) {
-        if constexpr (kSwz) return m + ((row >> 4) * (COLS / 32) + (c >> 2)) * kBlock + slot(row, c & 3);
-        else return m + row * kPitch + 4 * c;
-    }
     // four elements of a row, at a column that four divides
     __device__ __forceinline__ R *four(int row, int col) {
-        if constexpr (kSwz) return piece(row, col >> 3) + (col & 4);
-        else return m + row * kPitch + col;
+        if constexpr (kSwz) {
+            const int g = (col >> 3) & 3;
+            return m + ((row >> 4) * (COLS / 32) + (col >> 5)) * kBlock + 8 * (16 * g + ((row & 15) ^ (2 * g))) + ((col ^ (g << 2)) & 4);
+        } else {
+            return m + row * kPitch + col;
+        }
+    }
+    // 16-byte piece c of a row
+    __device__ __forceinline__ void put(int row, int c, lin_u32x4 v) {
+        if constexpr (kSwz) {
+            *reinterpret_cast<lin_u32x2 *>(four(row, 8 * c)) = __builtin_shufflevector(v, v, 0, 1);
+            *reinterpret_cast<lin_u32x2 *>(four(row, 8 * c + 4)) = __builtin_shufflevector(v, v, 2, 3);
+        } else {
+            *reinterpret_cast<lin_u32x4 *>(m + row * kPitch + 4 * c) = v;
+        }
     }
     __device__ __forceinline__ void oct(int r0, int u, int lane, F &lo, F &hi) {
-        if constexpr (kSwz) P::ld8(piece(r0 + (lane & 15), 4 * u + (lane >> 4)), lo, hi);
-        else P::ld8(m + (r0 + (lane & 15)) * kPitch + 32 * u + 8 * (lane >> 4), lo, hi);
+        const int row = r0 + (lane & 15), g = lane >> 4;
+        if constexpr (kSwz) {
+            P::ld8(m + ((row >> 4) * (COLS / 32) + u) * kBlock + 8 * (16 * g + ((row & 15) ^ (2 * g))), lo, hi);
+        } else {
+            lo = P::ld4(m + row * kPitch + 32 * u + 8 * g + lin_half(0, lane));
+            hi = P::ld4(m + row * kPitch + 32 * u + 8 * g + lin_half(1, lane));
+        }
     }
-    __device__ __forceinline__ F down(int r0, int c0, int step, int lane) {
-        const int g = lane >> 4, mm = lane & 15;
+    // half e of the eight rows
+    __device__ __forceinline__ F down(int u, int e, int c0, int lane) {
+        const int g = lane >> 4, mm = lane & 15, row = 32 * u + 8 * g + lin_half(e, lane);
         if constexpr (kSwz) {
             // LDS transpose read: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
             // lane 4p + q receives element q of chunk p of the rows 0..3
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
             return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                  (lds_s16x4 *)(four(r0 + 8 * g + (mm >> 2), c0 + step * (mm & 3)))));
+                                                  (lds_s16x4 *)(four(row + (mm >> 2), c0 + 4 * (mm & 3)))));
         } else {
-            return P::ld4_strided(m + (r0 + 8 * g) * kPitch + c0 + step * (mm >> 2) + (mm & 3), kPitch);
+            return P::ld4_strided(m + row * kPitch + c0 + mm, kPitch);
+        }
+    }
+    __device__ __forceinline__ F across(int u, int e, int b, int lane) {
+        const int g = lane >> 4, mm = lane & 15, row = 32 * u + 8 * g + lin_half(e, lane);
+        if constexpr (kSwz) {
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const int p = mm & 3;
+            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                  (lds_s16x4 *)(four(row + (mm >> 2), 32 * (b >> 1) + 8 * p + 4 * ((b ^ p) & 1)))));
+        } else {
+            const int p = mm >> 2;
+            return P::ld4_strided(m + row * kPitch + 32 * (b >> 1) + 8 * p + 4 * ((b ^ p) & 1) + (mm & 3), kPitch);
         }
     }
 };
@@ -172,7 +203,7 @@ struct LinRows {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int p = tid + j * NT;
-            *reinterpret_cast<lin_u32x4 *>(to.piece(p / kPer, p % kPer)) = r[j];
+            to.put(p / kPer, p % kPer, r[j]);
         }
     }
 };
@@ -265,12 +296,11 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[D / 16], LinTile<P, C, D> 
 #pragma unroll
     for (int u = 0; u < C / 32; ++u) {
         LinSplit<P, NS> lo, hi;
-        lo.of(P::f32(col[u][0]) * lds_f32x4(weight + 32 * u + 8 * g4));
-        hi.of(P::f32(col[u][1]) * lds_f32x4(weight + 32 * u + 8 * g4 + 4));
+        lo.of(P::f32(col[u][0]) * lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(0, lane)));
+        hi.of(P::f32(col[u][1]) * lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(1, lane)));
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
-            const typename P::F r0 = rows.down(32 * u, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
-            const typename P::F r1 = rows.down(32 * u + 4, 32 * (b >> 1) + 4 * (b & 1), 8, lane);
+            const typename P::F r0 = rows.across(u, 0, b, lane), r1 = rows.across(u, 1, b, lane);
 #pragma unroll
             for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[b] = P::mma2(S[b], r0, r1, lo.p[j], hi.p[j]);
         }
@@ -304,6 +334,9 @@ __device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C,
     }
     return acc;
 }
+
+// First of the four rows that tile t of a state has in this lane
+__device__ __forceinline__ int lin_row(int t, int lane) { return 32 * (t >> 1) + 8 * (lane >> 4) + lin_half(t & 1, lane); }
 
 // Lower block triangle of at most four rows, row by row: p -> (i, j), j <= i
 __device__ __forceinline__ void lin_pair(int p, int &i, int &j) {

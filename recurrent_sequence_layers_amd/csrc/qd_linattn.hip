@@ -25,17 +25,17 @@ dim3 lin_grid(long long units, int ncb) { return dim3(static_cast<unsigned>((uni
 
 // The state's tiles from and to [DV][DK]: wave's column, four rows at a time
 template <int DK>
-__device__ __forceinline__ void load_state(f32x4 (&S)[DK / 16], const float *from, int col, int g4) {
+__device__ __forceinline__ void load_state(f32x4 (&S)[DK / 16], const float *from, int col, int lane) {
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t)
-        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1))
+        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col) * DK + lin_row(t, lane))
                     : zero4();
 }
 template <int DK>
-__device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float *to, int col, int g4) {
+__device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float *to, int col, int lane) {
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t)
-        *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col) * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) = S[t];
+        *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col) * DK + lin_row(t, lane)) = S[t];
 }
 
 // Eight waves in two roles, a barrier a step.  At step n waves 0-3 hold the state and do chunk n's
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     const int col = 64 * cb + 16 * wave + r16;
     f32x4 S[DK / 16];
     load_state<DK>(S, seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
-                   col, g4);
+                   col, lane);
     char *go = static_cast<char *>(a.o) + tok0 * sdv + vcol;
     __syncthreads();
     __syncthreads();
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
 #pragma unroll
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[now].down(32 * u + 4 * e, 16 * wave, 4, lane);
+            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[now].down(u, e, 16 * wave, lane);
         // rows past the buffer's end, that of the last token's row, are dropped by their offset
         const __amdgpu_buffer_rsrc_t ro = lin_rsrc(go + static_cast<size_t>(t0) * sdv,
                                                    live > 0 ? (live - 1) * static_cast<int>(sdv) + 64 * P::kBytes : 0);
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         __syncthreads();
     }
     if ((c1 - c0) & 1) __syncthreads();          // the other role goes by pairs of steps
-    if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, g4);
+    if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, lane);
 }
 
 // The states alone, from zero (or S0, dS_T) over one segment: forwards with k, v and the decay to
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
     if (!lin_place(bhs * nseg, ncb, unit, cb)) return;
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
     const int slot = unit % nseg, bh = unit / nseg, b = bh / a.H, h = bh % a.H, seg = rev ? slot + 1 : slot;
-    const int tid = threadIdx.x, wave = lin_wave(), lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x, wave = lin_wave(), lane = lane_id(), r16 = lane & 15;
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
 
     f32x4 S[DK / 16];
     load_state<DK>(S, rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
-                          : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr), col, g4);
+                          : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr), col, lane);
     LinRows<P, C, DK, kNT> rk;
     LinRows<P, C, 64, kNT> rv;
     float gate = 0.f;
@@ -232,11 +232,11 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
 #pragma unroll
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[m & 1].down(32 * u + 4 * e, 16 * wave, 4, lane);
+            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[m & 1].down(u, e, 16 * wave, lane);
         lin_update<P, C, NS, DK>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
         __syncthreads();
     }
-    store_state<DK>(S, (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, g4);
+    store_state<DK>(S, (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, lane);
     if (cb == 0 && wave == 3 && lane == 0)
         a.fac[(static_cast<size_t>(rev) * bhs + bh) * a.segs + seg] = lin_exp2(static_cast<float>(total));
 }

@@ -142,7 +142,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     for (int t = 0; t < DV / 16; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            S[t][e] = from && mine ? from[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col] : 0.f;
+            S[t][e] = from && mine ? from[(lin_row(t, lane) + e) * DK + col] : 0.f;
     for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = 0;
     w.fetch(w.c0);
     for (int n = w.c0; n < w.c1; ++n) {
@@ -181,7 +181,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) kf[u][e] = lds.k.down(32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) kf[u][e] = lds.k.down(u, e, 16 * wave, lane);
             LinSplit<P, DG ? 3 : 1> sf[DV / 16];
 #pragma unroll
             for (int t = 0; t < DV / 16; ++t) sf[t].of(S[t]);
@@ -224,7 +224,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
                 for (int t = 0; t < DV / 16; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(S[t][e], d[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col], s);
+                    for (int e = 0; e < 4; ++e) s = fmaf(S[t][e], d[(lin_row(t, lane) + e) * DK + col], s);
             }
             for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
             if (lane == 0) a.edge[static_cast<size_t>(w.bh) * 8 + wave] = s;
@@ -247,12 +247,12 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
                                            : a.dS_T ? a.dS_T + w.bh * state : nullptr;
 #pragma unroll
     for (int t = 0; t < KC; ++t)
-        Rv[t] = from && mine_v ? *reinterpret_cast<const f32x4 *>(from + col * DK + 32 * (t >> 1) + 8 * g4 + 4 * (t & 1)) : zero4();
+        Rv[t] = from && mine_v ? *reinterpret_cast<const f32x4 *>(from + col * DK + lin_row(t, lane)) : zero4();
 #pragma unroll
     for (int t = 0; t < VC; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            Rk[t][e] = from && mine_k ? from[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col] : 0.f;
+            Rk[t][e] = from && mine_k ? from[(lin_row(t, lane) + e) * DK + col] : 0.f;
     for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = lds.p[1].m[e] = 0;
     w.fetch(w.c1 - 1);
     for (int n = w.c1 - 1; n >= w.c0; --n) {
@@ -284,7 +284,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) of[u][e] = lds.o.down(32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) of[u][e] = lds.o.down(u, e, 16 * wave, lane);
             LinSplit<P, 1> sf[KC];
 #pragma unroll
             for (int t = 0; t < KC; ++t) sf[t].of(Rv[t]);
@@ -309,7 +309,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
             for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) qf[u][e] = lds.q.down(32 * u + 4 * e, 16 * wave, 4, lane);
+                for (int e = 0; e < 2; ++e) qf[u][e] = lds.q.down(u, e, 16 * wave, lane);
             LinSplit<P, DG ? 3 : 1> sf[VC];
 #pragma unroll
             for (int t = 0; t < VC; ++t) sf[t].of(Rk[t]);
@@ -345,7 +345,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
 #pragma unroll
         for (int t = 0; t < VC; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) to[(32 * (t >> 1) + 8 * g4 + 4 * (t & 1) + e) * DK + col] = Rk[t][e];
+            for (int e = 0; e < 4; ++e) to[(lin_row(t, lane) + e) * DK + col] = Rk[t][e];
     }
 }
 
