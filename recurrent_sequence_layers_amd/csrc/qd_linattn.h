@@ -147,6 +147,15 @@ struct LinTile {
             *reinterpret_cast<lin_u32x4 *>(m + row * kPitch + 4 * c) = v;
         }
     }
+    __device__ __forceinline__ lin_u32x4 get(int row, int c) {
+        if constexpr (kSwz) {
+            const lin_u32x2 x = *reinterpret_cast<const lin_u32x2 *>(four(row, 8 * c));
+            const lin_u32x2 y = *reinterpret_cast<const lin_u32x2 *>(four(row, 8 * c + 4));
+            return __builtin_shufflevector(x, y, 0, 1, 2, 3);
+        } else {
+            return *reinterpret_cast<const lin_u32x4 *>(m + row * kPitch + 4 * c);
+        }
+    }
     __device__ __forceinline__ void oct(int r0, int u, int lane, F &lo, F &hi) {
         const int row = r0 + (lane & 15), g = lane >> 4;
         if constexpr (kSwz) {
@@ -182,6 +191,17 @@ struct LinTile {
         }
     }
 };
+
+// Rows of a tile to a buffer (what lies past its end is dropped), over NT threads
+template <class P, int C, int COLS, int NT>
+__device__ __forceinline__ void lin_store(LinTile<P, C, COLS> &from, __amdgpu_buffer_rsrc_t rs, int stride, int tid) {
+    constexpr int kPer = COLS * P::kBytes / 16;
+#pragma unroll
+    for (int j = 0; j < C * kPer / NT; ++j) {
+        const int p = tid + j * NT;
+        __builtin_amdgcn_raw_buffer_store_b128(from.get(p / kPer, p % kPer), rs, (p / kPer) * stride + (p % kPer) * 16, 0, 0);
+    }
+}
 
 // C rows of COLS elements (rows `stride` bytes apart) on their way to a tile, over NT threads
 template <class P, int C, int COLS, int NT>

@@ -46,7 +46,7 @@ template <class P, int DK>
 struct FwdLds {
     static constexpr int C = kLinChunk<P>;
     LinTile<P, C, DK> q[3], k[3];
-    LinTile<P, C, 64> v[3];
+    LinTile<P, C, 64> v[3], o[2];
     LinTile<P, C, C> p[2];
     LinGates<C> gates[3];
 };
@@ -76,6 +76,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         const char *gq = static_cast<const char *>(a.q) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gk = static_cast<const char *>(a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
         const char *gv = static_cast<const char *>(a.v) + tok0 * sdv + vcol;
+        char *go = static_cast<char *>(a.o) + tok0 * sdv + vcol;
         // two chunks on their way: the loads of one step are waited for two steps later
         struct Ahead {
             LinRows<P, C, DK, kNT> q, k;
@@ -91,6 +92,13 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         };
         int put = 0, now = 2;                    // slots of chunks n + 2 and n + 1
         auto step = [&](Ahead &r, int n) {
+            // the outputs of chunk n - 1; rows past the buffer's end, that of the last token's row,
+            // are dropped by their offset
+            const int t0 = max(n - 1, c0) * C, live = n > c0 && n <= c1 ? min(max(len - t0, 0), C) : 0;
+            lin_store<P, C, 64, kNT>(lds.o[(n - 1 - c0) & 1],
+                                     lin_rsrc(go + static_cast<size_t>(t0) * sdv,
+                                              live > 0 ? (live - 1) * static_cast<int>(sdv) + 64 * P::kBytes : 0),
+                                     static_cast<int>(sdv), tid);
             // also past the last chunk, with zeros: a branch here would make the waits for one
             // chunk's loads wait for the next one's too
             r.q.put(lds.q[put], tid);
@@ -117,7 +125,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         };
         fetch(even, c0);
         fetch(odd, c0 + 1);
-        for (int n = c0 - 2; n < c1; n += 2) {
+        for (int n = c0 - 2; n <= c1; n += 2) {
             step(even, n);
             step(odd, n + 1);
         }
@@ -129,12 +137,10 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     f32x4 S[DK / 16];
     load_state<DK>(S, seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
                    col, lane);
-    char *go = static_cast<char *>(a.o) + tok0 * sdv + vcol;
     __syncthreads();
     __syncthreads();
     int now = 0;
     for (int n = c0; n < c1; ++n) {
-        const int t0 = n * C, live = min(max(len - t0, 0), C);
         LinTile<P, C, DK> &q = lds.q[now], &k = lds.k[now];
         LinTile<P, C, C> &p = lds.p[(n - c0) & 1];
         const LinGates<C> &gates = lds.gates[now];
@@ -143,9 +149,6 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[now].down(u, e, 16 * wave, lane);
-        // rows past the buffer's end, that of the last token's row, are dropped by their offset
-        const __amdgpu_buffer_rsrc_t ro = lin_rsrc(go + static_cast<size_t>(t0) * sdv,
-                                                   live > 0 ? (live - 1) * static_cast<int>(sdv) + 64 * P::kBytes : 0);
         LinSplit<P, 1> sf[DK / 16];
 #pragma unroll
         for (int t = 0; t < DK / 16; ++t) sf[t].of(S[t]);
@@ -159,13 +162,14 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
                 p.oct(16 * i, u, lane, p0, p1);
                 acc = P::mma2(acc, vf[u][0], vf[u][1], p0, p1);
             }
-            lin_store4<P>(ro, (16 * i + r16) * static_cast<int>(sdv) + (16 * wave + 4 * g4) * P::kBytes, acc);
+            P::st4(lds.o[(n - c0) & 1].four(16 * i + r16, 16 * wave + 4 * g4), acc);
         }
         lin_update<P, C, NS, DK>(S, k, vf, gates.after, gates.all[0], lane);
         now = now == 2 ? 0 : now + 1;
         __syncthreads();
     }
-    if ((c1 - c0) & 1) __syncthreads();          // the other role goes by pairs of steps
+    __syncthreads();                             // the last chunk's outputs go in a step of their own
+    if (!((c1 - c0) & 1)) __syncthreads();       // and that role goes by pairs of steps
     if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, lane);
 }
 
@@ -375,7 +379,7 @@ bool lin_supported(int dtype, int dk, int dv) {
 }
 // 32-bit row offsets inside a chunk, and grids
 bool lin_fits(int B, int T, int H) {
-    return H <= (1 << 15) && static_cast<long long>(B) * H < (1LL << 26) && T <= 0x7fffff00;
+    return H <= (1 << 15) && static_cast<long long>(B) * H < (1LL << 26) && T <= 0x7fff0000;
 }
 
 size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv) {
