@@ -59,7 +59,7 @@ struct LinArgs {
     float *fwd, *rev;                // [B H][segs - 1][DV][DK]: states at the segments' borders
     float *fac;                      // [2][B H][segs]: a segment's decay
     float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
-    float *edge;                     // [B H][8]: <S_T, dS_T> by wave
+    float *edge;                     // [B H][4]: <S_T, dS_T> by wave
     float *head;                     // [B H]: sums of dg over tokens
 };
 
@@ -306,39 +306,89 @@ struct LinSplit {
 };
 
 // state += its chunk's part: S = all S + sum_t (row_t) (col_t weight_t), the rows from LDS and the
-// wave's columns in operand registers.
-template <class P, int C, int NS, int D>
-__device__ __forceinline__ void lin_update(f32x4 (&S)[D / 16], LinTile<P, C, D> &rows, const typename P::F (&col)[C / 32][2],
-                                           const float *weight, float all, int lane) {
+// wave's columns, NC tiles of 16, in operand registers.
+template <class P, int C, int NS, int D, int NC>
+__device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C, D> &rows,
+                                           const typename P::F (&col)[NC][C / 32][2], const float *weight, float all, int lane) {
     const int g4 = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < D / 16; ++b) S[b] *= all;
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) S[c][b] *= all;
 #pragma unroll
     for (int u = 0; u < C / 32; ++u) {
-        LinSplit<P, NS> lo, hi;
-        lo.of(P::f32(col[u][0]) * lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(0, lane)));
-        hi.of(P::f32(col[u][1]) * lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(1, lane)));
+        LinSplit<P, NS> lo[NC], hi[NC];
+        const f32x4 w0 = lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(0, lane));
+        const f32x4 w1 = lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(1, lane));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            lo[c].of(P::f32(col[c][u][0]) * w0);
+            hi[c].of(P::f32(col[c][u][1]) * w1);
+        }
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
             const typename P::F r0 = rows.across(u, 0, b, lane), r1 = rows.across(u, 1, b, lane);
 #pragma unroll
-            for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[b] = P::mma2(S[b], r0, r1, lo.p[j], hi.p[j]);
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[c][b] = P::mma2(S[c][b], r0, r1, lo[c].p[j], hi[c].p[j]);
         }
     }
 }
 
-// A 16-token tile's product with the state (NS addends of it): four columns of one token a lane.
-template <class P, int NS, int C, int D>
-__device__ __forceinline__ f32x4 lin_read(const LinSplit<P, NS> (&sf)[D / 16], LinTile<P, C, D> &rows, int r0, int lane) {
-    f32x4 acc = zero4();
+// The chunk's rows with the state (NS addends of it): acc[c][i] gets four columns of one token a
+// lane, token 16 i + l % 16.
+template <class P, int NS, int C, int D, int NC>
+__device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (&S)[NC][D / 16], LinTile<P, C, D> &rows, int lane) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i) acc[c][i] = zero4();
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
-        typename P::F x0, x1;
-        rows.oct(r0, u, lane, x0, x1);
+        LinSplit<P, NS> s0[NC], s1[NC];
 #pragma unroll
-        for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j) acc = P::mma2(acc, sf[2 * u].p[j], sf[2 * u + 1].p[j], x0, x1);
+        for (int c = 0; c < NC; ++c) {
+            s0[c].of(S[c][2 * u]);
+            s1[c].of(S[c][2 * u + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i) {
+            typename P::F x0, x1;
+            rows.oct(16 * i, u, lane, x0, x1);
+#pragma unroll
+            for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[c][i] = P::mma2(acc[c][i], s0[c].p[j], s1[c].p[j], x0, x1);
+        }
     }
-    return acc;
+}
+
+// The wave's columns of a tile as operands: from column c0 on, 16 a tile.
+template <class P, int C, int D, int NC>
+__device__ __forceinline__ void lin_columns(typename P::F (&col)[NC][C / 32][2], LinTile<P, C, D> &rows, int c0, int lane) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int u = 0; u < C / 32; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) col[c][u][e] = rows.down(u, e, c0 + 16 * c, lane);
+}
+
+// acc += the chunk's own part: the rows of p (element [token][other token]) with the columns.
+// LOWER: others up to the token; else from the token on.
+template <class P, bool LOWER, int C, int NC>
+__device__ __forceinline__ void lin_near(f32x4 (&acc)[NC][C / 16], LinTile<P, C, C> &p, const typename P::F (&col)[NC][C / 32][2],
+                                         int lane) {
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i)
+#pragma unroll
+        for (int u = LOWER ? 0 : i / 2; u < (LOWER ? i / 2 + 1 : C / 32); ++u) {
+            typename P::F p0, p1;
+            p.oct(16 * i, u, lane, p0, p1);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[c][i] = P::mma2(acc[c][i], col[c][u][0], col[c][u][1], p0, p1);
+        }
 }
 
 // A 16 x 16 block of products of LDS rows: lane l gets rows r0 + 4 (l / 16) + i with row c0 + l % 16.
@@ -358,6 +408,21 @@ __device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C,
 // First of the four rows that tile t of a state has in this lane
 __device__ __forceinline__ int lin_row(int t, int lane) { return 32 * (t >> 1) + 8 * (lane >> 4) + lin_half(t & 1, lane); }
 
+// A state's tiles from and to [columns][D]: the lane's column, four rows at a time
+template <int D>
+__device__ __forceinline__ void lin_load(f32x4 (&S)[D / 16], const float *from, int col, int lane) {
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) S[t] = zero4();
+    if (!from) return;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) S[t] = *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col) * D + lin_row(t, lane));
+}
+template <int D>
+__device__ __forceinline__ void lin_keep(const f32x4 (&S)[D / 16], float *to, int col, int lane) {
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col) * D + lin_row(t, lane)) = S[t];
+}
+
 // Lower block triangle of at most four rows, row by row: p -> (i, j), j <= i
 __device__ __forceinline__ void lin_pair(int p, int &i, int &j) {
     i = (p >= 1) + (p >= 3) + (p >= 6);
@@ -367,15 +432,6 @@ __device__ __forceinline__ void lin_pair(int p, int &i, int &j) {
 __device__ __forceinline__ int lin_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 // Two waves a SIMD: what the LDS leaves room for, and registers for loads ahead
 #define LIN_TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
-
-// Four consecutive elements to a buffer (dropped past its end)
-template <class P>
-__device__ __forceinline__ void lin_store4(__amdgpu_buffer_rsrc_t rs, int off, f32x4 v) {
-    if constexpr (P::kBytes == 2)
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(lin_u32x2, P::cvt(v)), rs, off, 0, 0);
-    else
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(lin_u32x4, v), rs, off, 0, 0);
-}
 
 // Tokens of sequence b
 __device__ __forceinline__ int lin_len(const LinArgs &a, int b) { return a.lens ? min(max(a.lens[b], 0), a.T) : a.T; }

@@ -23,21 +23,6 @@ __device__ __forceinline__ bool lin_place(int units, int ncb, int &unit, int &cb
 }
 dim3 lin_grid(long long units, int ncb) { return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * ncb)); }
 
-// The state's tiles from and to [DV][DK]: wave's column, four rows at a time
-template <int DK>
-__device__ __forceinline__ void load_state(f32x4 (&S)[DK / 16], const float *from, int col, int lane) {
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-        S[t] = from ? *reinterpret_cast<const f32x4 *>(from + static_cast<size_t>(col) * DK + lin_row(t, lane))
-                    : zero4();
-}
-template <int DK>
-__device__ __forceinline__ void store_state(const f32x4 (&S)[DK / 16], float *to, int col, int lane) {
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-        *reinterpret_cast<f32x4 *>(to + static_cast<size_t>(col) * DK + lin_row(t, lane)) = S[t];
-}
-
 // Eight waves in two roles, a barrier a step.  At step n waves 0-3 hold the state and do chunk n's
 // part with it: the outputs, then the state's update.  Waves 4-7 are ahead of them: they form P of
 // chunk n + 1 and bring chunk n + 2 from the registers, where the loads of the step before put it,
@@ -134,8 +119,8 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
 
     const size_t state = static_cast<size_t>(a.DV) * DK;
     const int col = 64 * cb + 16 * wave + r16;
-    f32x4 S[DK / 16];
-    load_state<DK>(S, seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
+    f32x4 S[1][DK / 16];
+    lin_load<DK>(S[0], seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
                    col, lane);
     __syncthreads();
     __syncthreads();
@@ -144,33 +129,22 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         LinTile<P, C, DK> &q = lds.q[now], &k = lds.k[now];
         LinTile<P, C, C> &p = lds.p[(n - c0) & 1];
         const LinGates<C> &gates = lds.gates[now];
-        typename P::F vf[C / 32][2];
+        typename P::F vf[1][C / 32][2];
+        lin_columns<P, C>(vf, lds.v[now], 16 * wave, lane);
+        f32x4 acc[1][C / 16];
+        lin_read<P, 1>(acc, S, q, lane);
 #pragma unroll
-        for (int u = 0; u < C / 32; ++u)
+        for (int i = 0; i < C / 16; ++i) acc[0][i] *= gates.before[16 * i + r16];
+        lin_near<P, true>(acc, p, vf, lane);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[now].down(u, e, 16 * wave, lane);
-        LinSplit<P, 1> sf[DK / 16];
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t) sf[t].of(S[t]);
-#pragma unroll
-        for (int i = 0; i < C / 16; ++i) {
-            f32x4 acc = lin_read<P>(sf, q, 16 * i, lane);
-            acc *= gates.before[16 * i + r16];
-#pragma unroll
-            for (int u = 0; u <= i / 2; ++u) {
-                typename P::F p0, p1;
-                p.oct(16 * i, u, lane, p0, p1);
-                acc = P::mma2(acc, vf[u][0], vf[u][1], p0, p1);
-            }
-            P::st4(lds.o[(n - c0) & 1].four(16 * i + r16, 16 * wave + 4 * g4), acc);
-        }
-        lin_update<P, C, NS, DK>(S, k, vf, gates.after, gates.all[0], lane);
+        for (int i = 0; i < C / 16; ++i) P::st4(lds.o[(n - c0) & 1].four(16 * i + r16, 16 * wave + 4 * g4), acc[0][i]);
+        lin_update<P, C, NS>(S, k, vf, gates.after, gates.all[0], lane);
         now = now == 2 ? 0 : now + 1;
         __syncthreads();
     }
     __syncthreads();                             // the last chunk's outputs go in a step of their own
     if (!((c1 - c0) & 1)) __syncthreads();       // and that role goes by pairs of steps
-    if (a.S_T && seg == a.segs - 1) store_state<DK>(S, a.S_T + bh * state, col, lane);
+    if (a.S_T && seg == a.segs - 1) lin_keep<DK>(S[0], a.S_T + bh * state, col, lane);
 }
 
 // The states alone, from zero (or S0, dS_T) over one segment: forwards with k, v and the decay to
@@ -204,8 +178,8 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
     const size_t state = static_cast<size_t>(a.DV) * DK;
     const int col = 64 * cb + 16 * wave + r16;
 
-    f32x4 S[DK / 16];
-    load_state<DK>(S, rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
+    f32x4 S[1][DK / 16];
+    lin_load<DK>(S[0], rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
                           : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr), col, lane);
     LinRows<P, C, DK, kNT> rk;
     LinRows<P, C, 64, kNT> rv;
@@ -232,15 +206,12 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
             if (m + 2 < count) fetch(m + 2);
         }
         const LinGates<C> &gates = lds.gates[m & 1];
-        typename P::F vf[C / 32][2];
-#pragma unroll
-        for (int u = 0; u < C / 32; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) vf[u][e] = lds.v[m & 1].down(u, e, 16 * wave, lane);
-        lin_update<P, C, NS, DK>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
+        typename P::F vf[1][C / 32][2];
+        lin_columns<P, C>(vf, lds.v[m & 1], 16 * wave, lane);
+        lin_update<P, C, NS>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
         __syncthreads();
     }
-    store_state<DK>(S, (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, lane);
+    lin_keep<DK>(S[0], (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, lane);
     if (cb == 0 && wave == 3 && lane == 0)
         a.fac[(static_cast<size_t>(rev) * bhs + bh) * a.segs + seg] = lin_exp2(static_cast<float>(total));
 }

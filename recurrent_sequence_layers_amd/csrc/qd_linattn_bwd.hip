@@ -31,93 +31,6 @@
 namespace qd {
 namespace {
 
-template <class P, int DK, int DV>
-struct BwdLds {
-    static constexpr int C = kLinChunk<P>, NW = (DK > DV ? DK : DV) / 16, NT = 64 * NW;
-    static constexpr int NB = (C / 16) * (C / 16 + 1) / 2;
-    using QK = LinRows<P, C, DK, NT>;
-    using VV = LinRows<P, C, DV, NT>;
-    LinTile<P, C, DK> q, k;
-    LinTile<P, C, DV> v, o;
-    LinTile<P, C, C> p[2];
-    LinGates<C> gates;
-    float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
-    float part[NW][C];                 // a or b, by the columns' wave
-};
-
-// Where a walk reads and writes.
-template <class P, int DK, int DV>
-struct Walk {
-    using L = BwdLds<P, DK, DV>;
-    static constexpr int C = L::C, NT = L::NT;
-    const LinArgs &a;
-    int b, h, bh, seg, c0, c1, len, tid, wave, lane, g4, r16;
-    size_t sdk, sdv;
-    const char *gq, *gk, *gv, *go;
-    typename L::QK rq, rk;
-    typename L::VV rv, ro;
-    float gate = 0.f;
-
-    __device__ __forceinline__ Walk(const LinArgs &a_, int unit) : a(a_) {
-        seg = unit % a.segs;
-        bh = unit / a.segs;
-        b = bh / a.H;
-        h = bh % a.H;
-        tid = threadIdx.x;
-        wave = lin_wave();
-        lane = lane_id();
-        g4 = lane >> 4;
-        r16 = lane & 15;
-        len = lin_len(a, b);
-        c0 = seg * a.seg_chunks;
-        c1 = min(c0 + a.seg_chunks, (a.T + C - 1) / C);
-        sdk = static_cast<size_t>(a.H) * DK * P::kBytes;
-        sdv = static_cast<size_t>(a.H) * DV * P::kBytes;
-        gq = static_cast<const char *>(a.q) + at(0, sdk, DK);
-        gk = static_cast<const char *>(a.k) + at(0, sdk, DK);
-        gv = static_cast<const char *>(a.v) + at(0, sdv, DV);
-        go = static_cast<const char *>(a.d_o) + at(0, sdv, DV);
-    }
-    __device__ __forceinline__ size_t at(int t, size_t stride, int d) const {
-        return (static_cast<size_t>(b) * a.T + t) * stride + static_cast<size_t>(h) * d * P::kBytes;
-    }
-    __device__ __forceinline__ int live(int n) const { return min(max(len - n * C, 0), C); }
-    __device__ __forceinline__ void fetch(int n) {
-        const int t0 = n * C, rows = live(n);
-        rq.load(gq + static_cast<size_t>(t0) * sdk, rows, static_cast<int>(sdk), tid);
-        rk.load(gk + static_cast<size_t>(t0) * sdk, rows, static_cast<int>(sdk), tid);
-        rv.load(gv + static_cast<size_t>(t0) * sdv, rows, static_cast<int>(sdv), tid);
-        ro.load(go + static_cast<size_t>(t0) * sdv, rows, static_cast<int>(sdv), tid);
-        if (wave == 0) gate = lin_gate(a, b, h, t0, rows, lane);
-    }
-    __device__ __forceinline__ void put(L &lds) const {
-        rq.put(lds.q, tid);
-        rk.put(lds.k, tid);
-        rv.put(lds.v, tid);
-        ro.put(lds.o, tid);
-        if (wave == 0) lin_gates(lds.gates, gate, lane);
-    }
-    // Output rows of chunk n, padding's included: they are written as zeros
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t out(void *base, int n, size_t stride, int d) const {
-        const int rows = min(a.T - n * C, C);
-        return lin_rsrc(static_cast<char *>(base) + at(n * C, stride, d), (rows - 1) * static_cast<int>(stride) + d * P::kBytes);
-    }
-    __device__ __forceinline__ float *tok(int which, int n) const {
-        return a.tok + (static_cast<size_t>(which) * a.B * a.H + bh) * a.T + n * C;
-    }
-};
-
-// a or b of one row: the product of the state's part with the row's own q or k, summed over columns
-template <class P, int C, int D>
-__device__ __forceinline__ void row_part(float *part, LinTile<P, C, D> &rows, int row, int col, f32x4 acc, int lane) {
-    const f32x4 y = P::f32(P::ld4(rows.four(row, col)));
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s = fmaf(acc[e], y[e], s);
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < 16) part[row] = s;
-}
 __device__ __forceinline__ float sum16(float x) {
     x += dpp_src<0xB1, 0xf>(x);    // quad_perm 1,0,3,2
     x += dpp_src<0x4E, 0xf>(x);    // quad_perm 2,3,0,1
@@ -125,237 +38,371 @@ __device__ __forceinline__ float sum16(float x) {
     return x + dpp_src<0x140, 0xf>(x);   // row_mirror
 }
 
+// Twelve waves, two barriers a chunk.  In either walk four waves hold a state, a quarter of its
+// columns each (backwards four more hold it by its other columns): in a chunk's first interval they
+// form its outputs, in the second they update the state.  The other waves meanwhile bring the next
+// chunk: first from the registers, where its loads went a chunk before, to LDS, then its decayed
+// products P.  Outputs wait in registers for the second interval, go to a tile of their chunk that
+// nobody reads any more (dq to q, dk to k, dv to v) and leave in whole rows, each thread storing
+// the pieces that it is about to replace.
+constexpr int kBwdThreads = 768;
+template <class P, int DK, int DV>
+struct BwdLds {
+    static constexpr int C = kLinChunk<P>, NB = (C / 16) * (C / 16 + 1) / 2;
+    struct Chunk {
+        LinTile<P, C, DK> q, k;
+        LinTile<P, C, DV> v, o;
+        LinGates<C> gates;
+    } c[2];
+    LinTile<P, C, C> p[2];
+    float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
+    float part[4][C];                  // a or b, by the columns' wave
+};
+
+// Where a workgroup walks, and its tensors' first bytes.
+template <class P, int DK, int DV>
+struct Walk {
+    static constexpr int C = kLinChunk<P>;
+    const LinArgs &a;
+    int b, h, bh, seg, c0, count, len, role, wave, lane, g4, r16;   // role: waves 0-3, 4-7, 8-11
+    size_t sdk, sdv;
+
+    __device__ __forceinline__ Walk(const LinArgs &a_, int unit) : a(a_) {
+        seg = unit % a.segs;
+        bh = unit / a.segs;
+        b = bh / a.H;
+        h = bh % a.H;
+        role = lin_wave() >> 2;
+        wave = lin_wave() & 3;
+        lane = lane_id();
+        g4 = lane >> 4;
+        r16 = lane & 15;
+        len = lin_len(a, b);
+        c0 = seg * a.seg_chunks;
+        count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
+        sdk = static_cast<size_t>(a.H) * DK * P::kBytes;
+        sdv = static_cast<size_t>(a.H) * DV * P::kBytes;
+    }
+    // The m-th chunk of the walk
+    template <bool REV>
+    __device__ __forceinline__ int chunk(int m) const { return REV ? c0 + count - 1 - m : c0 + m; }
+    __device__ __forceinline__ int live(int n) const { return min(max(len - n * C, 0), C); }
+    __device__ __forceinline__ size_t at(int t, size_t stride, int d) const {
+        return (static_cast<size_t>(b) * a.T + t) * stride + static_cast<size_t>(h) * d * P::kBytes;
+    }
+    // Output rows of chunk n, padding's included: those are written as zeros
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t out(void *base, int n, bool valid, size_t stride, int d) const {
+        const int rows = min(a.T - n * C, C);
+        return lin_rsrc(static_cast<char *>(base) + (valid ? at(n * C, stride, d) : 0),
+                        valid ? (rows - 1) * static_cast<int>(stride) + d * P::kBytes : 0);
+    }
+    // One of the terms of dg for chunk n: a thread a token
+    __device__ __forceinline__ void term(int which, int n, bool valid, int tid, float v) const {
+        const float *to = a.tok + (static_cast<size_t>(which) * a.B * a.H + bh) * a.T + (valid ? n * C : 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), lin_rsrc(to, valid ? min(a.T - n * C, C) * 4 : 0),
+                                              tid * 4, 0, 0);
+    }
+};
+
+// The loading waves, NW of them; `wave` counts from the first.  REV: the walk goes backwards and
+// forms P by its earlier tokens' rows, of q k and of do v; else by its later tokens' rows, of do v.
+template <class P, int DK, int DV, bool REV, bool DG, int NW>
+__device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
+    using L = BwdLds<P, DK, DV>;
+    constexpr int C = L::C, NB = L::NB, NT = 64 * NW;
+    const LinArgs &a = w.a;
+    const int sdk = static_cast<int>(w.sdk), sdv = static_cast<int>(w.sdv), tid = 64 * wave + w.lane;
+    LinRows<P, C, DK, NT> rq, rk;
+    LinRows<P, C, DV, NT> rv, ro;
+    float gate;
+    // every step has the same loads and stores, those past the walk's ends of nothing: with a
+    // branch around stores the waits for older loads would wait for them too
+    auto fetch = [&](int m) {
+        const int n = m < w.count ? w.template chunk<REV>(m) : w.c0, t0 = n * C, live = m < w.count ? w.live(n) : 0;
+        rq.load(static_cast<const char *>(a.q) + w.at(t0, w.sdk, DK), live, sdk, tid);
+        rk.load(static_cast<const char *>(a.k) + w.at(t0, w.sdk, DK), live, sdk, tid);
+        rv.load(static_cast<const char *>(a.v) + w.at(t0, w.sdv, DV), live, sdv, tid);
+        ro.load(static_cast<const char *>(a.d_o) + w.at(t0, w.sdv, DV), live, sdv, tid);
+        gate = lin_gate(a, w.b, w.h, t0, live, w.lane);
+    };
+    auto emit = [&](int m) {                     // the outputs of chunk m - 1, from the tiles of chunk m + 1
+        const bool valid = m >= 1 && m <= w.count;
+        const int n = valid ? w.template chunk<REV>(m - 1) : 0;
+        typename L::Chunk &c = lds.c[(m + 1) & 1];
+        if constexpr (REV) {
+            lin_store<P, C, DK, NT>(c.k, w.out(a.dk, n, valid, w.sdk, DK), sdk, tid);
+            lin_store<P, C, DV, NT>(c.v, w.out(a.dv, n, valid, w.sdv, DV), sdv, tid);
+        } else {
+            lin_store<P, C, DK, NT>(c.q, w.out(a.dq, n, valid, w.sdk, DK), sdk, tid);
+        }
+    };
+    fetch(0);
+    for (int m = -1; m < w.count; ++m) {
+        const bool valid = m >= 0;
+        const int n = valid ? w.template chunk<REV>(m) : 0;
+        typename L::Chunk &next = lds.c[(m + 1) & 1];
+        emit(m);
+        rq.put(next.q, tid);
+        rk.put(next.k, tid);
+        rv.put(next.v, tid);
+        ro.put(next.o, tid);
+        if (wave == NW - 1) lin_gates(next.gates, gate, w.lane);
+        fetch(m + 2);
+        if constexpr (DG && !REV) {
+            const int i = (tid >> 4) & (C / 16 - 1), e = tid & 15;
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < C / 16; ++j) {
+                if (j >= i) x += lds.cols[j * (j + 1) / 2 + i][e];
+                if (j <= i) x -= lds.rows[i * (i + 1) / 2 + j][e];
+            }
+            w.term(0, n, valid, tid, x);
+        }
+        __syncthreads();
+        for (int p = wave; p < NB; p += NW) {
+            int i, j;
+            lin_pair(p, i, j);                   // later tokens in block i, earlier ones in block j
+            if constexpr (REV) {
+                f32x4 qk = lin_block<P>(next.q, next.k, 16 * i, 16 * j, w.lane);
+                f32x4 ov = lin_block<P>(next.o, next.v, 16 * i, 16 * j, w.lane);
+                const int t = 16 * j + w.r16, s = 16 * i + 4 * w.g4;
+                const f32x4 hi = lds_f32x4(next.gates.hi + s) - next.gates.hi[t], lo = lds_f32x4(next.gates.lo + s) - next.gates.lo[t];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float d = lin_exp2(hi[e] + lo[e]);
+                    qk[e] = t <= s + e ? d * qk[e] : 0.f;
+                    ov[e] = t <= s + e ? d * ov[e] : 0.f;
+                }
+                P::st4(lds.p[0].four(t, s), qk);
+                P::st4(lds.p[1].four(t, s), ov);
+            } else {
+                f32x4 ov = lin_block<P>(next.v, next.o, 16 * j, 16 * i, w.lane);
+                const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
+                const f32x4 d = lin_between(next.gates, s, t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? d[e] * ov[e] : 0.f;
+                P::st4(lds.p[0].four(s, t), ov);
+                if constexpr (DG) {
+                    const f32x4 qk = lin_block<P>(next.k, next.q, 16 * j, 16 * i, w.lane);
+                    float row = 0.f;
+                    f32x4 col;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = t + e < s ? ov[e] * qk[e] : 0.f;
+                        row += x;
+                        col[e] = sum16(x);
+                    }
+                    row += __shfl_xor(row, 16);
+                    row += __shfl_xor(row, 32);
+                    if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
+                    if (w.lane < 16) lds.rows[p][w.r16] = row;
+                }
+            }
+        }
+        if constexpr (DG) {
+            const int t = tid & (C - 1);
+            w.term(REV ? 2 : 1, n, valid, tid, (lds.part[0][t] + lds.part[1][t]) + (lds.part[2][t] + lds.part[3][t]));
+        }
+        __syncthreads();
+    }
+    emit(w.count);
+}
+
+// a or b: the state's part of each output row with the row's own q or k, over a wave's columns
+template <class P, int C, int D, int NC>
+__device__ __forceinline__ void row_parts(float *part, LinTile<P, C, D> &rows, const f32x4 (&acc)[NC][C / 16], int c0, int lane) {
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const f32x4 y = P::f32(P::ld4(rows.four(16 * i + (lane & 15), c0 + 16 * c + 4 * (lane >> 4))));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = fmaf(acc[c][i][e], y[e], s);
+        }
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lane < 16) part[16 * i + lane] = s;
+    }
+}
+template <int C, int NC>
+__device__ __forceinline__ void scale(f32x4 (&acc)[NC][C / 16], const float *w, int r16) {
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i) {
+        const float x = w[16 * i + r16];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c][i] *= x;
+    }
+}
+// Outputs as elements, zeros in padding
+template <class P, int C, int NC>
+__device__ __forceinline__ void pack(typename P::F (&out)[NC][C / 16], const f32x4 (&acc)[NC][C / 16], int live, int r16) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i) out[c][i] = P::cvt(16 * i + r16 < live ? acc[c][i] : zero4());
+}
+template <class P, int C, int D, int NC>
+__device__ __forceinline__ void spill_out(LinTile<P, C, D> &to, const typename P::F (&out)[NC][C / 16], int c0, int lane) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i)
+            *reinterpret_cast<typename P::F *>(to.four(16 * i + (lane & 15), c0 + 16 * c + 4 * (lane >> 4))) = out[c][i];
+}
+// A state whose columns are key indices, from and to [DV][DK]
+template <int DK, int DV, int NC>
+__device__ __forceinline__ void load_across(f32x4 (&S)[NC][DV / 16], const float *from, int c0, int lane) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t) S[c][t] = zero4();
+    if (!from) return;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[c][t][e] = from[(lin_row(t, lane) + e) * DK + c0 + 16 * c + (lane & 15)];
+}
+
 // ---------------------------------------------------------------- dq, forwards
 template <class P, int DK, int DV, bool DG>
 __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     using L = BwdLds<P, DK, DV>;
-    constexpr int C = L::C, NB = L::NB, NW = L::NW, KC = DK / 16;
-    Walk<P, DK, DV> w(a, unit);
-    const int wave = w.wave, lane = w.lane, g4 = w.g4, r16 = w.r16;
-    const bool mine = wave < KC;
+    constexpr int C = L::C, NC = DK / 64;
+    const Walk<P, DK, DV> w(a, unit);
+    if (w.role > 0) return bring<P, DK, DV, false, DG, 8>(w, lds, w.wave + 4 * (w.role - 1));
+    const int lane = w.lane, c0 = 16 * NC * w.wave;
     const size_t state = static_cast<size_t>(DV) * DK;
-    const int col = 16 * wave + r16;             // key column of the state
-    f32x4 S[DV / 16];
-    const float *from = w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
-                                  : a.S0 ? a.S0 + w.bh * state : nullptr;
-#pragma unroll
-    for (int t = 0; t < DV / 16; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[t][e] = from && mine ? from[(lin_row(t, lane) + e) * DK + col] : 0.f;
-    for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = 0;
-    w.fetch(w.c0);
-    for (int n = w.c0; n < w.c1; ++n) {
-        __syncthreads();
-        w.put(lds);
-        __syncthreads();
-        if (n + 1 < w.c1) w.fetch(n + 1);
-        const int live = w.live(n);
-        for (int p = wave; p < NB; p += NW) {
-            int i, j;
-            lin_pair(p, i, j);
-            f32x4 acc = lin_block<P>(lds.v, lds.o, 16 * j, 16 * i, lane);
-            const int s = 16 * i + r16, t = 16 * j + 4 * g4;
-            const f32x4 d = lin_between(lds.gates, s, t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
-            P::st4(lds.p[0].four(s, t), acc);
-            if constexpr (DG) {
-                const f32x4 qk = lin_block<P>(lds.k, lds.q, 16 * j, 16 * i, lane);
-                float row = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float m = t + e < s ? acc[e] * qk[e] : 0.f;
-                    row += m;
-                    const float c = sum16(m);
-                    if (r16 == 0) lds.cols[p][4 * g4 + e] = c;
-                }
-                row += __shfl_xor(row, 16);
-                row += __shfl_xor(row, 32);
-                if (lane < 16) lds.rows[p][r16] = row;
-            }
+    f32x4 S[NC][DV / 16];
+    load_across<DK, DV>(S, w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
+                                     : a.S0 ? a.S0 + w.bh * state : nullptr, c0, lane);
+    __syncthreads();                             // the first chunk is brought
+    __syncthreads();
+    for (int m = 0; m < w.count; ++m) {
+        typename L::Chunk &x = lds.c[m & 1];
+        typename P::F kf[NC][C / 32][2], out[NC][C / 16];
+        {
+            f32x4 acc[NC][C / 16];
+            lin_columns<P, C>(kf, x.k, c0, lane);
+            lin_read<P, DG ? 3 : 1>(acc, S, x.o, lane);
+            scale<C>(acc, x.gates.before, w.r16);
+            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.q, acc, c0, lane);
+            lin_near<P, true>(acc, lds.p[0], kf, lane);
+            pack<P, C>(out, acc, w.live(w.c0 + m), w.r16);
         }
         __syncthreads();
-        if (mine) {
-            typename P::F kf[C / 32][2];
-#pragma unroll
-            for (int u = 0; u < C / 32; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) kf[u][e] = lds.k.down(u, e, 16 * wave, lane);
-            LinSplit<P, DG ? 3 : 1> sf[DV / 16];
-#pragma unroll
-            for (int t = 0; t < DV / 16; ++t) sf[t].of(S[t]);
-            const __amdgpu_buffer_rsrc_t rs = w.out(a.dq, n, w.sdk, DK);
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) {
-                const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.o, 16 * i, lane);
-                acc *= lds.gates.before[row];
-                if constexpr (DG) row_part<P>(lds.part[wave], lds.q, row, 16 * wave + 4 * g4, acc, lane);
-#pragma unroll
-                for (int u = 0; u <= i / 2; ++u) {
-                    typename P::F p0, p1;
-                    lds.p[0].oct(16 * i, u, lane, p0, p1);
-                    acc = P::mma2(acc, kf[u][0], kf[u][1], p0, p1);
-                }
-                lin_store4<P>(rs, row * static_cast<int>(w.sdk) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
-            }
-            lin_update<P, C, 3, DV>(S, lds.v, kf, lds.gates.after, lds.gates.all[0], lane);
-        }
-        if constexpr (DG) {
-            __syncthreads();
-            if (w.tid < C && n * C + w.tid < a.T) {
-                const int i = w.tid >> 4, r = w.tid & 15;
-                float x = 0.f, s = 0.f;
-                for (int m = i; m < C / 16; ++m) x += lds.cols[m * (m + 1) / 2 + i][r];
-                for (int m = 0; m <= i; ++m) x -= lds.rows[i * (i + 1) / 2 + m][r];
-#pragma unroll
-                for (int m = 0; m < KC; ++m) s += lds.part[m][w.tid];
-                w.tok(0, n)[w.tid] = x;
-                w.tok(1, n)[w.tid] = s;
-            }
-        }
+        spill_out<P, C>(x.q, out, c0, lane);
+        lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, x.gates.after, x.gates.all[0], lane);
+        __syncthreads();
     }
     if constexpr (DG) {
         if (w.seg == a.segs - 1) {               // <S_T, dS_T>
+            f32x4 d[NC][DV / 16];
+            load_across<DK, DV>(d, a.dS_T ? a.dS_T + w.bh * state : nullptr, c0, lane);
             float s = 0.f;
-            if (a.dS_T && mine) {
-                const float *d = a.dS_T + w.bh * state;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int t = 0; t < DV / 16; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(S[t][e], d[(lin_row(t, lane) + e) * DK + col], s);
-            }
-            for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-            if (lane == 0) a.edge[static_cast<size_t>(w.bh) * 8 + wave] = s;
+                    for (int e = 0; e < 4; ++e) s = fmaf(S[c][t][e], d[c][t][e], s);
+            for (int k = 1; k < 64; k *= 2) s += __shfl_xor(s, k);
+            if (lane == 0) a.edge[static_cast<size_t>(w.bh) * 4 + w.wave] = s;
         }
     }
 }
 
 // ---------------------------------------------------------------- dk and dv, backwards
-template <class P, int DK, int DV, bool DG>
-__device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
+// dv: the gradient's columns are value indices.
+template <class P, int DK, int DV>
+__device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, const float *from) {
     using L = BwdLds<P, DK, DV>;
-    constexpr int C = L::C, NB = L::NB, NW = L::NW, KC = DK / 16, VC = DV / 16;
-    Walk<P, DK, DV> w(a, unit);
-    const int wave = w.wave, lane = w.lane, g4 = w.g4, r16 = w.r16;
-    const bool mine_k = wave < KC, mine_v = wave < VC;
-    const size_t state = static_cast<size_t>(DV) * DK;
-    const int col = 16 * wave + r16;
-    f32x4 Rv[KC], Rk[VC];                        // columns are value indices; key indices
-    const float *from = w.seg < a.segs - 1 ? a.rev + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg) * state
-                                           : a.dS_T ? a.dS_T + w.bh * state : nullptr;
+    constexpr int C = L::C, NC = DV / 64;
+    const int lane = w.lane, c0 = 16 * NC * w.wave;
+    f32x4 R[NC][DK / 16];
 #pragma unroll
-    for (int t = 0; t < KC; ++t)
-        Rv[t] = from && mine_v ? *reinterpret_cast<const f32x4 *>(from + col * DK + lin_row(t, lane)) : zero4();
-#pragma unroll
-    for (int t = 0; t < VC; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            Rk[t][e] = from && mine_k ? from[(lin_row(t, lane) + e) * DK + col] : 0.f;
-    for (int e = w.tid; e < LinTile<P, C, C>::kElems; e += L::NT) lds.p[0].m[e] = lds.p[1].m[e] = 0;
-    w.fetch(w.c1 - 1);
-    for (int n = w.c1 - 1; n >= w.c0; --n) {
-        __syncthreads();
-        w.put(lds);
-        __syncthreads();
-        if (n > w.c0) w.fetch(n - 1);
-        const int live = w.live(n);
-        // by the earlier token t's row: p[0] for dv, p[1] for dk
-        for (int p = wave; p < NB; p += NW) {
-            int i, j;
-            lin_pair(p, i, j);                        // s in block i, t in block j
-            const int t = 16 * j + r16, s = 16 * i + 4 * g4;
-            f32x4 qk = lin_block<P>(lds.q, lds.k, 16 * i, 16 * j, lane);
-            f32x4 ov = lin_block<P>(lds.o, lds.v, 16 * i, 16 * j, lane);
-            const f32x4 hi = lds_f32x4(lds.gates.hi + s) - lds.gates.hi[t], lo = lds_f32x4(lds.gates.lo + s) - lds.gates.lo[t];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float d = lin_exp2(hi[e] + lo[e]);
-                qk[e] = t <= s + e ? d * qk[e] : 0.f;
-                ov[e] = t <= s + e ? d * ov[e] : 0.f;
-            }
-            P::st4(lds.p[0].four(t, s), qk);
-            P::st4(lds.p[1].four(t, s), ov);
+    for (int c = 0; c < NC; ++c) lin_load<DK>(R[c], from, c0 + 16 * c + w.r16, lane);
+    __syncthreads();                             // the first chunk is brought
+    __syncthreads();
+    for (int m = 0; m < w.count; ++m) {
+        typename L::Chunk &x = lds.c[m & 1];
+        typename P::F of[NC][C / 32][2], out[NC][C / 16];
+        {
+            f32x4 acc[NC][C / 16];
+            lin_columns<P, C>(of, x.o, c0, lane);
+            lin_read<P, 1>(acc, R, x.k, lane);
+            scale<C>(acc, x.gates.after, w.r16);
+            lin_near<P, false>(acc, lds.p[0], of, lane);
+            pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
-        if (mine_v) {
-            typename P::F of[C / 32][2];
-#pragma unroll
-            for (int u = 0; u < C / 32; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) of[u][e] = lds.o.down(u, e, 16 * wave, lane);
-            LinSplit<P, 1> sf[KC];
-#pragma unroll
-            for (int t = 0; t < KC; ++t) sf[t].of(Rv[t]);
-            const __amdgpu_buffer_rsrc_t rs = w.out(a.dv, n, w.sdv, DV);
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) {
-                const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.k, 16 * i, lane);
-                acc *= lds.gates.after[row];
-#pragma unroll
-                for (int u = i / 2; u < C / 32; ++u) {
-                    typename P::F p0, p1;
-                    lds.p[0].oct(16 * i, u, lane, p0, p1);
-                    acc = P::mma2(acc, of[u][0], of[u][1], p0, p1);
-                }
-                lin_store4<P>(rs, row * static_cast<int>(w.sdv) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
-            }
-            lin_update<P, C, 2, DK>(Rv, lds.q, of, lds.gates.before, lds.gates.all[0], lane);
-        }
-        if (mine_k) {
-            typename P::F qf[C / 32][2];
-#pragma unroll
-            for (int u = 0; u < C / 32; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) qf[u][e] = lds.q.down(u, e, 16 * wave, lane);
-            LinSplit<P, DG ? 3 : 1> sf[VC];
-#pragma unroll
-            for (int t = 0; t < VC; ++t) sf[t].of(Rk[t]);
-            const __amdgpu_buffer_rsrc_t rs = w.out(a.dk, n, w.sdk, DK);
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) {
-                const int row = 16 * i + r16;
-                f32x4 acc = lin_read<P>(sf, lds.v, 16 * i, lane);
-                acc *= lds.gates.after[row];
-                if constexpr (DG) row_part<P>(lds.part[wave], lds.k, row, 16 * wave + 4 * g4, acc, lane);
-#pragma unroll
-                for (int u = i / 2; u < C / 32; ++u) {
-                    typename P::F p0, p1;
-                    lds.p[1].oct(16 * i, u, lane, p0, p1);
-                    acc = P::mma2(acc, qf[u][0], qf[u][1], p0, p1);
-                }
-                lin_store4<P>(rs, row * static_cast<int>(w.sdk) + (16 * wave + 4 * g4) * P::kBytes, row < live ? acc : zero4());
-            }
-            lin_update<P, C, 3, DV>(Rk, lds.o, qf, lds.gates.before, lds.gates.all[0], lane);
-        }
-        if constexpr (DG) {
-            __syncthreads();
-            if (w.tid < C && n * C + w.tid < a.T) {
-                float s = 0.f;
-#pragma unroll
-                for (int m = 0; m < KC; ++m) s += lds.part[m][w.tid];
-                w.tok(2, n)[w.tid] = s;
-            }
-        }
-    }
-    if (a.dS0 && w.seg == 0 && mine_k) {
-        float *to = a.dS0 + w.bh * state;
-#pragma unroll
-        for (int t = 0; t < VC; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[(lin_row(t, lane) + e) * DK + col] = Rk[t][e];
+        spill_out<P, C>(x.v, out, c0, lane);
+        lin_update<P, C, 2>(R, x.q, of, x.gates.before, x.gates.all[0], lane);
+        __syncthreads();
     }
 }
+// dk: its columns are key indices.
+template <class P, int DK, int DV, bool DG, int NS>
+__device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, const float *from) {
+    using L = BwdLds<P, DK, DV>;
+    constexpr int C = L::C, NC = DK / 64;
+    const int lane = w.lane, c0 = 16 * NC * w.wave;
+    f32x4 R[NC][DV / 16];
+    load_across<DK, DV>(R, from, c0, lane);
+    __syncthreads();                             // the first chunk is brought
+    __syncthreads();
+    for (int m = 0; m < w.count; ++m) {
+        typename L::Chunk &x = lds.c[m & 1];
+        typename P::F qf[NC][C / 32][2], out[NC][C / 16];
+        {
+            f32x4 acc[NC][C / 16];
+            lin_columns<P, C>(qf, x.q, c0, lane);
+            lin_read<P, DG ? 3 : 1>(acc, R, x.v, lane);
+            scale<C>(acc, x.gates.after, w.r16);
+            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, c0, lane);
+            lin_near<P, false>(acc, lds.p[1], qf, lane);
+            pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
+        }
+        __syncthreads();
+        spill_out<P, C>(x.k, out, c0, lane);
+        lin_update<P, C, NS>(R, x.o, qf, x.gates.before, x.gates.all[0], lane);
+        __syncthreads();
+    }
+    const LinArgs &a = w.a;
+    if (a.dS0 && w.seg == 0) {
+        float *to = a.dS0 + static_cast<size_t>(w.bh) * DV * DK;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) to[(lin_row(t, lane) + e) * DK + c0 + 16 * c + w.r16] = R[c][t][e];
+    }
+}
+template <class P, int DK, int DV, bool DG, int NS>
+__device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
+    const Walk<P, DK, DV> w(a, unit);
+    if (w.role == 2) return bring<P, DK, DV, true, DG, 4>(w, lds, w.wave);
+    const size_t state = static_cast<size_t>(DV) * DK;
+    const float *from = w.seg < a.segs - 1 ? a.rev + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg) * state
+                                           : a.dS_T ? a.dS_T + w.bh * state : nullptr;
+    if (w.role == 0) dk_walk<P, DK, DV, DG, NS>(w, lds, from);
+    else dv_walk<P, DK, DV>(w, lds, from);
+}
 
-template <class P, int DK, int DV, bool DG>
-__global__ __launch_bounds__(64 * ((DK > DV ? DK : DV) / 16)) LIN_TWO_WAVES void lin_bwd_kernel(const LinArgs a) {
+template <class P, int DK, int DV, bool DG, int NS>
+__global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void lin_bwd_kernel(const LinArgs a) {
+    using L = BwdLds<P, DK, DV>;
     extern __shared__ __align__(16) char smem[];
-    auto &lds = *reinterpret_cast<BwdLds<P, DK, DV> *>(smem);
+    L &lds = *reinterpret_cast<L *>(smem);
+    // blocks of P off its triangle that a pair of tiles reads: never written again
+    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = 0;
+    __syncthreads();
     const int unit = blockIdx.x >> 1;
     if (blockIdx.x & 1) dq_walk<P, DK, DV, DG>(a, lds, unit);
-    else dkv_walk<P, DK, DV, DG>(a, lds, unit);
+    else dkv_walk<P, DK, DV, DG, NS>(a, lds, unit);
 }
 
 // ---------------------------------------------------------------- dg
@@ -373,7 +420,7 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
     auto get = [&](const float *p, int n, int i) { return i < C && n * C + i < a.T ? p[n * C + i] : 0.f; };
     if (threadIdx.x == 0) {
         double e = 0;
-        for (int w = 0; w < (a.DK > a.DV ? a.DK : a.DV) / 16; ++w) e += a.edge[static_cast<size_t>(bh) * 8 + w];
+        for (int w = 0; w < 4; ++w) e += a.edge[static_cast<size_t>(bh) * 4 + w];
         carry = e;
     }
     double total = 0;
@@ -455,9 +502,10 @@ template <class P, int DK, int DV>
 hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
     using L = BwdLds<P, DK, DV>;
     static_assert(sizeof(L) <= 160 * 1024, "LDS of a workgroup");
-    const dim3 grid(static_cast<unsigned>(2LL * a.B * a.H * a.segs)), blk(L::NT);
-    if (a.dg) hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, true>), grid, blk, sizeof(L), stream, a);
-    else hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, false>), grid, blk, sizeof(L), stream, a);
+    const dim3 grid(static_cast<unsigned>(2LL * a.B * a.H * a.segs)), blk(kBwdThreads);
+    if (a.dg) hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, true, 3>), grid, blk, sizeof(L), stream, a);
+    else if (a.dS0) hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, false, 3>), grid, blk, sizeof(L), stream, a);
+    else hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, false, 2>), grid, blk, sizeof(L), stream, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (a.dg) {
         hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
@@ -493,7 +541,7 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     const size_t bh = static_cast<size_t>(B) * H;
     size_t n = 0;
     if (segs > 1) n += 2 * bh * (segs - 1) * dk * dv + 2 * bh * segs;
-    if (dg) n += 3 * bh * T + 9 * bh;
+    if (dg) n += 3 * bh * T + 5 * bh;
     return n * sizeof(float);
 }
 
@@ -521,7 +569,7 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (a.dg) {
         a.tok = p;
         a.edge = a.tok + 3 * bh * a.T;
-        a.head = a.edge + 8 * bh;
+        a.head = a.edge + 4 * bh;
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
 }
