@@ -115,116 +115,133 @@ __device__ __forceinline__ float lin_exp(float x) {
 // bf16: a 16 x 32 block is 64 slots of 16 bytes; columns 8 g .. 8 g + 7 of row r sit in slot
 // 16 g + (r ^ 2 g), their halves swapped for odd g.  A cycle serves 128 bytes: eight lanes of an
 // oct read one g and eight rows; the sixteen lanes of a transposing read take four rows of four
-// g, whose slots and halves all differ; blocks are 1040 bytes apart, so what is written together,
-// sixteen pieces of a row, half by half, differs too.
+// g, whose slots and halves all differ; the 32-column strips are an odd number of slots long, so
+// what is written together, sixteen pieces of a row, half by half, differs too.
 // fp32: rows padded by 16 bytes.
+//
+// An address is a part that depends on the lane alone (LinLane) and one that the compiler knows.
 __device__ __forceinline__ int lin_half(int e, int lane) { return 4 * (e ^ ((lane >> 4) & 1)); }
+
+struct LinLane {
+    int lane, oct, across, down, four;
+    __device__ __forceinline__ LinLane(int l) : lane(l) {
+        const int g = l >> 4, r = l & 15, i = r >> 2, p = r & 3;
+        const int row = 8 * (g & 1) + 4 * (g & 1) + i, strip = (g >> 1) << 9;
+        oct = 8 * (16 * g + (r ^ (2 * g)));
+        // LDS transpose reads: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
+        // lane 4p + q receives element q of chunk p of the rows 0..3
+        across = strip + 8 * (16 * p + (row ^ (2 * p)));
+        down = strip + 8 * (16 * (p >> 1) + (row ^ (2 * (p >> 1)))) + 4 * ((p ^ (p >> 1)) & 1);
+        four = 8 * (16 * (g >> 1) + (r ^ (2 * (g >> 1)))) + 4 * ((g ^ (g >> 1)) & 1);
+    }
+};
 
 template <class P, int ROWS, int COLS>
 struct LinTile {
     using R = typename P::R;
     using F = typename P::F;
     static constexpr bool kSwz = P::kBytes == 2;
-    static constexpr int kBlock = 520, kPitch = COLS + 4;
-    static constexpr int kElems = kSwz ? (ROWS / 16) * (COLS / 32) * kBlock : ROWS * kPitch;
+    static constexpr int kStrip = ROWS / 16 * 512 + 8, kPitch = COLS + 4;
+    static constexpr int kElems = kSwz ? COLS / 32 * kStrip : ROWS * kPitch;
     R m[kElems];
 
-    // four elements of a row, at a column that four divides
-    __device__ __forceinline__ R *four(int row, int col) {
+    // four elements of row 16 i + l % 16 from column 16 t + 4 (l / 16) on
+    __device__ __forceinline__ R *four(int i, int t, const LinLane &l) {
+        if constexpr (kSwz) return m + (t >> 1) * kStrip + 512 * i + 256 * (t & 1) + (l.four ^ (32 * (t & 1)));
+        else return m + (16 * i + (l.lane & 15)) * kPitch + 16 * t + 4 * (l.lane >> 4);
+    }
+    // halves lo, hi of the eight columns 32 u + 8 g + .. of row 16 i + l % 16
+    __device__ __forceinline__ void oct(int i, int u, const LinLane &l, F &lo, F &hi) {
         if constexpr (kSwz) {
-            const int g = (col >> 3) & 3;
-            return m + ((row >> 4) * (COLS / 32) + (col >> 5)) * kBlock + 8 * (16 * g + ((row & 15) ^ (2 * g))) + ((col ^ (g << 2)) & 4);
+            P::ld8(m + u * kStrip + 512 * i + l.oct, lo, hi);
         } else {
-            return m + row * kPitch + col;
+            const R *p = m + (16 * i + (l.lane & 15)) * kPitch + 32 * u + 8 * (l.lane >> 4);
+            lo = P::ld4(p + lin_half(0, l.lane));
+            hi = P::ld4(p + lin_half(1, l.lane));
         }
     }
-    // 16-byte piece c of a row
-    __device__ __forceinline__ void put(int row, int c, lin_u32x4 v) {
+    // half e of the eight rows 32 u + 8 g + .. of column 16 t + l % 16
+    __device__ __forceinline__ F down(int u, int e, int t, const LinLane &l) {
+        if constexpr (kSwz) return transposed(m + (t >> 1) * kStrip + 1024 * u + 256 * (t & 1) + (l.down ^ (32 * ((e ^ t) & 1))));
+        else return P::ld4_strided(m + f32_row(u, e, l) * kPitch + 16 * t + (l.lane & 15), kPitch);
+    }
+    // the same of the column that is row l % 16 of a state's tile t
+    __device__ __forceinline__ F across(int u, int e, int t, const LinLane &l) {
         if constexpr (kSwz) {
-            *reinterpret_cast<lin_u32x2 *>(four(row, 8 * c)) = __builtin_shufflevector(v, v, 0, 1);
-            *reinterpret_cast<lin_u32x2 *>(four(row, 8 * c + 4)) = __builtin_shufflevector(v, v, 2, 3);
+            return transposed(m + (t >> 1) * kStrip + 1024 * u + 4 * (t & 1) + (l.across ^ (32 * e)));
         } else {
-            *reinterpret_cast<lin_u32x4 *>(m + row * kPitch + 4 * c) = v;
+            const int p = (l.lane & 15) >> 2;
+            return P::ld4_strided(m + f32_row(u, e, l) * kPitch + 32 * (t >> 1) + 8 * p + 4 * ((t ^ p) & 1) + (l.lane & 3), kPitch);
         }
     }
-    __device__ __forceinline__ lin_u32x4 get(int row, int c) {
-        if constexpr (kSwz) {
-            const lin_u32x2 x = *reinterpret_cast<const lin_u32x2 *>(four(row, 8 * c));
-            const lin_u32x2 y = *reinterpret_cast<const lin_u32x2 *>(four(row, 8 * c + 4));
-            return __builtin_shufflevector(x, y, 0, 1, 2, 3);
+
+private:
+    __device__ __forceinline__ static int f32_row(int u, int e, const LinLane &l) { return 32 * u + 8 * (l.lane >> 4) + lin_half(e, l.lane); }
+    __device__ __forceinline__ static F transposed(R *p) {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        return __builtin_bit_cast(F, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+    }
+};
+
+// How NT threads share the 16-byte pieces of C rows of COLS elements
+template <class P, int C, int COLS, int NT>
+struct LinPieces {
+    using T = LinTile<P, C, COLS>;
+    static constexpr int kPer = COLS * P::kBytes / 16, N = C * kPer / NT, kRows = NT / kPer;
+    static_assert(C * kPer % NT == 0 && N >= 1 && (!T::kSwz || kRows % 16 == 0), "pieces must divide over the threads");
+    int row, c;
+    __device__ __forceinline__ LinPieces(int tid) : row(tid / kPer), c(tid % kPer) {}
+    __device__ __forceinline__ int from(int j, int stride) const { return (row + j * kRows) * stride + 16 * c; }
+    __device__ __forceinline__ typename P::R *at(T &t, int j, int half) const {
+        if constexpr (T::kSwz) {
+            const int g = c & 3;
+            return t.m + (c >> 2) * T::kStrip + (row >> 4) * 512 + 8 * (16 * g + ((row & 15) ^ (2 * g))) + 4 * ((half ^ c) & 1) +
+                   j * (kRows / 16) * 512;
         } else {
-            return *reinterpret_cast<const lin_u32x4 *>(m + row * kPitch + 4 * c);
+            return t.m + (row + j * kRows) * T::kPitch + 4 * c;
         }
     }
-    __device__ __forceinline__ void oct(int r0, int u, int lane, F &lo, F &hi) {
-        const int row = r0 + (lane & 15), g = lane >> 4;
-        if constexpr (kSwz) {
-            P::ld8(m + ((row >> 4) * (COLS / 32) + u) * kBlock + 8 * (16 * g + ((row & 15) ^ (2 * g))), lo, hi);
+    __device__ __forceinline__ void put(T &t, int j, lin_u32x4 v) const {
+        if constexpr (T::kSwz) {
+            *reinterpret_cast<lin_u32x2 *>(at(t, j, 0)) = __builtin_shufflevector(v, v, 0, 1);
+            *reinterpret_cast<lin_u32x2 *>(at(t, j, 1)) = __builtin_shufflevector(v, v, 2, 3);
         } else {
-            lo = P::ld4(m + row * kPitch + 32 * u + 8 * g + lin_half(0, lane));
-            hi = P::ld4(m + row * kPitch + 32 * u + 8 * g + lin_half(1, lane));
+            *reinterpret_cast<lin_u32x4 *>(at(t, j, 0)) = v;
         }
     }
-    // half e of the eight rows
-    __device__ __forceinline__ F down(int u, int e, int c0, int lane) {
-        const int g = lane >> 4, mm = lane & 15, row = 32 * u + 8 * g + lin_half(e, lane);
-        if constexpr (kSwz) {
-            // LDS transpose read: lane 4i + p of a group of 16 reads row i, four columns at chunk p;
-            // lane 4p + q receives element q of chunk p of the rows 0..3
-            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                  (lds_s16x4 *)(four(row + (mm >> 2), c0 + 4 * (mm & 3)))));
-        } else {
-            return P::ld4_strided(m + row * kPitch + c0 + mm, kPitch);
-        }
-    }
-    __device__ __forceinline__ F across(int u, int e, int b, int lane) {
-        const int g = lane >> 4, mm = lane & 15, row = 32 * u + 8 * g + lin_half(e, lane);
-        if constexpr (kSwz) {
-            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const int p = mm & 3;
-            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                  (lds_s16x4 *)(four(row + (mm >> 2), 32 * (b >> 1) + 8 * p + 4 * ((b ^ p) & 1)))));
-        } else {
-            const int p = mm >> 2;
-            return P::ld4_strided(m + row * kPitch + 32 * (b >> 1) + 8 * p + 4 * ((b ^ p) & 1) + (mm & 3), kPitch);
-        }
+    __device__ __forceinline__ lin_u32x4 get(T &t, int j) const {
+        if constexpr (T::kSwz)
+            return __builtin_shufflevector(*reinterpret_cast<const lin_u32x2 *>(at(t, j, 0)),
+                                           *reinterpret_cast<const lin_u32x2 *>(at(t, j, 1)), 0, 1, 2, 3);
+        else
+            return *reinterpret_cast<const lin_u32x4 *>(at(t, j, 0));
     }
 };
 
 // Rows of a tile to a buffer (what lies past its end is dropped), over NT threads
 template <class P, int C, int COLS, int NT>
 __device__ __forceinline__ void lin_store(LinTile<P, C, COLS> &from, __amdgpu_buffer_rsrc_t rs, int stride, int tid) {
-    constexpr int kPer = COLS * P::kBytes / 16;
+    const LinPieces<P, C, COLS, NT> at(tid);
 #pragma unroll
-    for (int j = 0; j < C * kPer / NT; ++j) {
-        const int p = tid + j * NT;
-        __builtin_amdgcn_raw_buffer_store_b128(from.get(p / kPer, p % kPer), rs, (p / kPer) * stride + (p % kPer) * 16, 0, 0);
-    }
+    for (int j = 0; j < at.N; ++j) __builtin_amdgcn_raw_buffer_store_b128(at.get(from, j), rs, at.from(j, stride), 0, 0);
 }
 
 // C rows of COLS elements (rows `stride` bytes apart) on their way to a tile, over NT threads
 template <class P, int C, int COLS, int NT>
 struct LinRows {
-    static constexpr int kPer = COLS * P::kBytes / 16;   // 16-byte pieces a row
-    static constexpr int N = C * kPer / NT;
-    static_assert(C * kPer % NT == 0 && N >= 1, "pieces must divide over the threads");
-    lin_u32x4 r[N];
+    using Pieces = LinPieces<P, C, COLS, NT>;
+    lin_u32x4 r[Pieces::N];
 
     __device__ __forceinline__ void load(const void *base, int rows, int stride, int tid) {
+        const Pieces at(tid);
         const __amdgpu_buffer_rsrc_t rs = lin_rsrc(base, rows > 0 ? (rows - 1) * stride + COLS * P::kBytes : 0);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int p = tid + j * NT;
-            r[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (p / kPer) * stride + (p % kPer) * 16, 0, 0);
-        }
+        for (int j = 0; j < at.N; ++j) r[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, at.from(j, stride), 0, 0);
     }
     __device__ __forceinline__ void put(LinTile<P, C, COLS> &to, int tid) const {
+        const Pieces at(tid);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int p = tid + j * NT;
-            to.put(p / kPer, p % kPer, r[j]);
-        }
+        for (int j = 0; j < at.N; ++j) at.put(to, j, r[j]);
     }
 };
 
@@ -309,8 +326,9 @@ struct LinSplit {
 // wave's columns, NC tiles of 16, in operand registers.
 template <class P, int C, int NS, int D, int NC>
 __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C, D> &rows,
-                                           const typename P::F (&col)[NC][C / 32][2], const float *weight, float all, int lane) {
-    const int g4 = lane >> 4;
+                                           const typename P::F (&col)[NC][C / 32][2], const float *weight, float all,
+                                           const LinLane &l) {
+    const float *w = weight + 8 * (l.lane >> 4);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -318,8 +336,7 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C,
 #pragma unroll
     for (int u = 0; u < C / 32; ++u) {
         LinSplit<P, NS> lo[NC], hi[NC];
-        const f32x4 w0 = lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(0, lane));
-        const f32x4 w1 = lds_f32x4(weight + 32 * u + 8 * g4 + lin_half(1, lane));
+        const f32x4 w0 = lds_f32x4(w + 32 * u + lin_half(0, l.lane)), w1 = lds_f32x4(w + 32 * u + lin_half(1, l.lane));
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             lo[c].of(P::f32(col[c][u][0]) * w0);
@@ -327,7 +344,7 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C,
         }
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
-            const typename P::F r0 = rows.across(u, 0, b, lane), r1 = rows.across(u, 1, b, lane);
+            const typename P::F r0 = rows.across(u, 0, b, l), r1 = rows.across(u, 1, b, l);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -339,7 +356,8 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C,
 // The chunk's rows with the state (NS addends of it): acc[c][i] gets four columns of one token a
 // lane, token 16 i + l % 16.
 template <class P, int NS, int C, int D, int NC>
-__device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (&S)[NC][D / 16], LinTile<P, C, D> &rows, int lane) {
+__device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (&S)[NC][D / 16], LinTile<P, C, D> &rows,
+                                         const LinLane &l) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -355,7 +373,7 @@ __device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) {
             typename P::F x0, x1;
-            rows.oct(16 * i, u, lane, x0, x1);
+            rows.oct(i, u, l, x0, x1);
 #pragma unroll
             for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j)
 #pragma unroll
@@ -364,42 +382,42 @@ __device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (
     }
 }
 
-// The wave's columns of a tile as operands: from column c0 on, 16 a tile.
+// The wave's columns of a tile as operands: from tile of columns t0 on.
 template <class P, int C, int D, int NC>
-__device__ __forceinline__ void lin_columns(typename P::F (&col)[NC][C / 32][2], LinTile<P, C, D> &rows, int c0, int lane) {
+__device__ __forceinline__ void lin_columns(typename P::F (&col)[NC][C / 32][2], LinTile<P, C, D> &rows, int t0, const LinLane &l) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int u = 0; u < C / 32; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) col[c][u][e] = rows.down(u, e, c0 + 16 * c, lane);
+            for (int e = 0; e < 2; ++e) col[c][u][e] = rows.down(u, e, t0 + c, l);
 }
 
 // acc += the chunk's own part: the rows of p (element [token][other token]) with the columns.
 // LOWER: others up to the token; else from the token on.
 template <class P, bool LOWER, int C, int NC>
 __device__ __forceinline__ void lin_near(f32x4 (&acc)[NC][C / 16], LinTile<P, C, C> &p, const typename P::F (&col)[NC][C / 32][2],
-                                         int lane) {
+                                         const LinLane &l) {
 #pragma unroll
     for (int i = 0; i < C / 16; ++i)
 #pragma unroll
         for (int u = LOWER ? 0 : i / 2; u < (LOWER ? i / 2 + 1 : C / 32); ++u) {
             typename P::F p0, p1;
-            p.oct(16 * i, u, lane, p0, p1);
+            p.oct(i, u, l, p0, p1);
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c][i] = P::mma2(acc[c][i], col[c][u][0], col[c][u][1], p0, p1);
         }
 }
 
-// A 16 x 16 block of products of LDS rows: lane l gets rows r0 + 4 (l / 16) + i with row c0 + l % 16.
+// A 16 x 16 block of products of LDS rows: lane l gets rows 16 i + 4 (l / 16) + e with row 16 j + l % 16.
 template <class P, int C, int D>
-__device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C, D> &cols, int r0, int c0, int lane) {
+__device__ __forceinline__ f32x4 lin_block(LinTile<P, C, D> &rows, LinTile<P, C, D> &cols, int i, int j, const LinLane &l) {
     f32x4 acc = zero4();
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
         typename P::F x0, x1, y0, y1;
-        rows.oct(r0, u, lane, x0, x1);
-        cols.oct(c0, u, lane, y0, y1);
+        rows.oct(i, u, l, x0, x1);
+        cols.oct(j, u, l, y0, y1);
         acc = P::mma2(acc, x0, x1, y0, y1);
     }
     return acc;

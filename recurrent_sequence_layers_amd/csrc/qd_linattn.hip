@@ -47,6 +47,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     if (!lin_place(a.B * a.H * a.segs, ncb, unit, cb)) return;
     const int seg = unit % a.segs, bh = unit / a.segs, b = bh / a.H, h = bh % a.H;
     const int tid = threadIdx.x & (kNT - 1), role = lin_wave() >> 2, wave = lin_wave() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const LinLane l(lane);
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, (a.T + C - 1) / C);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
@@ -96,12 +97,12 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
                 for (int p = wave; p < NB; p += 4) {
                     int i, j;
                     lin_pair(p, i, j);
-                    f32x4 acc = lin_block<P>(lds.k[now], lds.q[now], 16 * j, 16 * i, lane);
+                    f32x4 acc = lin_block<P>(lds.k[now], lds.q[now], j, i, l);
                     const int s = 16 * i + r16, t = 16 * j + 4 * g4;
                     const f32x4 d = lin_between(gates, s, t);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
-                    P::st4(lds.p[(n + 1 - c0) & 1].four(s, t), acc);
+                    P::st4(lds.p[(n + 1 - c0) & 1].four(i, j, l), acc);
                 }
             }
             now = put;
@@ -130,15 +131,15 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         LinTile<P, C, C> &p = lds.p[(n - c0) & 1];
         const LinGates<C> &gates = lds.gates[now];
         typename P::F vf[1][C / 32][2];
-        lin_columns<P, C>(vf, lds.v[now], 16 * wave, lane);
+        lin_columns<P, C>(vf, lds.v[now], wave, l);
         f32x4 acc[1][C / 16];
-        lin_read<P, 1>(acc, S, q, lane);
+        lin_read<P, 1>(acc, S, q, l);
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) acc[0][i] *= gates.before[16 * i + r16];
-        lin_near<P, true>(acc, p, vf, lane);
+        lin_near<P, true>(acc, p, vf, l);
 #pragma unroll
-        for (int i = 0; i < C / 16; ++i) P::st4(lds.o[(n - c0) & 1].four(16 * i + r16, 16 * wave + 4 * g4), acc[0][i]);
-        lin_update<P, C, NS>(S, k, vf, gates.after, gates.all[0], lane);
+        for (int i = 0; i < C / 16; ++i) P::st4(lds.o[(n - c0) & 1].four(i, wave, l), acc[0][i]);
+        lin_update<P, C, NS>(S, k, vf, gates.after, gates.all[0], l);
         now = now == 2 ? 0 : now + 1;
         __syncthreads();
     }
@@ -169,6 +170,7 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
     const int slot = unit % nseg, bh = unit / nseg, b = bh / a.H, h = bh % a.H, seg = rev ? slot + 1 : slot;
     const int tid = threadIdx.x, wave = lin_wave(), lane = lane_id(), r16 = lane & 15;
+    const LinLane l(lane);
     const int len = lin_len(a, b);
     const int c0 = seg * a.seg_chunks, count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
@@ -207,8 +209,8 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
         }
         const LinGates<C> &gates = lds.gates[m & 1];
         typename P::F vf[1][C / 32][2];
-        lin_columns<P, C>(vf, lds.v[m & 1], 16 * wave, lane);
-        lin_update<P, C, NS>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], lane);
+        lin_columns<P, C>(vf, lds.v[m & 1], wave, l);
+        lin_update<P, C, NS>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], l);
         __syncthreads();
     }
     lin_keep<DK>(S[0], (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, lane);

@@ -66,8 +66,9 @@ struct Walk {
     const LinArgs &a;
     int b, h, bh, seg, c0, count, len, role, wave, lane, g4, r16;   // role: waves 0-3, 4-7, 8-11
     size_t sdk, sdv;
+    LinLane l;
 
-    __device__ __forceinline__ Walk(const LinArgs &a_, int unit) : a(a_) {
+    __device__ __forceinline__ Walk(const LinArgs &a_, int unit) : a(a_), l(lane_id()) {
         seg = unit % a.segs;
         bh = unit / a.segs;
         b = bh / a.H;
@@ -163,8 +164,8 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             int i, j;
             lin_pair(p, i, j);                   // later tokens in block i, earlier ones in block j
             if constexpr (REV) {
-                f32x4 qk = lin_block<P>(next.q, next.k, 16 * i, 16 * j, w.lane);
-                f32x4 ov = lin_block<P>(next.o, next.v, 16 * i, 16 * j, w.lane);
+                f32x4 qk = lin_block<P>(next.q, next.k, i, j, w.l);
+                f32x4 ov = lin_block<P>(next.o, next.v, i, j, w.l);
                 const int t = 16 * j + w.r16, s = 16 * i + 4 * w.g4;
                 const f32x4 hi = lds_f32x4(next.gates.hi + s) - next.gates.hi[t], lo = lds_f32x4(next.gates.lo + s) - next.gates.lo[t];
 #pragma unroll
@@ -173,17 +174,17 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
                     qk[e] = t <= s + e ? d * qk[e] : 0.f;
                     ov[e] = t <= s + e ? d * ov[e] : 0.f;
                 }
-                P::st4(lds.p[0].four(t, s), qk);
-                P::st4(lds.p[1].four(t, s), ov);
+                P::st4(lds.p[0].four(j, i, w.l), qk);
+                P::st4(lds.p[1].four(j, i, w.l), ov);
             } else {
-                f32x4 ov = lin_block<P>(next.v, next.o, 16 * j, 16 * i, w.lane);
+                f32x4 ov = lin_block<P>(next.v, next.o, j, i, w.l);
                 const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
                 const f32x4 d = lin_between(next.gates, s, t);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? d[e] * ov[e] : 0.f;
-                P::st4(lds.p[0].four(s, t), ov);
+                P::st4(lds.p[0].four(i, j, w.l), ov);
                 if constexpr (DG) {
-                    const f32x4 qk = lin_block<P>(next.k, next.q, 16 * j, 16 * i, w.lane);
+                    const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
                     float row = 0.f;
                     f32x4 col;
 #pragma unroll
@@ -210,19 +211,20 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
 
 // a or b: the state's part of each output row with the row's own q or k, over a wave's columns
 template <class P, int C, int D, int NC>
-__device__ __forceinline__ void row_parts(float *part, LinTile<P, C, D> &rows, const f32x4 (&acc)[NC][C / 16], int c0, int lane) {
+__device__ __forceinline__ void row_parts(float *part, LinTile<P, C, D> &rows, const f32x4 (&acc)[NC][C / 16], int t0,
+                                          const LinLane &l) {
 #pragma unroll
     for (int i = 0; i < C / 16; ++i) {
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const f32x4 y = P::f32(P::ld4(rows.four(16 * i + (lane & 15), c0 + 16 * c + 4 * (lane >> 4))));
+            const f32x4 y = P::f32(P::ld4(rows.four(i, t0 + c, l)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) s = fmaf(acc[c][i][e], y[e], s);
         }
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (lane < 16) part[16 * i + lane] = s;
+        if (l.lane < 16) part[16 * i + l.lane] = s;
     }
 }
 template <int C, int NC>
@@ -243,12 +245,12 @@ __device__ __forceinline__ void pack(typename P::F (&out)[NC][C / 16], const f32
         for (int i = 0; i < C / 16; ++i) out[c][i] = P::cvt(16 * i + r16 < live ? acc[c][i] : zero4());
 }
 template <class P, int C, int D, int NC>
-__device__ __forceinline__ void spill_out(LinTile<P, C, D> &to, const typename P::F (&out)[NC][C / 16], int c0, int lane) {
+__device__ __forceinline__ void spill_out(LinTile<P, C, D> &to, const typename P::F (&out)[NC][C / 16], int t0, const LinLane &l) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int i = 0; i < C / 16; ++i)
-            *reinterpret_cast<typename P::F *>(to.four(16 * i + (lane & 15), c0 + 16 * c + 4 * (lane >> 4))) = out[c][i];
+            *reinterpret_cast<typename P::F *>(to.four(i, t0 + c, l)) = out[c][i];
 }
 // A state whose columns are key indices, from and to [DV][DK]
 template <int DK, int DV, int NC>
@@ -273,7 +275,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = DK / 64;
     const Walk<P, DK, DV> w(a, unit);
     if (w.role > 0) return bring<P, DK, DV, false, DG, 8>(w, lds, w.wave + 4 * (w.role - 1));
-    const int lane = w.lane, c0 = 16 * NC * w.wave;
+    const int lane = w.lane, t0 = NC * w.wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
@@ -285,16 +287,16 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         typename P::F kf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
-            lin_columns<P, C>(kf, x.k, c0, lane);
-            lin_read<P, DG ? 3 : 1>(acc, S, x.o, lane);
+            lin_columns<P, C>(kf, x.k, t0, w.l);
+            lin_read<P, DG ? 3 : 1>(acc, S, x.o, w.l);
             scale<C>(acc, x.gates.before, w.r16);
-            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.q, acc, c0, lane);
-            lin_near<P, true>(acc, lds.p[0], kf, lane);
+            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.q, acc, t0, w.l);
+            lin_near<P, true>(acc, lds.p[0], kf, w.l);
             pack<P, C>(out, acc, w.live(w.c0 + m), w.r16);
         }
         __syncthreads();
-        spill_out<P, C>(x.q, out, c0, lane);
-        lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, x.gates.after, x.gates.all[0], lane);
+        spill_out<P, C>(x.q, out, t0, w.l);
+        lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, x.gates.after, x.gates.all[0], w.l);
         __syncthreads();
     }
     if constexpr (DG) {
@@ -320,7 +322,7 @@ template <class P, int DK, int DV>
 __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, const float *from) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NC = DV / 64;
-    const int lane = w.lane, c0 = 16 * NC * w.wave;
+    const int lane = w.lane, t0 = NC * w.wave, c0 = 16 * t0;
     f32x4 R[NC][DK / 16];
 #pragma unroll
     for (int c = 0; c < NC; ++c) lin_load<DK>(R[c], from, c0 + 16 * c + w.r16, lane);
@@ -331,15 +333,15 @@ __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename P::F of[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
-            lin_columns<P, C>(of, x.o, c0, lane);
-            lin_read<P, 1>(acc, R, x.k, lane);
+            lin_columns<P, C>(of, x.o, t0, w.l);
+            lin_read<P, 1>(acc, R, x.k, w.l);
             scale<C>(acc, x.gates.after, w.r16);
-            lin_near<P, false>(acc, lds.p[0], of, lane);
+            lin_near<P, false>(acc, lds.p[0], of, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
-        spill_out<P, C>(x.v, out, c0, lane);
-        lin_update<P, C, 2>(R, x.q, of, x.gates.before, x.gates.all[0], lane);
+        spill_out<P, C>(x.v, out, t0, w.l);
+        lin_update<P, C, 2>(R, x.q, of, x.gates.before, x.gates.all[0], w.l);
         __syncthreads();
     }
 }
@@ -348,7 +350,7 @@ template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, const float *from) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NC = DK / 64;
-    const int lane = w.lane, c0 = 16 * NC * w.wave;
+    const int lane = w.lane, t0 = NC * w.wave, c0 = 16 * t0;
     f32x4 R[NC][DV / 16];
     load_across<DK, DV>(R, from, c0, lane);
     __syncthreads();                             // the first chunk is brought
@@ -358,16 +360,16 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename P::F qf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
-            lin_columns<P, C>(qf, x.q, c0, lane);
-            lin_read<P, DG ? 3 : 1>(acc, R, x.v, lane);
+            lin_columns<P, C>(qf, x.q, t0, w.l);
+            lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
             scale<C>(acc, x.gates.after, w.r16);
-            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, c0, lane);
-            lin_near<P, false>(acc, lds.p[1], qf, lane);
+            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
+            lin_near<P, false>(acc, lds.p[1], qf, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
-        spill_out<P, C>(x.k, out, c0, lane);
-        lin_update<P, C, NS>(R, x.o, qf, x.gates.before, x.gates.all[0], lane);
+        spill_out<P, C>(x.k, out, t0, w.l);
+        lin_update<P, C, NS>(R, x.o, qf, x.gates.before, x.gates.all[0], w.l);
         __syncthreads();
     }
     const LinArgs &a = w.a;
