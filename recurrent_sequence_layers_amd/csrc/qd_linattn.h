@@ -59,7 +59,7 @@ struct LinArgs {
     float *fwd, *rev;                // [B H][segs - 1][DV][DK]: states at the segments' borders
     float *fac;                      // [2][B H][segs]: a segment's decay
     float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
-    float *edge;                     // [B H][4]: <S_T, dS_T> by wave
+    float *edge;                     // [B H][DK / 16]: <S_T, dS_T> by wave
     float *head;                     // [B H]: sums of dg over tokens
 };
 

@@ -56,7 +56,7 @@ struct BwdLds {
     } c[2];
     LinTile<P, C, C> p[2];
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
-    float part[4][C];                  // a or b, by the columns' wave
+    float part[8][C];                  // a or b, by the columns' wave
 };
 
 // Where a workgroup walks, and its tensors' first bytes.
@@ -107,7 +107,8 @@ struct Walk {
 
 // The loading waves, NW of them; `wave` counts from the first.  REV: the walk goes backwards and
 // forms P by its earlier tokens' rows, of q k and of do v; else by its later tokens' rows, of do v.
-template <class P, int DK, int DV, bool REV, bool DG, int NW>
+// NS: the waves that hold what a or b is of.
+template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS>
 __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NB = L::NB, NT = 64 * NW;
@@ -201,8 +202,10 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             }
         }
         if constexpr (DG) {
-            const int t = tid & (C - 1);
-            w.term(REV ? 2 : 1, n, valid, tid, (lds.part[0][t] + lds.part[1][t]) + (lds.part[2][t] + lds.part[3][t]));
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < NS; ++k) s += lds.part[k][tid & (C - 1)];
+            w.term(REV ? 2 : 1, n, valid, tid, s);
         }
         __syncthreads();
     }
@@ -272,10 +275,11 @@ __device__ __forceinline__ void load_across(f32x4 (&S)[NC][DV / 16], const float
 template <class P, int DK, int DV, bool DG>
 __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     using L = BwdLds<P, DK, DV>;
-    constexpr int C = L::C, NC = DK / 64;
+    constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
-    if (w.role > 0) return bring<P, DK, DV, false, DG, 8>(w, lds, w.wave + 4 * (w.role - 1));
-    const int lane = w.lane, t0 = NC * w.wave, c0 = 16 * t0;
+    const int wave = 4 * w.role + w.wave;
+    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS>(w, lds, wave - NS);
+    const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
@@ -287,10 +291,10 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         typename P::F kf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
-            lin_columns<P, C>(kf, x.k, t0, w.l);
             lin_read<P, DG ? 3 : 1>(acc, S, x.o, w.l);
             scale<C>(acc, x.gates.before, w.r16);
-            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.q, acc, t0, w.l);
+            if constexpr (DG) row_parts<P>(lds.part[wave], x.q, acc, t0, w.l);
+            lin_columns<P, C>(kf, x.k, t0, w.l);
             lin_near<P, true>(acc, lds.p[0], kf, w.l);
             pack<P, C>(out, acc, w.live(w.c0 + m), w.r16);
         }
@@ -311,7 +315,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s = fmaf(S[c][t][e], d[c][t][e], s);
             for (int k = 1; k < 64; k *= 2) s += __shfl_xor(s, k);
-            if (lane == 0) a.edge[static_cast<size_t>(w.bh) * 4 + w.wave] = s;
+            if (lane == 0) a.edge[static_cast<size_t>(w.bh) * NS + wave] = s;
         }
     }
 }
@@ -360,10 +364,10 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename P::F qf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
-            lin_columns<P, C>(qf, x.q, t0, w.l);
             lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
             scale<C>(acc, x.gates.after, w.r16);
             if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
+            lin_columns<P, C>(qf, x.q, t0, w.l);
             lin_near<P, false>(acc, lds.p[1], qf, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
@@ -386,7 +390,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
 template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     const Walk<P, DK, DV> w(a, unit);
-    if (w.role == 2) return bring<P, DK, DV, true, DG, 4>(w, lds, w.wave);
+    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4>(w, lds, w.wave);
     const size_t state = static_cast<size_t>(DV) * DK;
     const float *from = w.seg < a.segs - 1 ? a.rev + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg) * state
                                            : a.dS_T ? a.dS_T + w.bh * state : nullptr;
@@ -422,7 +426,7 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
     auto get = [&](const float *p, int n, int i) { return i < C && n * C + i < a.T ? p[n * C + i] : 0.f; };
     if (threadIdx.x == 0) {
         double e = 0;
-        for (int w = 0; w < 4; ++w) e += a.edge[static_cast<size_t>(bh) * 4 + w];
+        for (int w = 0; w < a.DK / 16; ++w) e += a.edge[static_cast<size_t>(bh) * (a.DK / 16) + w];
         carry = e;
     }
     double total = 0;
@@ -543,7 +547,7 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     const size_t bh = static_cast<size_t>(B) * H;
     size_t n = 0;
     if (segs > 1) n += 2 * bh * (segs - 1) * dk * dv + 2 * bh * segs;
-    if (dg) n += 3 * bh * T + 5 * bh;
+    if (dg) n += 3 * bh * T + bh * (dk / 16 + 1);
     return n * sizeof(float);
 }
 
@@ -571,7 +575,7 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (a.dg) {
         a.tok = p;
         a.edge = a.tok + 3 * bh * a.T;
-        a.head = a.edge + 4 * bh;
+        a.head = a.edge + bh * (a.DK / 16);
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
 }
