@@ -52,8 +52,8 @@ struct BwdLds {
     struct Chunk {
         LinTile<P, C, DK> q, k;
         LinTile<P, C, DV> v, o;
-        LinGates<C> gates;
     } c[2];
+    LinGates<C> gates[3];
     LinTile<P, C, C> p[2];
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
     float part[8][C];                  // a or b, by the columns' wave
@@ -105,18 +105,95 @@ struct Walk {
     }
 };
 
-// The loading waves, NW of them; `wave` counts from the first.  REV: the walk goes backwards and
-// forms P by its earlier tokens' rows, of q k and of do v; else by its later tokens' rows, of do v.
+// The decays, by one of the states' waves: those of chunk m + 2 in chunk m's second interval, where
+// these waves have the least to do.
+template <class P, int DK, int DV, bool REV>
+struct Decays {
+    const Walk<P, DK, DV> &w;
+    float next;
+    __device__ __forceinline__ float fetch(int m) const {
+        const int n = m < w.count ? w.template chunk<REV>(m) : w.c0;
+        return lin_gate(w.a, w.b, w.h, n * w.C, m < w.count ? w.live(n) : 0, w.lane);
+    }
+    // before the first chunk
+    __device__ __forceinline__ Decays(const Walk<P, DK, DV> &w_, BwdLds<P, DK, DV> &lds) : w(w_), next(0.f) {
+        if (w.role || w.wave) return;
+        lin_gates(lds.gates[0], fetch(0), w.lane);
+        lin_gates(lds.gates[1], fetch(1), w.lane);
+        next = fetch(2);
+    }
+    __device__ __forceinline__ void ahead(BwdLds<P, DK, DV> &lds, int m) {
+        if (w.role || w.wave) return;
+        lin_gates(lds.gates[(m + 2) % 3], next, w.lane);
+        next = fetch(m + 3);
+    }
+};
+
+// One block of the products of the next chunk, m + 1.  REV: the walk goes backwards and forms P by
+// its earlier tokens' rows, of q k and of do v; else by its later tokens' rows, of do v.
+template <class P, int DK, int DV, bool REV, bool DG>
+__device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int m, int p) {
+    typename BwdLds<P, DK, DV>::Chunk &next = lds.c[(m + 1) & 1];
+    const LinGates<kLinChunk<P>> &gates = lds.gates[(m + 1) % 3];
+    int i, j;
+    lin_pair(p, i, j);                           // later tokens in block i, earlier ones in block j
+    if constexpr (REV) {
+        f32x4 qk = lin_block<P>(next.q, next.k, i, j, w.l);
+        f32x4 ov = lin_block<P>(next.o, next.v, i, j, w.l);
+        const int t = 16 * j + w.r16, s = 16 * i + 4 * w.g4;
+        const f32x4 hi = lds_f32x4(gates.hi + s) - gates.hi[t], lo = lds_f32x4(gates.lo + s) - gates.lo[t];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d = lin_exp2(hi[e] + lo[e]);
+            qk[e] *= d;
+            ov[e] *= d;
+        }
+        if (i == j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                qk[e] = t <= s + e ? qk[e] : 0.f;
+                ov[e] = t <= s + e ? ov[e] : 0.f;
+            }
+        }
+        P::st4(lds.p[0].four(j, i, w.l), qk);
+        P::st4(lds.p[1].four(j, i, w.l), ov);
+    } else {
+        f32x4 ov = lin_block<P>(next.v, next.o, j, i, w.l);
+        const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
+        ov *= lin_between(gates, s, t);
+        if (i == j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? ov[e] : 0.f;
+        }
+        P::st4(lds.p[0].four(i, j, w.l), ov);
+        if constexpr (DG) {
+            const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
+            f32x4 col;
+            float row = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = t + e < s ? ov[e] * qk[e] : 0.f;
+                row += x;
+                col[e] = sum16(x);
+            }
+            row += __shfl_xor(row, 16);
+            row += __shfl_xor(row, 32);
+            if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
+            if (w.lane < 16) lds.rows[p][w.r16] = row;
+        }
+    }
+}
+
+// The loading waves, NW of them; `wave` counts from the first.  They form the blocks up to LAST.
 // NS: the waves that hold what a or b is of.
-template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS>
+template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS, int LAST>
 __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
     using L = BwdLds<P, DK, DV>;
-    constexpr int C = L::C, NB = L::NB, NT = 64 * NW;
+    constexpr int C = L::C, NT = 64 * NW;
     const LinArgs &a = w.a;
     const int sdk = static_cast<int>(w.sdk), sdv = static_cast<int>(w.sdv), tid = 64 * wave + w.lane;
     LinRows<P, C, DK, NT> rq, rk;
     LinRows<P, C, DV, NT> rv, ro;
-    float gate;
     // every step has the same loads and stores, those past the walk's ends of nothing: with a
     // branch around stores the waits for older loads would wait for them too
     auto fetch = [&](int m) {
@@ -125,7 +202,6 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         rk.load(static_cast<const char *>(a.k) + w.at(t0, w.sdk, DK), live, sdk, tid);
         rv.load(static_cast<const char *>(a.v) + w.at(t0, w.sdv, DV), live, sdv, tid);
         ro.load(static_cast<const char *>(a.d_o) + w.at(t0, w.sdv, DV), live, sdv, tid);
-        gate = lin_gate(a, w.b, w.h, t0, live, w.lane);
     };
     auto emit = [&](int m) {                     // the outputs of chunk m - 1, from the tiles of chunk m + 1
         const bool valid = m >= 1 && m <= w.count;
@@ -148,7 +224,6 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         rk.put(next.k, tid);
         rv.put(next.v, tid);
         ro.put(next.o, tid);
-        if (wave == NW - 1) lin_gates(next.gates, gate, w.lane);
         fetch(m + 2);
         if constexpr (DG && !REV) {
             const int i = (tid >> 4) & (C / 16 - 1), e = tid & 15;
@@ -161,46 +236,7 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             w.term(0, n, valid, tid, x);
         }
         __syncthreads();
-        for (int p = wave; p < NB; p += NW) {
-            int i, j;
-            lin_pair(p, i, j);                   // later tokens in block i, earlier ones in block j
-            if constexpr (REV) {
-                f32x4 qk = lin_block<P>(next.q, next.k, i, j, w.l);
-                f32x4 ov = lin_block<P>(next.o, next.v, i, j, w.l);
-                const int t = 16 * j + w.r16, s = 16 * i + 4 * w.g4;
-                const f32x4 hi = lds_f32x4(next.gates.hi + s) - next.gates.hi[t], lo = lds_f32x4(next.gates.lo + s) - next.gates.lo[t];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = lin_exp2(hi[e] + lo[e]);
-                    qk[e] = t <= s + e ? d * qk[e] : 0.f;
-                    ov[e] = t <= s + e ? d * ov[e] : 0.f;
-                }
-                P::st4(lds.p[0].four(j, i, w.l), qk);
-                P::st4(lds.p[1].four(j, i, w.l), ov);
-            } else {
-                f32x4 ov = lin_block<P>(next.v, next.o, j, i, w.l);
-                const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
-                const f32x4 d = lin_between(next.gates, s, t);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? d[e] * ov[e] : 0.f;
-                P::st4(lds.p[0].four(i, j, w.l), ov);
-                if constexpr (DG) {
-                    const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
-                    float row = 0.f;
-                    f32x4 col;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = t + e < s ? ov[e] * qk[e] : 0.f;
-                        row += x;
-                        col[e] = sum16(x);
-                    }
-                    row += __shfl_xor(row, 16);
-                    row += __shfl_xor(row, 32);
-                    if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
-                    if (w.lane < 16) lds.rows[p][w.r16] = row;
-                }
-            }
-        }
+        for (int p = wave; p < LAST; p += NW) product<P, DK, DV, REV, DG>(w, lds, m, p);
         if constexpr (DG) {
             float s = 0.f;
 #pragma unroll
@@ -241,11 +277,18 @@ __device__ __forceinline__ void scale(f32x4 (&acc)[NC][C / 16], const float *w, 
 }
 // Outputs as elements, zeros in padding
 template <class P, int C, int NC>
-__device__ __forceinline__ void pack(typename P::F (&out)[NC][C / 16], const f32x4 (&acc)[NC][C / 16], int live, int r16) {
+__device__ __forceinline__ void pack(typename P::F (&out)[NC][C / 16], f32x4 (&acc)[NC][C / 16], int live, int r16) {
+    if (live < C) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i)
+                if (16 * i + r16 >= live) acc[c][i] = zero4();
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < C / 16; ++i) out[c][i] = P::cvt(16 * i + r16 < live ? acc[c][i] : zero4());
+        for (int i = 0; i < C / 16; ++i) out[c][i] = P::cvt(acc[c][i]);
 }
 template <class P, int C, int D, int NC>
 __device__ __forceinline__ void spill_out(LinTile<P, C, D> &to, const typename P::F (&out)[NC][C / 16], int t0, const LinLane &l) {
@@ -278,21 +321,29 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
     const int wave = 4 * w.role + w.wave;
-    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS>(w, lds, wave - NS);
+    // with eight waves on the state, whose update is short, four of them take a block each
+    constexpr int LAST = NS == 8 && L::NB == 10 ? 6 : L::NB;
+    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS, LAST>(w, lds, wave - NS);
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
                                      : a.S0 ? a.S0 + w.bh * state : nullptr, c0, lane);
+    Decays<P, DK, DV, false> decays(w, lds);
+    auto help = [&](int m) {
+        if (LAST < L::NB && w.role == 1) product<P, DK, DV, false, DG>(w, lds, m, LAST + w.wave);
+    };
     __syncthreads();                             // the first chunk is brought
+    help(-1);
     __syncthreads();
     for (int m = 0; m < w.count; ++m) {
         typename L::Chunk &x = lds.c[m & 1];
+        const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F kf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
             lin_read<P, DG ? 3 : 1>(acc, S, x.o, w.l);
-            scale<C>(acc, x.gates.before, w.r16);
+            scale<C>(acc, gates.before, w.r16);
             if constexpr (DG) row_parts<P>(lds.part[wave], x.q, acc, t0, w.l);
             lin_columns<P, C>(kf, x.k, t0, w.l);
             lin_near<P, true>(acc, lds.p[0], kf, w.l);
@@ -300,7 +351,9 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         }
         __syncthreads();
         spill_out<P, C>(x.q, out, t0, w.l);
-        lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, x.gates.after, x.gates.all[0], w.l);
+        lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, gates.after, gates.all[0], w.l);
+        decays.ahead(lds, m);
+        help(m);
         __syncthreads();
     }
     if constexpr (DG) {
@@ -334,18 +387,19 @@ __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     __syncthreads();
     for (int m = 0; m < w.count; ++m) {
         typename L::Chunk &x = lds.c[m & 1];
+        const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F of[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
             lin_columns<P, C>(of, x.o, t0, w.l);
             lin_read<P, 1>(acc, R, x.k, w.l);
-            scale<C>(acc, x.gates.after, w.r16);
+            scale<C>(acc, gates.after, w.r16);
             lin_near<P, false>(acc, lds.p[0], of, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
         spill_out<P, C>(x.v, out, t0, w.l);
-        lin_update<P, C, 2>(R, x.q, of, x.gates.before, x.gates.all[0], w.l);
+        lin_update<P, C, 2>(R, x.q, of, gates.before, gates.all[0], w.l);
         __syncthreads();
     }
 }
@@ -357,15 +411,17 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     const int lane = w.lane, t0 = NC * w.wave, c0 = 16 * t0;
     f32x4 R[NC][DV / 16];
     load_across<DK, DV>(R, from, c0, lane);
+    Decays<P, DK, DV, true> decays(w, lds);
     __syncthreads();                             // the first chunk is brought
     __syncthreads();
     for (int m = 0; m < w.count; ++m) {
         typename L::Chunk &x = lds.c[m & 1];
+        const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F qf[NC][C / 32][2], out[NC][C / 16];
         {
             f32x4 acc[NC][C / 16];
             lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
-            scale<C>(acc, x.gates.after, w.r16);
+            scale<C>(acc, gates.after, w.r16);
             if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
             lin_columns<P, C>(qf, x.q, t0, w.l);
             lin_near<P, false>(acc, lds.p[1], qf, w.l);
@@ -373,7 +429,8 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         }
         __syncthreads();
         spill_out<P, C>(x.k, out, t0, w.l);
-        lin_update<P, C, NS>(R, x.o, qf, x.gates.before, x.gates.all[0], w.l);
+        lin_update<P, C, NS>(R, x.o, qf, gates.before, gates.all[0], w.l);
+        decays.ahead(lds, m);
         __syncthreads();
     }
     const LinArgs &a = w.a;
@@ -390,7 +447,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
 template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     const Walk<P, DK, DV> w(a, unit);
-    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4>(w, lds, w.wave);
+    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4, BwdLds<P, DK, DV>::NB>(w, lds, w.wave);
     const size_t state = static_cast<size_t>(DV) * DK;
     const float *from = w.seg < a.segs - 1 ? a.rev + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg) * state
                                            : a.dS_T ? a.dS_T + w.bh * state : nullptr;
