@@ -54,10 +54,13 @@ struct LinArgs {
     void *dq, *dk, *dv;
     float *dg;                       // like g, or null
     float *dS0;                      // or null
-    // schedule, filled in by the launch: the time axis in `segs` segments of seg_chunks chunks
-    int segs, seg_chunks;
-    float *fwd, *rev;                // [B H][segs - 1][DV][DK]: states at the segments' borders
-    float *fac;                      // [2][B H][segs]: a segment's decay
+    // schedule, filled in by the launch.  The time axis is cut into `segs` segments of seg_chunks
+    // chunks, walked side by side.  Their first states come of `subs` shorter pieces a segment,
+    // sub_chunks each, walked from zero by a launch before: fwd of every segment but the last, rev
+    // of every one but the first
+    int segs, seg_chunks, subs, sub_chunks;
+    float *fwd, *rev;                // [B H][(segs - 1) subs][DV][DK]
+    float *fac;                      // [2][B H][(segs - 1) subs]: a piece's decay
     float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
     float *edge;                     // [B H][DK / 16]: <S_T, dS_T> by wave
     float *head;                     // [B H]: sums of dg over tokens
@@ -70,8 +73,14 @@ hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
 hipError_t launch_lin_step(int dtype, const LinArgs &a, float *S, hipStream_t stream);   // T = 1
 size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg);
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
-// exact: fp32 results come of the states, not only element outputs
+// Workspace of the states at the segments' borders, and the launches that find them (exact: fp32
+// results come of the states, not only element outputs).
+size_t lin_states_floats(const LinArgs &a, int directions);
+float *lin_states_place(LinArgs &a, float *ws, int directions);      // the workspace behind them
 hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, bool exact, hipStream_t stream);
+// The segments for `units` walks (workgroups, one a compute unit) of a chunk sequence; `heads` of
+// them times `directions` states
+void lin_plan(int dtype, LinArgs &a, long long units, int directions, double state_cost);
 hipError_t launch_lin_copy(float *to, const float *from, size_t n, hipStream_t stream);  // from null: zeros
 
 // Tokens of a chunk.  fp32 rows of 64 would not fit the LDS twice.
@@ -450,6 +459,19 @@ __device__ __forceinline__ void lin_pair(int p, int &i, int &j) {
 __device__ __forceinline__ int lin_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 // Two waves a SIMD: what the LDS leaves room for, and registers for loads ahead
 #define LIN_TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
+
+// The state before segment seg of head bh, and its gradient behind it: of the last piece before,
+// of the first one behind
+__device__ __forceinline__ const float *lin_before(const LinArgs &a, int bh, int seg) {
+    const size_t state = static_cast<size_t>(a.DV) * a.DK;
+    if (seg == 0) return a.S0 ? a.S0 + bh * state : nullptr;
+    return a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) * a.subs + seg * a.subs - 1) * state;
+}
+__device__ __forceinline__ const float *lin_behind(const LinArgs &a, int bh, int seg) {
+    const size_t state = static_cast<size_t>(a.DV) * a.DK;
+    if (seg == a.segs - 1) return a.dS_T ? a.dS_T + bh * state : nullptr;
+    return a.rev + (static_cast<size_t>(bh) * (a.segs - 1) * a.subs + seg * a.subs) * state;
+}
 
 // Tokens of sequence b
 __device__ __forceinline__ int lin_len(const LinArgs &a, int b) { return a.lens ? min(max(a.lens[b], 0), a.T) : a.T; }

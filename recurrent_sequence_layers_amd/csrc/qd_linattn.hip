@@ -49,7 +49,9 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     const int tid = threadIdx.x & (kNT - 1), role = lin_wave() >> 2, wave = lin_wave() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
     const LinLane l(lane);
     const int len = lin_len(a, b);
-    const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, (a.T + C - 1) / C);
+    // a sequence that ends before the segment leaves it without chunks
+    const int c0 = seg * a.seg_chunks, c1 = max(c0, min(c0 + a.seg_chunks, (len + C - 1) / C));
+    if (c1 == c0 && !(a.S_T && seg == a.segs - 1)) return;
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
     const size_t tok0 = static_cast<size_t>(b) * a.T;
     const size_t vcol = (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
@@ -121,8 +123,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     const size_t state = static_cast<size_t>(a.DV) * DK;
     const int col = 64 * cb + 16 * wave + r16;
     f32x4 S[1][DK / 16];
-    lin_load<DK>(S[0], seg > 0 ? a.fwd + (static_cast<size_t>(bh) * (a.segs - 1) + seg - 1) * state : a.S0 ? a.S0 + bh * state : nullptr,
-                   col, lane);
+    lin_load<DK>(S[0], lin_before(a, bh, seg), col, lane);
     __syncthreads();
     __syncthreads();
     int now = 0;
@@ -148,9 +149,9 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     if (a.S_T && seg == a.segs - 1) lin_keep<DK>(S[0], a.S_T + bh * state, col, lane);
 }
 
-// The states alone, from zero (or S0, dS_T) over one segment: forwards with k, v and the decay to
-// the segment's end, backwards with q, do and the decay from its start.  Four waves; the next
-// chunk goes to LDS while this one is used.
+// The states alone, from zero (or S0, dS_T) over one piece of a segment: forwards with k, v and the
+// decay to the piece's end, backwards with q, do and the decay from its start.  Four waves; the
+// next chunk goes to LDS while this one is used.
 template <class P, int DK>
 struct StateLds {
     static constexpr int C = kLinChunk<P>;
@@ -159,20 +160,21 @@ struct StateLds {
     LinGates<C> gates[2];
 };
 template <class P, int DK, int NS>
-__global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinArgs a, const int first_rev) {
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(3, 3))) void lin_state_kernel(const LinArgs a, const int first_rev) {
     using L = StateLds<P, DK>;
     constexpr int C = L::C;
     extern __shared__ __align__(16) char smem[];
     L &lds = *reinterpret_cast<L *>(smem);
-    const int ncb = a.DV / 64, nseg = a.segs - 1, bhs = a.B * a.H;
+    const int ncb = a.DV / 64, slots = (a.segs - 1) * a.subs, bhs = a.B * a.H;
     int unit, cb;
-    if (!lin_place(bhs * nseg, ncb, unit, cb)) return;
+    if (!lin_place(bhs * slots, ncb, unit, cb)) return;
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
-    const int slot = unit % nseg, bh = unit / nseg, b = bh / a.H, h = bh % a.H, seg = rev ? slot + 1 : slot;
+    const int slot = unit % slots, bh = unit / slots, b = bh / a.H, h = bh % a.H, piece = rev ? slot + a.subs : slot;
     const int tid = threadIdx.x, wave = lin_wave(), lane = lane_id(), r16 = lane & 15;
     const LinLane l(lane);
     const int len = lin_len(a, b);
-    const int c0 = seg * a.seg_chunks, count = min(a.seg_chunks, (a.T + C - 1) / C - c0);
+    const int c0 = piece / a.subs * a.seg_chunks + piece % a.subs * a.sub_chunks, nc = (len + C - 1) / C;
+    const int count = max(0, min(min(a.sub_chunks, a.seg_chunks - piece % a.subs * a.sub_chunks), nc - c0));
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
     const size_t tok0 = static_cast<size_t>(b) * a.T;
     const char *gk = static_cast<const char *>(rev ? a.q : a.k) + tok0 * sdk + static_cast<size_t>(h) * DK * P::kBytes;
@@ -181,8 +183,9 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
     const int col = 64 * cb + 16 * wave + r16;
 
     f32x4 S[1][DK / 16];
-    lin_load<DK>(S[0], rev ? (seg == a.segs - 1 && a.dS_T ? a.dS_T + bh * state : nullptr)
-                          : (seg == 0 && a.S0 ? a.S0 + bh * state : nullptr), col, lane);
+    const bool first = rev ? slot == slots - 1 : slot == 0;
+    const float *from = rev ? a.dS_T : a.S0;
+    lin_load<DK>(S[0], first && from ? from + bh * state : nullptr, col, lane);
     LinRows<P, C, DK, kNT> rk;
     LinRows<P, C, 64, kNT> rv;
     float gate = 0.f;
@@ -198,9 +201,11 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
         rv.put(lds.v[m & 1], tid);
         if (wave == 3) total += lin_gates(lds.gates[m & 1], gate, lane);
     };
-    fetch(0);
-    put(0);
-    if (count > 1) fetch(1);
+    if (count > 0) {
+        fetch(0);
+        put(0);
+        if (count > 1) fetch(1);
+    }
     __syncthreads();
     for (int m = 0; m < count; ++m) {
         if (m + 1 < count) {
@@ -213,26 +218,40 @@ __global__ __launch_bounds__(kNT) LIN_TWO_WAVES void lin_state_kernel(const LinA
         lin_update<P, C, NS>(S, lds.k[m & 1], vf, rev ? gates.before : gates.after, gates.all[0], l);
         __syncthreads();
     }
-    lin_keep<DK>(S[0], (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * nseg + slot) * state, col, lane);
+    lin_keep<DK>(S[0], (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * slots + slot) * state, col, lane);
     if (cb == 0 && wave == 3 && lane == 0)
-        a.fac[(static_cast<size_t>(rev) * bhs + bh) * a.segs + seg] = lin_exp2(static_cast<float>(total));
+        a.fac[(static_cast<size_t>(rev) * bhs + bh) * slots + slot] = lin_exp2(static_cast<float>(total));
 }
 
-// Local states to states at the borders: forwards slot j becomes the state behind segment j,
-// backwards the gradient of the state before segment j + 1.
+// The pieces' own states to the states at the segments' borders: forwards slot j becomes the state
+// behind piece j, backwards the gradient of the state before its piece; written where a segment
+// begins.  Eight pieces are on their way at a time.
 __global__ __launch_bounds__(kNT) void lin_join_kernel(const LinArgs a, const int first_rev) {
+    constexpr int AHEAD = 8;
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
-    const int nseg = a.segs - 1, per = a.DV * a.DK / 4, bhs = a.B * a.H;
+    const int slots = (a.segs - 1) * a.subs, per = a.DV * a.DK / 4, bhs = a.B * a.H;
     const long long idx = static_cast<long long>(blockIdx.x) * kNT + threadIdx.x;
     if (idx >= static_cast<long long>(bhs) * per) return;
     const int bh = static_cast<int>(idx / per);
-    f32x4 *p = reinterpret_cast<f32x4 *>((rev ? a.rev : a.fwd)) + static_cast<size_t>(bh) * nseg * per + idx % per;
-    const float *fac = a.fac + (static_cast<size_t>(rev) * bhs + bh) * a.segs;
-    f32x4 S = p[static_cast<size_t>(rev ? nseg - 1 : 0) * per];
-    for (int m = 1; m < nseg; ++m) {
-        const int j = rev ? nseg - 1 - m : m;
-        S = p[static_cast<size_t>(j) * per] + S * fac[rev ? j + 1 : j];
-        p[static_cast<size_t>(j) * per] = S;
+    f32x4 *p = reinterpret_cast<f32x4 *>(rev ? a.rev : a.fwd) + static_cast<size_t>(bh) * slots * per + idx % per;
+    const float *fac = a.fac + (static_cast<size_t>(rev) * bhs + bh) * slots;
+    f32x4 S = zero4();
+    for (int m = 0; m < slots; m += AHEAD) {
+        f32x4 x[AHEAD];
+        float f[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int j = rev ? slots - 1 - min(m + k, slots - 1) : min(m + k, slots - 1);
+            x[k] = p[static_cast<size_t>(j) * per];
+            f[k] = fac[j];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (m + k >= slots) break;
+            const int j = rev ? slots - 1 - (m + k) : m + k;
+            S = m + k == 0 ? x[k] : x[k] + S * f[k];
+            if ((rev ? j : j + 1) % a.subs == 0) p[static_cast<size_t>(j) * per] = S;
+        }
     }
 }
 
@@ -330,21 +349,6 @@ hipError_t step_typed(const LinArgs &a, float *S, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Segments of the forward: from two workgroups a compute unit on, the time axis stays whole.
-struct LinPlan {
-    int segs, seg_chunks;
-};
-LinPlan fwd_plan(int dtype, int B, int T, int H, int dv) {
-    const int C = lin_chunk(dtype);
-    const long long units = static_cast<long long>(B) * H * (dv / 64), nc = (static_cast<long long>(T) + C - 1) / C;
-    long long segs = 1;
-    if (units > 0 && units < 256) segs = 512 / units;
-    if (segs > nc / 4) segs = nc / 4;
-    if (segs < 1) segs = 1;
-    const long long per = nc ? (nc + segs - 1) / segs : 1;
-    return LinPlan{static_cast<int>(nc ? (nc + per - 1) / per : 1), static_cast<int>(per)};
-}
-
 }  // namespace
 
 bool lin_supported(int dtype, int dk, int dv) {
@@ -355,16 +359,66 @@ bool lin_fits(int B, int T, int H) {
     return H <= (1 << 15) && static_cast<long long>(B) * H < (1LL << 26) && T <= 0x7fff0000;
 }
 
+// A walk of n chunks takes n + 3 steps, workgroups go in rounds of one a compute unit, and cutting
+// the axis costs two launches (about five steps) and the states: a chunk of a piece costs
+// state_cost of a step, three workgroups a compute unit side by side.
+void lin_plan(int dtype, LinArgs &a, long long units, int directions, double state_cost) {
+    const long long C = lin_chunk(dtype), nc = (a.T + C - 1) / C, cus = 256;
+    double best = 0;
+    a.segs = 1;
+    a.seg_chunks = static_cast<int>(nc);
+    for (long long want = 1; want <= 64 && want * 4 <= nc + 3; ++want) {
+        const long long per = (nc + want - 1) / want, segs = (nc + per - 1) / per;
+        const double rounds = static_cast<double>((units * segs + cus - 1) / cus);
+        double cost = rounds * (per + 3);
+        if (segs > 1) cost += 5 + state_cost * units * per * (segs - 1) / cus;
+        if (want == 1 || cost < best) {
+            best = cost;
+            a.segs = static_cast<int>(segs);
+            a.seg_chunks = static_cast<int>(per);
+        }
+    }
+    a.subs = 1;
+    a.sub_chunks = a.seg_chunks;
+    if (a.segs > 1) {
+        const long long walks = static_cast<long long>(a.B) * a.H * (a.DV / 64) * (a.segs - 1) * directions;
+        long long subs = 3 * cus / walks;
+        if (subs > a.seg_chunks / 4) subs = a.seg_chunks / 4;
+        if (subs > 1) {
+            a.sub_chunks = static_cast<int>((a.seg_chunks + subs - 1) / subs);
+            a.subs = (a.seg_chunks + a.sub_chunks - 1) / a.sub_chunks;
+        }
+    }
+}
+size_t lin_states_floats(const LinArgs &a, int directions) {
+    if (a.segs == 1) return 0;
+    const size_t slots = static_cast<size_t>(a.B) * a.H * (a.segs - 1) * a.subs;
+    return directions * slots * a.DK * a.DV + (2 * slots + 3) / 4 * 4;
+}
+float *lin_states_place(LinArgs &a, float *ws, int directions) {
+    if (a.segs == 1) return ws;
+    const size_t n = static_cast<size_t>(a.B) * a.H * (a.segs - 1) * a.subs * a.DK * a.DV;
+    a.fwd = ws;
+    a.rev = ws + n;
+    a.fac = ws + directions * n;
+    return ws + lin_states_floats(a, directions);
+}
+
+namespace {
+// A step with the state alone takes half of one with the outputs.
+void fwd_plan(int dtype, LinArgs &a) { lin_plan(dtype, a, static_cast<long long>(a.B) * a.H * (a.DV / 64), 1, 0.5); }
+}  // namespace
+
 size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv) {
-    const LinPlan p = fwd_plan(dtype, B, T, H, dv);
-    if (p.segs == 1) return 0;
-    const size_t bh = static_cast<size_t>(B) * H;
-    return (bh * (p.segs - 1) * dk * dv + 2 * bh * p.segs) * sizeof(float);
+    LinArgs a{};
+    a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
+    fwd_plan(dtype, a);
+    return lin_states_floats(a, 1) * sizeof(float);
 }
 
 hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, bool exact, hipStream_t stream) {
     const int first = fwd ? 0 : 1, count = (fwd ? 1 : 0) + (rev ? 1 : 0);
-    dim3 grid = lin_grid(static_cast<long long>(a.B) * a.H * (a.segs - 1), a.DV / 64);
+    dim3 grid = lin_grid(static_cast<long long>(a.B) * a.H * (a.segs - 1) * a.subs, a.DV / 64);
     grid.y = count;
     if (dtype == 1) states_typed<Bf16>(a, grid, first, exact, stream);
     else states_typed<F32>(a, grid, first, exact, stream);
@@ -383,14 +437,10 @@ hipError_t launch_lin_copy(float *to, const float *from, size_t n, hipStream_t s
 hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     const size_t bh = static_cast<size_t>(a.B) * a.H, state = static_cast<size_t>(a.DV) * a.DK;
     if (a.T == 0) return a.S_T && a.S_T != a.S0 ? launch_lin_copy(a.S_T, a.S0, bh * state, stream) : hipSuccess;
-    const LinPlan p = fwd_plan(dtype, a.B, a.T, a.H, a.DV);
-    a.segs = p.segs;
-    a.seg_chunks = p.seg_chunks;
-    if (p.segs > 1) {
-        a.fwd = static_cast<float *>(ws);
-        a.fac = a.fwd + bh * (p.segs - 1) * state;
+    fwd_plan(dtype, a);
+    lin_states_place(a, static_cast<float *>(ws), 1);
+    if (a.segs > 1)
         if (hipError_t e = launch_lin_states(dtype, a, true, false, a.S_T != nullptr, stream)) return e;
-    }
     return dtype == 1 ? fwd_typed<Bf16>(a, stream) : fwd_typed<F32>(a, stream);
 }
 

@@ -327,8 +327,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
-    load_across<DK, DV>(S, w.seg > 0 ? a.fwd + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg - 1) * state
-                                     : a.S0 ? a.S0 + w.bh * state : nullptr, c0, lane);
+    load_across<DK, DV>(S, lin_before(a, w.bh, w.seg), c0, lane);
     Decays<P, DK, DV, false> decays(w, lds);
     auto help = [&](int m) {
         if (LAST < L::NB && w.role == 1) product<P, DK, DV, false, DG>(w, lds, m, LAST + w.wave);
@@ -448,9 +447,7 @@ template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     const Walk<P, DK, DV> w(a, unit);
     if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4, BwdLds<P, DK, DV>::NB>(w, lds, w.wave);
-    const size_t state = static_cast<size_t>(DV) * DK;
-    const float *from = w.seg < a.segs - 1 ? a.rev + (static_cast<size_t>(w.bh) * (a.segs - 1) + w.seg) * state
-                                           : a.dS_T ? a.dS_T + w.bh * state : nullptr;
+    const float *from = lin_behind(a, w.bh, w.seg);
     if (w.role == 0) dk_walk<P, DK, DV, DG, NS>(w, lds, from);
     else dv_walk<P, DK, DV>(w, lds, from);
 }
@@ -582,30 +579,19 @@ hipError_t bwd_typed(const LinArgs &a, hipStream_t stream) {
     return a.DV == 128 ? bwd_sized<P, 64, 128>(a, stream) : bwd_sized<P, 64, 64>(a, stream);
 }
 
-// Both walks of every head are 2 B H workgroups, one a compute unit; fewer than the card has cut
-// the time axis.
-void bwd_plan(int dtype, int B, int T, int H, int &segs, int &seg_chunks) {
-    const int C = lin_chunk(dtype);
-    const long long units = 2LL * B * H, nc = (static_cast<long long>(T) + C - 1) / C;
-    long long s = units > 0 ? 256 / units : 1;
-    if (s > nc / 4) s = nc / 4;
-    if (s < 1) s = 1;
-    const long long per = nc ? (nc + s - 1) / s : 1;
-    segs = static_cast<int>(nc ? (nc + per - 1) / per : 1);
-    seg_chunks = static_cast<int>(per);
-}
+// Both walks of every head are 2 B H workgroups.  A chunk's step is long here, and the states of
+// both directions cost a quarter of it.
+void bwd_plan(int dtype, LinArgs &a) { lin_plan(dtype, a, 2LL * a.B * a.H, 2, 0.25); }
 
 }  // namespace
 
 size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg) {
     if (static_cast<long long>(B) * H * T == 0) return 0;
-    int segs, per;
-    bwd_plan(dtype, B, T, H, segs, per);
+    LinArgs a{};
+    a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
+    bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    size_t n = 0;
-    if (segs > 1) n += 2 * bh * (segs - 1) * dk * dv + 2 * bh * segs;
-    if (dg) n += 3 * bh * T + bh * (dk / 16 + 1);
-    return n * sizeof(float);
+    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 1) : 0)) * sizeof(float);
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -620,15 +606,10 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
         }
         return hipGetLastError();
     }
-    bwd_plan(dtype, a.B, a.T, a.H, a.segs, a.seg_chunks);
-    float *p = static_cast<float *>(ws);
-    if (a.segs > 1) {
-        a.fwd = p;
-        a.rev = a.fwd + bh * (a.segs - 1) * state;
-        a.fac = a.rev + bh * (a.segs - 1) * state;
-        p = a.fac + 2 * bh * a.segs;
+    bwd_plan(dtype, a);
+    float *p = lin_states_place(a, static_cast<float *>(ws), 2);
+    if (a.segs > 1)
         if (hipError_t e = launch_lin_states(dtype, a, true, true, a.dg || a.dS0, stream)) return e;
-    }
     if (a.dg) {
         a.tok = p;
         a.edge = a.tok + 3 * bh * a.T;
