@@ -62,8 +62,8 @@ struct LinArgs {
     float *fwd, *rev;                // [B H][(segs - 1) subs][DV][DK]
     float *fac;                      // [2][B H][(segs - 1) subs]: a piece's decay
     float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
-    float *edge;                     // [B H][DK / 16]: <S_T, dS_T> by wave
-    float *head;                     // [B H]: sums of dg over tokens
+    float *edge, *edge0;             // [B H][DK / 16], [B H][4]: <S_T, dS_T> and <S0, dS0> by wave
+    float *chain, *head;             // [B H][chunks]: c; [B][chunks][H]: sums of dg over tokens
 };
 
 bool lin_supported(int dtype, int dk, int dv);

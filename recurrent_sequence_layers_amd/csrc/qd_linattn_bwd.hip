@@ -24,19 +24,18 @@
 // x_t = sum_{s>t} M[s][t] - sum_{i<t} M[t][i], whose prefix sums are the third term, and c comes
 // from a chain over the chunks: with E_n = <S, R> behind chunk n, c_n = E_n - sum b and
 // E_{n-1} = c_n + sum a, from E = <S_T, dS_T> on.  a and b are taken before anything is rounded
-// (the state split as in qd_linattn.h), since dg is fp32.
+// (the state split as in qd_linattn.h), since dg is fp32.  The chain adds up their roundings; what
+// it misses <S0, dS0> by at its other end is taken back in proportion to the squares of the terms
+// that it has passed, which is where it came from.
 #include "qd_internal.h"
 #include "qd_linattn.h"
+#include "qd_mixer.h"
 
 namespace qd {
 namespace {
 
-__device__ __forceinline__ float sum16(float x) {
-    x += dpp_src<0xB1, 0xf>(x);    // quad_perm 1,0,3,2
-    x += dpp_src<0x4E, 0xf>(x);    // quad_perm 2,3,0,1
-    x += dpp_src<0x141, 0xf>(x);   // row_half_mirror
-    return x + dpp_src<0x140, 0xf>(x);   // row_mirror
-}
+__device__ __forceinline__ float sum16(float x) { return group_sum(x, 16); }
+__device__ __forceinline__ float sum64(float x) { return group_sum(x, 64); }
 
 // Twelve waves, two barriers a chunk.  In either walk four waves hold a state, a quarter of its
 // columns each (backwards four more hold it by its other columns): in a chunk's first interval they
@@ -314,6 +313,22 @@ __device__ __forceinline__ void load_across(f32x4 (&S)[NC][DV / 16], const float
             for (int e = 0; e < 4; ++e) S[c][t][e] = from[(lin_row(t, lane) + e) * DK + c0 + 16 * c + (lane & 15)];
 }
 
+// The inner product of a wave's columns with those of [DV][DK] (null: zeros)
+template <int DK, int DV, int NC>
+__device__ __forceinline__ float inner(const f32x4 (&S)[NC][DV / 16], const float *other, int c0, int lane) {
+    if (!other) return 0.f;
+    f32x4 d[NC][DV / 16];
+    load_across<DK, DV>(d, other, c0, lane);
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = fmaf(S[c][t][e], d[c][t][e], s);
+    return sum64(s);
+}
+
 // ---------------------------------------------------------------- dq, forwards
 template <class P, int DK, int DV, bool DG>
 __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
@@ -357,16 +372,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     }
     if constexpr (DG) {
         if (w.seg == a.segs - 1) {               // <S_T, dS_T>
-            f32x4 d[NC][DV / 16];
-            load_across<DK, DV>(d, a.dS_T ? a.dS_T + w.bh * state : nullptr, c0, lane);
-            float s = 0.f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int t = 0; t < DV / 16; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(S[c][t][e], d[c][t][e], s);
-            for (int k = 1; k < 64; k *= 2) s += __shfl_xor(s, k);
+            const float s = inner<DK, DV>(S, a.dS_T ? a.dS_T + w.bh * state : nullptr, c0, lane);
             if (lane == 0) a.edge[static_cast<size_t>(w.bh) * NS + wave] = s;
         }
     }
@@ -433,6 +439,10 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         __syncthreads();
     }
     const LinArgs &a = w.a;
+    if (DG && w.seg == 0) {                      // <S0, dS0>
+        const float s = inner<DK, DV>(R, a.S0 ? a.S0 + static_cast<size_t>(w.bh) * DV * DK : nullptr, c0, lane);
+        if (lane == 0) a.edge0[static_cast<size_t>(w.bh) * 4 + w.wave] = s;
+    }
     if (a.dS0 && w.seg == 0) {
         float *to = a.dS0 + static_cast<size_t>(w.bh) * DV * DK;
 #pragma unroll
@@ -466,97 +476,141 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
 }
 
 // ---------------------------------------------------------------- dg
-// One workgroup a (sequence, head): the chain of c over the chunks from the last, 64 at a time, a
-// chunk a wave.  Bound by the latency of its few passes over three numbers a token.
-constexpr int kDgWaves = 16, kDgChunks = 512;
+constexpr int kDgWaves = 16, kDgChunks = 1024;
+
+// The chain of c over a head's chunks: one workgroup, a chunk a wave for its sums, then one wave from
+// the last chunk on, 1024 at a time.  Bound by the latency of these few passes.
 template <int C>
-__global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) {
-    __shared__ double sa[kDgChunks], sb[kDgChunks];
-    __shared__ double carry, wsum[kDgWaves];
-    const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, wave = wave_id(), lane = lane_id();
+__global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a) {
+    __shared__ double sd[kDgChunks], sb[kDgChunks], sv[kDgChunks];
+    __shared__ double total[kDgWaves][2];
+    const int bh = blockIdx.x, b = bh / a.H, wave = wave_id(), lane = lane_id();
     const size_t bhs = static_cast<size_t>(a.B) * a.H;
-    const float *x = a.tok + static_cast<size_t>(bh) * a.T, *ta = x + bhs * a.T, *tb = ta + bhs * a.T;
-    const int len = lin_len(a, b), nc = (a.T + C - 1) / C;
-    auto get = [&](const float *p, int n, int i) { return i < C && n * C + i < a.T ? p[n * C + i] : 0.f; };
-    if (threadIdx.x == 0) {
-        double e = 0;
-        for (int w = 0; w < a.DK / 16; ++w) e += a.edge[static_cast<size_t>(bh) * (a.DK / 16) + w];
-        carry = e;
+    const float *ta = a.tok + (bhs + bh) * a.T, *tb = ta + bhs * a.T;
+    const int nc = (lin_len(a, b) + C - 1) / C, all = (a.T + C - 1) / C;
+    float *c = a.chain + static_cast<size_t>(bh) * all;
+    // sum a - sum b, sum b and the squares of a chunk's terms
+    auto sums = [&](int first, int count) {
+        constexpr int AHEAD = 4;
+        for (int m = wave; m < count; m += AHEAD * kDgWaves) {
+            float va[AHEAD], vb[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int n = m + k * kDgWaves, t = (first + n) * C + lane;
+                const bool in = n < count && lane < C && t < a.T;
+                va[k] = in ? ta[t] : 0.f;
+                vb[k] = in ? tb[t] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float x = sum64(va[k]), y = sum64(vb[k]), v = sum64(fmaf(va[k], va[k], vb[k] * vb[k]));
+                if (lane == 0 && m + k * kDgWaves < count) {
+                    sd[m + k * kDgWaves] = static_cast<double>(x) - y;
+                    sb[m + k * kDgWaves] = y;
+                    sv[m + k * kDgWaves] = v;
+                }
+            }
+        }
+        __syncthreads();
+    };
+    double D = 0, V = 0;
+    for (int last = nc; last > 0; last -= kDgChunks) {
+        const int first = max(last - kDgChunks, 0);
+        sums(first, last - first);
+        for (int m = threadIdx.x; m < last - first; m += 64 * kDgWaves) {
+            D += sd[m];
+            V += sv[m];
+        }
+        __syncthreads();
     }
-    double total = 0;
+    for (int k = 1; k < 64; k *= 2) {
+        D += __shfl_xor(D, k);
+        V += __shfl_xor(V, k);
+    }
+    if (lane == 0) {
+        total[wave][0] = D;
+        total[wave][1] = V;
+    }
+    __syncthreads();
+    double E = 0, E0 = 0;
+    D = V = 0;
+    for (int w = 0; w < kDgWaves; ++w) {
+        D += total[w][0];
+        V += total[w][1];
+    }
+    for (int w = 0; w < a.DK / 16; ++w) E += a.edge[static_cast<size_t>(bh) * (a.DK / 16) + w];
+    for (int w = 0; w < 4; ++w) E0 += a.edge0[static_cast<size_t>(bh) * 4 + w];
+    const double missed = E + D - E0, part = V > 0 ? missed / V : 0;
+    double passed = 0;
     for (int last = nc; last > 0; last -= kDgChunks) {
         const int first = max(last - kDgChunks, 0), count = last - first;
-        for (int m = wave; m < count; m += kDgWaves) {
-            float va = get(ta, first + m, lane), vb = get(tb, first + m, lane);
-            for (int d = 1; d < 64; d *= 2) {
-                va += __shfl_xor(va, d);
-                vb += __shfl_xor(vb, d);
-            }
-            if (lane == 0) {
-                sa[m] = va;
-                sb[m] = vb;
-            }
-        }
-        __syncthreads();
+        if (nc > kDgChunks) sums(first, count);      // else they are still there
         if (wave == 0) {
-            // c_n = E + sum of (a - b) over later chunks - b_n; a lane's chunks are consecutive, from the last on
+            // a lane's chunks are consecutive, from the last on
             constexpr int PER = kDgChunks / 64;
-            double d[PER], mine = 0;
-#pragma unroll
+            double d = 0, v = 0;
             for (int i = 0; i < PER; ++i) {
                 const int m = count - 1 - (lane * PER + i);
-                d[i] = m >= 0 ? sa[m] - sb[m] : 0.0;
-                mine += d[i];
+                if (m >= 0) {
+                    d += sd[m];
+                    v += sv[m];
+                }
             }
-            double run = mine;
+            double dd = d, vv = v;
             for (int s = 1; s < 64; s *= 2) {
-                const double y = __shfl_up(run, s);
-                if (lane >= s) run += y;
+                const double y = __shfl_up(dd, s), z = __shfl_up(vv, s);
+                if (lane >= s) {
+                    dd += y;
+                    vv += z;
+                }
             }
-            double e = carry + run - mine;
-            const double end = carry + __shfl(run, 63);
-#pragma unroll
+            double e = E + dd - d, p = passed + vv - v;
             for (int i = 0; i < PER; ++i) {
                 const int m = count - 1 - (lane * PER + i);
-                if (m >= 0) sa[m] = e - sb[m];
-                e += d[i];
+                if (m < 0) break;
+                c[first + m] = static_cast<float>(e - sb[m] - part * (p + 0.5 * sv[m]));
+                e += sd[m];
+                p += sv[m];
             }
-            if (lane == 0) carry = end;
+            E += __shfl(dd, 63);
+            passed += __shfl(vv, 63);
         }
         __syncthreads();
-        for (int m = wave; m < count; m += kDgWaves) {
-            const int n = first + m;
-            const float y = get(x, n, lane) + get(tb, n, lane);
-            const float before = wave_inclusive_sum(y) - y;
-            const float back = wave_inclusive_sum(get(ta, n, 63 - lane));
-            const float behind = __shfl(back, 63 - lane);
-            const int t = n * C + lane;
-            if (lane < C && t < a.T) {
-                const float v = t < len ? static_cast<float>(sa[m] + static_cast<double>(before + behind)) : 0.f;
-                if (a.decay == kTokenDecay) a.dg[(static_cast<size_t>(b) * a.T + t) * a.H + h] = v;
-                else total += v;
-            }
-        }
-        __syncthreads();
+    }
+}
+
+// dg of a chunk of sixteen heads: a wave a head, rows of heads through LDS.
+template <int C>
+__global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) {
+    __shared__ float out[64][kDgWaves + 1];
+    const int nc = (a.T + C - 1) / C, n = blockIdx.x % nc, b = blockIdx.x / nc, h0 = blockIdx.y * kDgWaves;
+    const int wave = wave_id(), lane = lane_id(), h = h0 + wave;
+    const size_t bhs = static_cast<size_t>(a.B) * a.H, bh = static_cast<size_t>(b) * a.H + h;
+    const int len = lin_len(a, b), live = min(max(len - n * C, 0), C);
+    float v = 0.f;
+    if (h < a.H && live > 0) {
+        const float *x = a.tok + bh * a.T + n * C, *ta = x + bhs * a.T, *tb = ta + bhs * a.T;
+        const int back = 63 - lane;
+        const float y = lane < live ? x[lane] + tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
+        const float before = wave_inclusive_sum(y) - y;
+        const float behind = __shfl(wave_inclusive_sum(z), back);
+        v = lane < live ? a.chain[bh * nc + n] + (before + behind) : 0.f;
     }
     if (a.decay == kHeadDecay) {
-        for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-        if (lane == 0) wsum[wave] = total;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            double s = 0;
-            for (int w = 0; w < kDgWaves; ++w) s += wsum[w];
-            a.head[bh] = static_cast<float>(s);
-        }
+        v = sum64(v);
+        if (h < a.H && lane == 0) a.head[(static_cast<size_t>(b) * nc + n) * a.H + h] = v;
+        return;
     }
+    out[lane][wave] = v;
+    __syncthreads();
+    const int t = threadIdx.x / kDgWaves, k = threadIdx.x % kDgWaves;
+    if (t < C && n * C + t < a.T && h0 + k < a.H)
+        a.dg[(static_cast<size_t>(b) * a.T + n * C + t) * a.H + h0 + k] = out[t][k];
 }
-__global__ __launch_bounds__(256) void lin_dg_head_kernel(const LinArgs a) {
-    const int h = blockIdx.x * 256 + threadIdx.x;
-    if (h >= a.H) return;
-    double s = 0;
-    for (int b = 0; b < (a.T ? a.B : 0); ++b) s += a.head[static_cast<size_t>(b) * a.H + h];
-    a.dg[h] = static_cast<float>(s);
-}
+struct HeadStore {
+    float *to;
+    __device__ __forceinline__ void operator()(long long h, float v) const { to[h] = v; }
+};
 
 template <class P, int DK, int DV>
 hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
@@ -568,8 +622,10 @@ hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
     else hipLaunchKernelGGL((lin_bwd_kernel<P, DK, DV, false, 2>), grid, blk, sizeof(L), stream, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (a.dg) {
-        hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
-        if (a.decay == kHeadDecay) hipLaunchKernelGGL(lin_dg_head_kernel, dim3((a.H + 255) / 256), dim3(256), 0, stream, a);
+        const unsigned nc = (a.T + L::C - 1) / L::C;
+        hipLaunchKernelGGL(lin_chain_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
+        hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(nc * a.B, (a.H + kDgWaves - 1) / kDgWaves), dim3(64 * kDgWaves), 0, stream, a);
+        if (a.decay == kHeadDecay) column_sum(a.head, static_cast<int>(nc * a.B), a.H, HeadStore{a.dg}, stream);
     }
     return hipGetLastError();
 }
@@ -591,7 +647,7 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 1) : 0)) * sizeof(float);
+    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 4) + 2 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -600,10 +656,7 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
         // no tokens: dS0 = dS_T, and sums over tokens are zero
         if (a.dS0 && bh)
             if (hipError_t e = launch_lin_copy(a.dS0, a.dS_T, bh * state, stream)) return e;
-        if (a.dg && a.decay == kHeadDecay && a.H) {
-            a.T = 0;
-            hipLaunchKernelGGL(lin_dg_head_kernel, dim3((a.H + 255) / 256), dim3(256), 0, stream, a);
-        }
+        if (a.dg && a.decay == kHeadDecay && a.H) column_sum(a.dg, 0, a.H, HeadStore{a.dg}, stream);
         return hipGetLastError();
     }
     bwd_plan(dtype, a);
@@ -613,7 +666,9 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (a.dg) {
         a.tok = p;
         a.edge = a.tok + 3 * bh * a.T;
-        a.head = a.edge + bh * (a.DK / 16);
+        a.edge0 = a.edge + bh * (a.DK / 16);
+        a.chain = a.edge0 + bh * 4;
+        a.head = a.chain + bh * ((a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype));
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
 }
