@@ -338,10 +338,13 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C,
                                            const typename P::F (&col)[NC][C / 32][2], const float *weight, float all,
                                            const LinLane &l) {
     const float *w = weight + 8 * (l.lane >> 4);
+    constexpr bool kApart = P::kBytes == 4;      // the chunk's sum by itself: fewer roundings at the state's size
+    if constexpr (!kApart) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int b = 0; b < D / 16; ++b) S[c][b] *= all;
+            for (int b = 0; b < D / 16; ++b) S[c][b] *= all;
+    }
 #pragma unroll
     for (int u = 0; u < C / 32; ++u) {
         LinSplit<P, NS> lo[NC], hi[NC];
@@ -355,9 +358,17 @@ __device__ __forceinline__ void lin_update(f32x4 (&S)[NC][D / 16], LinTile<P, C,
         for (int b = 0; b < D / 16; ++b) {
             const typename P::F r0 = rows.across(u, 0, b, l), r1 = rows.across(u, 1, b, l);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c) {
+                if constexpr (kApart) {
+                    static_assert(C == 32, "one sum a chunk");
+                    const f32x4 sum = P::mma2(zero4(), r0, r1, lo[c].p[0], hi[c].p[0]);
 #pragma unroll
-                for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[c][b] = P::mma2(S[c][b], r0, r1, lo[c].p[j], hi[c].p[j]);
+                    for (int e = 0; e < 4; ++e) S[c][b][e] = fmaf(S[c][b][e], all, sum[e]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < LinSplit<P, NS>::N; ++j) S[c][b] = P::mma2(S[c][b], r0, r1, lo[c].p[j], hi[c].p[j]);
+                }
+            }
         }
     }
 }
@@ -383,10 +394,15 @@ __device__ __forceinline__ void lin_read(f32x4 (&acc)[NC][C / 16], const f32x4 (
         for (int i = 0; i < C / 16; ++i) {
             typename P::F x0, x1;
             rows.oct(i, u, l, x0, x1);
+            if constexpr (P::kBytes == 4) {      // sums of 32 products, then their sum
 #pragma unroll
-            for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j)
+                for (int c = 0; c < NC; ++c) acc[c][i] += P::mma2(zero4(), s0[c].p[0], s1[c].p[0], x0, x1);
+            } else {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) acc[c][i] = P::mma2(acc[c][i], s0[c].p[j], s1[c].p[j], x0, x1);
+                for (int j = LinSplit<P, NS>::N - 1; j >= 0; --j)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) acc[c][i] = P::mma2(acc[c][i], s0[c].p[j], s1[c].p[j], x0, x1);
+            }
         }
     }
 }
