@@ -128,58 +128,69 @@ struct Decays {
     }
 };
 
-// One block of the products of the next chunk, m + 1.  REV: the walk goes backwards and forms P by
-// its earlier tokens' rows, of q k and of do v; else by its later tokens' rows, of do v.
-template <class P, int DK, int DV, bool REV, bool DG>
+// The products of the next chunk, m + 1, decayed.  Backwards by its earlier tokens' rows: a row of
+// blocks, later tokens in block I, all of it in flight at once (block by block each waits for its
+// own LDS reads, and the second interval is this role's to hold up).
+template <class P, int I, int C, int D>
+__device__ __forceinline__ void products_back(LinTile<P, C, D> &later, LinTile<P, C, D> &earlier, const LinGates<C> &gates,
+                                              LinTile<P, C, C> &to, const LinLane &l) {
+    if constexpr (I < C / 16) {
+        const int g4 = l.lane >> 4, r16 = l.lane & 15, s = 16 * I + 4 * g4;
+        f32x4 x[I + 1];
+#pragma unroll
+        for (int j = 0; j <= I; ++j) x[j] = zero4();
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+            typename P::F a0, a1, b0[I + 1], b1[I + 1];
+            later.oct(I, u, l, a0, a1);
+#pragma unroll
+            for (int j = 0; j <= I; ++j) earlier.oct(j, u, l, b0[j], b1[j]);
+#pragma unroll
+            for (int j = 0; j <= I; ++j) x[j] = P::mma2(x[j], a0, a1, b0[j], b1[j]);
+        }
+        const f32x4 hi = lds_f32x4(gates.hi + s), lo = lds_f32x4(gates.lo + s);
+#pragma unroll
+        for (int j = 0; j <= I; ++j) {
+            const int t = 16 * j + r16;
+            const float ht = gates.hi[t], lt = gates.lo[t];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = x[j][e] * lin_exp2((hi[e] - ht) + (lo[e] - lt));
+                x[j][e] = j < I || t <= s + e ? v : 0.f;
+            }
+            P::st4(to.four(j, I, l), x[j]);
+        }
+    }
+}
+// Forwards by its later tokens' rows, of do v; for dg with M's sums over the block.
+template <class P, int DK, int DV, bool DG>
 __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int m, int p) {
     typename BwdLds<P, DK, DV>::Chunk &next = lds.c[(m + 1) & 1];
     const LinGates<kLinChunk<P>> &gates = lds.gates[(m + 1) % 3];
     int i, j;
-    lin_pair(p, i, j);                           // later tokens in block i, earlier ones in block j
-    if constexpr (REV) {
-        f32x4 qk = lin_block<P>(next.q, next.k, i, j, w.l);
-        f32x4 ov = lin_block<P>(next.o, next.v, i, j, w.l);
-        const int t = 16 * j + w.r16, s = 16 * i + 4 * w.g4;
-        const f32x4 hi = lds_f32x4(gates.hi + s) - gates.hi[t], lo = lds_f32x4(gates.lo + s) - gates.lo[t];
+    lin_pair(p, i, j);
+    f32x4 ov = lin_block<P>(next.v, next.o, j, i, w.l);
+    const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
+    ov *= lin_between(gates, s, t);
+    if (i == j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? ov[e] : 0.f;
+    }
+    P::st4(lds.p[0].four(i, j, w.l), ov);
+    if constexpr (DG) {
+        const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
+        f32x4 col;
+        float row = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float d = lin_exp2(hi[e] + lo[e]);
-            qk[e] *= d;
-            ov[e] *= d;
+            const float x = t + e < s ? ov[e] * qk[e] : 0.f;
+            row += x;
+            col[e] = sum16(x);
         }
-        if (i == j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                qk[e] = t <= s + e ? qk[e] : 0.f;
-                ov[e] = t <= s + e ? ov[e] : 0.f;
-            }
-        }
-        P::st4(lds.p[0].four(j, i, w.l), qk);
-        P::st4(lds.p[1].four(j, i, w.l), ov);
-    } else {
-        f32x4 ov = lin_block<P>(next.v, next.o, j, i, w.l);
-        const int s = 16 * i + w.r16, t = 16 * j + 4 * w.g4;
-        ov *= lin_between(gates, s, t);
-        if (i == j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? ov[e] : 0.f;
-        }
-        P::st4(lds.p[0].four(i, j, w.l), ov);
-        if constexpr (DG) {
-            const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
-            f32x4 col;
-            float row = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = t + e < s ? ov[e] * qk[e] : 0.f;
-                row += x;
-                col[e] = sum16(x);
-            }
-            row += __shfl_xor(row, 16);
-            row += __shfl_xor(row, 32);
-            if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
-            if (w.lane < 16) lds.rows[p][w.r16] = row;
-        }
+        row += __shfl_xor(row, 16);
+        row += __shfl_xor(row, 32);
+        if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
+        if (w.lane < 16) lds.rows[p][w.r16] = row;
     }
 }
 
@@ -235,7 +246,25 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             w.term(0, n, valid, tid, x);
         }
         __syncthreads();
-        for (int p = wave; p < LAST; p += NW) product<P, DK, DV, REV, DG>(w, lds, m, p);
+        if constexpr (REV) {
+            // five blocks a wave (fp32: two or one)
+            const LinGates<C> &gates = lds.gates[(m + 1) % 3];
+            if (wave == 0) {
+                products_back<P, 3>(next.q, next.k, gates, lds.p[0], w.l);
+                products_back<P, 0>(next.q, next.k, gates, lds.p[0], w.l);
+            } else if (wave == 1) {
+                products_back<P, 3>(next.o, next.v, gates, lds.p[1], w.l);
+                products_back<P, 0>(next.o, next.v, gates, lds.p[1], w.l);
+            } else if (wave == 2) {
+                products_back<P, 2>(next.q, next.k, gates, lds.p[0], w.l);
+                products_back<P, 1>(next.q, next.k, gates, lds.p[0], w.l);
+            } else {
+                products_back<P, 2>(next.o, next.v, gates, lds.p[1], w.l);
+                products_back<P, 1>(next.o, next.v, gates, lds.p[1], w.l);
+            }
+        } else {
+            for (int p = wave; p < LAST; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
+        }
         if constexpr (DG) {
             float s = 0.f;
 #pragma unroll
@@ -336,8 +365,8 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
     const int wave = 4 * w.role + w.wave;
-    // with eight waves on the state, whose update is short, four of them take a block each
-    constexpr int LAST = NS == 8 && L::NB == 10 ? 6 : L::NB;
+    // with eight waves on the state, whose update is short, six of them take a block each
+    constexpr int LAST = NS == 8 && L::NB == 10 ? 4 : L::NB;
     if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS, LAST>(w, lds, wave - NS);
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
@@ -345,7 +374,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     load_across<DK, DV>(S, lin_before(a, w.bh, w.seg), c0, lane);
     Decays<P, DK, DV, false> decays(w, lds);
     auto help = [&](int m) {
-        if (LAST < L::NB && w.role == 1) product<P, DK, DV, false, DG>(w, lds, m, LAST + w.wave);
+        if (LAST < L::NB && wave >= 2) product<P, DK, DV, DG>(w, lds, m, LAST + wave - 2);
     };
     __syncthreads();                             // the first chunk is brought
     help(-1);
@@ -579,6 +608,40 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
     }
 }
 
+// The same chain for the chunk n by one wave, for few chunks: no launch of its own.
+constexpr int kFewChunks = 16;
+template <int C>
+__device__ __forceinline__ float few_chain(const LinArgs &a, size_t bh, const float *ta, const float *tb, int nc, int n, int lane) {
+    float sa[kFewChunks], sb[kFewChunks];
+#pragma unroll
+    for (int m = 0; m < kFewChunks; ++m) {
+        const bool in = m < nc && lane < C && m * C + lane < a.T;
+        sa[m] = in ? ta[m * C + lane] : 0.f;
+        sb[m] = in ? tb[m * C + lane] : 0.f;
+    }
+    double D = 0, V = 0, later = 0, passed = 0;
+    float own = 0.f;
+#pragma unroll
+    for (int m = 0; m < kFewChunks; ++m) {
+        const float v = sum64(fmaf(sa[m], sa[m], sb[m] * sb[m])), y = sum64(sb[m]);
+        const double d = static_cast<double>(sum64(sa[m])) - y;
+        D += d;
+        V += v;
+        if (m > n) {
+            later += d;
+            passed += v;
+        }
+        if (m == n) {
+            passed += 0.5 * v;
+            own = y;
+        }
+    }
+    double E = 0, E0 = 0;
+    for (int w = 0; w < a.DK / 16; ++w) E += a.edge[bh * (a.DK / 16) + w];
+    for (int w = 0; w < 4; ++w) E0 += a.edge0[bh * 4 + w];
+    return static_cast<float>(E + later - own - (V > 0 ? (E + D - E0) / V * passed : 0));
+}
+
 // dg of a chunk of sixteen heads: a wave a head, rows of heads through LDS.
 template <int C>
 __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) {
@@ -594,7 +657,8 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
         const float y = lane < live ? x[lane] + tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
         const float before = wave_inclusive_sum(y) - y;
         const float behind = __shfl(wave_inclusive_sum(z), back);
-        v = lane < live ? a.chain[bh * nc + n] + (before + behind) : 0.f;
+        const float c = nc <= kFewChunks ? few_chain<C>(a, bh, ta - n * C, tb - n * C, nc, n, lane) : a.chain[bh * nc + n];
+        v = lane < live ? c + (before + behind) : 0.f;
     }
     if (a.decay == kHeadDecay) {
         v = sum64(v);
@@ -623,7 +687,7 @@ hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
     if (hipError_t e = hipGetLastError()) return e;
     if (a.dg) {
         const unsigned nc = (a.T + L::C - 1) / L::C;
-        hipLaunchKernelGGL(lin_chain_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
+        if (nc > kFewChunks) hipLaunchKernelGGL(lin_chain_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
         hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(nc * a.B, (a.H + kDgWaves - 1) / kDgWaves), dim3(64 * kDgWaves), 0, stream, a);
         if (a.decay == kHeadDecay) column_sum(a.head, static_cast<int>(nc * a.B), a.H, HeadStore{a.dg}, stream);
     }
