@@ -414,7 +414,9 @@ int qdelta_group_norm_bwd(const void *x, const float *weight, const float *bias,
  *   lens      as for qdelta_conv_fwd: padding is not read and its rows of o are left as they were.
  *   d_k, d_v in {64, 128}; H <= 32768.
  * Evaluated in chunks of 64 (fp32: 32) tokens: a NaN or an infinity in a token reaches the outputs
- * of its whole chunk, the earlier tokens' too.  T == 0 writes S_T = S0 (or zeros).
+ * of its whole chunk, the earlier tokens' too; a decay below 2^-126 over part of a chunk is zero,
+ * and a growing one (g > 0) has to stay below 2^127 over any part of a chunk.  T == 0 writes
+ * S_T = S0 (or zeros).
  * workspace: at least qdelta_linattn_fwd_workspace_bytes (0 where B*H*d_v/64 workgroups fill the
  * card; else the states of the segments that the time axis is cut into), 16-byte aligned.
  */

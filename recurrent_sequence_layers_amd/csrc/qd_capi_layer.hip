@@ -22,8 +22,8 @@ int status(hipError_t e) { return e == hipSuccess ? QD_OK : QD_ERR_HIP; }
 int decay_of(const float *g, int per_head) { return !g ? qd::kNoDecay : per_head ? qd::kHeadDecay : qd::kTokenDecay; }
 size_t decay_bytes(int B, int T, int H, int per_head) { return per_head ? prod(H, 4) : prod(prod(B, T), H, 4); }
 
-bool lin_ok(int B, int T, int H, int d_k, int d_v, int dtype) {
-    return qd::lin_supported(dtype, d_k, d_v) && qd::lin_fits(B, T, H);
+bool lin_ok(int B, int T, int H, int d_k, int d_v, int dtype, qd::LinCall call) {
+    return qd::lin_supported(dtype, d_k, d_v) && qd::lin_fits(dtype, B, T, H, call);
 }
 bool norm_ok(int N, int C, int dtype) { return (dtype == QD_F32 || dtype == QD_BF16) && qd::block_norm_fits(dtype, N, C); }
 
@@ -32,7 +32,7 @@ bool norm_ok(int N, int C, int dtype) { return (dtype == QD_F32 || dtype == QD_B
 extern "C" {
 
 size_t qdelta_linattn_fwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int dtype) {
-    if (B <= 0 || T <= 0 || H <= 0 || !lin_ok(B, T, H, d_k, d_v, dtype)) return 0;
+    if (B <= 0 || T <= 0 || H <= 0 || !lin_ok(B, T, H, d_k, d_v, dtype, qd::kLinFwd)) return 0;
     return qd::lin_fwd_workspace(dtype, B, T, H, d_k, d_v);
 }
 
@@ -40,7 +40,7 @@ int qdelta_linattn_fwd(const void *q, const void *k, const void *v, const float 
                        float *S_T, int B, int T, int H, int d_k, int d_v, int g_per_head, int dtype, void *workspace,
                        size_t ws_bytes, void *stream) {
     if (B < 0 || T < 0 || H < 0) return QD_ERR_INVALID_ARG;
-    if (!lin_ok(B, T, H, d_k, d_v, dtype)) return QD_ERR_UNSUPPORTED;
+    if (!lin_ok(B, T, H, d_k, d_v, dtype, qd::kLinFwd)) return QD_ERR_UNSUPPORTED;
     if (prod(B, H) == 0) return QD_OK;
     if (T > 0 && (!q || !k || !v || !o)) return QD_ERR_INVALID_ARG;
     const size_t need = qdelta_linattn_fwd_workspace_bytes(B, T, H, d_k, d_v, dtype);
@@ -59,7 +59,7 @@ int qdelta_linattn_fwd(const void *q, const void *k, const void *v, const float 
 int qdelta_linattn_step(const void *q, const void *k, const void *v, const float *g, float *S, void *o, int N, int H, int d_k,
                         int d_v, int g_per_head, int dtype, void *stream) {
     if (N < 0 || H < 0) return QD_ERR_INVALID_ARG;
-    if (!lin_ok(N, 1, H, d_k, d_v, dtype)) return QD_ERR_UNSUPPORTED;
+    if (!lin_ok(N, 1, H, d_k, d_v, dtype, qd::kLinStep)) return QD_ERR_UNSUPPORTED;
     if (prod(N, H) == 0) return QD_OK;
     if (!q || !k || !v || !S || !o) return QD_ERR_INVALID_ARG;
     if (!all_aligned({q, k, v, S, o})) return QD_ERR_INVALID_ARG;
@@ -73,7 +73,7 @@ int qdelta_linattn_step(const void *q, const void *k, const void *v, const float
 }
 
 size_t qdelta_linattn_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int want_dg, int dtype) {
-    if (B <= 0 || T <= 0 || H <= 0 || !lin_ok(B, T, H, d_k, d_v, dtype)) return 0;
+    if (B <= 0 || T <= 0 || H <= 0 || !lin_ok(B, T, H, d_k, d_v, dtype, qd::kLinBwd)) return 0;
     return qd::lin_bwd_workspace(dtype, B, T, H, d_k, d_v, want_dg != 0);
 }
 
@@ -81,7 +81,7 @@ int qdelta_linattn_bwd(const void *q, const void *k, const void *v, const float 
                        const void *d_o, const float *dS_T, void *dq, void *dk, void *dv, float *dg, float *dS0, int B, int T,
                        int H, int d_k, int d_v, int g_per_head, int dtype, void *workspace, size_t ws_bytes, void *stream) {
     if (B < 0 || T < 0 || H < 0) return QD_ERR_INVALID_ARG;
-    if (!lin_ok(B, T, H, d_k, d_v, dtype)) return QD_ERR_UNSUPPORTED;
+    if (!lin_ok(B, T, H, d_k, d_v, dtype, qd::kLinBwd)) return QD_ERR_UNSUPPORTED;
     if (H == 0) return QD_OK;
     if (!g && dg) return QD_ERR_INVALID_ARG;
     if (prod(B, T) > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return QD_ERR_INVALID_ARG;

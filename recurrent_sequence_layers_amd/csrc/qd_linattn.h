@@ -60,14 +60,15 @@ struct LinArgs {
     // of every one but the first
     int segs, seg_chunks, subs, sub_chunks;
     float *fwd, *rev;                // [B H][(segs - 1) subs][DV][DK]
-    float *fac;                      // [2][B H][(segs - 1) subs]: a piece's decay
+    float *fac;                      // [2][B H][(segs - 1) subs]: the root of a piece's decay
     float *tok;                      // [3][B H][T]: terms of dg, see qd_linattn_bwd.hip
     float *edge, *edge0;             // [B H][DK / 16], [B H][4]: <S_T, dS_T> and <S0, dS0> by wave
     float *chain, *head;             // [B H][chunks]: c; [B][chunks][H]: sums of dg over tokens
 };
 
 bool lin_supported(int dtype, int dk, int dv);
-bool lin_fits(int B, int T, int H);
+enum LinCall { kLinStep, kLinFwd, kLinBwd };
+bool lin_fits(int dtype, int B, int T, int H, LinCall call);
 size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv);
 hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream);
 hipError_t launch_lin_step(int dtype, const LinArgs &a, float *S, hipStream_t stream);   // T = 1

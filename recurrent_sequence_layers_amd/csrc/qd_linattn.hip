@@ -220,12 +220,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
     }
     lin_keep<DK>(S[0], (rev ? a.rev : a.fwd) + (static_cast<size_t>(bh) * slots + slot) * state, col, lane);
     if (cb == 0 && wave == 3 && lane == 0)
-        a.fac[(static_cast<size_t>(rev) * bhs + bh) * slots + slot] = lin_exp2(static_cast<float>(total));
+        a.fac[(static_cast<size_t>(rev) * bhs + bh) * slots + slot] = lin_exp2(static_cast<float>(0.5 * total));
 }
 
 // The pieces' own states to the states at the segments' borders: forwards slot j becomes the state
 // behind piece j, backwards the gradient of the state before its piece; written where a segment
-// begins.  Eight pieces are on their way at a time.
+// begins.  Eight pieces are on their way at a time.  A piece's decay is there as its root: it may
+// lie beyond fp32 where its product with a state does not.
 __global__ __launch_bounds__(kNT) void lin_join_kernel(const LinArgs a, const int first_rev) {
     constexpr int AHEAD = 8;
     const bool rev = first_rev + static_cast<int>(blockIdx.y) > 0;
@@ -249,7 +250,7 @@ __global__ __launch_bounds__(kNT) void lin_join_kernel(const LinArgs a, const in
         for (int k = 0; k < AHEAD; ++k) {
             if (m + k >= slots) break;
             const int j = rev ? slots - 1 - (m + k) : m + k;
-            S = m + k == 0 ? x[k] : x[k] + S * f[k];
+            S = m + k == 0 ? x[k] : x[k] + S * f[k] * f[k];
             if ((rev ? j : j + 1) % a.subs == 0) p[static_cast<size_t>(j) * per] = S;
         }
     }
@@ -354,9 +355,13 @@ hipError_t step_typed(const LinArgs &a, float *S, hipStream_t stream) {
 bool lin_supported(int dtype, int dk, int dv) {
     return (dtype == 0 || dtype == 1) && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
 }
-// 32-bit row offsets inside a chunk, and grids
-bool lin_fits(int B, int T, int H) {
-    return H <= (1 << 15) && static_cast<long long>(B) * H < (1LL << 26) && T <= 0x7fff0000;
+// Row offsets inside a chunk stay within 31 bits, and launches within 2^32 threads: of the walks,
+// 256 threads a head for a token, 1024 forwards, 1536 backwards, and of dg, 1024 a chunk.
+bool lin_fits(int dtype, int B, int T, int H, LinCall call) {
+    const long long lim = (1LL << 32) - (1 << 16), per = call == kLinStep ? 256 : call == kLinFwd ? 1024 : 1536;
+    const long long chunks = B * ((static_cast<long long>(T) + lin_chunk(dtype) - 1) / lin_chunk(dtype));
+    return H <= (1 << 15) && T <= 0x7fff0000 && static_cast<long long>(B) * H * per < lim &&
+           (call != kLinBwd || chunks * 1024 < lim);
 }
 
 // A walk of n chunks takes n + 3 steps, workgroups go in rounds of one a compute unit, and cutting
