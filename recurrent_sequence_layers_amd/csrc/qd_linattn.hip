@@ -52,6 +52,9 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     // a sequence that ends before the segment leaves it without chunks
     const int c0 = seg * a.seg_chunks, c1 = max(c0, min(c0 + a.seg_chunks, (len + C - 1) / C));
     if (c1 == c0 && !(a.S_T && seg == a.segs - 1)) return;
+    // in one chunk P is a sum of two: over few tokens its roundings would not average out, and the
+    // other chunks' tile is free
+    const bool few = c1 - c0 == 1;
     const size_t sdk = static_cast<size_t>(a.H) * DK * P::kBytes, sdv = static_cast<size_t>(a.H) * a.DV * P::kBytes;
     const size_t tok0 = static_cast<size_t>(b) * a.T;
     const size_t vcol = (static_cast<size_t>(h) * a.DV + 64 * cb) * P::kBytes;
@@ -105,6 +108,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
                     P::st4(lds.p[(n + 1 - c0) & 1].four(i, j, l), acc);
+                    if (P::kBytes == 2 && few) P::st4(lds.p[1].four(i, j, l), acc - P::f32(P::cvt(acc)));
                 }
             }
             now = put;
@@ -138,6 +142,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) acc[0][i] *= gates.before[16 * i + r16];
         lin_near<P, true>(acc, p, vf, l);
+        if (P::kBytes == 2 && few) lin_near<P, true>(acc, lds.p[1], vf, l);
 #pragma unroll
         for (int i = 0; i < C / 16; ++i) P::st4(lds.o[(n - c0) & 1].four(i, wave, l), acc[0][i]);
         lin_update<P, C, NS>(S, k, vf, gates.after, gates.all[0], l);
@@ -186,6 +191,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
     const bool first = rev ? slot == slots - 1 : slot == 0;
     const float *from = rev ? a.dS_T : a.S0;
     lin_load<DK>(S[0], first && from ? from + bh * state : nullptr, col, lane);
+    if (first && !rev && a.entry) lin_keep<DK>(S[0], a.entry + bh * state, col, lane);
     LinRows<P, C, DK, kNT> rk;
     LinRows<P, C, 64, kNT> rv;
     float gate = 0.f;
@@ -418,7 +424,7 @@ size_t lin_fwd_workspace(int dtype, int B, int T, int H, int dk, int dv) {
     LinArgs a{};
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     fwd_plan(dtype, a);
-    return lin_states_floats(a, 1) * sizeof(float);
+    return (lin_states_floats(a, 1) + (a.segs > 1 ? static_cast<size_t>(B) * H * dk * dv : 0)) * sizeof(float);
 }
 
 hipError_t launch_lin_states(int dtype, const LinArgs &a, bool fwd, bool rev, bool exact, hipStream_t stream) {
@@ -443,9 +449,13 @@ hipError_t launch_lin_fwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     const size_t bh = static_cast<size_t>(a.B) * a.H, state = static_cast<size_t>(a.DV) * a.DK;
     if (a.T == 0) return a.S_T && a.S_T != a.S0 ? launch_lin_copy(a.S_T, a.S0, bh * state, stream) : hipSuccess;
     fwd_plan(dtype, a);
-    lin_states_place(a, static_cast<float *>(ws), 1);
-    if (a.segs > 1)
+    float *entry = lin_states_place(a, static_cast<float *>(ws), 1);
+    if (a.segs > 1) {
+        // a last segment may be done before a first one begins
+        if (a.S_T && a.S_T == a.S0) a.entry = entry;
         if (hipError_t e = launch_lin_states(dtype, a, true, false, a.S_T != nullptr, stream)) return e;
+        if (a.entry) a.S0 = a.entry;
+    }
     return dtype == 1 ? fwd_typed<Bf16>(a, stream) : fwd_typed<F32>(a, stream);
 }
 

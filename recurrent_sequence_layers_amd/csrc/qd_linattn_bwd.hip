@@ -56,6 +56,12 @@ struct BwdLds {
     LinTile<P, C, C> p[2];
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
     float part[8][C];                  // a or b, by the columns' wave
+
+    // Walks of one chunk have P as a sum of two: over few tokens its roundings would not average out.
+    // What the first rounds away is in the second chunk's tiles, which have no other use then.
+    using Tri = LinTile<P, C, C>;
+    static_assert(sizeof(Tri) <= sizeof(c[1].q) && sizeof(Tri) <= sizeof(c[1].o), "a tile for the second addend");
+    __device__ __forceinline__ Tri &low(int i) { return i ? reinterpret_cast<Tri &>(c[1].o) : reinterpret_cast<Tri &>(c[1].q); }
 };
 
 // Where a workgroup walks, and its tensors' first bytes.
@@ -86,6 +92,7 @@ struct Walk {
     // The m-th chunk of the walk
     template <bool REV>
     __device__ __forceinline__ int chunk(int m) const { return REV ? c0 + count - 1 - m : c0 + m; }
+    __device__ __forceinline__ bool few() const { return P::kBytes == 2 && count == 1; }
     __device__ __forceinline__ int live(int n) const { return min(max(len - n * C, 0), C); }
     __device__ __forceinline__ size_t at(int t, size_t stride, int d) const {
         return (static_cast<size_t>(b) * a.T + t) * stride + static_cast<size_t>(h) * d * P::kBytes;
@@ -133,7 +140,7 @@ struct Decays {
 // own LDS reads, and the second interval is this role's to hold up).
 template <class P, int I, int C, int D>
 __device__ __forceinline__ void products_back(LinTile<P, C, D> &later, LinTile<P, C, D> &earlier, const LinGates<C> &gates,
-                                              LinTile<P, C, C> &to, const LinLane &l) {
+                                              LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
     if constexpr (I < C / 16) {
         const int g4 = l.lane >> 4, r16 = l.lane & 15, s = 16 * I + 4 * g4;
         f32x4 x[I + 1];
@@ -159,6 +166,7 @@ __device__ __forceinline__ void products_back(LinTile<P, C, D> &later, LinTile<P
                 x[j][e] = j < I || t <= s + e ? v : 0.f;
             }
             P::st4(to.four(j, I, l), x[j]);
+            if (low) P::st4(low->four(j, I, l), x[j] - P::f32(P::cvt(x[j])));
         }
     }
 }
@@ -177,6 +185,7 @@ __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         for (int e = 0; e < 4; ++e) ov[e] = t + e <= s ? ov[e] : 0.f;
     }
     P::st4(lds.p[0].four(i, j, w.l), ov);
+    if (w.few()) P::st4(lds.low(0).four(i, j, w.l), ov - P::f32(P::cvt(ov)));
     if constexpr (DG) {
         const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
         f32x4 col;
@@ -230,10 +239,12 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         const int n = valid ? w.template chunk<REV>(m) : 0;
         typename L::Chunk &next = lds.c[(m + 1) & 1];
         emit(m);
-        rq.put(next.q, tid);
-        rk.put(next.k, tid);
-        rv.put(next.v, tid);
-        ro.put(next.o, tid);
+        if (m < 0 || !w.few()) {
+            rq.put(next.q, tid);
+            rk.put(next.k, tid);
+            rv.put(next.v, tid);
+            ro.put(next.o, tid);
+        }
         fetch(m + 2);
         if constexpr (DG && !REV) {
             const int i = (tid >> 4) & (C / 16 - 1), e = tid & 15;
@@ -249,18 +260,19 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         if constexpr (REV) {
             // five blocks a wave (fp32: two or one)
             const LinGates<C> &gates = lds.gates[(m + 1) % 3];
+            LinTile<P, C, C> *const low0 = w.few() && m < 0 ? &lds.low(0) : nullptr, *const low1 = w.few() && m < 0 ? &lds.low(1) : nullptr;
             if (wave == 0) {
-                products_back<P, 3>(next.q, next.k, gates, lds.p[0], w.l);
-                products_back<P, 0>(next.q, next.k, gates, lds.p[0], w.l);
+                products_back<P, 3>(next.q, next.k, gates, lds.p[0], low0, w.l);
+                products_back<P, 0>(next.q, next.k, gates, lds.p[0], low0, w.l);
             } else if (wave == 1) {
-                products_back<P, 3>(next.o, next.v, gates, lds.p[1], w.l);
-                products_back<P, 0>(next.o, next.v, gates, lds.p[1], w.l);
+                products_back<P, 3>(next.o, next.v, gates, lds.p[1], low1, w.l);
+                products_back<P, 0>(next.o, next.v, gates, lds.p[1], low1, w.l);
             } else if (wave == 2) {
-                products_back<P, 2>(next.q, next.k, gates, lds.p[0], w.l);
-                products_back<P, 1>(next.q, next.k, gates, lds.p[0], w.l);
+                products_back<P, 2>(next.q, next.k, gates, lds.p[0], low0, w.l);
+                products_back<P, 1>(next.q, next.k, gates, lds.p[0], low0, w.l);
             } else {
-                products_back<P, 2>(next.o, next.v, gates, lds.p[1], w.l);
-                products_back<P, 1>(next.o, next.v, gates, lds.p[1], w.l);
+                products_back<P, 2>(next.o, next.v, gates, lds.p[1], low1, w.l);
+                products_back<P, 1>(next.o, next.v, gates, lds.p[1], low1, w.l);
             }
         } else {
             for (int p = wave; p < LAST; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
@@ -390,6 +402,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
             if constexpr (DG) row_parts<P>(lds.part[wave], x.q, acc, t0, w.l);
             lin_columns<P, C>(kf, x.k, t0, w.l);
             lin_near<P, true>(acc, lds.p[0], kf, w.l);
+            if (w.few()) lin_near<P, true>(acc, lds.low(0), kf, w.l);
             pack<P, C>(out, acc, w.live(w.c0 + m), w.r16);
         }
         __syncthreads();
@@ -429,6 +442,7 @@ __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
             lin_read<P, 1>(acc, R, x.k, w.l);
             scale<C>(acc, gates.after, w.r16);
             lin_near<P, false>(acc, lds.p[0], of, w.l);
+            if (w.few()) lin_near<P, false>(acc, lds.low(0), of, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
@@ -459,6 +473,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
             if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
             lin_columns<P, C>(qf, x.q, t0, w.l);
             lin_near<P, false>(acc, lds.p[1], qf, w.l);
+            if (w.few()) lin_near<P, false>(acc, lds.low(1), qf, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         }
         __syncthreads();
@@ -497,7 +512,7 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
     extern __shared__ __align__(16) char smem[];
     L &lds = *reinterpret_cast<L *>(smem);
     // blocks of P off its triangle that a pair of tiles reads: never written again
-    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = 0;
+    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = lds.low(0).m[e] = lds.low(1).m[e] = 0;
     __syncthreads();
     const int unit = blockIdx.x >> 1;
     if (blockIdx.x & 1) dq_walk<P, DK, DV, DG>(a, lds, unit);

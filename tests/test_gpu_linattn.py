@@ -183,6 +183,38 @@ def test_the_state_may_be_updated_in_place(qd):
         assert S2 is S and torch.equal(S, want[1]) and torch.equal(o, want[0])
 
 
+@pytest.mark.parametrize("B,H,T,lens", [(1, 1, 4000, None), (3, 2, 2000, [2000, 5, 0]), (2, 20, 4000, [64, 4000]), (1, 3, 1200, [1])])
+def test_the_state_in_place_over_a_cut_time_axis(qd, B, H, T, lens):
+    """The last segment may end, and write S_T, before the first one has read S0."""
+    for dtype in ("bf16", "f32"):
+        x = inputs(B, T, H, 64, 128, dtype, 17)
+        assert qd.qdelta_linattn_fwd_workspace_bytes(B, T, H, 64, 128, DT[dtype]) > 0
+        n = None if lens is None else dev(torch.tensor(lens, dtype=torch.int32))
+        want = call(qd, "qdelta_linattn_fwd", x, FWD, lens=n)
+        a = [dev(x[k]) for k in FWD]
+        for _ in range(3):
+            S = a[4].clone()
+            o, S2 = qd.qdelta_linattn_fwd(*a[:4], S, n, S_T=S)
+            assert S2 is S and torch.equal(S, want[1]) and torch.equal(o, want[0])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("T", [1, 2, 17, 64])
+def test_one_chunk_rounds_once(qd, T, dk, dv):
+    """Without a state, what one chunk rounds to bf16 inside is a sum of two: 2^-8 of 2^-8 is left of
+    each term, beside the rounding of the output."""
+    x = inputs(1, T, 1, dk, dv, "bf16", 18, state=False)
+    want, S_T, so, sS = layer.linattn_fwd(*[x[n] for n in FWD])
+    o, S = call(qd, "qdelta_linattn_fwd", x, FWD)
+    near(o, want, so, x, "o", parts=2.0 ** -8)
+    near(S, S_T, sS, x, "S_T")
+    grads, scale = layer.linattn_bwd(*[x[n] for n in BWD])
+    for want_dg in (True, False):
+        got = call(qd, "qdelta_linattn_bwd", x, BWD, want_dg=want_dg)
+        for n in ("dq", "dk", "dv"):
+            near(got[n], grads[n], scale[n], x, n, parts=2.0 ** -8)
+
+
 def test_no_tokens_no_sequences(qd):
     x = inputs(2, 0, 3, 64, 128, "bf16", 12)
     o, S = call(qd, "qdelta_linattn_fwd", x, FWD)
