@@ -29,6 +29,7 @@ norms with the gate, the scale and the residual sum:
 """
 import contextlib
 import ctypes
+import math
 import os
 
 from . import inputs  # noqa: F401  (seeded workload generators)
@@ -40,6 +41,8 @@ QD_F32, QD_BF16 = 0, 1
 # bytes of device scratch qdelta_chunk_fwd_noalloc holds per device (QDELTA_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 32 << 20
 _lib = None
+# torch's own current device and stream handle, without the checks around them; set with the library
+_get_device = _raw_stream = None
 
 
 class QDeltaError(RuntimeError):
@@ -48,7 +51,7 @@ class QDeltaError(RuntimeError):
 
 def load_library():
     """Load libqdelta.so (built in-tree by ``python -m recurrent_sequence_layers_amd.build``)."""
-    global _lib
+    global _lib, _get_device, _raw_stream
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -111,6 +114,8 @@ def load_library():
             ("block_norm_bwd", i, [vp] * 15 + [i] * 4 + [vp, sz, vp])):
         fn = getattr(lib, "qdelta_" + name)
         fn.restype, fn.argtypes = restype, argtypes
+    import torch
+    _get_device, _raw_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
     _lib = lib
     return lib
 
@@ -437,22 +442,23 @@ def _int_sizes(sizes):
 
 def _shape(t, name, dims):
     """Shape of a device tensor with `dims` dimensions."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise QDeltaError(f"{name} must be a device tensor")
-    if t.dim() != dims:
-        raise QDeltaError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return _int_sizes(t.shape)
+    shape = t.shape
+    if len(shape) != dims:
+        raise QDeltaError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    return _int_sizes(shape)
 
 
 def _check_all(device, checks):
     """_check for each (tensor, name, dtype, shape), and that every tensor is on `device`.  A
     decode step is a few microseconds on the GPU, so what is right costs four comparisons."""
+    index = device.index
     for t, name, dtype, shape in checks:
         if t is None:
             continue
         try:
-            if t.dtype == dtype and t.device == device and (shape is None or t.shape == shape) and t.is_contiguous():
+            if t.dtype is dtype and t.get_device() == index and (shape is None or t.shape == shape) and t.is_contiguous():
                 continue
         except AttributeError:
             pass
@@ -468,9 +474,9 @@ def _enter(stream, device):
     """(context, stream handle) for a call's allocations and launches: `device` and the stream
     current, and no context at all where they are already."""
     import torch
-    if stream is None and device.index == torch.cuda.current_device():
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the handle without a Stream object around it
-        return _NO_CONTEXT, raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+    if stream is None and device.index == (_get_device or torch.cuda.current_device)():
+        # the handle without a Stream object around it
+        return _NO_CONTEXT, _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     s = _launch_stream(stream, device)
     return torch.cuda.stream(s), s.cuda_stream
 
@@ -768,12 +774,12 @@ def qdelta_group_norm_bwd(x, groups: int, weight, bias, gate, stats, dy, silu: b
 def _linattn_inputs(q, k, v, g, token_dims):
     """Sizes (tokens.., heads, d_k, d_v), whether g is per head, and the checks of what a token has."""
     import torch
-    shape = tuple(_shape(q, "q", token_dims + 2))
-    d_v = _shape(v, "v", token_dims + 2)[-1]
+    shape, value = _shape(q, "q", token_dims + 2), _shape(v, "v", token_dims + 2)
     dt, head = q.dtype, shape[:-1]
-    per_head = isinstance(g, torch.Tensor) and g.dim() == 1
-    return shape + (d_v,), per_head, [(q, "q", dt, None), (k, "k", dt, shape), (v, "v", dt, head + (d_v,)),
-                                      (g, "g", torch.float32, head[-1:] if per_head else head)]
+    per_head = g is not None and len(getattr(g, "shape", ())) == 1
+    return (*shape, value[-1]), per_head, [(q, "q", dt, None), (k, "k", dt, shape),
+                                           (v, "v", dt, value if value[:-1] == head else (*head, value[-1])),
+                                           (g, "g", torch.float32, head[-1:] if per_head else head)]
 
 
 def qdelta_linattn_fwd_workspace_bytes(B, T, H, d_k, d_v, dtype) -> int:
@@ -864,17 +870,14 @@ _GATE_ACTS = {"linear": 0, "sigmoid": 1, "silu": 2}
 
 def _block_norm_sizes(y, act):
     """(rows, channels) of y [..,C] and the gate's code."""
-    import torch
-    if not isinstance(y, torch.Tensor) or not y.is_cuda:
+    if not getattr(y, "is_cuda", False):
         raise QDeltaError("y must be a device tensor")
-    if y.dim() < 1:
+    shape = y.shape
+    if not shape:
         raise QDeltaError("y must have at least 1 dimension")
     if act not in _GATE_ACTS:
         raise QDeltaError(f"act must be one of {', '.join(_GATE_ACTS)}, got {act!r}")
-    rows = 1
-    for d in y.shape[:-1]:
-        rows *= d
-    return *_int_sizes((rows, y.shape[-1])), _GATE_ACTS[act]
+    return *_int_sizes((math.prod(shape[:-1]), shape[-1])), _GATE_ACTS[act]
 
 
 def qdelta_block_norm_fwd(y, x=None, post=None, gate=None, scale=None, pre=None, act: str = "silu", eps: float = 1e-5, h=None,
@@ -892,8 +895,9 @@ def qdelta_block_norm_fwd(y, x=None, post=None, gate=None, scale=None, pre=None,
     context, handle = _enter(stream, y.device)
     with context:
         dt, dev, f32, code = y.dtype, y.device, torch.float32, _dtype_code(y.dtype)
-        _check_all(dev, [(y, "y", dt, None), (x, "x", dt, y.shape), (gate, "gate", dt, y.shape), (post, "post", f32, (C,)),
-                         (scale, "scale", f32, (C,)), (pre, "pre", f32, (C,))])
+        rows, channels = y.shape, (C,)
+        _check_all(dev, [(y, "y", dt, None), (x, "x", dt, rows), (gate, "gate", dt, rows), (post, "post", f32, channels),
+                         (scale, "scale", f32, channels), (pre, "pre", f32, channels)])
         h = _result(h, "h", y, dev)
         if pre is not None:
             n = _result(n, "n", y, dev)

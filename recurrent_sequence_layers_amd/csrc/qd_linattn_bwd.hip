@@ -203,9 +203,9 @@ __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     }
 }
 
-// The loading waves, NW of them; `wave` counts from the first.  They form the blocks up to LAST.
-// NS: the waves that hold what a or b is of.
-template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS, int LAST>
+// The loading waves, NW of them; `wave` counts from the first.  NS: the waves that hold what a or b
+// is of.
+template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS>
 __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NT = 64 * NW;
@@ -275,7 +275,7 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
                 products_back<P, 1>(next.o, next.v, gates, lds.p[1], low1, w.l);
             }
         } else {
-            for (int p = wave; p < LAST; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
+            for (int p = wave; p < L::NB; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
         }
         if constexpr (DG) {
             float s = 0.f;
@@ -377,19 +377,13 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
     const int wave = 4 * w.role + w.wave;
-    // with eight waves on the state, whose update is short, six of them take a block each
-    constexpr int LAST = NS == 8 && L::NB == 10 ? 4 : L::NB;
-    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS, LAST>(w, lds, wave - NS);
+    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS>(w, lds, wave - NS);
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, lin_before(a, w.bh, w.seg), c0, lane);
     Decays<P, DK, DV, false> decays(w, lds);
-    auto help = [&](int m) {
-        if (LAST < L::NB && wave >= 2) product<P, DK, DV, DG>(w, lds, m, LAST + wave - 2);
-    };
     __syncthreads();                             // the first chunk is brought
-    help(-1);
     __syncthreads();
     for (int m = 0; m < w.count; ++m) {
         typename L::Chunk &x = lds.c[m & 1];
@@ -409,7 +403,6 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         spill_out<P, C>(x.q, out, t0, w.l);
         lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, gates.after, gates.all[0], w.l);
         decays.ahead(lds, m);
-        help(m);
         __syncthreads();
     }
     if constexpr (DG) {
@@ -500,7 +493,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
 template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     const Walk<P, DK, DV> w(a, unit);
-    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4, BwdLds<P, DK, DV>::NB>(w, lds, w.wave);
+    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4>(w, lds, w.wave);
     const float *from = lin_behind(a, w.bh, w.seg);
     if (w.role == 0) dk_walk<P, DK, DV, DG, NS>(w, lds, from);
     else dv_walk<P, DK, DV>(w, lds, from);
