@@ -53,7 +53,7 @@ struct BwdLds {
         LinTile<P, C, DV> v, o;
     } c[2];
     LinGates<C> gates[3];
-    LinTile<P, C, C> p[2];
+    LinTile<P, C, C> p[3];             // 0: of do v forwards, q k backwards; 1, 2 in turn: of do v backwards
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
     float part[8][C];                  // a or b, by the columns' wave
 
@@ -265,14 +265,14 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
                 products_back<P, 3>(next.q, next.k, gates, lds.p[0], low0, w.l);
                 products_back<P, 0>(next.q, next.k, gates, lds.p[0], low0, w.l);
             } else if (wave == 1) {
-                products_back<P, 3>(next.o, next.v, gates, lds.p[1], low1, w.l);
-                products_back<P, 0>(next.o, next.v, gates, lds.p[1], low1, w.l);
+                products_back<P, 3>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
+                products_back<P, 0>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
             } else if (wave == 2) {
                 products_back<P, 2>(next.q, next.k, gates, lds.p[0], low0, w.l);
                 products_back<P, 1>(next.q, next.k, gates, lds.p[0], low0, w.l);
             } else {
-                products_back<P, 2>(next.o, next.v, gates, lds.p[1], low1, w.l);
-                products_back<P, 1>(next.o, next.v, gates, lds.p[1], low1, w.l);
+                products_back<P, 2>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
+                products_back<P, 1>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
             }
         } else {
             for (int p = wave; p < L::NB; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
@@ -459,17 +459,22 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename L::Chunk &x = lds.c[m & 1];
         const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F qf[NC][C / 32][2], out[NC][C / 16];
-        {
-            f32x4 acc[NC][C / 16];
-            lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
-            scale<C>(acc, gates.after, w.r16);
-            if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
+        f32x4 acc[NC][C / 16];
+        lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
+        scale<C>(acc, gates.after, w.r16);
+        // the chunk's own part; for dg it waits for the second interval: with three addends to read,
+        // these waves are the first one's longest (fp32, 4096 x 16 x 128 x 128: 272 -> 261 us; with
+        // one addend it is the other way round, 57 -> 59 us at 8 x 1000 x 16 x 128 x 64, bf16)
+        auto own = [&] {
             lin_columns<P, C>(qf, x.q, t0, w.l);
-            lin_near<P, false>(acc, lds.p[1], qf, w.l);
+            lin_near<P, false>(acc, lds.p[1 + (m & 1)], qf, w.l);
             if (w.few()) lin_near<P, false>(acc, lds.low(1), qf, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
-        }
+        };
+        if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
+        else own();
         __syncthreads();
+        if constexpr (DG) own();
         spill_out<P, C>(x.k, out, t0, w.l);
         lin_update<P, C, NS>(R, x.o, qf, gates.before, gates.all[0], w.l);
         decays.ahead(lds, m);
@@ -505,7 +510,7 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
     extern __shared__ __align__(16) char smem[];
     L &lds = *reinterpret_cast<L *>(smem);
     // blocks of P off its triangle that a pair of tiles reads: never written again
-    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = lds.low(0).m[e] = lds.low(1).m[e] = 0;
+    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = lds.p[2].m[e] = lds.low(0).m[e] = lds.low(1).m[e] = 0;
     __syncthreads();
     const int unit = blockIdx.x >> 1;
     if (blockIdx.x & 1) dq_walk<P, DK, DV, DG>(a, lds, unit);
