@@ -115,6 +115,21 @@ struct Walk {
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), lin_rsrc(to, valid ? min(a.T - n * C, C) * 4 : 0),
                                               tid * 4, 0, 0);
     }
+    // a (backwards b) of chunk n from its NS parts, with its sum and that of its squares: one wave
+    template <bool REV, int NS, class L>
+    __device__ __forceinline__ void terms(const L &lds, int n) const {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) s += lds.part[k][lane & (C - 1)];
+        term(REV ? 2 : 1, n, true, lane, s);
+        s = lane < C ? s : 0.f;
+        const float sum = wave_inclusive_sum(s), squares = wave_inclusive_sum(s * s);
+        float *to = a.sums + (static_cast<size_t>(bh) * ((a.T + C - 1) / C) + n) * 4 + (REV ? 2 : 0);
+        if (lane == 63) {
+            to[0] = sum;
+            to[1] = squares;
+        }
+    }
 };
 
 // The decays, by one of the states' waves: those of chunk m + 2 in chunk m's second interval, where
@@ -209,9 +224,8 @@ __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     }
 }
 
-// The loading waves, NW of them; `wave` counts from the first.  NS: the waves that hold what a or b
-// is of.
-template <class P, int DK, int DV, bool REV, bool DG, int NW, int NS>
+// The loading waves, NW of them; `wave` counts from the first.
+template <class P, int DK, int DV, bool REV, bool DG, int NW>
 __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NT = 64 * NW;
@@ -282,12 +296,6 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             }
         } else {
             for (int p = wave; p < L::NB; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
-        }
-        if constexpr (DG) {
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < NS; ++k) s += lds.part[k][tid & (C - 1)];
-            w.term(REV ? 2 : 1, n, valid, tid, s);
         }
         __syncthreads();
     }
@@ -383,7 +391,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
     const int wave = 4 * w.role + w.wave;
-    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, NS>(w, lds, wave - NS);
+    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS>(w, lds, wave - NS);
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
@@ -408,6 +416,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         __syncthreads();
         spill_out<P, C>(x.q, out, t0, w.l);
         lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, gates.after, gates.all[0], w.l);
+        if (DG && wave == 1) w.template terms<false, NS>(lds, w.c0 + m);
         decays.ahead(lds, m);
         __syncthreads();
     }
@@ -483,6 +492,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         if constexpr (DG) own();
         spill_out<P, C>(x.k, out, t0, w.l);
         lin_update<P, C, NS>(R, x.o, qf, gates.before, gates.all[0], w.l);
+        if (DG && w.wave == 1) w.template terms<true, 4>(lds, w.template chunk<true>(m));
         decays.ahead(lds, m);
         __syncthreads();
     }
@@ -504,7 +514,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
 template <class P, int DK, int DV, bool DG, int NS>
 __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds, int unit) {
     const Walk<P, DK, DV> w(a, unit);
-    if (w.role == 2) return bring<P, DK, DV, true, DG, 4, 4>(w, lds, w.wave);
+    if (w.role == 2) return bring<P, DK, DV, true, DG, 4>(w, lds, w.wave);
     const float *from = lin_behind(a, w.bh, w.seg);
     if (w.role == 0) dk_walk<P, DK, DV, DG, NS>(w, lds, from);
     else dv_walk<P, DK, DV>(w, lds, from);
@@ -526,73 +536,84 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
 // ---------------------------------------------------------------- dg
 constexpr int kDgWaves = 16, kDgChunks = 1024;
 
-// The chain of c over a head's chunks: one workgroup, a chunk a wave for its sums, then one wave from
-// the last chunk on, 1024 at a time.  Bound by the latency of these few passes.
-template <int C>
-__global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a) {
+// The chain of c for chunk n by one wave, from all the chunks' sums.
+__device__ __forceinline__ double wave_total(double x) {
+    x += lin_dpp<0x111, 0xf>(x);
+    x += lin_dpp<0x112, 0xf>(x);
+    x += lin_dpp<0x114, 0xf>(x);
+    x += lin_dpp<0x118, 0xf>(x);
+    x += lin_dpp<0x142, 0xa>(x);
+    x += lin_dpp<0x143, 0xc>(x);
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+struct Ends {
+    double last, first;              // <S_T, dS_T>, <S0, dS0>
+    __device__ __forceinline__ Ends(const LinArgs &a, size_t bh) : last(0), first(0) {
+        for (int w = 0; w < a.DK / 16; ++w) last += a.edge[bh * (a.DK / 16) + w];
+        for (int w = 0; w < 4; ++w) first += a.edge0[bh * 4 + w];
+    }
+};
+__device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, int n, int lane) {
+    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc;
+    double D = 0, V = 0, later = 0, passed = 0, own = 0;
+    for (int m = lane; m < nc; m += kWave) {
+        const f32x4 x = sums[m];
+        const double d = static_cast<double>(x[0]) - x[2], v = static_cast<double>(x[1]) + x[3];
+        D += d;
+        V += v;
+        later += m > n ? d : 0;
+        passed += m > n ? v : m == n ? 0.5 * v : 0;
+        own += m == n ? x[2] : 0;
+    }
+    D = wave_total(D);
+    V = wave_total(V);
+    const Ends e(a, bh);
+    return static_cast<float>(e.last + wave_total(later) - wave_total(own) -
+                              (V > 0 ? (e.last + D - e.first) / V * wave_total(passed) : 0));
+}
+
+// The same for all of a head's chunks, where they are many: one workgroup, from the last chunk on,
+// 1024 at a time.
+constexpr int kFewChunks = 256;
+__global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a, const int nc) {
     __shared__ double sd[kDgChunks], sb[kDgChunks], sv[kDgChunks];
     __shared__ double total[kDgWaves][2];
-    const int bh = blockIdx.x, b = bh / a.H, wave = wave_id(), lane = lane_id();
-    const size_t bhs = static_cast<size_t>(a.B) * a.H;
-    const float *ta = a.tok + (bhs + bh) * a.T, *tb = ta + bhs * a.T;
-    const int nc = (lin_len(a, b) + C - 1) / C, all = (a.T + C - 1) / C;
-    float *c = a.chain + static_cast<size_t>(bh) * all;
-    // sum a - sum b, sum b and the squares of a chunk's terms
-    auto sums = [&](int first, int count) {
-        constexpr int AHEAD = 4;
-        for (int m = wave; m < count; m += AHEAD * kDgWaves) {
-            float va[AHEAD], vb[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int n = m + k * kDgWaves, t = (first + n) * C + lane;
-                const bool in = n < count && lane < C && t < a.T;
-                va[k] = in ? ta[t] : 0.f;
-                vb[k] = in ? tb[t] : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const float x = sum64(va[k]), y = sum64(vb[k]), v = sum64(fmaf(va[k], va[k], vb[k] * vb[k]));
-                if (lane == 0 && m + k * kDgWaves < count) {
-                    sd[m + k * kDgWaves] = static_cast<double>(x) - y;
-                    sb[m + k * kDgWaves] = y;
-                    sv[m + k * kDgWaves] = v;
-                }
-            }
-        }
-        __syncthreads();
-    };
+    const size_t bh = blockIdx.x;
+    const int wave = wave_id(), lane = lane_id();
+    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc;
+    float *c = a.chain + bh * nc;
     double D = 0, V = 0;
-    for (int last = nc; last > 0; last -= kDgChunks) {
-        const int first = max(last - kDgChunks, 0);
-        sums(first, last - first);
-        for (int m = threadIdx.x; m < last - first; m += 64 * kDgWaves) {
-            D += sd[m];
-            V += sv[m];
-        }
-        __syncthreads();
+    for (int m = threadIdx.x; m < nc; m += 64 * kDgWaves) {
+        const f32x4 x = sums[m];
+        D += static_cast<double>(x[0]) - x[2];
+        V += static_cast<double>(x[1]) + x[3];
     }
-    for (int k = 1; k < 64; k *= 2) {
-        D += __shfl_xor(D, k);
-        V += __shfl_xor(V, k);
-    }
+    D = wave_total(D);
+    V = wave_total(V);
     if (lane == 0) {
         total[wave][0] = D;
         total[wave][1] = V;
     }
     __syncthreads();
-    double E = 0, E0 = 0;
     D = V = 0;
     for (int w = 0; w < kDgWaves; ++w) {
         D += total[w][0];
         V += total[w][1];
     }
-    for (int w = 0; w < a.DK / 16; ++w) E += a.edge[static_cast<size_t>(bh) * (a.DK / 16) + w];
-    for (int w = 0; w < 4; ++w) E0 += a.edge0[static_cast<size_t>(bh) * 4 + w];
-    const double missed = E + D - E0, part = V > 0 ? missed / V : 0;
-    double passed = 0;
+    const Ends ends(a, bh);
+    double E = ends.last, passed = 0;
+    const double part = V > 0 ? (E + D - ends.first) / V : 0;
     for (int last = nc; last > 0; last -= kDgChunks) {
         const int first = max(last - kDgChunks, 0), count = last - first;
-        if (nc > kDgChunks) sums(first, count);      // else they are still there
+        for (int m = threadIdx.x; m < count; m += 64 * kDgWaves) {
+            const f32x4 x = sums[first + m];
+            sd[m] = static_cast<double>(x[0]) - x[2];
+            sb[m] = x[2];
+            sv[m] = static_cast<double>(x[1]) + x[3];
+        }
+        __syncthreads();
         if (wave == 0) {
             // a lane's chunks are consecutive, from the last on
             constexpr int PER = kDgChunks / 64;
@@ -627,41 +648,6 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
     }
 }
 
-// The same chain for the chunk n by one wave, for few chunks: no launch of its own (7 chunks 39.7 ->
-// 37.1 us of the whole call, 16 chunks 85.7 -> 84.8; more would not fit the registers).
-constexpr int kFewChunks = 16;
-template <int C>
-__device__ __forceinline__ float few_chain(const LinArgs &a, size_t bh, const float *ta, const float *tb, int nc, int n, int lane) {
-    float sa[kFewChunks], sb[kFewChunks];
-#pragma unroll
-    for (int m = 0; m < kFewChunks; ++m) {
-        const bool in = m < nc && lane < C && m * C + lane < a.T;
-        sa[m] = in ? ta[m * C + lane] : 0.f;
-        sb[m] = in ? tb[m * C + lane] : 0.f;
-    }
-    double D = 0, V = 0, later = 0, passed = 0;
-    float own = 0.f;
-#pragma unroll
-    for (int m = 0; m < kFewChunks; ++m) {
-        const float v = sum64(fmaf(sa[m], sa[m], sb[m] * sb[m])), y = sum64(sb[m]);
-        const double d = static_cast<double>(sum64(sa[m])) - y;
-        D += d;
-        V += v;
-        if (m > n) {
-            later += d;
-            passed += v;
-        }
-        if (m == n) {
-            passed += 0.5 * v;
-            own = y;
-        }
-    }
-    double E = 0, E0 = 0;
-    for (int w = 0; w < a.DK / 16; ++w) E += a.edge[bh * (a.DK / 16) + w];
-    for (int w = 0; w < 4; ++w) E0 += a.edge0[bh * 4 + w];
-    return static_cast<float>(E + later - own - (V > 0 ? (E + D - E0) / V * passed : 0));
-}
-
 // dg of a chunk of sixteen heads: a wave a head, rows of heads through LDS.
 template <int C>
 __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) {
@@ -677,7 +663,7 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
         const float y = lane < live ? x[lane] + tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
         const float before = wave_inclusive_sum(y) - y;
         const float behind = __shfl(wave_inclusive_sum(z), back);
-        const float c = nc <= kFewChunks ? few_chain<C>(a, bh, ta - n * C, tb - n * C, nc, n, lane) : a.chain[bh * nc + n];
+        const float c = nc <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.chain[bh * nc + n];
         v = lane < live ? c + (before + behind) : 0.f;
     }
     if (a.decay == kHeadDecay) {
@@ -707,7 +693,7 @@ hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
     if (hipError_t e = hipGetLastError()) return e;
     if (a.dg) {
         const unsigned nc = (a.T + L::C - 1) / L::C;
-        if (nc > kFewChunks) hipLaunchKernelGGL(lin_chain_kernel<L::C>, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a);
+        if (nc > kFewChunks) hipLaunchKernelGGL(lin_chain_kernel, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a, static_cast<int>(nc));
         hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(nc * a.B, (a.H + kDgWaves - 1) / kDgWaves), dim3(64 * kDgWaves), 0, stream, a);
         if (a.decay == kHeadDecay) column_sum(a.head, static_cast<int>(nc * a.B), a.H, HeadStore{a.dg}, stream);
     }
@@ -731,7 +717,7 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 4) + 2 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
+    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 4) + 6 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -748,11 +734,13 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (a.segs > 1)
         if (hipError_t e = launch_lin_states(dtype, a, true, true, a.dg || a.dS0, stream)) return e;
     if (a.dg) {
-        a.tok = p;
+        const size_t chunks = (a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype);
+        a.sums = p;
+        a.tok = a.sums + 4 * bh * chunks;
         a.edge = a.tok + 3 * bh * a.T;
         a.edge0 = a.edge + bh * (a.DK / 16);
         a.chain = a.edge0 + bh * 4;
-        a.head = a.chain + bh * ((a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype));
+        a.head = a.chain + bh * chunks;
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
 }
