@@ -31,9 +31,9 @@ __device__ __forceinline__ bool lin_place(int units, int ncb, int &unit, int &cb
 dim3 lin_grid(long long units, int ncb) { return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * ncb)); }
 
 // Eight waves in two roles, a barrier a step.  At step n waves 0-3 hold the state and do chunk n's
-// part with it: the outputs, then the state's update.  Waves 4-7 are ahead of them: they form P of
-// chunk n + 1 and bring chunk n + 2 from the registers, where the loads of the step before put it,
-// to LDS.
+// part with it: the outputs, then the state's update.  Waves 4-7 are ahead of them: they bring chunk
+// n + 2 from the registers, where the loads of two steps before put it, to LDS.  All of them form P of
+// chunk n + 1, two blocks of a row at a time, shared so that the roles take equally long.
 template <class P, int DK>
 struct FwdLds {
     static constexpr int C = kLinChunk<P>;
@@ -43,17 +43,69 @@ struct FwdLds {
     LinGates<C> gates[3];
 };
 
+// Blocks J .. J + N - 1 of row I of P, all in flight at once.  low: what the bf16 of it rounds away
+template <class P, int I, int J, int N, int C, int D>
+__device__ __forceinline__ void lin_products(LinTile<P, C, D> &q, LinTile<P, C, D> &k, const LinGates<C> &gates, LinTile<P, C, C> &to,
+                                             LinTile<P, C, C> *low, const LinLane &l) {
+    static_assert(I < C / 16 && J + N - 1 <= I, "the lower triangle");
+    f32x4 x[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = zero4();
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        typename P::F q0, q1, k0[N], k1[N];
+        q.oct(I, u, l, q0, q1);
+#pragma unroll
+        for (int n = 0; n < N; ++n) k.oct(J + n, u, l, k0[n], k1[n]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] = P::mma2(x[n], k0[n], k1[n], q0, q1);
+    }
+    const int s = 16 * I + (l.lane & 15);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int t = 16 * (J + n) + 4 * (l.lane >> 4);
+        const f32x4 d = lin_between(gates, s, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = J + n < I || t + e <= s ? d[e] * x[n][e] : 0.f;
+        P::st4(to.four(I, J + n, l), x[n]);
+        if (P::kBytes == 2 && low) P::st4(low->four(I, J + n, l), x[n] - P::f32(P::cvt(x[n])));
+    }
+}
+// A wave's share of them: the loading waves (role 1) take seven of ten, the states' waves three; all
+// ten with three addends to a state, and in fp32, where the states' waves have more to do.
+template <class P, int NS, int C, int D>
+__device__ __forceinline__ void lin_share(int role, int wave, LinTile<P, C, D> &q, LinTile<P, C, D> &k, const LinGates<C> &gates,
+                                          LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
+    if constexpr (C == 64) {
+        if (role == 1) {
+            if (wave == 0) lin_products<P, 3, 0, 2>(q, k, gates, to, low, l);
+            else if (wave == 1) lin_products<P, 3, 2, 2>(q, k, gates, to, low, l);
+            else if (wave == 2) lin_products<P, 2, 0, 2>(q, k, gates, to, low, l);
+            else lin_products<P, 2, 2, 1>(q, k, gates, to, low, l);
+        }
+        if (role == (NS == 3 ? 1 : 0)) {
+            if (wave == 0) lin_products<P, 1, 0, 1>(q, k, gates, to, low, l);
+            else if (wave == 1) lin_products<P, 1, 1, 1>(q, k, gates, to, low, l);
+            else if (wave == 2) lin_products<P, 0, 0, 1>(q, k, gates, to, low, l);
+        }
+    } else if (role == 1) {
+        if (wave == 0) lin_products<P, 1, 0, 1>(q, k, gates, to, low, l);
+        else if (wave == 1) lin_products<P, 1, 1, 1>(q, k, gates, to, low, l);
+        else if (wave == 2) lin_products<P, 0, 0, 1>(q, k, gates, to, low, l);
+    }
+}
+
 template <class P, int DK, int NS>
 __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const LinArgs a) {
     using L = FwdLds<P, DK>;
-    constexpr int C = L::C, NB = (C / 16) * (C / 16 + 1) / 2;
+    constexpr int C = L::C;
     extern __shared__ __align__(16) char smem[];
     L &lds = *reinterpret_cast<L *>(smem);
     const int ncb = a.DV / 64;
     int unit, cb;
     if (!lin_place(a.B * a.H * a.segs, ncb, unit, cb)) return;
     const int seg = unit % a.segs, bh = unit / a.segs, b = bh / a.H, h = bh % a.H;
-    const int tid = threadIdx.x & (kNT - 1), role = lin_wave() >> 2, wave = lin_wave() & 3, lane = lane_id(), g4 = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x & (kNT - 1), role = lin_wave() >> 2, wave = lin_wave() & 3, lane = lane_id(), r16 = lane & 15;
     const LinLane l(lane);
     const int len = lin_len(a, b);
     // a sequence that ends before the segment leaves it without chunks
@@ -104,20 +156,8 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
             r.v.put(lds.v[put], tid);
             if (wave == 3) lin_gates(lds.gates[put], r.gate, lane);
             fetch(r, n + 4);
-            if (n + 1 >= c0 && n + 1 < c1) {
-                const LinGates<C> &gates = lds.gates[now];
-                for (int p = wave; p < NB; p += 4) {
-                    int i, j;
-                    lin_pair(p, i, j);
-                    f32x4 acc = lin_block<P>(lds.k[now], lds.q[now], j, i, l);
-                    const int s = 16 * i + r16, t = 16 * j + 4 * g4;
-                    const f32x4 d = lin_between(gates, s, t);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = t + e <= s ? d[e] * acc[e] : 0.f;
-                    P::st4(lds.p[(n + 1 - c0) & 1].four(i, j, l), acc);
-                    if (P::kBytes == 2 && few) P::st4(lds.p[1].four(i, j, l), acc - P::f32(P::cvt(acc)));
-                }
-            }
+            if (n + 1 >= c0 && n + 1 < c1)
+                lin_share<P, NS>(1, wave, lds.q[now], lds.k[now], lds.gates[now], lds.p[(n + 1 - c0) & 1], few ? &lds.p[1] : nullptr, l);
             now = put;
             put = put == 2 ? 0 : put + 1;
             __syncthreads();
@@ -136,6 +176,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
     f32x4 S[1][DK / 16];
     lin_load<DK>(S[0], lin_before(a, bh, seg), col, lane);
     __syncthreads();
+    if (c0 < c1) lin_share<P, NS>(0, wave, lds.q[0], lds.k[0], lds.gates[0], lds.p[0], few ? &lds.p[1] : nullptr, l);
     __syncthreads();
     int now = 0;
     for (int n = c0; n < c1; ++n) {
@@ -154,6 +195,7 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
         for (int i = 0; i < C / 16; ++i) P::st4(lds.o[(n - c0) & 1].four(i, wave, l), acc[0][i]);
         lin_update<P, C, NS>(S, k, vf, gates.after, gates.all[0], l);
         now = now == 2 ? 0 : now + 1;
+        if (n + 1 < c1) lin_share<P, NS>(0, wave, lds.q[now], lds.k[now], lds.gates[now], lds.p[(n + 1 - c0) & 1], few ? &lds.p[1] : nullptr, l);
         __syncthreads();
     }
     __syncthreads();                             // the last chunk's outputs go in a step of their own
