@@ -59,7 +59,10 @@ struct BwdLds {
         LinTile<P, C, DV> v, o;
     } c[2];
     LinGates<C> gates[3];
-    LinTile<P, C, C> p[3];             // 0: of do v forwards, q k backwards; 1, 2 in turn: of do v backwards
+    // Of do v forwards; of q k and of do v backwards.  With dg the latter is read in the second
+    // interval: bf16 forms it in the first one, fp32 in the second one before, so it has two in turn.
+    LinTile<P, C, C> p[P::kBytes == 4 ? 3 : 2];
+    __device__ __forceinline__ LinTile<P, C, C> &second(bool dg, int m) { return p[P::kBytes == 4 && dg ? 1 + (m & 1) : 1]; }
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
     float part[8][C];                  // a or b, by the columns' wave
 
@@ -156,39 +159,85 @@ struct Decays {
     }
 };
 
-// The products of the next chunk, m + 1, decayed.  Backwards by its earlier tokens' rows: a row of
-// blocks, later tokens in block I, all of it in flight at once (block by block each waits for its
-// own LDS reads, and the second interval is this role's to hold up).
-template <class P, int I, int C, int D>
+// A chunk's products, decayed.  Backwards by its earlier tokens' rows: blocks J .. J + N - 1 of earlier
+// tokens with the later ones of block I, all of it in flight at once (block by block each waits for
+// its own LDS reads).
+template <class P, int I, int J, int N, int C, int D>
 __device__ __forceinline__ void products_back(LinTile<P, C, D> &later, LinTile<P, C, D> &earlier, const LinGates<C> &gates,
                                               LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
-    if constexpr (I < C / 16) {
-        const int g4 = l.lane >> 4, r16 = l.lane & 15, s = 16 * I + 4 * g4;
-        f32x4 x[I + 1];
+    static_assert(I < C / 16 && J + N - 1 <= I, "the lower triangle");
+    const int g4 = l.lane >> 4, r16 = l.lane & 15, s = 16 * I + 4 * g4;
+    f32x4 x[N];
 #pragma unroll
-        for (int j = 0; j <= I; ++j) x[j] = zero4();
+    for (int n = 0; n < N; ++n) x[n] = zero4();
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
-            typename P::F a0, a1, b0[I + 1], b1[I + 1];
-            later.oct(I, u, l, a0, a1);
+    for (int u = 0; u < D / 32; ++u) {
+        typename P::F a0, a1, b0[N], b1[N];
+        later.oct(I, u, l, a0, a1);
 #pragma unroll
-            for (int j = 0; j <= I; ++j) earlier.oct(j, u, l, b0[j], b1[j]);
+        for (int n = 0; n < N; ++n) earlier.oct(J + n, u, l, b0[n], b1[n]);
 #pragma unroll
-            for (int j = 0; j <= I; ++j) x[j] = P::mma2(x[j], a0, a1, b0[j], b1[j]);
+        for (int n = 0; n < N; ++n) x[n] = P::mma2(x[n], a0, a1, b0[n], b1[n]);
+    }
+    const f32x4 hi = lds_f32x4(gates.hi + s), lo = lds_f32x4(gates.lo + s);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int t = 16 * (J + n) + r16;
+        const float ht = gates.hi[t], lt = gates.lo[t];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v = x[n][e] * lin_exp2((hi[e] - ht) + (lo[e] - lt));
+            x[n][e] = J + n < I || t <= s + e ? v : 0.f;
         }
-        const f32x4 hi = lds_f32x4(gates.hi + s), lo = lds_f32x4(gates.lo + s);
-#pragma unroll
-        for (int j = 0; j <= I; ++j) {
-            const int t = 16 * j + r16;
-            const float ht = gates.hi[t], lt = gates.lo[t];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v = x[j][e] * lin_exp2((hi[e] - ht) + (lo[e] - lt));
-                x[j][e] = j < I || t <= s + e ? v : 0.f;
-            }
-            P::st4(to.four(j, I, l), x[j]);
-            if (low) P::st4(low->four(j, I, l), x[j] - P::f32(P::cvt(x[j])));
+        P::st4(to.four(J + n, I, l), x[n]);
+        if (low) P::st4(low->four(J + n, I, l), x[n] - P::f32(P::cvt(x[n])));
+    }
+}
+// All of them by four waves: three, two, three and two blocks.
+template <class P, int C, int D>
+__device__ __forceinline__ void back_by_four(int wave, LinTile<P, C, D> &later, LinTile<P, C, D> &earlier, const LinGates<C> &gates,
+                                             LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
+    if (wave == 0) {
+        products_back<P, 3, 0, 2>(later, earlier, gates, to, low, l);
+        products_back<P, 0, 0, 1>(later, earlier, gates, to, low, l);
+    } else if (wave == 1) {
+        products_back<P, 3, 2, 2>(later, earlier, gates, to, low, l);
+    } else if (wave == 2) {
+        products_back<P, 2, 0, 3>(later, earlier, gates, to, low, l);
+    } else {
+        products_back<P, 1, 0, 2>(later, earlier, gates, to, low, l);
+    }
+}
+// By two waves, five blocks each (fp32: two and one).
+template <class P, int C, int D>
+__device__ __forceinline__ void back_by_two(int wave, LinTile<P, C, D> &later, LinTile<P, C, D> &earlier, const LinGates<C> &gates,
+                                            LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
+    if constexpr (C == 64) {
+        if (wave == 0) {
+            products_back<P, 3, 0, 4>(later, earlier, gates, to, low, l);
+            products_back<P, 0, 0, 1>(later, earlier, gates, to, low, l);
+        } else {
+            products_back<P, 2, 0, 3>(later, earlier, gates, to, low, l);
+            products_back<P, 1, 0, 2>(later, earlier, gates, to, low, l);
         }
+    } else {
+        if (wave == 0) products_back<P, 0, 0, 1>(later, earlier, gates, to, low, l);
+        else products_back<P, 1, 0, 2>(later, earlier, gates, to, low, l);
+    }
+}
+// By eight waves, four that load and four of the states'.
+template <class P, int C, int D>
+__device__ __forceinline__ void back_by_eight(bool loads, int wave, LinTile<P, C, D> &later, LinTile<P, C, D> &earlier,
+                                              const LinGates<C> &gates, LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
+    if (!loads) {
+        if (wave == 0) products_back<P, 3, 0, 2>(later, earlier, gates, to, low, l);
+        else if (wave == 1) products_back<P, 3, 2, 2>(later, earlier, gates, to, low, l);
+        else if (wave == 2) products_back<P, 2, 0, 2>(later, earlier, gates, to, low, l);
+        else products_back<P, 2, 2, 1>(later, earlier, gates, to, low, l);
+    } else {
+        if (wave == 0) products_back<P, 1, 0, 1>(later, earlier, gates, to, low, l);
+        else if (wave == 1) products_back<P, 1, 1, 1>(later, earlier, gates, to, low, l);
+        else if (wave == 2) products_back<P, 0, 0, 1>(later, earlier, gates, to, low, l);
     }
 }
 // Forwards by its later tokens' rows, of do v; for dg with M's sums over the block.
@@ -224,8 +273,8 @@ __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     }
 }
 
-// The loading waves, NW of them; `wave` counts from the first.
-template <class P, int DK, int DV, bool REV, bool DG, int NW>
+// The loading waves, NW of them; `wave` counts from the first.  Forwards they form the blocks up to LAST.
+template <class P, int DK, int DV, bool REV, bool DG, int NW, int LAST = BwdLds<P, DK, DV>::NB>
 __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, int wave) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NT = 64 * NW;
@@ -265,6 +314,10 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             rv.put(next.v, tid);
             ro.put(next.o, tid);
         }
+        if constexpr (DG && REV && C == 64) {    // while the registers are free
+            typename L::Chunk &x = lds.c[m & 1];
+            if (valid) back_by_eight<P>(true, wave, x.o, x.v, lds.gates[m % 3], lds.p[1], w.few() ? &lds.low(1) : nullptr, w.l);
+        }
         fetch(m + 2);
         if constexpr (DG && !REV) {
             const int i = (tid >> 4) & (C / 16 - 1), e = tid & 15;
@@ -278,24 +331,13 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         }
         __syncthreads();
         if constexpr (REV) {
-            // five blocks a wave (fp32: two or one)
             const LinGates<C> &gates = lds.gates[(m + 1) % 3];
-            LinTile<P, C, C> *const low0 = w.few() && m < 0 ? &lds.low(0) : nullptr, *const low1 = w.few() && m < 0 ? &lds.low(1) : nullptr;
-            if (wave == 0) {
-                products_back<P, 3>(next.q, next.k, gates, lds.p[0], low0, w.l);
-                products_back<P, 0>(next.q, next.k, gates, lds.p[0], low0, w.l);
-            } else if (wave == 1) {
-                products_back<P, 3>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
-                products_back<P, 0>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
-            } else if (wave == 2) {
-                products_back<P, 2>(next.q, next.k, gates, lds.p[0], low0, w.l);
-                products_back<P, 1>(next.q, next.k, gates, lds.p[0], low0, w.l);
-            } else {
-                products_back<P, 2>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
-                products_back<P, 1>(next.o, next.v, gates, lds.p[1 + ((m + 1) & 1)], low1, w.l);
-            }
+            const bool low = w.few() && m < 0;
+            if constexpr (DG && C == 64) back_by_four<P>(wave, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
+            else if (wave & 1) back_by_two<P>(wave >> 1, next.o, next.v, gates, lds.second(DG, m + 1), low ? &lds.low(1) : nullptr, w.l);
+            else back_by_two<P>(wave >> 1, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
         } else {
-            for (int p = wave; p < L::NB; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
+            for (int p = wave; p < LAST; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
         }
         __syncthreads();
     }
@@ -391,13 +433,19 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     constexpr int C = L::C, NC = 1, NS = DK / 16;
     const Walk<P, DK, DV> w(a, unit);
     const int wave = 4 * w.role + w.wave;
-    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS>(w, lds, wave - NS);
+    // with eight waves on the state, whose second interval is short, six of them take a block each
+    constexpr int LAST = NS == 8 && L::NB == 10 ? 4 : L::NB;
+    if (wave >= NS) return bring<P, DK, DV, false, DG, 12 - NS, LAST>(w, lds, wave - NS);
     const int lane = w.lane, t0 = wave, c0 = 16 * t0;
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, lin_before(a, w.bh, w.seg), c0, lane);
     Decays<P, DK, DV, false> decays(w, lds);
+    auto help = [&](int m) {
+        if (LAST < L::NB && wave >= 2) product<P, DK, DV, DG>(w, lds, m, LAST + wave - 2);
+    };
     __syncthreads();                             // the first chunk is brought
+    help(-1);
     __syncthreads();
     for (int m = 0; m < w.count; ++m) {
         typename L::Chunk &x = lds.c[m & 1];
@@ -414,6 +462,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
             pack<P, C>(out, acc, w.live(w.c0 + m), w.r16);
         }
         __syncthreads();
+        help(m);
         spill_out<P, C>(x.q, out, t0, w.l);
         lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, gates.after, gates.all[0], w.l);
         if (DG && wave == 1) w.template terms<false, NS>(lds, w.c0 + m);
@@ -430,7 +479,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
 
 // ---------------------------------------------------------------- dk and dv, backwards
 // dv: the gradient's columns are value indices.
-template <class P, int DK, int DV>
+template <class P, int DK, int DV, bool DG>
 __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV> &lds, const float *from) {
     using L = BwdLds<P, DK, DV>;
     constexpr int C = L::C, NC = DV / 64;
@@ -444,6 +493,8 @@ __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename L::Chunk &x = lds.c[m & 1];
         const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F of[NC][C / 32][2], out[NC][C / 16];
+        // dk's products, which for dg are for the second interval
+        if constexpr (DG && C == 64) back_by_eight<P>(false, w.wave, x.o, x.v, gates, lds.p[1], w.few() ? &lds.low(1) : nullptr, w.l);
         {
             f32x4 acc[NC][C / 16];
             lin_columns<P, C>(of, x.o, t0, w.l);
@@ -482,7 +533,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         // one addend it is the other way round, 57 -> 59 us at 8 x 1000 x 16 x 128 x 64, bf16)
         auto own = [&] {
             lin_columns<P, C>(qf, x.q, t0, w.l);
-            lin_near<P, false>(acc, lds.p[1 + (m & 1)], qf, w.l);
+            lin_near<P, false>(acc, lds.second(DG, m), qf, w.l);
             if (w.few()) lin_near<P, false>(acc, lds.low(1), qf, w.l);
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         };
@@ -517,7 +568,7 @@ __device__ __forceinline__ void dkv_walk(const LinArgs &a, BwdLds<P, DK, DV> &ld
     if (w.role == 2) return bring<P, DK, DV, true, DG, 4>(w, lds, w.wave);
     const float *from = lin_behind(a, w.bh, w.seg);
     if (w.role == 0) dk_walk<P, DK, DV, DG, NS>(w, lds, from);
-    else dv_walk<P, DK, DV>(w, lds, from);
+    else dv_walk<P, DK, DV, DG>(w, lds, from);
 }
 
 template <class P, int DK, int DV, bool DG, int NS>
@@ -526,7 +577,7 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
     extern __shared__ __align__(16) char smem[];
     L &lds = *reinterpret_cast<L *>(smem);
     // blocks of P off its triangle that a pair of tiles reads: never written again
-    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = lds.p[2].m[e] = lds.low(0).m[e] = lds.low(1).m[e] = 0;
+    for (int e = threadIdx.x; e < LinTile<P, L::C, L::C>::kElems; e += kBwdThreads) lds.p[0].m[e] = lds.p[1].m[e] = lds.p[sizeof(lds.p) / sizeof(lds.p[0]) - 1].m[e] = lds.low(0).m[e] = lds.low(1).m[e] = 0;
     __syncthreads();
     const int unit = blockIdx.x >> 1;
     if (blockIdx.x & 1) dq_walk<P, DK, DV, DG>(a, lds, unit);
