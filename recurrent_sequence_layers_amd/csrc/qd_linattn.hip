@@ -4,7 +4,7 @@
 // Bound by HBM: q, k, v read once, o written once.  A workgroup walks the chunks of one (sequence,
 // head, 64 value columns): four waves hold the state, sixteen columns each, and four more bring what
 // they need.  The column blocks of a head are put on the same XCD, so its L2 serves the second
-// reading of q and k.  8 x 4096 tokens, 16 heads, 128 x 128, bf16 (539 MB): 136 to 147 us, 3.7 to 4.0
+// reading of q and k.  8 x 4096 tokens, 16 heads, 128 x 128, bf16 (539 MB): 128 to 130 us, 4.1 to 4.2
 // TB/s of the 4.9 that a copy reaches; the same loads, barriers and stores without the products take
 // 127.  Four waves that load, compute and store in turn took 294 us, the two roles 179, and outputs in
 // whole rows instead of eight bytes a lane 149 where they had been 175.
@@ -12,7 +12,7 @@
 // Where (sequence, head, column block) leaves the card short of workgroups the time axis is cut into
 // segments: a first launch walks each segment but the last from zero, a second one joins the
 // segments' states, and the main one starts every segment from its own.  65536 tokens of 16 heads:
-// 1963 us uncut, 440 cut in eight, 136 of them for the states, which read k and v once more.
+// 1617 us uncut, 402 to 414 cut in eight, 136 of them for the states, which read k and v once more.
 #include "qd_internal.h"
 #include "qd_linattn.h"
 
@@ -71,9 +71,10 @@ __device__ __forceinline__ void lin_products(LinTile<P, C, D> &q, LinTile<P, C, 
         if (P::kBytes == 2 && low) P::st4(low->four(I, J + n, l), x[n] - P::f32(P::cvt(x[n])));
     }
 }
-// A wave's share of them: the loading waves (role 1) take seven of ten, the states' waves three (all ten on
-// the loading waves: 144 -> 128 us at the size above, 46 -> 38 for seven prompts of up to 1900 tokens
-// and 12 heads); in fp32, where the states' waves have more to do, the loading waves all three.
+// A wave's share of them: the loading waves (role 1) take seven of ten, the states' waves three. With
+// all ten on the loading waves the size above takes 144 us, and seven prompts of up to 1900 tokens,
+// 12 heads, 46 instead of 38. In fp32, where the states' waves have more to do, the loading waves
+// take all three.
 template <class P, int C, int D>
 __device__ __forceinline__ void lin_share(int role, int wave, LinTile<P, C, D> &q, LinTile<P, C, D> &k, const LinGates<C> &gates,
                                           LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
@@ -428,10 +429,10 @@ bool lin_fits(int dtype, int B, int T, int H, LinCall call) {
 // A walk of n chunks takes n + 3 steps, workgroups go in rounds of one a compute unit, and cutting
 // the axis costs two launches (about five steps) and the states: a chunk of a piece costs
 // state_cost of a step, three workgroups a compute unit side by side.  Uncut and cut, in us: forward
-// 2048 x 16 heads 64 and 31, 2 x 4096 x 16 122 and 63; gradients 2048 x 8 heads 184 and 57, 2 x 1024 x
-// 16 100 and 63, 4096 x 4 heads of 64 x 64 in fp32 468 and 51.  A sequence of seven chunks is left
-// whole.  Pieces: as long as their segments, 65536 x 16 takes 538 us instead of 440, 2 x 4096 x 16 69
-// instead of 63.
+// 2048 x 16 heads 50 and 29, 2 x 4096 x 16 96 and 57; gradients 2048 x 8 heads 165 and 49, 2 x 1024 x
+// 16 89 and 56, 4096 x 4 heads of 64 x 64 in fp32 442 and 41.  A sequence of seven chunks is left
+// whole.  Pieces: as long as their segments, 65536 x 16 takes 504 us instead of 414, 2 x 4096 x 16 63
+// instead of 57.
 void lin_plan(int dtype, LinArgs &a, long long units, int directions, double state_cost) {
     const long long C = lin_chunk(dtype), nc = (a.T + C - 1) / C, cus = 256;
     double best = 0;

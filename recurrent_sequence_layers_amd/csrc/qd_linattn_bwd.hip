@@ -37,17 +37,18 @@ namespace {
 __device__ __forceinline__ float sum16(float x) { return group_sum(x, 16); }
 __device__ __forceinline__ float sum64(float x) { return group_sum(x, 64); }
 
-// 8 x 4096 tokens, 16 heads, 128 x 128, bf16, the decays' gradient too: 400 to 424 us, without it 321.
+// 8 x 4096 tokens, 16 heads, 128 x 128, bf16, the decays' gradient too: 394 to 400 us, without it 327.
 // The 944 MB would take 191 at the rate of a copy; the products, half of them for the 24 bits that dg
 // is of, 242 at that of a large product.  The vector units, which split the states and their addends,
-// are 52 % busy, the matrix units 33 %, and no wave waits long: dq's walk alone takes 312, the other 376.
+// are 52 % busy, the matrix units 33 %, and the shares are even: the slowest waves of a chunk's two
+// intervals take 4900 and 5200 cycles in dq's walk, 5200 and 5700 in the other.
 //
 // Twelve waves, two barriers a chunk.  Forwards four or eight waves hold the state, sixteen columns
 // each; backwards four hold it by its key columns and four by its value columns, a quarter each (one
 // of either a wave reads the LDS twice as often: 411 -> 443 us).  In a chunk's first interval they form
 // its outputs, in the second they update the state.  The other waves meanwhile bring the next
 // chunk: first from the registers, where its loads went a chunk before, to LDS, then its decayed
-// products P.  Outputs wait in registers for the second interval, go to a tile of their chunk that
+// products P, of which states' waves that have less to do take some.  Outputs wait in registers for the second interval, go to a tile of their chunk that
 // nobody reads any more (dq to q, dk to k, dv to v) and leave in whole rows, each thread storing
 // the pieces that it is about to replace.
 constexpr int kBwdThreads = 768;
@@ -627,7 +628,7 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
 
 // The same for all of a head's chunks, where they are many: one workgroup, from the last chunk on,
 // 1024 at a time.
-constexpr int kFewChunks = 256;
+constexpr int kFewChunks = 256;             // a call of 7 chunks 34 us, by a launch 38; 64: 89, 94; 256: 152, 154; 2048: 1070, 1044
 __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a, const int nc) {
     __shared__ double sd[kDgChunks], sb[kDgChunks], sv[kDgChunks];
     __shared__ double total[kDgWaves][2];
