@@ -60,8 +60,12 @@ struct BwdLds {
         LinTile<P, C, DV> v, o;
     } c[2];
     LinGates<C> gates[3];
-    // Of do v forwards; of q k and of do v backwards.  With dg the latter is read in the second
-    // interval: bf16 forms it in the first one, fp32 in the second one before, so it has two in turn.
+    // Of do v forwards; of q k and of do v backwards.  Where the latter is read in the second interval,
+    // bf16 forms it in the first one, fp32 in the second one before, so it has two in turn.
+    // That is so for dg, whose three addends make reading the state the first interval's longest part
+    // (fp32, 4096 x 16 x 128 x 128: 272 -> 261 us), and without it for bf16 while the registers last: 8 x
+    // 1000 x 16 x 64 x 64 38.9 -> 37.4 us, 64 x 128 57.2 -> 55.5, but 128 x 128 spills, 324 -> 325.
+    static constexpr bool later(bool dg) { return dg || (C == 64 && DK + DV < 256); }
     LinTile<P, C, C> p[P::kBytes == 4 ? 3 : 2];
     __device__ __forceinline__ LinTile<P, C, C> &second(bool dg, int m) { return p[P::kBytes == 4 && dg ? 1 + (m & 1) : 1]; }
     float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
@@ -226,11 +230,12 @@ __device__ __forceinline__ void back_by_two(int wave, LinTile<P, C, D> &later, L
         else products_back<P, 1, 0, 2>(later, earlier, gates, to, low, l);
     }
 }
-// By eight waves, four that load and four of the states'.
+// By eight waves: seven of ten by four of them, three by the others, with less time (few): the
+// loading ones, or without dg those that hold dk.
 template <class P, int C, int D>
-__device__ __forceinline__ void back_by_eight(bool loads, int wave, LinTile<P, C, D> &later, LinTile<P, C, D> &earlier,
+__device__ __forceinline__ void back_by_eight(bool few, int wave, LinTile<P, C, D> &later, LinTile<P, C, D> &earlier,
                                               const LinGates<C> &gates, LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
-    if (!loads) {
+    if (!few) {
         if (wave == 0) products_back<P, 3, 0, 2>(later, earlier, gates, to, low, l);
         else if (wave == 1) products_back<P, 3, 2, 2>(later, earlier, gates, to, low, l);
         else if (wave == 2) products_back<P, 2, 0, 2>(later, earlier, gates, to, low, l);
@@ -334,7 +339,7 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         if constexpr (REV) {
             const LinGates<C> &gates = lds.gates[(m + 1) % 3];
             const bool low = w.few() && m < 0;
-            if constexpr (DG && C == 64) back_by_four<P>(wave, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
+            if constexpr (C == 64 && L::later(DG)) back_by_four<P>(wave, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
             else if (wave & 1) back_by_two<P>(wave >> 1, next.o, next.v, gates, lds.second(DG, m + 1), low ? &lds.low(1) : nullptr, w.l);
             else back_by_two<P>(wave >> 1, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
         } else {
@@ -494,8 +499,8 @@ __device__ __forceinline__ void dv_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename L::Chunk &x = lds.c[m & 1];
         const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F of[NC][C / 32][2], out[NC][C / 16];
-        // dk's products, which for dg are for the second interval
-        if constexpr (DG && C == 64) back_by_eight<P>(false, w.wave, x.o, x.v, gates, lds.p[1], w.few() ? &lds.low(1) : nullptr, w.l);
+        // dk's products, where they are for the second interval
+        if constexpr (C == 64 && L::later(DG)) back_by_eight<P>(false, w.wave, x.o, x.v, gates, lds.p[1], w.few() ? &lds.low(1) : nullptr, w.l);
         {
             f32x4 acc[NC][C / 16];
             lin_columns<P, C>(of, x.o, t0, w.l);
@@ -526,12 +531,11 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         typename L::Chunk &x = lds.c[m & 1];
         const LinGates<C> &gates = lds.gates[m % 3];
         typename P::F qf[NC][C / 32][2], out[NC][C / 16];
+        if constexpr (!DG && C == 64 && L::later(DG)) back_by_eight<P>(true, w.wave, x.o, x.v, gates, lds.p[1], w.few() ? &lds.low(1) : nullptr, w.l);
         f32x4 acc[NC][C / 16];
         lin_read<P, DG ? 3 : 1>(acc, R, x.v, w.l);
         scale<C>(acc, gates.after, w.r16);
-        // the chunk's own part; for dg it waits for the second interval: with three addends to read,
-        // these waves are the first one's longest (fp32, 4096 x 16 x 128 x 128: 272 -> 261 us; with
-        // one addend it is the other way round, 57 -> 59 us at 8 x 1000 x 16 x 128 x 64, bf16)
+        // the chunk's own part
         auto own = [&] {
             lin_columns<P, C>(qf, x.q, t0, w.l);
             lin_near<P, false>(acc, lds.second(DG, m), qf, w.l);
@@ -539,9 +543,9 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
             pack<P, C>(out, acc, w.live(w.template chunk<true>(m)), w.r16);
         };
         if constexpr (DG) row_parts<P>(lds.part[w.wave], x.k, acc, t0, w.l);
-        else own();
+        if constexpr (!L::later(DG)) own();
         __syncthreads();
-        if constexpr (DG) own();
+        if constexpr (L::later(DG)) own();
         spill_out<P, C>(x.k, out, t0, w.l);
         lin_update<P, C, NS>(R, x.o, qf, gates.before, gates.all[0], w.l);
         if (DG && w.wave == 1) w.template terms<true, 4>(lds, w.template chunk<true>(m));
