@@ -48,9 +48,9 @@ __device__ __forceinline__ float sum64(float x) { return group_sum(x, 64); }
 // of either a wave reads the LDS twice as often: 411 -> 443 us).  In a chunk's first interval they form
 // its outputs, in the second they update the state.  The other waves meanwhile bring the next
 // chunk: first from the registers, where its loads went a chunk before, to LDS, then its decayed
-// products P, of which states' waves that have less to do take some.  Outputs wait in registers for the second interval, go to a tile of their chunk that
-// nobody reads any more (dq to q, dk to k, dv to v) and leave in whole rows, each thread storing
-// the pieces that it is about to replace.
+// products P, of which states' waves that have less to do take some.  Outputs wait in registers for
+// the second interval, go to a tile of their chunk that nobody reads any more (dq to q, dk to k, dv to
+// v) and leave in whole rows, each thread storing the pieces that it is about to replace.
 constexpr int kBwdThreads = 768;
 template <class P, int DK, int DV>
 struct BwdLds {
