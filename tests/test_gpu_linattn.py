@@ -215,6 +215,16 @@ def test_one_chunk_rounds_once(qd, T, dk, dv):
             near(got[n], grads[n], scale[n], x, n, parts=2.0 ** -8)
 
 
+@pytest.mark.parametrize("T,lens", [(8192, None), (8200, None), (34000, [33000])])
+def test_decays_gradient_over_many_chunks(qd, T, lens):
+    """The chain of dg over 256 chunks, 257, and more than 1024 of which the last are padding."""
+    x = inputs(1, T, 1, 64, 64, "f32", 19)
+    want, scale = layer.linattn_bwd(*[x[n] for n in BWD], lens=lens)
+    got = call(qd, "qdelta_linattn_bwd", x, BWD, lens=None if lens is None else dev(torch.tensor(lens, dtype=torch.int32)))
+    for n in ("dg", "dq", "dS0"):
+        near(got[n], want[n], scale[n], x, n)
+
+
 def test_no_tokens_no_sequences(qd):
     x = inputs(2, 0, 3, 64, 128, "bf16", 12)
     o, S = call(qd, "qdelta_linattn_fwd", x, FWD)
