@@ -64,7 +64,7 @@ struct LinArgs {
     float *entry;                    // [B H][DV][DK]: S0, where S_T overwrites it; or null
     float *sums;                     // [B H][chunks][4]: a chunk's a, a^2, b and b^2, see qd_linattn_bwd.hip
     float *tok;                      // [3][B H][T]: terms of dg
-    float *edge, *edge0;             // [B H][DK / 16], [B H][4]: <S_T, dS_T> and <S0, dS0> by wave
+    float *edge;                     // [B H][segs + 1][8]: <S, R> at the segments' borders, by wave
     float *chain, *head;             // [B H][chunks]: c; [B][chunks][H]: sums of dg over tokens
 };
 

@@ -23,10 +23,10 @@
 // Every term is one that g_t scales: no difference of large sums.  The walks write a, b and
 // x_t = sum_{s>t} M[s][t] - sum_{i<t} M[t][i], whose prefix sums are the third term, and c comes
 // from a chain over the chunks: with E_n = <S, R> behind chunk n, c_n = E_n - sum b and
-// E_{n-1} = c_n + sum a, from E = <S_T, dS_T> on.  a and b are taken before anything is rounded
-// (the state split as in qd_linattn.h), since dg is fp32.  The chain adds up their roundings; what
-// it misses <S0, dS0> by at its other end is taken back in proportion to the squares of the terms
-// that it has passed, which is where it came from.
+// E_{n-1} = c_n + sum a, from the segment's end on (<S_T, dS_T>, or what the states at the border give).
+// a and b are taken before anything is rounded (the state split as in qd_linattn.h), since dg is fp32.
+// The chain adds up their roundings; what it misses <S, R> by at the segment's start is taken back in
+// proportion to the squares of the terms that it has passed, which is where it came from.
 #include "qd_internal.h"
 #include "qd_linattn.h"
 #include "qd_mixer.h"
@@ -117,6 +117,8 @@ struct Walk {
         return lin_rsrc(static_cast<char *>(base) + (valid ? at(n * C, stride, d) : 0),
                         valid ? (rows - 1) * static_cast<int>(stride) + d * P::kBytes : 0);
     }
+    // <S, R> before segment k
+    __device__ __forceinline__ float *edge(int k) const { return a.edge + (static_cast<size_t>(bh) * (a.segs + 1) + k) * 8; }
     // One of the terms of dg for chunk n: a thread a token
     __device__ __forceinline__ void term(int which, int n, bool valid, int tid, float v) const {
         const float *to = a.tok + (static_cast<size_t>(which) * a.B * a.H + bh) * a.T + (valid ? n * C : 0);
@@ -446,6 +448,12 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     const size_t state = static_cast<size_t>(DV) * DK;
     f32x4 S[NC][DV / 16];
     load_across<DK, DV>(S, lin_before(a, w.bh, w.seg), c0, lane);
+    if constexpr (DG) {
+        if (w.seg > 0) {
+            const float s = inner<DK, DV>(S, lin_behind(a, w.bh, w.seg - 1), c0, lane);
+            if (lane == 0) w.edge(w.seg)[wave] = s;
+        }
+    }
     Decays<P, DK, DV, false> decays(w, lds);
     auto help = [&](int m) {
         if (LAST < L::NB && wave >= 2) product<P, DK, DV, DG>(w, lds, m, LAST + wave - 2);
@@ -478,7 +486,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
     if constexpr (DG) {
         if (w.seg == a.segs - 1) {               // <S_T, dS_T>
             const float s = inner<DK, DV>(S, a.dS_T ? a.dS_T + w.bh * state : nullptr, c0, lane);
-            if (lane == 0) a.edge[static_cast<size_t>(w.bh) * NS + wave] = s;
+            if (lane == 0) w.edge(a.segs)[wave] = s;
         }
     }
 }
@@ -555,7 +563,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     const LinArgs &a = w.a;
     if (DG && w.seg == 0) {                      // <S0, dS0>
         const float s = inner<DK, DV>(R, a.S0 ? a.S0 + static_cast<size_t>(w.bh) * DV * DK : nullptr, c0, lane);
-        if (lane == 0) a.edge0[static_cast<size_t>(w.bh) * 4 + w.wave] = s;
+        if (lane == 0) w.edge(0)[w.wave] = s;
     }
     if (a.dS0 && w.seg == 0) {
         float *to = a.dS0 + static_cast<size_t>(w.bh) * DV * DK;
@@ -605,43 +613,48 @@ __device__ __forceinline__ double wave_total(double x) {
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 struct Ends {
-    double last, first;              // <S_T, dS_T>, <S0, dS0>
-    __device__ __forceinline__ Ends(const LinArgs &a, size_t bh) : last(0), first(0) {
-        for (int w = 0; w < a.DK / 16; ++w) last += a.edge[bh * (a.DK / 16) + w];
-        for (int w = 0; w < 4; ++w) first += a.edge0[bh * 4 + w];
+    int first, count;                // the segment's chunks
+    double before, behind;           // <S, R> at its borders
+    __device__ __forceinline__ Ends(const LinArgs &a, size_t bh, int nc, int seg)
+        : first(seg * a.seg_chunks), count(min(a.seg_chunks, nc - first)), before(0), behind(0) {
+        const float *e = a.edge + (bh * (a.segs + 1) + seg) * 8;
+        for (int w = 0; w < (seg ? a.DK / 16 : 4); ++w) before += e[w];
+        for (int w = 0; w < a.DK / 16; ++w) behind += e[8 + w];
     }
 };
 __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, int n, int lane) {
-    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc;
+    const Ends e(a, bh, nc, n / a.seg_chunks);
+    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc + e.first;
+    const int at = n - e.first;
     double D = 0, V = 0, later = 0, passed = 0, own = 0;
-    for (int m = lane; m < nc; m += kWave) {
+    for (int m = lane; m < e.count; m += kWave) {
         const f32x4 x = sums[m];
         const double d = static_cast<double>(x[0]) - x[2], v = static_cast<double>(x[1]) + x[3];
         D += d;
         V += v;
-        later += m > n ? d : 0;
-        passed += m > n ? v : m == n ? 0.5 * v : 0;
-        own += m == n ? x[2] : 0;
+        later += m > at ? d : 0;
+        passed += m > at ? v : m == at ? 0.5 * v : 0;
+        own += m == at ? x[2] : 0;
     }
     D = wave_total(D);
     V = wave_total(V);
-    const Ends e(a, bh);
-    return static_cast<float>(e.last + wave_total(later) - wave_total(own) -
-                              (V > 0 ? (e.last + D - e.first) / V * wave_total(passed) : 0));
+    return static_cast<float>(e.behind + wave_total(later) - wave_total(own) -
+                              (V > 0 ? (e.behind + D - e.before) / V * wave_total(passed) : 0));
 }
 
-// The same for all of a head's chunks, where they are many: one workgroup, from the last chunk on,
+// The same for all of a segment's chunks, where they are many: one workgroup, from the last chunk on,
 // 1024 at a time.
 constexpr int kFewChunks = 256;             // a call of 7 chunks 34 us, by a launch 38; 64: 89, 94; 256: 152, 154; 2048: 1070, 1044
 __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a, const int nc) {
     __shared__ double sd[kDgChunks], sb[kDgChunks], sv[kDgChunks];
     __shared__ double total[kDgWaves][2];
-    const size_t bh = blockIdx.x;
+    const size_t bh = blockIdx.x / a.segs;
     const int wave = wave_id(), lane = lane_id();
-    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc;
-    float *c = a.chain + bh * nc;
+    const Ends ends(a, bh, nc, blockIdx.x % a.segs);
+    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc + ends.first;
+    float *c = a.chain + bh * nc + ends.first;
     double D = 0, V = 0;
-    for (int m = threadIdx.x; m < nc; m += 64 * kDgWaves) {
+    for (int m = threadIdx.x; m < ends.count; m += 64 * kDgWaves) {
         const f32x4 x = sums[m];
         D += static_cast<double>(x[0]) - x[2];
         V += static_cast<double>(x[1]) + x[3];
@@ -658,10 +671,9 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
         D += total[w][0];
         V += total[w][1];
     }
-    const Ends ends(a, bh);
-    double E = ends.last, passed = 0;
-    const double part = V > 0 ? (E + D - ends.first) / V : 0;
-    for (int last = nc; last > 0; last -= kDgChunks) {
+    double E = ends.behind, passed = 0;
+    const double part = V > 0 ? (E + D - ends.before) / V : 0;
+    for (int last = ends.count; last > 0; last -= kDgChunks) {
         const int first = max(last - kDgChunks, 0), count = last - first;
         for (int m = threadIdx.x; m < count; m += 64 * kDgWaves) {
             const f32x4 x = sums[first + m];
@@ -719,7 +731,7 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
         const float y = lane < live ? x[lane] + tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
         const float before = wave_inclusive_sum(y) - y;
         const float behind = __shfl(wave_inclusive_sum(z), back);
-        const float c = nc <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.chain[bh * nc + n];
+        const float c = a.seg_chunks <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.chain[bh * nc + n];
         v = lane < live ? c + (before + behind) : 0.f;
     }
     if (a.decay == kHeadDecay) {
@@ -749,7 +761,7 @@ hipError_t bwd_sized(const LinArgs &a, hipStream_t stream) {
     if (hipError_t e = hipGetLastError()) return e;
     if (a.dg) {
         const unsigned nc = (a.T + L::C - 1) / L::C;
-        if (nc > kFewChunks) hipLaunchKernelGGL(lin_chain_kernel, dim3(static_cast<unsigned>(a.B * a.H)), dim3(64 * kDgWaves), 0, stream, a, static_cast<int>(nc));
+        if (a.seg_chunks > kFewChunks) hipLaunchKernelGGL(lin_chain_kernel, dim3(static_cast<unsigned>(a.B * a.H * a.segs)), dim3(64 * kDgWaves), 0, stream, a, static_cast<int>(nc));
         hipLaunchKernelGGL(lin_dg_kernel<L::C>, dim3(nc * a.B, (a.H + kDgWaves - 1) / kDgWaves), dim3(64 * kDgWaves), 0, stream, a);
         if (a.decay == kHeadDecay) column_sum(a.head, static_cast<int>(nc * a.B), a.H, HeadStore{a.dg}, stream);
     }
@@ -773,7 +785,7 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * (dk / 16 + 4) + 6 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
+    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * 8 * (a.segs + 1) + 6 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -794,8 +806,7 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
         a.sums = p;
         a.tok = a.sums + 4 * bh * chunks;
         a.edge = a.tok + 3 * bh * a.T;
-        a.edge0 = a.edge + bh * (a.DK / 16);
-        a.chain = a.edge0 + bh * 4;
+        a.chain = a.edge + bh * 8 * (a.segs + 1);
         a.head = a.chain + bh * chunks;
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
