@@ -225,6 +225,21 @@ def test_decays_gradient_over_many_chunks(qd, T, lens):
         near(got[n], want[n], scale[n], x, n)
 
 
+def test_decays_gradient_of_many_heads_over_many_chunks(qd):
+    """Heads enough to leave the time axis whole, 257 chunks of it; each head has the same inputs, so
+    one is checked and the others are it."""
+    H, T = 128, 8200
+    x = inputs(1, T, 1, 64, 64, "f32", 20)
+    want, scale = layer.linattn_bwd(*[x[n] for n in BWD])
+    wide = {n: x[n].expand(*[H if (n in ("S0", "dS_T") and i == 1) or (n not in ("S0", "dS_T") and i == 2) else s
+                             for i, s in enumerate(x[n].shape)]).contiguous() for n in BWD}
+    got = call(qd, "qdelta_linattn_bwd", wide, BWD)
+    for n, axis in (("dq", 2), ("dk", 2), ("dv", 2), ("dg", 2), ("dS0", 1)):
+        one = got[n].narrow(axis, 0, 1)
+        near(one, want[n], scale[n], x, n)
+        assert torch.equal(got[n], one.expand_as(got[n])), n
+
+
 def test_no_tokens_no_sequences(qd):
     x = inputs(2, 0, 3, 64, 128, "bf16", 12)
     o, S = call(qd, "qdelta_linattn_fwd", x, FWD)
