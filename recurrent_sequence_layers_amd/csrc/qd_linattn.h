@@ -39,6 +39,13 @@ namespace qd {
 
 enum LinDecay { kNoDecay = 0, kTokenDecay = 1, kHeadDecay = 2 };
 
+// A chunk's sums of a and b and of their squares, for the chain of qd_linattn_bwd.hip.  The squares
+// are in 64 bits: those of ordinary fp32 terms leave fp32's range.
+struct LinSums {
+    float a, b;
+    double aa, bb;
+};
+
 struct LinArgs {
     const void *q, *k, *v;           // [B][T][H][DK], [B][T][H][DK], [B][T][H][DV]
     const float *g;                  // null, [B][T][H] or [H], by `decay`
@@ -62,7 +69,7 @@ struct LinArgs {
     float *fwd, *rev;                // [B H][(segs - 1) subs][DV][DK]
     float *fac;                      // [2][B H][(segs - 1) subs]: the root of a piece's decay
     float *entry;                    // [B H][DV][DK]: S0, where S_T overwrites it; or null
-    float *sums;                     // [B H][chunks][4]: a chunk's a, a^2, b and b^2, see qd_linattn_bwd.hip
+    LinSums *sums;                   // [B H][chunks]
     float *tok;                      // [3][B H][T]: terms of dg
     float *edge;                     // [B H][segs + 1][8]: <S, R> at the segments' borders, by wave
     float *chain, *head;             // [B H][chunks]: c; [B][chunks][H]: sums of dg over tokens
@@ -280,6 +287,18 @@ __device__ __forceinline__ double lin_dpp(double x) {
     const uint64_t v = __builtin_bit_cast(uint64_t, x);
     const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, true);
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sum over a wave, in every lane
+__device__ __forceinline__ double lin_total(double x) {
+    x += lin_dpp<0x111, 0xf>(x);
+    x += lin_dpp<0x112, 0xf>(x);
+    x += lin_dpp<0x114, 0xf>(x);
+    x += lin_dpp<0x118, 0xf>(x);
+    x += lin_dpp<0x142, 0xa>(x);
+    x += lin_dpp<0x143, 0xc>(x);
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 // One wave.  A decay of zero (g = -inf) forgets all that came before: 4096 powers of two make

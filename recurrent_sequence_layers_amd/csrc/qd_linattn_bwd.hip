@@ -133,11 +133,12 @@ struct Walk {
         for (int k = 0; k < NS; ++k) s += lds.part[k][lane & (C - 1)];
         term(REV ? 2 : 1, n, true, lane, s);
         s = lane < C ? s : 0.f;
-        const float sum = wave_inclusive_sum(s), squares = wave_inclusive_sum(s * s);
-        float *to = a.sums + (static_cast<size_t>(bh) * ((a.T + C - 1) / C) + n) * 4 + (REV ? 2 : 0);
+        const float sum = wave_inclusive_sum(s);
+        const double squares = lin_total(static_cast<double>(s) * s);
+        LinSums &to = a.sums[static_cast<size_t>(bh) * ((a.T + C - 1) / C) + n];
         if (lane == 63) {
-            to[0] = sum;
-            to[1] = squares;
+            (REV ? to.b : to.a) = sum;
+            (REV ? to.bb : to.aa) = squares;
         }
     }
 };
@@ -600,18 +601,6 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
 // ---------------------------------------------------------------- dg
 constexpr int kDgWaves = 16, kDgChunks = 1024;
 
-// The chain of c for chunk n by one wave, from all the chunks' sums.
-__device__ __forceinline__ double wave_total(double x) {
-    x += lin_dpp<0x111, 0xf>(x);
-    x += lin_dpp<0x112, 0xf>(x);
-    x += lin_dpp<0x114, 0xf>(x);
-    x += lin_dpp<0x118, 0xf>(x);
-    x += lin_dpp<0x142, 0xa>(x);
-    x += lin_dpp<0x143, 0xc>(x);
-    const uint64_t v = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
 struct Ends {
     int first, count;                // the segment's chunks
     double before, behind;           // <S, R> at its borders
@@ -622,24 +611,25 @@ struct Ends {
         for (int w = 0; w < a.DK / 16; ++w) behind += e[8 + w];
     }
 };
+// The chain of c for chunk n by one wave, from all the chunks' sums.
 __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, int n, int lane) {
     const Ends e(a, bh, nc, n / a.seg_chunks);
-    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc + e.first;
+    const LinSums *sums = a.sums + bh * nc + e.first;
     const int at = n - e.first;
     double D = 0, V = 0, later = 0, passed = 0, own = 0;
     for (int m = lane; m < e.count; m += kWave) {
-        const f32x4 x = sums[m];
-        const double d = static_cast<double>(x[0]) - x[2], v = static_cast<double>(x[1]) + x[3];
+        const LinSums x = sums[m];
+        const double d = static_cast<double>(x.a) - x.b, v = x.aa + x.bb;
         D += d;
         V += v;
         later += m > at ? d : 0;
         passed += m > at ? v : m == at ? 0.5 * v : 0;
-        own += m == at ? x[2] : 0;
+        own += m == at ? x.b : 0;
     }
-    D = wave_total(D);
-    V = wave_total(V);
-    return static_cast<float>(e.behind + wave_total(later) - wave_total(own) -
-                              (V > 0 ? (e.behind + D - e.before) / V * wave_total(passed) : 0));
+    D = lin_total(D);
+    V = lin_total(V);
+    return static_cast<float>(e.behind + lin_total(later) - lin_total(own) -
+                              (V > 0 ? (e.behind + D - e.before) / V * lin_total(passed) : 0));
 }
 
 // The same for all of a segment's chunks, where they are many: one workgroup, from the last chunk on,
@@ -651,16 +641,16 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
     const size_t bh = blockIdx.x / a.segs;
     const int wave = wave_id(), lane = lane_id();
     const Ends ends(a, bh, nc, blockIdx.x % a.segs);
-    const f32x4 *sums = reinterpret_cast<const f32x4 *>(a.sums) + bh * nc + ends.first;
+    const LinSums *sums = a.sums + bh * nc + ends.first;
     float *c = a.chain + bh * nc + ends.first;
     double D = 0, V = 0;
     for (int m = threadIdx.x; m < ends.count; m += 64 * kDgWaves) {
-        const f32x4 x = sums[m];
-        D += static_cast<double>(x[0]) - x[2];
-        V += static_cast<double>(x[1]) + x[3];
+        const LinSums x = sums[m];
+        D += static_cast<double>(x.a) - x.b;
+        V += x.aa + x.bb;
     }
-    D = wave_total(D);
-    V = wave_total(V);
+    D = lin_total(D);
+    V = lin_total(V);
     if (lane == 0) {
         total[wave][0] = D;
         total[wave][1] = V;
@@ -676,10 +666,10 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
     for (int last = ends.count; last > 0; last -= kDgChunks) {
         const int first = max(last - kDgChunks, 0), count = last - first;
         for (int m = threadIdx.x; m < count; m += 64 * kDgWaves) {
-            const f32x4 x = sums[first + m];
-            sd[m] = static_cast<double>(x[0]) - x[2];
-            sb[m] = x[2];
-            sv[m] = static_cast<double>(x[1]) + x[3];
+            const LinSums x = sums[first + m];
+            sd[m] = static_cast<double>(x.a) - x.b;
+            sb[m] = x.b;
+            sv[m] = x.aa + x.bb;
         }
         __syncthreads();
         if (wave == 0) {
@@ -785,7 +775,8 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * 8 * (a.segs + 1) + 6 * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) * sizeof(float);
+    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * 8 * (a.segs + 1) + (2 + sizeof(LinSums) / 4) * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) *
+           sizeof(float);
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -803,8 +794,8 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
         if (hipError_t e = launch_lin_states(dtype, a, true, true, a.dg || a.dS0, stream)) return e;
     if (a.dg) {
         const size_t chunks = (a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype);
-        a.sums = p;
-        a.tok = a.sums + 4 * bh * chunks;
+        a.sums = reinterpret_cast<LinSums *>(p);
+        a.tok = reinterpret_cast<float *>(a.sums + bh * chunks);
         a.edge = a.tok + 3 * bh * a.T;
         a.chain = a.edge + bh * 8 * (a.segs + 1);
         a.head = a.chain + bh * chunks;
