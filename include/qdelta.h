@@ -436,7 +436,10 @@ int qdelta_linattn_step(const void *q, const void *k, const void *v, const float
  *   d_o [B][T][H][d_v] elements, dS_T [B][H][d_v][d_k] fp32 or NULL (zero)
  *   dq, dk [B][T][H][d_k], dv [B][T][H][d_v] elements
  *   dg        like g, fp32, or NULL (not written); with g_per_head summed over tokens and
- *             sequences; NULL when g is
+ *             sequences; NULL when g is.  Zero where g is -INFINITY.  Elsewhere its error is
+ *             relative to the terms around it (the inner product of the state and its gradient
+ *             at the ends of the token's chunk), not to itself: where a token's own decay is
+ *             strong and its neighbours' are not, dg / exp(g) is rounding noise.
  *   dS0       [B][H][d_v][d_k] fp32 or NULL (not written)
  * workspace: at least qdelta_linattn_bwd_workspace_bytes (want_dg: whether dg is given), 16-byte
  * aligned, overwritten.

@@ -39,10 +39,10 @@ namespace qd {
 
 enum LinDecay { kNoDecay = 0, kTokenDecay = 1, kHeadDecay = 2 };
 
-// A chunk's sums of a and b and of their squares, for the chain of qd_linattn_bwd.hip.  The squares
-// are in 64 bits: those of ordinary fp32 terms leave fp32's range.
+// A chunk's sums of a and b and of their squares, and its decay, for the chain of qd_linattn_bwd.hip.
+// The squares are in 64 bits: those of ordinary fp32 terms leave fp32's range.
 struct LinSums {
-    float a, b;
+    float a, b, all, unused;
     double aa, bb;
 };
 

@@ -20,12 +20,15 @@
 //   a_s = e^{G_s} do_s S q_s,  b_i = e^{G_C - G_i} v_i R k_i,  M = D o (Q K^T) o (dO V^T),
 //   c = e^{G_C} <S, R>.
 //
-// Every term is one that g_t scales: no difference of large sums.  The walks write a, b and
-// x_t = sum_{s>t} M[s][t] - sum_{i<t} M[t][i], whose prefix sums are the third term, and c comes
-// from a chain over the chunks: with E_n = <S, R> behind chunk n, c_n = E_n - sum b and
-// E_{n-1} = c_n + sum a, from the segment's end on (<S_T, dS_T>, or what the states at the border give).
+// Every term is one that g_t scales, and within a chunk each sum is of such terms alone, so behind a
+// strong decay they are as small as dg is.  The walks write a, b and the third term: sums over
+// parts of M's rows and columns, block by block.  c comes from a chain over the chunks: with
+// E_n = <S, R> behind chunk n, c_n = E_n - sum b and E_{n-1} = c_n + sum a, from the segment's end on
+// (<S_T, dS_T>, or what the states at the border give).  That is a difference: c is as exact as <S, R>
+// at its chunk's ends is, not as itself, unless the chunk's whole decay is zero in fp32.  Then c is
+// zero, and the chain ends on either side of the chunk with its own sums.
 // a and b are taken before anything is rounded (the state split as in qd_linattn.h), since dg is fp32.
-// The chain adds up their roundings; what it misses <S, R> by at the segment's start is taken back in
+// The chain adds up their roundings; what it misses <S, R> by at its start is taken back in
 // proportion to the squares of the terms that it has passed, which is where it came from.
 #include "qd_internal.h"
 #include "qd_linattn.h"
@@ -36,6 +39,20 @@ namespace {
 
 __device__ __forceinline__ float sum16(float x) { return group_sum(x, 16); }
 __device__ __forceinline__ float sum64(float x) { return group_sum(x, 64); }
+// Sums over 16 lanes: from this one on, and of those before it
+__device__ __forceinline__ float behind16(float x) {
+    x += dpp_src<0x101, 0xf>(x);   // row_shl:1
+    x += dpp_src<0x102, 0xf>(x);
+    x += dpp_src<0x104, 0xf>(x);
+    return x + dpp_src<0x108, 0xf>(x);
+}
+__device__ __forceinline__ float before16(float x) {
+    x = dpp_src<0x111, 0xf>(x);    // row_shr:1
+    x += dpp_src<0x111, 0xf>(x);
+    x += dpp_src<0x112, 0xf>(x);
+    x += dpp_src<0x114, 0xf>(x);
+    return x + dpp_src<0x118, 0xf>(x);
+}
 
 // 8 x 4096 tokens, 16 heads, 128 x 128, bf16, the decays' gradient too: 394 to 400 us, without it 327.
 // The 944 MB would take 191 at the rate of a copy; the products, half of them for the 24 bits that dg
@@ -68,7 +85,9 @@ struct BwdLds {
     static constexpr bool later(bool dg) { return dg || (C == 64 && DK + DV < 256); }
     LinTile<P, C, C> p[P::kBytes == 4 ? 3 : 2];
     __device__ __forceinline__ LinTile<P, C, C> &second(bool dg, int m) { return p[P::kBytes == 4 && dg ? 1 + (m & 1) : 1]; }
-    float rows[NB][16], cols[NB][16];  // strict row and column sums of M's blocks
+    // Of M's blocks the sums of rows and of columns; of those on the diagonal, in rows, what is from
+    // each token on and before it
+    float rows[NB][16], cols[NB][16];
     float part[8][C];                  // a or b, by the columns' wave
 
     // Walks of one chunk have P as a sum of two: over few tokens its roundings would not average out.
@@ -125,9 +144,10 @@ struct Walk {
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), lin_rsrc(to, valid ? min(a.T - n * C, C) * 4 : 0),
                                               tid * 4, 0, 0);
     }
-    // a (backwards b) of chunk n from its NS parts, with its sum and that of its squares: one wave
+    // a (backwards b) of chunk n from its NS parts, with its sum and that of its squares (forwards the
+    // chunk's decay too): one wave
     template <bool REV, int NS, class L>
-    __device__ __forceinline__ void terms(const L &lds, int n) const {
+    __device__ __forceinline__ void terms(const L &lds, int n, float all) const {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NS; ++k) s += lds.part[k][lane & (C - 1)];
@@ -139,6 +159,7 @@ struct Walk {
         if (lane == 63) {
             (REV ? to.b : to.a) = sum;
             (REV ? to.bb : to.aa) = squares;
+            if (!REV) to.all = all;
         }
     }
 };
@@ -267,17 +288,25 @@ __device__ __forceinline__ void product(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
     if (w.few()) P::st4(lds.low(0).four(i, j, w.l), ov - P::f32(P::cvt(ov)));
     if constexpr (DG) {
         const f32x4 qk = lin_block<P>(next.k, next.q, j, i, w.l);
-        f32x4 col;
         float row = 0.f;
+        if (i == j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = t + e < s ? ov[e] * qk[e] : 0.f;
-            row += x;
-            col[e] = sum16(x);
+            for (int e = 0; e < 4; ++e) {        // from token s on, the columns before it
+                const float x = behind16(t + e < s ? ov[e] * qk[e] : 0.f);
+                row += t + e < s ? x : 0.f;
+            }
+        } else {
+            f32x4 col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = ov[e] * qk[e];
+                row += x;
+                col[e] = sum16(x);
+            }
+            if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
         }
         row += __shfl_xor(row, 16);
         row += __shfl_xor(row, 32);
-        if (w.r16 == 0) *reinterpret_cast<f32x4 *>(&lds.cols[p][4 * w.g4]) = col;
         if (w.lane < 16) lds.rows[p][w.r16] = row;
     }
 }
@@ -329,14 +358,25 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
         }
         fetch(m + 2);
         if constexpr (DG && !REV) {
+            // token e of block i: the rows from it on of the blocks to its left, the columns before it
+            // of those below, all of what is both
             const int i = (tid >> 4) & (C / 16 - 1), e = tid & 15;
-            float x = 0.f;
+            float row = 0.f, col = 0.f;
 #pragma unroll
             for (int j = 0; j < C / 16; ++j) {
-                if (j >= i) x += lds.cols[j * (j + 1) / 2 + i][e];
-                if (j <= i) x -= lds.rows[i * (i + 1) / 2 + j][e];
+                if (j < i) row += lds.rows[i * (i + 1) / 2 + j][e];
+                if (j > i) col += lds.cols[j * (j + 1) / 2 + i][e];
             }
-            w.term(0, n, valid, tid, x);
+#pragma unroll
+            for (int j = 2; j < C / 16; ++j)
+#pragma unroll
+                for (int k = 0; k < j - 1; ++k)
+                    if (k < i && i < j) {        // e and the rows behind it, and those before it
+                        const float x = lds.rows[j * (j + 1) / 2 + k][e];
+                        row += x;
+                        col += x;
+                    }
+            w.term(0, n, valid, tid, lds.rows[i * (i + 3) / 2][e] + behind16(row) + before16(col));
         }
         __syncthreads();
         if constexpr (REV) {
@@ -480,7 +520,7 @@ __device__ __forceinline__ void dq_walk(const LinArgs &a, BwdLds<P, DK, DV> &lds
         help(m);
         spill_out<P, C>(x.q, out, t0, w.l);
         lin_update<P, C, DG ? 3 : 2>(S, x.v, kf, gates.after, gates.all[0], w.l);
-        if (DG && wave == 1) w.template terms<false, NS>(lds, w.c0 + m);
+        if (DG && wave == 1) w.template terms<false, NS>(lds, w.c0 + m, gates.all[0]);
         decays.ahead(lds, m);
         __syncthreads();
     }
@@ -557,7 +597,7 @@ __device__ __forceinline__ void dk_walk(const Walk<P, DK, DV> &w, BwdLds<P, DK, 
         if constexpr (L::later(DG)) own();
         spill_out<P, C>(x.k, out, t0, w.l);
         lin_update<P, C, NS>(R, x.o, qf, gates.before, gates.all[0], w.l);
-        if (DG && w.wave == 1) w.template terms<true, 4>(lds, w.template chunk<true>(m));
+        if (DG && w.wave == 1) w.template terms<true, 4>(lds, w.template chunk<true>(m), 0.f);
         decays.ahead(lds, m);
         __syncthreads();
     }
@@ -616,8 +656,25 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
     const Ends e(a, bh, nc, n / a.seg_chunks);
     const LinSums *sums = a.sums + bh * nc + e.first;
     const int at = n - e.first;
-    double D = 0, V = 0, later = 0, passed = 0, own = 0;
+    // what forgets all ends the chain: behind it <S, R> is its sum of b, before it that of a
+    int lo = -1, hi = e.count;
     for (int m = lane; m < e.count; m += kWave) {
+        if (sums[m].all != 0.f) continue;
+        if (m <= at) lo = m;
+        else hi = min(hi, m);
+    }
+    if (__any(lo >= 0 || hi < e.count)) {
+#pragma unroll
+        for (int k = 1; k < kWave; k *= 2) {
+            lo = max(lo, __shfl_xor(lo, k));
+            hi = min(hi, __shfl_xor(hi, k));
+        }
+    }
+    if (lo == at) return 0.f;
+    const double start = lo >= 0 ? sums[lo].b : e.before, end = hi < e.count ? sums[hi].a : e.behind;
+    double D = 0, V = 0, later = 0, passed = 0, own = 0;
+    for (int m = lane; m < hi; m += kWave) {
+        if (m <= lo) continue;
         const LinSums x = sums[m];
         const double d = static_cast<double>(x.a) - x.b, v = x.aa + x.bb;
         D += d;
@@ -628,8 +685,7 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
     }
     D = lin_total(D);
     V = lin_total(V);
-    return static_cast<float>(e.behind + lin_total(later) - lin_total(own) -
-                              (V > 0 ? (e.behind + D - e.before) / V * lin_total(passed) : 0));
+    return static_cast<float>(end + lin_total(later) - lin_total(own) - (V > 0 ? (end + D - start) / V * lin_total(passed) : 0));
 }
 
 // The same for all of a segment's chunks, where they are many: one workgroup, from the last chunk on,
@@ -644,10 +700,19 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs 
     const LinSums *sums = a.sums + bh * nc + ends.first;
     float *c = a.chain + bh * nc + ends.first;
     double D = 0, V = 0;
+    bool forgets = false;
     for (int m = threadIdx.x; m < ends.count; m += 64 * kDgWaves) {
         const LinSums x = sums[m];
         D += static_cast<double>(x.a) - x.b;
         V += x.aa + x.bb;
+        forgets = forgets || x.all == 0.f;
+    }
+    if (__syncthreads_or(forgets)) {             // several chains: a chunk at a time
+        for (int m = wave; m < ends.count; m += kDgWaves) {
+            const float x = chain_at(a, bh, nc, ends.first + m, lane);
+            if (lane == 0) c[m] = x;
+        }
+        return;
     }
     D = lin_total(D);
     V = lin_total(V);
@@ -718,11 +783,11 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
     if (h < a.H && live > 0) {
         const float *x = a.tok + bh * a.T + n * C, *ta = x + bhs * a.T, *tb = ta + bhs * a.T;
         const int back = 63 - lane;
-        const float y = lane < live ? x[lane] + tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
-        const float before = wave_inclusive_sum(y) - y;
+        const float pairs = lane < live ? x[lane] : 0.f, y = lane < live ? tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
+        const float upto = __shfl_up(wave_inclusive_sum(y), 1), before = lane ? upto : 0.f;
         const float behind = __shfl(wave_inclusive_sum(z), back);
         const float c = a.seg_chunks <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.chain[bh * nc + n];
-        v = lane < live ? c + (before + behind) : 0.f;
+        v = lane < live ? c + (pairs + (before + behind)) : 0.f;
     }
     if (a.decay == kHeadDecay) {
         v = sum64(v);
