@@ -223,12 +223,18 @@ template <class Store>
 __global__ __launch_bounds__(kColThreads) void column_sum_kernel(const float *__restrict__ m, int rows, long long cols,
                                                                  Store store) {
     __shared__ ColShared s;
-    column_sum_block(m, rows, cols, blockIdx.x, store, s);
+    for (long long block = blockIdx.x; block * 64 < cols; block += gridDim.x) {
+        column_sum_block(m, rows, cols, block, store, s);
+        __syncthreads();                         // s is written again
+    }
 }
+// A launch has fewer than 2^32 threads; one of more is cut short without an error.
+constexpr long long kColBlocks = 1LL << 21;
 template <class Store>
 void column_sum(const float *m, int rows, long long cols, Store store, hipStream_t stream) {
-    hipLaunchKernelGGL((column_sum_kernel<Store>), dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(kColThreads), 0,
-                       stream, m, rows, cols, store);
+    const long long blocks = (cols + 63) / 64;
+    hipLaunchKernelGGL((column_sum_kernel<Store>), dim3(static_cast<unsigned>(blocks < kColBlocks ? blocks : kColBlocks)),
+                       dim3(kColThreads), 0, stream, m, rows, cols, store);
 }
 
 }  // namespace qd
