@@ -91,7 +91,8 @@ struct Gate {
 };
 __device__ __forceinline__ Gate gate_of(float z, int act) {
     if (act == 0) return Gate{z, 1.f};
-    const float p = sigmoidf(z), q = p * (1.f - p);
+    // 1 - p as e^-z p, which keeps its digits where p is near one
+    const float e = __builtin_amdgcn_exp2f(-z * kLog2e), p = sigmoidf(z), q = p * (fminf(e, 3.0e38f) * p);
     return act == 1 ? Gate{p, q} : Gate{z * p, fmaf(z, q, p)};
 }
 
