@@ -39,11 +39,12 @@ namespace qd {
 
 enum LinDecay { kNoDecay = 0, kTokenDecay = 1, kHeadDecay = 2 };
 
-// A chunk's sums of a and b and of their squares, and its decay, for the chain of qd_linattn_bwd.hip.
-// The squares are in 64 bits: those of ordinary fp32 terms leave fp32's range.
+// A chunk's sums of a and b and its decay, for the chain of qd_linattn_bwd.hip.  size_a, size_b: means
+// of |a| and |b| over 64 tokens, which stay within fp32 where squares, and sums, would not.
 struct LinSums {
-    float a, b, all, unused;
-    double aa, bb;
+    float a, b, size_a, size_b, all;
+    float c;                         // by the chain, where it is a launch of its own
+    __device__ __forceinline__ double weight() const { return static_cast<double>(size_a) * size_a + static_cast<double>(size_b) * size_b; }
 };
 
 struct LinArgs {
@@ -72,7 +73,8 @@ struct LinArgs {
     LinSums *sums;                   // [B H][chunks]
     float *tok;                      // [3][B H][T]: terms of dg
     float *edge;                     // [B H][segs + 1][8]: <S, R> at the segments' borders, by wave
-    float *chain, *head;             // [B H][chunks]: c; [B][chunks][H]: sums of dg over tokens
+    double *chain;                   // [B H][chunks][2]: c before what is missed is taken back, and its share of that
+    float *head;                     // [B][chunks][H]: sums of dg over tokens
 };
 
 bool lin_supported(int dtype, int dk, int dv);
@@ -287,18 +289,6 @@ __device__ __forceinline__ double lin_dpp(double x) {
     const uint64_t v = __builtin_bit_cast(uint64_t, x);
     const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, true);
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xf, true);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-// Sum over a wave, in every lane
-__device__ __forceinline__ double lin_total(double x) {
-    x += lin_dpp<0x111, 0xf>(x);
-    x += lin_dpp<0x112, 0xf>(x);
-    x += lin_dpp<0x114, 0xf>(x);
-    x += lin_dpp<0x118, 0xf>(x);
-    x += lin_dpp<0x142, 0xa>(x);
-    x += lin_dpp<0x143, 0xc>(x);
-    const uint64_t v = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 // One wave.  A decay of zero (g = -inf) forgets all that came before: 4096 powers of two make

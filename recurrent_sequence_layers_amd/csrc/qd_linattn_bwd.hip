@@ -29,7 +29,7 @@
 // zero, and the chain ends on either side of the chunk with its own sums.
 // a and b are taken before anything is rounded (the state split as in qd_linattn.h), since dg is fp32.
 // The chain adds up their roundings; what it misses <S, R> by at its start is taken back in
-// proportion to the squares of the terms that it has passed, which is where it came from.
+// proportion to the squares of the sizes of the terms that it has passed, which is where it came from.
 #include "qd_internal.h"
 #include "qd_linattn.h"
 #include "qd_mixer.h"
@@ -144,8 +144,8 @@ struct Walk {
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), lin_rsrc(to, valid ? min(a.T - n * C, C) * 4 : 0),
                                               tid * 4, 0, 0);
     }
-    // a (backwards b) of chunk n from its NS parts, with its sum and that of its squares (forwards the
-    // chunk's decay too): one wave
+    // a (backwards b) of chunk n from its NS parts, with its sum and mean size (forwards the chunk's
+    // decay too): one wave
     template <bool REV, int NS, class L>
     __device__ __forceinline__ void terms(const L &lds, int n, float all) const {
         float s = 0.f;
@@ -153,12 +153,11 @@ struct Walk {
         for (int k = 0; k < NS; ++k) s += lds.part[k][lane & (C - 1)];
         term(REV ? 2 : 1, n, true, lane, s);
         s = lane < C ? s : 0.f;
-        const float sum = wave_inclusive_sum(s);
-        const double squares = lin_total(static_cast<double>(s) * s);
+        const float sum = wave_inclusive_sum(s), size = wave_inclusive_sum(fabsf(s) * (1.f / 64));
         LinSums &to = a.sums[static_cast<size_t>(bh) * ((a.T + C - 1) / C) + n];
         if (lane == 63) {
             (REV ? to.b : to.a) = sum;
-            (REV ? to.bb : to.aa) = squares;
+            (REV ? to.size_b : to.size_a) = size;
             if (!REV) to.all = all;
         }
     }
@@ -641,6 +640,18 @@ __global__ __launch_bounds__(kBwdThreads) __attribute__((amdgpu_waves_per_eu(3, 
 // ---------------------------------------------------------------- dg
 constexpr int kDgWaves = 16, kDgChunks = 1024;
 
+// Sum over a wave, in every lane
+__device__ __forceinline__ double lin_total(double x) {
+    x += lin_dpp<0x111, 0xf>(x);
+    x += lin_dpp<0x112, 0xf>(x);
+    x += lin_dpp<0x114, 0xf>(x);
+    x += lin_dpp<0x118, 0xf>(x);
+    x += lin_dpp<0x142, 0xa>(x);
+    x += lin_dpp<0x143, 0xc>(x);
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
 struct Ends {
     int first, count;                // the segment's chunks
     double before, behind;           // <S, R> at its borders
@@ -676,7 +687,7 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
     for (int m = lane; m < hi; m += kWave) {
         if (m <= lo) continue;
         const LinSums x = sums[m];
-        const double d = static_cast<double>(x.a) - x.b, v = x.aa + x.bb;
+        const double d = static_cast<double>(x.a) - x.b, v = x.weight();
         D += d;
         V += v;
         later += m > at ? d : 0;
@@ -688,85 +699,106 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
     return static_cast<float>(end + lin_total(later) - lin_total(own) - (V > 0 ? (end + D - start) / V * lin_total(passed) : 0));
 }
 
-// The same for all of a segment's chunks, where they are many: one workgroup, from the last chunk on,
-// 1024 at a time.
+// The same for all of a segment's chunks, where they are many: one workgroup, 1024 chunks at a time, from
+// the last one on; then from the first one on, since what a chain misses is known at its start.
 constexpr int kFewChunks = 256;             // a call of 7 chunks 34 us, by a launch 38; 64: 89, 94; 256: 152, 154; 2048: 1070, 1044
 __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a, const int nc) {
-    __shared__ double sd[kDgChunks], sb[kDgChunks], sv[kDgChunks];
-    __shared__ double total[kDgWaves][2];
+    __shared__ float sa[kDgChunks], sb[kDgChunks];
+    __shared__ double sv[kDgChunks];             // negative: the chunk forgets all
+    __shared__ double missed, part[kDgWaves];    // by a term's weight: of the first chain, and of a wave's last chunk that forgets
+    __shared__ bool any[kDgWaves];
     const size_t bh = blockIdx.x / a.segs;
     const int wave = wave_id(), lane = lane_id();
     const Ends ends(a, bh, nc, blockIdx.x % a.segs);
-    const LinSums *sums = a.sums + bh * nc + ends.first;
-    float *c = a.chain + bh * nc + ends.first;
-    double D = 0, V = 0;
-    bool forgets = false;
-    for (int m = threadIdx.x; m < ends.count; m += 64 * kDgWaves) {
-        const LinSums x = sums[m];
-        D += static_cast<double>(x.a) - x.b;
-        V += x.aa + x.bb;
-        forgets = forgets || x.all == 0.f;
-    }
-    if (__syncthreads_or(forgets)) {             // several chains: a chunk at a time
-        for (int m = wave; m < ends.count; m += kDgWaves) {
-            const float x = chain_at(a, bh, nc, ends.first + m, lane);
-            if (lane == 0) c[m] = x;
-        }
-        return;
-    }
-    D = lin_total(D);
-    V = lin_total(V);
-    if (lane == 0) {
-        total[wave][0] = D;
-        total[wave][1] = V;
-    }
-    __syncthreads();
-    D = V = 0;
-    for (int w = 0; w < kDgWaves; ++w) {
-        D += total[w][0];
-        V += total[w][1];
-    }
+    LinSums *sums = a.sums + bh * nc + ends.first;
+    double *far = a.chain + 2 * (bh * nc + ends.first);
     double E = ends.behind, passed = 0;
-    const double part = V > 0 ? (E + D - ends.before) / V : 0;
     for (int last = ends.count; last > 0; last -= kDgChunks) {
         const int first = max(last - kDgChunks, 0), count = last - first;
         for (int m = threadIdx.x; m < count; m += 64 * kDgWaves) {
             const LinSums x = sums[first + m];
-            sd[m] = static_cast<double>(x.a) - x.b;
+            sa[m] = x.a;
             sb[m] = x.b;
-            sv[m] = x.aa + x.bb;
+            sv[m] = x.all == 0.f ? -1. : x.weight();
         }
         __syncthreads();
         if (wave == 0) {
-            // a lane's chunks are consecutive, from the last on
+            // a lane's chunks are consecutive, from the last on.  cut: one of them, or of those of the
+            // lanes before, forgets, and d and v are of what is behind it
             constexpr int PER = kDgChunks / 64;
             double d = 0, v = 0;
-            for (int i = 0; i < PER; ++i) {
-                const int m = count - 1 - (lane * PER + i);
-                if (m >= 0) {
-                    d += sd[m];
-                    v += sv[m];
-                }
-            }
-            double dd = d, vv = v;
-            for (int s = 1; s < 64; s *= 2) {
-                const double y = __shfl_up(dd, s), z = __shfl_up(vv, s);
-                if (lane >= s) {
-                    dd += y;
-                    vv += z;
-                }
-            }
-            double e = E + dd - d, p = passed + vv - v;
+            int cut = 0;
             for (int i = 0; i < PER; ++i) {
                 const int m = count - 1 - (lane * PER + i);
                 if (m < 0) break;
-                c[first + m] = static_cast<float>(e - sb[m] - part * (p + 0.5 * sv[m]));
-                e += sd[m];
-                p += sv[m];
+                if (sv[m] < 0) {
+                    cut = 1;
+                    d = sa[m];
+                    v = 0;
+                } else {
+                    d += static_cast<double>(sa[m]) - sb[m];
+                    v += sv[m];
+                }
             }
-            E += __shfl(dd, 63);
-            passed += __shfl(vv, 63);
+            for (int s = 1; s < 64; s *= 2) {
+                const double y = __shfl_up(d, s), z = __shfl_up(v, s);
+                const int q = __shfl_up(cut, s);
+                if (lane >= s && !cut) {
+                    d += y;
+                    v += z;
+                    cut = q;
+                }
+            }
+            double e = __shfl_up(d, 1), p = __shfl_up(v, 1);
+            const int before = __shfl_up(cut, 1);
+            if (lane == 0) e = p = 0;
+            if (lane == 0 || !before) {
+                e += E;
+                p += passed;
+            }
+            for (int i = 0; i < PER; ++i) {
+                const int m = count - 1 - (lane * PER + i);
+                if (m < 0) break;
+                double *to = far + 2 * static_cast<size_t>(first + m);
+                const double own = e - sb[m];
+                if (sv[m] < 0) {                 // what the chain behind it has missed
+                    to[0] = 0;
+                    to[1] = p > 0 ? own / p : 0;
+                    e = sa[m];
+                    p = 0;
+                } else {
+                    to[0] = own;
+                    to[1] = p + 0.5 * sv[m];
+                    e = own + sa[m];
+                    p += sv[m];
+                }
+            }
+            const bool cut_all = __shfl(cut, 63);
+            E = __shfl(d, 63) + (cut_all ? 0 : E);
+            passed = __shfl(v, 63) + (cut_all ? 0 : passed);
         }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) missed = passed > 0 ? (E - ends.before) / passed : 0;
+    __syncthreads();
+    double share = missed;                       // of the chain that goes on into these chunks
+    for (int first = 0; first < ends.count; first += 64 * kDgWaves) {
+        const int m = first + threadIdx.x;
+        const bool valid = m < ends.count, forgets = valid && sums[m].all == 0.f;
+        const double own = valid ? far[2 * static_cast<size_t>(m)] : 0, weight = valid ? far[2 * static_cast<size_t>(m) + 1] : 0;
+        const uint64_t mask = __ballot(forgets), lower = mask & ((1ull << lane) - 1);
+        if (lane == 0) any[wave] = mask != 0;
+        if (mask && lane == 63 - __builtin_clzll(mask)) part[wave] = weight;
+        const double near = __shfl(weight, lower ? 63 - __builtin_clzll(lower) : 0);
+        __syncthreads();
+        double mine = share;
+        for (int w = 0; w < kDgWaves; ++w) {
+            if (!any[w]) continue;
+            if (w < wave) mine = part[w];
+            share = part[w];
+        }
+        if (lower) mine = near;
+        if (valid) sums[m].c = forgets ? 0.f : static_cast<float>(own - mine * weight);
         __syncthreads();
     }
 }
@@ -786,7 +818,7 @@ __global__ __launch_bounds__(64 * kDgWaves) void lin_dg_kernel(const LinArgs a) 
         const float pairs = lane < live ? x[lane] : 0.f, y = lane < live ? tb[lane] : 0.f, z = back < live ? ta[back] : 0.f;
         const float upto = __shfl_up(wave_inclusive_sum(y), 1), before = lane ? upto : 0.f;
         const float behind = __shfl(wave_inclusive_sum(z), back);
-        const float c = a.seg_chunks <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.chain[bh * nc + n];
+        const float c = a.seg_chunks <= kFewChunks ? chain_at(a, bh, nc, n, lane) : a.sums[bh * nc + n].c;
         v = lane < live ? c + (pairs + (before + behind)) : 0.f;
     }
     if (a.decay == kHeadDecay) {
@@ -840,8 +872,9 @@ size_t lin_bwd_workspace(int dtype, int B, int T, int H, int dk, int dv, bool dg
     a.B = B; a.T = T; a.H = H; a.DK = dk; a.DV = dv;
     bwd_plan(dtype, a);
     const size_t bh = static_cast<size_t>(B) * H;
-    return (lin_states_floats(a, 2) + (dg ? 3 * bh * T + bh * 8 * (a.segs + 1) + (2 + sizeof(LinSums) / 4) * bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype)) : 0)) *
-           sizeof(float);
+    const size_t chunks = bh * ((T + lin_chunk(dtype) - 1) / lin_chunk(dtype));
+    const size_t terms = dg ? chunks * (sizeof(LinSums) + 2 * sizeof(double) + sizeof(float)) + (3 * bh * T + bh * 8 * (a.segs + 1)) * sizeof(float) : 0;
+    return lin_states_floats(a, 2) * sizeof(float) + terms;
 }
 
 hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
@@ -858,12 +891,12 @@ hipError_t launch_lin_bwd(int dtype, LinArgs a, void *ws, hipStream_t stream) {
     if (a.segs > 1)
         if (hipError_t e = launch_lin_states(dtype, a, true, true, a.dg || a.dS0, stream)) return e;
     if (a.dg) {
-        const size_t chunks = (a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype);
-        a.sums = reinterpret_cast<LinSums *>(p);
-        a.tok = reinterpret_cast<float *>(a.sums + bh * chunks);
+        const size_t chunks = bh * ((a.T + lin_chunk(dtype) - 1) / lin_chunk(dtype));
+        a.chain = reinterpret_cast<double *>(p);
+        a.sums = reinterpret_cast<LinSums *>(a.chain + 2 * chunks);
+        a.tok = reinterpret_cast<float *>(a.sums + chunks);
         a.edge = a.tok + 3 * bh * a.T;
-        a.chain = a.edge + bh * 8 * (a.segs + 1);
-        a.head = a.chain + bh * chunks;
+        a.head = a.edge + bh * 8 * (a.segs + 1);
     }
     return dtype == 1 ? bwd_typed<Bf16>(a, stream) : bwd_typed<F32>(a, stream);
 }
