@@ -385,7 +385,9 @@ __device__ __forceinline__ void bring(const Walk<P, DK, DV> &w, BwdLds<P, DK, DV
             else if (wave & 1) back_by_two<P>(wave >> 1, next.o, next.v, gates, lds.second(DG, m + 1), low ? &lds.low(1) : nullptr, w.l);
             else back_by_two<P>(wave >> 1, next.q, next.k, gates, lds.p[0], low ? &lds.low(0) : nullptr, w.l);
         } else {
-            for (int p = wave; p < LAST; p += NW) product<P, DK, DV, DG>(w, lds, m, p);
+            // two of eight waves take two of ten blocks: none of the diagonal's, whose sums take longer
+            for (int p = wave; p < LAST; p += NW)
+                product<P, DK, DV, DG>(w, lds, m, NW == 8 && L::NB == 10 ? 0x8764952031ull >> 4 * p & 15 : p);
         }
         __syncthreads();
     }
@@ -667,32 +669,40 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
     const Ends e(a, bh, nc, n / a.seg_chunks);
     const LinSums *sums = a.sums + bh * nc + e.first;
     const int at = n - e.first;
-    // what forgets all ends the chain: behind it <S, R> is its sum of b, before it that of a
-    int lo = -1, hi = e.count;
-    for (int m = lane; m < e.count; m += kWave) {
-        if (sums[m].all != 0.f) continue;
-        if (m <= at) lo = m;
-        else hi = min(hi, m);
-    }
-    if (__any(lo >= 0 || hi < e.count)) {
+    double start = e.before, end = e.behind, D, V, later, passed, own;
+    auto chunks = [&](int lo, int hi) {          // sums over those between; whether one of them forgets
+        bool forgets = false;
+        D = V = later = passed = own = 0;
+        for (int m = lane; m < hi; m += kWave) {
+            if (m <= lo) continue;
+            const LinSums x = sums[m];
+            const double d = static_cast<double>(x.a) - x.b, v = x.weight();
+            D += d;
+            V += v;
+            later += m > at ? d : 0;
+            passed += m > at ? v : m == at ? 0.5 * v : 0;
+            own += m == at ? x.b : 0;
+            forgets = forgets || x.all == 0.f;
+        }
+        return __any(forgets);
+    };
+    if (chunks(-1, e.count)) {
+        // what forgets all ends the chain: behind it <S, R> is its sum of b, before it that of a
+        int lo = -1, hi = e.count;
+        for (int m = lane; m < e.count; m += kWave) {
+            if (sums[m].all != 0.f) continue;
+            if (m <= at) lo = m;
+            else hi = min(hi, m);
+        }
 #pragma unroll
         for (int k = 1; k < kWave; k *= 2) {
             lo = max(lo, __shfl_xor(lo, k));
             hi = min(hi, __shfl_xor(hi, k));
         }
-    }
-    if (lo == at) return 0.f;
-    const double start = lo >= 0 ? sums[lo].b : e.before, end = hi < e.count ? sums[hi].a : e.behind;
-    double D = 0, V = 0, later = 0, passed = 0, own = 0;
-    for (int m = lane; m < hi; m += kWave) {
-        if (m <= lo) continue;
-        const LinSums x = sums[m];
-        const double d = static_cast<double>(x.a) - x.b, v = x.weight();
-        D += d;
-        V += v;
-        later += m > at ? d : 0;
-        passed += m > at ? v : m == at ? 0.5 * v : 0;
-        own += m == at ? x.b : 0;
+        if (lo == at) return 0.f;
+        if (lo >= 0) start = sums[lo].b;
+        if (hi < e.count) end = sums[hi].a;
+        chunks(lo, hi);
     }
     D = lin_total(D);
     V = lin_total(V);
@@ -701,7 +711,8 @@ __device__ __forceinline__ float chain_at(const LinArgs &a, size_t bh, int nc, i
 
 // The same for all of a segment's chunks, where they are many: one workgroup, 1024 chunks at a time, from
 // the last one on; then from the first one on, since what a chain misses is known at its start.
-constexpr int kFewChunks = 256;             // a call of 7 chunks 34 us, by a launch 38; 64: 89, 94; 256: 152, 154; 2048: 1070, 1044
+// A call of 7 chunks 34 us, by this launch 39; 64 399, 410; 256 782, 783; 512 1617, 1573; 2048 7212, 6630.
+constexpr int kFewChunks = 256;
 __global__ __launch_bounds__(64 * kDgWaves) void lin_chain_kernel(const LinArgs a, const int nc) {
     __shared__ float sa[kDgChunks], sb[kDgChunks];
     __shared__ double sv[kDgChunks];             // negative: the chunk forgets all

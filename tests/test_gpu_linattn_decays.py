@@ -130,3 +130,19 @@ def test_forgetting_tokens_over_many_chunks(qd):
     assert torch.equal(got, one.expand_as(got)) and not one[:, [1000, 1001, 4100, 8199]].any()
     for part in (slice(0, 1000), slice(1002, 4100), slice(4101, 8199)):
         near(one[:, part], want["dg"][:, part], scale["dg"][:, part], x, f"dg of {part}")
+
+
+@pytest.mark.parametrize("H,T", [(128, 8200), (3, 8200), (3, 40)])
+def test_one_heads_decays_leave_the_others_alone(qd, H, T):
+    """A head that forgets at every token, one that does at some, over 257 chunks in one walk, a cut time
+    axis and two chunks: the other heads' gradients are the same bits as without."""
+    x = inputs(1, T, 1, 64, 64, "f32", 37)
+    a = {n: dev(x[n]).repeat_interleave(H, 1 if n in ("S0", "dS_T") else 2) for n in BWD}
+    first = qd.qdelta_linattn_bwd(*[a[n] for n in BWD])
+    a["g"][:, :, 0] = float("-inf")
+    a["g"][:, ::7, 1] = float("-inf")
+    got = qd.qdelta_linattn_bwd(*[a[n] for n in BWD])
+    assert not got["dg"][:, :, 0].any() and not got["dg"][:, ::7, 1].any() and bool(got["dg"].isfinite().all())
+    for n, v in got.items():
+        axis = 1 if n == "dS0" else 2
+        assert torch.equal(v.narrow(axis, 2, H - 2), first[n].narrow(axis, 2, H - 2)), n
