@@ -416,7 +416,8 @@ int qdelta_group_norm_bwd(const void *x, const float *weight, const float *bias,
  * Evaluated in chunks of 64 (fp32: 32) tokens: a NaN or an infinity in a token reaches the outputs
  * of its whole chunk, the earlier tokens' too; a decay below 2^-126 over part of a chunk is zero,
  * and a growing one (g > 0) has to stay below 2^127 over any part of a chunk.  T == 0 writes
- * S_T = S0 (or zeros).
+ * S_T = S0 (or zeros).  In bf16 what enters the state is kept to 24 bits where S_T is given and to
+ * 16 where it is not, so the last bits of o depend on whether it is.
  * workspace: at least qdelta_linattn_fwd_workspace_bytes (0 where B*H*d_v/64 workgroups fill the
  * card; else the states of the segments that the time axis is cut into), 16-byte aligned.
  */
@@ -441,6 +442,8 @@ int qdelta_linattn_step(const void *q, const void *k, const void *v, const float
  *             at the ends of the token's chunk), not to itself: where a token's own decay is
  *             strong and its neighbours' are not, dg / exp(g) is rounding noise.
  *   dS0       [B][H][d_v][d_k] fp32 or NULL (not written)
+ * In bf16 the last bits of dq, dk and dv depend on whether dg and dS0 are given, as those of o do
+ * on S_T.
  * workspace: at least qdelta_linattn_bwd_workspace_bytes (want_dg: whether dg is given), 16-byte
  * aligned, overwritten.
  */

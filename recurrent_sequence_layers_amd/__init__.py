@@ -793,7 +793,7 @@ def qdelta_linattn_fwd(q, k, v, g=None, S0=None, lens=None, o=None, S_T=None, wa
     decays, fp32 [B,T,H], or [H] for every token alike, or None (no decay); S0 [B,H,d_v,d_k] fp32 or
     None.  lens [B] int32: the tokens of each right-padded sequence; rows of o past them are left as
     they were (zeros in an o allocated here).  Returns (o, S_T); S_T is None when want_state is
-    False, and may be passed as S0.  workspace: at least qdelta_linattn_fwd_workspace_bytes(...)
+    False (in bf16 the last bits of o depend on that), and may be passed as S0.  workspace: at least qdelta_linattn_fwd_workspace_bytes(...)
     bytes, allocated here when None and needed."""
     import torch
     lib = load_library()
@@ -839,8 +839,9 @@ def qdelta_linattn_bwd(q, k, v, g, S0, d_o, dS_T=None, want_dS0: bool = True, wa
     """Gradients of sum(o * d_o) + sum(S_T * dS_T) for qdelta_linattn_fwd on the same inputs.  With
     lens, rows past a sequence's end are not read, d_o's neither, and their gradients are zero.
     Returns a dict with dq, dk, dv (like their inputs), dg (like g, fp32; for a g of [H] summed over
-    tokens and sequences; None without g or unless want_dg) and dS0 (None unless want_dS0; also
-    given when S0 is None).  ``out`` may supply any of them; ``workspace`` a device buffer of at
+    tokens and sequences; None without g or unless want_dg; zero where g is -inf, elsewhere as exact
+    as the terms around the token are, not as itself) and dS0 (None unless want_dS0; also given when
+    S0 is None).  In bf16 the last bits of dq, dk and dv depend on want_dg and want_dS0.  ``out`` may supply any of them; ``workspace`` a device buffer of at
     least qdelta_linattn_bwd_workspace_bytes(...) bytes (allocated when None)."""
     import torch
     lib = load_library()

@@ -13,13 +13,16 @@
 //
 // Bound by HBM: every tensor is read once and written once.  A row sits in the registers of LG
 // lanes, one or two 16-byte vectors each; the grid is persistent, so a lane keeps its columns'
-// weights and gathers its columns' sums over all its rows, and the next row's vectors are on their
-// way while this one is reduced.  A channel count that the vector does not divide ends in a vector
+// weights and gathers its columns' sums over all its rows; forwards the next row's vectors are on
+// their way while this one is reduced.  A channel count that the vector does not divide ends in a vector
 // that starts earlier and overlaps the one before it: what overlaps is the same in both, and
 // counts once.  Rows that would not fit a workgroup's registers take the looping form, which reads
 // a row again for each of its passes.  32768 rows of 2048 in bf16 with post norm, gate, scale, residual
 // and pre norm: 133 us forward (671 MB, 5.05 TB/s), 220 backward (1074 MB, 4.9 TB/s, 7 us of it the
-// sums over the rows' partial sums), as fast as a copy; 64 rows are a launch, 4.4 us.
+// sums over the rows' partial sums), as fast as a copy; 64 rows are a launch, 4.4 us.  Backwards rows
+// above 2048 (fp32: 4096) take more registers than 1024 threads leave a lane, 8 (29) are spilled: 16384
+// x 4096 bf16 284 us where its bytes take 218.  The looping form is far from its bytes: 4096 x 12288
+// bf16 278 forward (102) and 1063 backward (163), where its sums go through memory for every row.
 #include "qd_block_norm.h"
 #include "qd_internal.h"
 #include "qd_mixer.h"

@@ -4,7 +4,7 @@
 // Bound by HBM: q, k, v read once, o written once.  A workgroup walks the chunks of one (sequence,
 // head, 64 value columns): four waves hold the state, sixteen columns each, and four more bring what
 // they need.  The column blocks of a head are put on the same XCD, so its L2 serves the second
-// reading of q and k.  8 x 4096 tokens, 16 heads, 128 x 128, bf16 (539 MB): 128 to 130 us, 4.1 to 4.2
+// reading of q and k.  8 x 4096 tokens, 16 heads, 128 x 128, bf16 (539 MB): 129 to 135 us, 4.0 to 4.2
 // TB/s of the 4.9 that a copy reaches; the same loads, barriers and stores without the products take
 // 127.  Four waves that load, compute and store in turn took 294 us, the two roles 179, and outputs in
 // whole rows instead of eight bytes a lane 149 where they had been 175.
@@ -12,7 +12,7 @@
 // Where (sequence, head, column block) leaves the card short of workgroups the time axis is cut into
 // segments: a first launch walks each segment but the last from zero, a second one joins the
 // segments' states, and the main one starts every segment from its own.  65536 tokens of 16 heads:
-// 1617 us uncut, 402 to 414 cut in eight, 136 of them for the states, which read k and v once more.
+// 1617 us uncut, 402 to 414 cut in eight, 138 of them for the states, which read k and v once more.
 #include "qd_internal.h"
 #include "qd_linattn.h"
 
@@ -73,8 +73,8 @@ __device__ __forceinline__ void lin_products(LinTile<P, C, D> &q, LinTile<P, C, 
 }
 // A wave's share of them: the loading waves (role 1) take seven of ten, the states' waves three. With
 // all ten on the loading waves the size above takes 144 us, and seven prompts of up to 1900 tokens,
-// 12 heads, 46 instead of 38. In fp32, where the states' waves have more to do, the loading waves
-// take all three.
+// 12 heads, 46 instead of 38 (other lengths up to 1900: up to 42). In fp32, where the states' waves
+// have more to do, the loading waves take all three.
 template <class P, int C, int D>
 __device__ __forceinline__ void lin_share(int role, int wave, LinTile<P, C, D> &q, LinTile<P, C, D> &k, const LinGates<C> &gates,
                                           LinTile<P, C, C> &to, LinTile<P, C, C> *low, const LinLane &l) {
@@ -209,8 +209,8 @@ __global__ __launch_bounds__(2 * kNT) LIN_TWO_WAVES void lin_fwd_kernel(const Li
 
 // The states alone, from zero (or S0, dS_T) over one piece of a segment: forwards with k, v and the
 // decay to the piece's end, backwards with q, do and the decay from its start.  Four waves; the
-// next chunk goes to LDS while this one is used.  Bound by HBM and the matrix products alike: 470 MB
-// of the 65536 tokens above at 3.5 TB/s with three addends, 3.8 with two.
+// next chunk goes to LDS while this one is used.  Short of HBM's rate: 470 MB of the 65536 tokens above
+// at 3.4 TB/s with three addends, 3.8 with two; vector units 40 % busy, matrix units 28 %.
 template <class P, int DK>
 struct StateLds {
     static constexpr int C = kLinChunk<P>;

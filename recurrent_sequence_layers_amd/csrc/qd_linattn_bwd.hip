@@ -54,11 +54,12 @@ __device__ __forceinline__ float before16(float x) {
     return x + dpp_src<0x118, 0xf>(x);
 }
 
-// 8 x 4096 tokens, 16 heads, 128 x 128, bf16, the decays' gradient too: 394 to 400 us, without it 327.
-// The 944 MB would take 191 at the rate of a copy; the products, half of them for the 24 bits that dg
-// is of, 242 at that of a large product.  The vector units, which split the states and their addends,
-// are 52 % busy, the matrix units 33 %, and the shares are even: the slowest waves of a chunk's two
-// intervals take 4900 and 5200 cycles in dq's walk, 5200 and 5700 in the other.
+// 8 x 4096 tokens, 16 heads, 128 x 128, bf16, the decays' gradient too: 394 to 416 us, without it 323.
+// The 944 MB would take 191 at the rate of a copy, and the two walks' 1.5 GB past the L2 305; the
+// products, half of them for the 24 bits that dg is of, 242 at that of a large product.  The vector
+// units, which split the states and their addends, are 56 % busy, the matrix units 36 %.  With dg the
+// roles' registers do not quite fit the 168 that twelve waves leave each: 20 are spilled (fp32 30),
+// without it 3.
 //
 // Twelve waves, two barriers a chunk.  Forwards four or eight waves hold the state, sixteen columns
 // each; backwards four hold it by its key columns and four by its value columns, a quarter each (one
